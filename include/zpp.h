@@ -276,6 +276,119 @@ ZPP_API zpp_status zpp_dequant_reduce_local(const void* codes, const float* scal
                                             float post_scale, void* out, zpp_dtype out_dt,
                                             cudaStream_t stream);
 
+/*
+ * The optimiser step and the product with quantised weights: what happens to a weight on
+ * either side of the collectives (no counterpart in the pages, which take both from the
+ * training framework around them). The three calls below obey the conventions above; every
+ * sum, state and norm is fp32 or wider inside.
+ */
+
+/* Global gradient norm and clip factor over a list of tensors, on the device:
+ *   norm = |pre_scale| * sqrt(sum over all tensors and elements of g^2)
+ *   coef = pre_scale * (norm > max_norm ? max_norm / norm : 1)
+ * coef is what zpp_adamw_step takes as grad_scale, so a step needs no host round trip.
+ * When the norm is not finite (an element is Inf or NaN, or the sum of squares leaves fp32's
+ * range) coef is NaN, which makes zpp_adamw_step skip the step.
+ *   grads       : HOST array [num_tensors] of device pointers, 16-byte aligned, each to
+ *                 sizes[t] contiguous elements of g_dt (ZPP_F16, ZPP_BF16 or ZPP_F32)
+ *   sizes       : HOST array [num_tensors], 0 allowed (its pointer is then not read); the
+ *                 sum at most ZPP_MAX_ELEMS. Read during the call only, as grads.
+ *   num_tensors : 0 .. ZPP_MAX_TENSORS (0: norm 0)
+ *   pre_scale   : finite (e.g. 1 / loss scale); max_norm: > 0, +Inf for no clipping
+ *   workspace   : device floats, at least zpp_grad_norm_workspace(sum of sizes, num_tensors);
+ *                 not shared with another stream's call in flight
+ *   out         : device, out[0] = norm, out[1] = coef
+ * The sums run in a fixed order (no atomics): the same input gives the same bits.
+ */
+ZPP_API zpp_status zpp_grad_norm(const void* const* grads, const int64_t* sizes,
+                                 int32_t num_tensors, zpp_dtype g_dt, float pre_scale,
+                                 float max_norm, float* workspace, float* out,
+                                 cudaStream_t stream);
+
+/* Floats of workspace for zpp_grad_norm; -1 on a negative argument. */
+ZPP_API int64_t zpp_grad_norm_workspace(int64_t total_elems, int32_t num_tensors);
+
+/* One tensor of an AdamW step; all pointers are device pointers. */
+typedef struct zpp_adamw_tensor {
+  float* param;            /* [n] fp32 master weights, updated */
+  const void* grad;        /* [n] of g_dt */
+  void* exp_avg;           /* m: [n] fp32, or [n] e4m3 codes with state_bits 8; updated */
+  void* exp_avg_sq;        /* v: [n] fp32, or [n] e4m3 codes of sqrt(v); updated */
+  float* exp_avg_scale;    /* state_bits 8: [ceil(n / ZPP_STATE_BLOCK)], updated; else unused */
+  float* exp_avg_sq_scale; /* as above, for sqrt(v) */
+  void* weight;            /* out, NULL or [n] of w_dt: the updated weights rounded */
+  int64_t n;               /* elements, 0 allowed (the pointers are then not read) */
+} zpp_adamw_tensor;
+
+typedef struct zpp_adamw_params {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;  /* 1 for the first step (bias correction) */
+  uint32_t seed; /* state_bits 8: seeds the stochastic rounding */
+} zpp_adamw_params;
+
+#define ZPP_STATE_BLOCK 256 /* elements per fp8 state scale */
+
+/*
+ * One AdamW step (decoupled weight decay) over a list of tensors. With c = *grad_scale (1
+ * when NULL) and t = step, per element:
+ *   g = c * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   weight = param rounded to nearest even into w_dt (the shard zpp_quant_blockwise reads)
+ * If c is not finite the whole step is skipped: nothing is written.
+ *
+ * state_bits 8: m and r = sqrt(v) are held as e4m3 codes with one fp32 scale per
+ * ZPP_STATE_BLOCK consecutive elements of a tensor (the last block may be shorter; amax over
+ * its finite values),
+ *   scale = amax * fl(1/448), value = code * scale  (448 * fl(1/amax) not finite: scale 0, codes 0)
+ * The step itself uses the unrounded m and v. Rounding is stochastic: with x = value * (448 * fl(1/amax))
+ * and h the e4m3 spacing at |x|, the code is floor(|x| / h + u) h with u = (k + 1/2) / 65536,
+ * k 16 bits of a hash of (seed, step, element number): the low ones for m, the high ones for
+ * r. So a running average moves in expectation even where its change is far below h (round
+ * to nearest would freeze it), and equal inputs give equal bits. r > 0 keeps at least the
+ * smallest code, so a denominator never collapses. Element numbers count blocks through
+ * the list: tensor t's element i has ZPP_STATE_BLOCK * (blocks of tensors 0..t-1) + i. An Inf
+ * or NaN gradient makes its own element's states NaN, no other's.
+ *   hash: all mod 2^32, key = (seed * 0x9E3779B9) ^ (step * 0x510E527F), i split in lo, hi:
+ *     x = lo * 0x9E3779B9 + hi * 0xA54FF53B + key;  x = (x ^ x >> 16) * 0xBB67AE85 + key
+ *     x = (x ^ x >> 15) * 0x9B05688D;               bits = x ^ x >> 16
+ *
+ *   tensors     : HOST array [num_tensors], read during the call only; the n sum to at most
+ *                 ZPP_MAX_ELEMS; param, grad, exp_avg, exp_avg_sq, weight 16-byte aligned
+ *   num_tensors : 0 .. ZPP_MAX_TENSORS
+ *   g_dt        : ZPP_F16, ZPP_BF16 or ZPP_F32; w_dt: ZPP_F16 or ZPP_BF16 (ZPP_F32 with a
+ *                 non-NULL weight: ZPP_ERR_UNSUPPORTED)
+ *   state_bits  : 32 or 8
+ *   hp          : HOST, read during the call: lr and weight_decay finite, 0 <= beta1, beta2 < 1,
+ *                 eps >= 0 and finite, step >= 1
+ *   grad_scale  : device, 4-byte aligned, or NULL
+ */
+ZPP_API zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors,
+                                  zpp_dtype g_dt, zpp_dtype w_dt, int32_t state_bits,
+                                  const zpp_adamw_params* hp, const float* grad_scale,
+                                  cudaStream_t stream);
+
+/*
+ * y = x W^T (+ bias) for a few vectors x, straight from the codes of a [rows][cols] matrix
+ * quantised row-major by zpp_quant_blockwise (blocks may run across rows):
+ *   y[j][r] = sum_c q[r][c] * scales[(r * cols + c) / block] * x[j][c]  (+ bias[r])
+ * Products and sums are fp32 (code times x is exact), y is rounded once.
+ *   codes, scales : as zpp_quant_blockwise writes them for n = rows * cols <= ZPP_MAX_ELEMS
+ *   rows, cols    : 0 <= rows < 2^31, 1 <= cols < 2^31; block, bits as in zpp_quant_blockwise
+ *   x             : [vecs] rows of cols elements of x_dt (ZPP_F16 or ZPP_BF16; ZPP_F32 ->
+ *                   ZPP_ERR_UNSUPPORTED), row j at x + j * x_stride, x_stride >= cols
+ *   vecs          : 0 .. 65535. Meant for a handful (decoding); every 32 read the codes once
+ *                   more, so for many vectors dequantise and use a matrix product
+ *   bias          : NULL or [rows] of x_dt
+ *   y             : out, row j at y + j * y_stride, y_stride >= rows, of y_dt (any zpp_dtype)
+ * x and y must be 16-byte aligned, bias 2-byte; the strides (in elements) may be any.
+ */
+ZPP_API zpp_status zpp_matvec_blockwise(const void* codes, const float* scales, int64_t rows,
+                                        int64_t cols, int32_t block, int32_t bits, const void* x,
+                                        zpp_dtype x_dt, int64_t vecs, int64_t x_stride,
+                                        const void* bias, void* y, zpp_dtype y_dt,
+                                        int64_t y_stride, cudaStream_t stream);
+
 /* Bytes of packed codes for n elements: n for INT8, ceil(n/2) for INT4; -1 on bad bits. */
 ZPP_API int64_t zpp_code_bytes(int64_t n, int32_t bits);
 

@@ -6,7 +6,9 @@ current CUDA stream, and raise on a non-OK status. Every step of the computation
 in the library's kernels: there is no CPU path, and a missing library or a CPU tensor
 is an error.
 """
+import array
 import ctypes
+import math
 import os
 import re
 
@@ -14,6 +16,7 @@ from . import build as _build
 
 ZPP_OK, ZPP_ERR_INVALID_ARG, ZPP_ERR_MISALIGNED, ZPP_ERR_UNSUPPORTED, ZPP_ERR_CUDA = range(5)
 ZPP_F16, ZPP_BF16, ZPP_F32 = 0, 1, 2
+ZPP_STATE_BLOCK = 256
 
 HEADER = os.path.join(_build.ROOT, "include", "zpp.h")
 
@@ -24,6 +27,19 @@ class Topology(ctypes.Structure):
 
 class LocalRange(ctypes.Structure):
     _fields_ = [("begin", ctypes.c_int32), ("end", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """One tensor of zpp_adamw_step (device addresses, element count)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq",
+                                               "exp_avg_scale", "exp_avg_sq_scale", "weight")] + [
+        ("n", ctypes.c_int64)]
+
+
+class AdamwParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps",
+                                               "weight_decay")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint32)]
 
 
 class ZppError(RuntimeError):
@@ -70,6 +86,10 @@ def lib():
         "zpp_dequant_reduce_local": [vp, vp, i64, i32, i32, i32, ctypes.c_float, vp, i32, vp],
         "zpp_device_fault": [ctypes.POINTER(ctypes.c_uint32), i32],
         "zpp_wait_selftest": [ctypes.c_uint64, vp],
+        "zpp_grad_norm": [vp, vp, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp],
+        "zpp_adamw_step": [vp, i32, i32, i32, i32, vp, vp, vp],
+        "zpp_matvec_blockwise": [vp, vp, i64, i64, i32, i32, vp, i32, i64, i64, vp, vp, i32, i64,
+                                 vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -79,6 +99,8 @@ def lib():
     L.zpp_code_bytes.restype = i64
     L.zpp_num_scales.argtypes = [i64, i32]
     L.zpp_num_scales.restype = i64
+    L.zpp_grad_norm_workspace.argtypes = [i64, i32]
+    L.zpp_grad_norm_workspace.restype = i64
     L.zpp_status_string.argtypes = [ctypes.c_int]
     L.zpp_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -180,6 +202,36 @@ def zpp_device_fault(clear=False):
 
 def zpp_wait_selftest(limit_ns, stream=0):
     return lib().zpp_wait_selftest(limit_ns, stream)
+
+
+def zpp_grad_norm(grad_ptrs, sizes, g_dt, pre_scale, max_norm, workspace, out, stream=0):
+    """grad_ptrs, sizes: Python sequences (marshalled into host arrays for the call)."""
+    ptrs, lens = array.array("q", grad_ptrs), array.array("q", sizes)
+    return lib().zpp_grad_norm(ptrs.buffer_info()[0], lens.buffer_info()[0], len(ptrs), g_dt,
+                               pre_scale, max_norm, workspace, out, stream)
+
+
+def zpp_grad_norm_workspace(total_elems, num_tensors):
+    return int(lib().zpp_grad_norm_workspace(total_elems, num_tensors))
+
+
+def zpp_adamw_step(tensors, g_dt, w_dt, state_bits, hp, grad_scale=0, stream=0):
+    """tensors: a sequence of AdamwTensor, or an array('q') with their fields one after the
+    other; hp: an AdamwParams."""
+    if isinstance(tensors, array.array):
+        num, at = len(tensors) // 8, tensors.buffer_info()[0]
+    else:
+        num = len(tensors)
+        tensors = (AdamwTensor * max(num, 1))(*tensors)
+        at = ctypes.addressof(tensors)
+    return lib().zpp_adamw_step(at, num, g_dt, w_dt, state_bits, ctypes.addressof(hp),
+                                grad_scale, stream)
+
+
+def zpp_matvec_blockwise(codes, scales, rows, cols, block, bits, x, x_dt, vecs, x_stride, bias, y,
+                         y_dt, y_stride, stream=0):
+    return lib().zpp_matvec_blockwise(codes, scales, rows, cols, block, bits, x, x_dt, vecs,
+                                      x_stride, bias, y, y_dt, y_stride, stream)
 
 
 def zpp_code_bytes(n, bits):
@@ -496,6 +548,155 @@ def dequant_reduce_local(codes, scales, slice_len, block, bits, sources, post_sc
                                     sources, float(post_scale), out.data_ptr(), _dt(out.dtype),
                                     _stream(codes)), "zpp_dequant_reduce_local")
     return out
+
+
+# ------------------------------------------------------------- the weights' other operators
+def _dev_list(ts, name, dtypes):
+    """Checks a list of tensors that one call reads or writes: one dtype of `dtypes`,
+    contiguous CUDA tensors on one device. Returns (addresses, element counts)."""
+    torch = _torch()
+    T = torch.Tensor
+    kinds = {t.dtype for t in ts}
+    if len(kinds) != 1 or kinds.pop() not in dtypes:
+        raise ValueError(f"{name}: every tensor needs one dtype of {tuple(dtypes)}")
+    if len(set(map(T.get_device, ts))) != 1:
+        raise ValueError("all tensors of a call must be on one device")
+    if not all(map(T.is_contiguous, ts)) or not ts[0].is_cuda:
+        _cuda(*ts)
+    return array.array("q", map(T.data_ptr, ts)), list(map(T.numel, ts))
+
+
+def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
+    """The global norm of a list of gradient tensors (one fp16 / bf16 / fp32 dtype) times
+    |pre_scale|, and the factor that clips it to `max_norm` (None: no clipping) with
+    pre_scale folded in -> fp32 [2] (norm, factor) on the device. The factor is NaN when the
+    norm is not finite: adamw_step then skips the step."""
+    torch = _torch()
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    if not grads:
+        raise ValueError("grad_norm needs at least one tensor")
+    ptrs, sizes = _dev_list(grads, "grads", (torch.float16, torch.bfloat16, torch.float32))
+    return _grad_norm(ptrs, sizes, grads[0], max_norm, pre_scale, out)
+
+
+def _grad_norm(ptrs, sizes, like, max_norm, pre_scale, out=None):
+    torch = _torch()
+    if out is not None:
+        _need(out, "out", 2, (torch.float32,))
+        _cuda(like, out)
+    else:
+        out = torch.empty(2, dtype=torch.float32, device=like.device)
+    work = torch.empty(zpp_grad_norm_workspace(sum(sizes), len(sizes)), dtype=torch.float32,
+                       device=like.device)
+    _check(zpp_grad_norm(ptrs, sizes, _dt(like.dtype), float(pre_scale),
+                         math.inf if max_norm is None else float(max_norm), work.data_ptr(),
+                         out.data_ptr(), _stream(like)), "zpp_grad_norm")
+    return out
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.999), eps=1e-8,
+               weight_decay=0.0, grad_scale=None, weights=None, scales=None, seed=0):
+    """One AdamW step over lists of tensors (or single tensors), in place.
+
+    params: fp32. grads: one of fp16 / bf16 / fp32. exp_avg, exp_avg_sq: fp32 states; with
+    `scales` = (m scales, v scales) they are float8_e4m3fn codes (of m and of sqrt(v)) with one
+    fp32 scale per 256 elements, [ceil(n / 256)] for each tensor. weights: fp16 / bf16 tensors
+    that receive the rounded parameters. grad_scale: fp32 device tensor whose first element
+    multiplies every gradient; if it is not finite the step changes nothing. step counts from
+    1; seed (0 .. 2^32 - 1) is that of the 8-bit states' stochastic rounding."""
+    torch = _torch()
+    aslist = lambda v: [v] if isinstance(v, torch.Tensor) else list(v)  # noqa: E731
+    f32 = (torch.float32,)
+    params, grads = aslist(params), aslist(grads)
+    lists = [("params", params, f32), ("grads", grads, (torch.float16, torch.bfloat16) + f32)]
+    state = f32 if scales is None else (torch.float8_e4m3fn,)
+    lists += [("exp_avg", aslist(exp_avg), state), ("exp_avg_sq", aslist(exp_avg_sq), state)]
+    if scales is not None:
+        lists += [("scales[0]", aslist(scales[0]), f32), ("scales[1]", aslist(scales[1]), f32)]
+    if weights is not None:
+        lists.append(("weights", aslist(weights), (torch.float16, torch.bfloat16)))
+    if not params:
+        raise ValueError("adamw_step needs at least one tensor")
+    if not 0 <= seed < 1 << 32:
+        raise ValueError("seed: 0 .. 2^32 - 1")
+    ptrs, device = {}, params[0].get_device()
+    for name, ts, dtypes in lists:
+        if len(ts) != len(params):
+            raise ValueError(f"{name}: {len(ts)} tensors, expected {len(params)}")
+        ptrs[name], sizes = _dev_list(ts, name, dtypes)
+        if ts[0].get_device() != device:
+            raise ValueError("all tensors of a call must be on one device")
+        want = ptrs.setdefault("n", sizes)
+        if name.startswith("scales"):
+            want = [-(-n // ZPP_STATE_BLOCK) for n in want]
+        if sizes != want:
+            i = next(i for i, (a, b) in enumerate(zip(sizes, want)) if a != b)
+            raise ValueError(f"{name}[{i}]: {sizes[i]} elements, expected {want[i]}")
+    T = len(params)
+    tab = array.array("q", bytes(64 * T))
+    for k, name in enumerate(("params", "grads", "exp_avg", "exp_avg_sq", "scales[0]",
+                              "scales[1]", "weights")):
+        if name in ptrs:
+            tab[k::8] = ptrs[name]
+    tab[7::8] = array.array("q", ptrs["n"])
+    hp = AdamwParams(lr, betas[0], betas[1], eps, weight_decay, step, seed)
+    _adamw(tab, grads[0], lists[-1][1][0] if weights is not None else None,
+           32 if scales is None else 8, hp, grad_scale)
+
+
+def _adamw(tab, grad, weight, state_bits, hp, grad_scale):
+    torch = _torch()
+    if grad_scale is not None:
+        _need(grad_scale, "grad_scale", dtypes=(torch.float32,))
+        if grad_scale.numel() < 1:
+            raise ValueError("grad_scale: at least one element")
+        _cuda(grad, grad_scale)
+    _check(zpp_adamw_step(tab, _dt(grad.dtype), ZPP_BF16 if weight is None else _dt(weight.dtype),
+                          state_bits, hp, 0 if grad_scale is None else grad_scale.data_ptr(),
+                          _stream(grad)), "zpp_adamw_step")
+
+
+def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None, y=None):
+    """x [..., cols] (fp16 / bf16; rows of cols contiguous elements, any row stride) times the
+    transposed [rows][cols] matrix that quant_blockwise gave (codes, scales) for -> y [..., rows]
+    of `dtype` (default: x's). bias: [rows] of x's dtype. y: an output buffer, same form as x."""
+    torch = _torch()
+    _need(x, "x", dtypes=(torch.float16, torch.bfloat16))
+    if x.dim() < 1 or x.shape[-1] < 1 or rows < 0:
+        raise ValueError("x: [..., cols] with cols >= 1, and rows >= 0")
+    cols = x.shape[-1]
+    n, ok = rows * cols, _sizes_ok(rows * cols, block, bits)
+    _need(codes, "codes", zpp_code_bytes(n, bits) if ok else None, _bytes_dtypes())
+    _need(scales, "scales", zpp_num_scales(n, block) if ok else None, (torch.float32,))
+    if bias is not None:
+        _need(bias, "bias", rows, (x.dtype,))
+    vecs, x_stride = _rows(x, "x")
+    if y is None:
+        y = torch.empty(x.shape[:-1] + (rows,), dtype=dtype or x.dtype, device=x.device)
+        y_stride = rows
+    else:
+        _need(y, "y", vecs * rows, (torch.float16, torch.bfloat16, torch.float32))
+        if y.shape != x.shape[:-1] + (rows,) or (dtype is not None and y.dtype != dtype):
+            raise ValueError(f"y: {tuple(y.shape)} of {y.dtype} does not fit the call")
+        y_stride = _rows(y, "y")[1]
+    _cuda(codes, scales, *(t for t in (bias,) if t is not None))
+    if not x.is_cuda or any(t.device != x.device for t in (codes, y)):
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    _check(zpp_matvec_blockwise(codes.data_ptr(), scales.data_ptr(), rows, cols, block, bits,
+                                x.data_ptr(), _dt(x.dtype), vecs, x_stride,
+                                0 if bias is None else bias.data_ptr(), y.data_ptr(),
+                                _dt(y.dtype), y_stride, _stream(x)), "zpp_matvec_blockwise")
+    return y
+
+
+def _rows(t, name):
+    """(rows, row stride) of a tensor seen as rows of contiguous elements."""
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // cols if cols else 0), cols
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be contiguous and at least a row apart")
+    return t.shape[0], t.stride(0)
 
 
 class QgzBuffers:

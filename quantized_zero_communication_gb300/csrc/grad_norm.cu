@@ -1,0 +1,78 @@
+// grad_norm.cu -- K7: the global gradient norm over a list of tensors, and the factor that
+// clips it, left on the device for the optimiser step.
+//
+//   norm = |pre| sqrt(sum g^2),  coef = pre * min(1, max_norm / norm), NaN if the norm is not
+//   finite.
+//
+// One pass over the gradients; each CTA sums one chunk of one tensor in fp32 and writes a
+// partial, a single CTA adds the partials (in fp64) in a fixed order.
+#include "zpp_device.cuh"
+#include "zpp_launch.h"
+
+namespace zpp {
+
+__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int kind) {
+  if (kind == 2) return static_cast<const float*>(p)[i];
+  const uint16_t b = static_cast<const uint16_t*>(p)[i];
+  return kind == 0 ? bits16_to_float(b, F16()) : bits16_to_float(b, BF16());
+}
+
+template <typename T>
+__device__ __forceinline__ T block_sum(T v) {  // valid in thread 0; blockDim.x <= 1024
+  __shared__ T part[32];
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  v = threadIdx.x < warps ? part[threadIdx.x] : T(0);
+  if (threadIdx.x < 32)
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant__ NormTable tab,
+                                                           int kind, float* __restrict__ partial) {
+  int lo = 0, hi = tab.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.first[mid] <= static_cast<int>(blockIdx.x)) lo = mid;
+    else hi = mid;
+  }
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kNormChunk;
+  const int64_t end = min(tab.n[lo], begin + kNormChunk);
+  float sum = 0.0f;
+  for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
+    const float g = load_as_f32(tab.ptr[lo], i, kind);
+    sum = __fmaf_rn(g, g, sum);
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(1024) k_norm_finish(const float* __restrict__ partial, int count,
+                                                      float pre_scale, float max_norm,
+                                                      float* __restrict__ out) {
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < count; i += 1024) sum += static_cast<double>(partial[i]);
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    const float norm = static_cast<float>(sqrt(sum)) * fabsf(pre_scale);
+    out[0] = norm;
+    out[1] = !isfinite(norm) ? __int_as_float(0x7fc00000)
+                             : pre_scale * (norm > max_norm ? max_norm / norm : 1.0f);
+  }
+}
+
+cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
+                             float* workspace, float* out, cudaStream_t s) {
+  const int chunks = tab.first[tab.count];
+  if (chunks > 0) {
+    k_norm_partial<<<chunks, kThreads, 0, s>>>(tab, g_kind, workspace);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  k_norm_finish<<<1, 1024, 0, s>>>(workspace, chunks, pre_scale, max_norm, out);
+  return cudaGetLastError();
+}
+
+}  // namespace zpp

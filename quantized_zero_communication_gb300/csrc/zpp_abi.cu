@@ -2,6 +2,8 @@
 // kernel selection, status codes, and the same-run 256-bit copy kernel.
 #include <zpp.h>
 
+#include <cmath>
+
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
 
@@ -296,6 +298,157 @@ zpp_status zpp_dequant_reduce_local(const void* codes, const float* scales, int6
   return from_cuda(zpp::launch_dequant_reduce(codes, scales, slice, slice, block, bits, sources, 1,
                                               0, 1, 1, post_scale, out, static_cast<int>(out_dt),
                                               stream));
+}
+
+namespace {
+bool valid_dtype(zpp_dtype t) { return t == ZPP_F16 || t == ZPP_BF16 || t == ZPP_F32; }
+bool is_finite(double v) { return v - v == 0.0; }
+}  // namespace
+
+int64_t zpp_grad_norm_workspace(int64_t total_elems, int32_t num_tensors) {
+  if (total_elems < 0 || num_tensors < 0) return -1;
+  // every tensor rounds up to whole chunks; one float more for an empty list
+  return total_elems / zpp::kNormChunk + num_tensors + 1;
+}
+
+zpp_status zpp_grad_norm(const void* const* grads, const int64_t* sizes, int32_t num_tensors,
+                         zpp_dtype g_dt, float pre_scale, float max_norm, float* workspace,
+                         float* out, cudaStream_t stream) {
+  if (num_tensors < 0 || num_tensors > ZPP_MAX_TENSORS || !valid_dtype(g_dt))
+    return ZPP_ERR_INVALID_ARG;
+  if (num_tensors > 0 && (!grads || !sizes)) return ZPP_ERR_INVALID_ARG;
+  if (!is_finite(pre_scale) || !(max_norm > 0.0f)) return ZPP_ERR_INVALID_ARG;
+  if (!workspace || !out) return ZPP_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int32_t t = 0; t < num_tensors; ++t) {
+    if (sizes[t] < 0 || sizes[t] > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+    total += sizes[t];
+    if (total > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+    if (sizes[t] > 0 && !grads[t]) return ZPP_ERR_INVALID_ARG;
+  }
+  for (int32_t t = 0; t < num_tensors; ++t)
+    if (sizes[t] > 0 && !aligned(grads[t], 16)) return ZPP_ERR_MISALIGNED;
+  if (!aligned(workspace, 4) || !aligned(out, 4)) return ZPP_ERR_MISALIGNED;
+  zpp::NormTable tab;
+  tab.count = num_tensors;
+  tab.first[0] = 0;
+  for (int32_t t = 0; t < num_tensors; ++t) {
+    tab.ptr[t] = grads[t];
+    tab.n[t] = sizes[t];
+    tab.first[t + 1] = tab.first[t] + static_cast<int32_t>(zpp::norm_chunks(sizes[t]));
+  }
+  return from_cuda(zpp::launch_grad_norm(tab, static_cast<int>(g_dt), pre_scale, max_norm,
+                                         workspace, out, stream));
+}
+
+zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, zpp_dtype g_dt,
+                          zpp_dtype w_dt, int32_t state_bits, const zpp_adamw_params* hp,
+                          const float* grad_scale, cudaStream_t stream) {
+  static_assert(zpp::kStateBlock == ZPP_STATE_BLOCK, "state block");
+  if (num_tensors < 0 || num_tensors > ZPP_MAX_TENSORS || (num_tensors > 0 && !tensors) || !hp)
+    return ZPP_ERR_INVALID_ARG;
+  if (!valid_dtype(g_dt) || !valid_dtype(w_dt) || (state_bits != 8 && state_bits != 32))
+    return ZPP_ERR_INVALID_ARG;
+  if (!is_finite(hp->lr) || !is_finite(hp->weight_decay) || !is_finite(hp->eps) || hp->eps < 0.0 ||
+      !(hp->beta1 >= 0.0 && hp->beta1 < 1.0) || !(hp->beta2 >= 0.0 && hp->beta2 < 1.0) ||
+      hp->step < 1)
+    return ZPP_ERR_INVALID_ARG;
+  int64_t total = 0;
+  bool any_weight = false;
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    const zpp_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+    total += t.n;
+    if (total > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return ZPP_ERR_INVALID_ARG;
+    if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return ZPP_ERR_INVALID_ARG;
+    any_weight |= t.weight != nullptr;
+  }
+  if (any_weight && w_dt == ZPP_F32) return ZPP_ERR_UNSUPPORTED;
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    const zpp_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.exp_avg, 16) ||
+        !aligned(t.exp_avg_sq, 16) || !aligned(t.weight, 16))
+      return ZPP_ERR_MISALIGNED;
+    if (state_bits == 8 && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4)))
+      return ZPP_ERR_MISALIGNED;
+  }
+  if (!aligned(grad_scale, 4)) return ZPP_ERR_MISALIGNED;
+
+  zpp::AdamwTable tab;
+  const double t = static_cast<double>(hp->step);
+  const double bc1 = 1.0 - std::pow(hp->beta1, t), bc2 = 1.0 - std::pow(hp->beta2, t);
+  zpp::AdamwArgs& a = tab.a;
+  a.beta1 = static_cast<float>(hp->beta1);
+  a.one_minus_beta1 = static_cast<float>(1.0 - hp->beta1);
+  a.beta2 = static_cast<float>(hp->beta2);
+  a.one_minus_beta2 = static_cast<float>(1.0 - hp->beta2);
+  a.step_size = static_cast<float>(hp->lr / bc1);
+  a.inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
+  a.eps = static_cast<float>(hp->eps);
+  a.decay = static_cast<float>(hp->lr * hp->weight_decay);
+  a.key = (hp->seed * 0x9E3779B9u) ^ (static_cast<uint32_t>(hp->step) * 0x510E527Fu);
+  a.grad_scale = grad_scale;
+  a.g_kind = static_cast<int32_t>(g_dt);
+  a.w_kind = static_cast<int32_t>(w_dt);
+  tab.first_block = 0;
+  int64_t blocks = 0;
+  for (int32_t i = 0; i < num_tensors;) {  // one launch per kAdamwTensors non-empty tensors
+    tab.count = 0;
+    tab.first[0] = 0;
+    tab.first_block = blocks;
+    for (; i < num_tensors && tab.count < zpp::kAdamwTensors; ++i) {
+      const zpp_adamw_tensor& s = tensors[i];
+      if (s.n == 0) continue;
+      const int32_t c = tab.count++;
+      tab.t[c] = zpp::AdamwTensor{s.param,         s.grad,             s.exp_avg, s.exp_avg_sq,
+                                  s.exp_avg_scale, s.exp_avg_sq_scale, s.weight,  s.n};
+      tab.first[c + 1] = tab.first[c] + static_cast<int32_t>(zpp::adamw_chunks(s.n));
+      blocks += (s.n + ZPP_STATE_BLOCK - 1) / ZPP_STATE_BLOCK;
+    }
+    if (tab.count == 0) break;
+    const zpp_status st = from_cuda(zpp::launch_adamw(tab, state_bits, stream));
+    if (st != ZPP_OK) return st;
+  }
+  return ZPP_OK;
+}
+
+zpp_status zpp_matvec_blockwise(const void* codes, const float* scales, int64_t rows, int64_t cols,
+                                int32_t block, int32_t bits, const void* x, zpp_dtype x_dt,
+                                int64_t vecs, int64_t x_stride, const void* bias, void* y,
+                                zpp_dtype y_dt, int64_t y_stride, cudaStream_t stream) {
+  if (!valid_bits(bits) || !valid_block(block)) return ZPP_ERR_INVALID_ARG;
+  if (!valid_dtype(x_dt) || !valid_dtype(y_dt)) return ZPP_ERR_INVALID_ARG;
+  constexpr int64_t kDim = int64_t{1} << 31;
+  if (rows < 0 || rows >= kDim || cols < 1 || cols >= kDim || vecs < 0 || vecs > 65535)
+    return ZPP_ERR_INVALID_ARG;
+  if (rows > ZPP_MAX_ELEMS / cols) return ZPP_ERR_INVALID_ARG;
+  if (x_stride < cols || x_stride > ZPP_MAX_ELEMS || y_stride < rows || y_stride > ZPP_MAX_ELEMS)
+    return ZPP_ERR_INVALID_ARG;
+  if (rows == 0 || vecs == 0) return ZPP_OK;
+  if (!codes || !scales || !x || !y) return ZPP_ERR_INVALID_ARG;
+  if (x_dt == ZPP_F32) return ZPP_ERR_UNSUPPORTED;
+  if (!aligned(codes, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(scales, 4) ||
+      !aligned(bias, 2))
+    return ZPP_ERR_MISALIGNED;
+  zpp::MatvecArgs a;
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.scales = scales;
+  a.rows = rows;
+  a.cols = cols;
+  a.block = block;
+  a.bits = bits;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_bf16 = x_dt == ZPP_BF16;
+  a.vecs = vecs;
+  a.x_stride = x_stride;
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.y = y;
+  a.y_kind = static_cast<int32_t>(y_dt);
+  a.y_stride = y_stride;
+  return from_cuda(zpp::launch_matvec(a, stream));
 }
 
 zpp_status zpp_device_fault(uint32_t* flags, int32_t clear) {

@@ -74,6 +74,70 @@ cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
 // K6: 256-bit device copy (the same-run HBM reference).
 cudaError_t launch_copy(const void* src, void* dst, int64_t bytes, cudaStream_t s);
 
+// K7: sums of squares over a list of tensors (one partial per CTA into `workspace`), then
+// norm and clip factor. The list travels in the kernel's parameter space.
+constexpr int kNormChunk = 16384;  // elements per CTA
+struct NormTable {
+  const void* ptr[kMaxTensors];
+  int64_t n[kMaxTensors];
+  int32_t first[kMaxTensors + 1];  // CTAs of the tensors before this one
+  int32_t count;
+};
+inline int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
+cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
+                             float* workspace, float* out, cudaStream_t s);
+
+// K8: one AdamW step over a list of tensors; at most kAdamwTensors per launch (their
+// descriptors travel in the kernel's parameter space, which holds 32,764 bytes).
+constexpr int kAdamwTensors = 448;
+constexpr int kAdamwChunk = 2048;  // elements per CTA
+constexpr int kStateBlock = 256;   // = ZPP_STATE_BLOCK
+struct AdamwTensor {
+  float* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* weight;
+  int64_t n;
+};
+struct AdamwArgs {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  float step_size;      // lr / (1 - beta1^t)
+  float inv_root_bc2;   // 1 / sqrt(1 - beta2^t)
+  float eps, decay;     // decay = lr * weight_decay
+  uint32_t key;         // of the rounding hash
+  const float* grad_scale;
+  int32_t g_kind, w_kind;  // zpp_dtype of grad and weight
+};
+struct AdamwTable {
+  AdamwTensor t[kAdamwTensors];
+  int32_t first[kAdamwTensors + 1];  // chunks of the tensors before this one
+  int32_t count;
+  int64_t first_block;               // state blocks of the tensors of earlier launches
+  AdamwArgs a;
+};
+inline int64_t adamw_chunks(int64_t n) { return (n + kAdamwChunk - 1) / kAdamwChunk; }
+cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s);
+
+// K9: y = x W^T (+ bias) from block-quantised codes. x_bf16: x and bias are bf16, else fp16;
+// y_kind as a zpp_dtype.
+struct MatvecArgs {
+  const uint8_t* codes;
+  const float* scales;
+  int64_t rows, cols;
+  int32_t block, bits;
+  const uint16_t* x;
+  int32_t x_bf16;
+  int64_t vecs, x_stride;
+  const uint16_t* bias;
+  void* y;
+  int32_t y_kind;
+  int64_t y_stride;
+};
+cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s);
+
 // Grid size when every CTA owns `per_cta` consecutive tiles and exits (no grid-stride
 // loop): on GB300 a streaming kernel launched this way sustains more HBM bandwidth than
 // a persistent grid sized to the SM count.

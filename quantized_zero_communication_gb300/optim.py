@@ -1,0 +1,126 @@
+"""AdamW over the tensors of a parameter shard: fp32 master weights, states in fp32 or in
+8 bits, one library call per step (``zpp_adamw_step``), and one more when the gradient norm
+is clipped (``zpp_grad_norm``). Everything stays on the device; a step never synchronises.
+
+The 16-bit tensors in ``weights`` receive the updated parameters, ready for the next
+all-gather's ``quant_blockwise``.
+"""
+import array
+
+from . import binding as _b
+
+
+class AdamW:
+    """AdamW (decoupled weight decay) over a list of contiguous fp32 CUDA tensors.
+
+    state_bits 32 holds both states in fp32; 8 holds m and sqrt(v) as float8_e4m3fn codes
+    with one fp32 scale per 256 elements, rounded stochastically from `seed` and the step
+    (see include/zpp.h). weights: fp16 or bf16 tensors of the parameters' sizes that each
+    step fills, or None. exp_avg, exp_avg_sq, scales and step resume from a saved state()
+    (the tensors are taken over, not copied); by default the states start at zero.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *,
+                 state_bits=32, weights=None, seed=0, exp_avg=None, exp_avg_sq=None, scales=None,
+                 step=0):
+        torch = _b._torch()
+        f32 = (torch.float32,)
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("AdamW needs at least one tensor")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits: 8 or 32")
+        if (exp_avg is None) != (exp_avg_sq is None):
+            raise ValueError("exp_avg and exp_avg_sq come together")
+        if (scales is not None) != (state_bits == 8 and exp_avg is not None):
+            raise ValueError("scales come with exp_avg and exp_avg_sq of state_bits 8")
+        if not 0 <= seed < 1 << 32:
+            raise ValueError("seed: 0 .. 2^32 - 1")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.state_bits, self.seed, self.steps = state_bits, seed, step
+        self._sizes = [p.numel() for p in self.params]
+        self._blocks = [-(-n // _b.ZPP_STATE_BLOCK) for n in self._sizes]
+        code = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+
+        def states(given, sizes, dtype):
+            if given is not None:
+                return list(given)
+            # one buffer, every tensor's part 256 elements aligned
+            at, end = [], 0
+            for n in sizes:
+                at.append(end)
+                end += -(-n // 256) * 256
+            # (as bytes: zero is all bits zero in both types)
+            flat = torch.zeros(end * dtype.itemsize, dtype=torch.uint8,
+                               device=self.params[0].device).view(dtype)
+            return [flat[o:o + n] for o, n in zip(at, sizes)]
+
+        self.exp_avg = states(exp_avg, self._sizes, code)
+        self.exp_avg_sq = states(exp_avg_sq, self._sizes, code)
+        self.scales = None
+        if state_bits == 8:
+            self.scales = tuple(states(s, self._blocks, torch.float32)
+                                for s in (scales or (None, None)))
+        self.weights = None if weights is None else list(weights)
+        self._lists = [("params", 0, self.params, self._sizes, f32),
+                       ("exp_avg", 2, self.exp_avg, self._sizes, (code,)),
+                       ("exp_avg_sq", 3, self.exp_avg_sq, self._sizes, (code,))]
+        if state_bits == 8:
+            self._lists += [(f"scales[{k}]", 4 + k, self.scales[k], self._blocks, f32)
+                            for k in (0, 1)]
+        if self.weights is not None:
+            self._lists.append(("weights", 6, self.weights, self._sizes,
+                                (torch.float16, torch.bfloat16)))
+        self._table = array.array("q", bytes(64 * len(self.params)))
+        self._table[7::8] = array.array("q", self._sizes)
+        for entry in self._lists:
+            self._enter(*entry)
+
+    def _enter(self, name, column, tensors, sizes, dtypes):
+        """Checks a list and writes its addresses into the call's table."""
+        if len(tensors) != len(sizes):
+            raise ValueError(f"{name}: {len(tensors)} tensors, expected {len(sizes)}")
+        ptrs, got = _b._dev_list(tensors, name, dtypes)
+        if got != sizes:
+            i = next(i for i, (a, b) in enumerate(zip(got, sizes)) if a != b)
+            raise ValueError(f"{name}[{i}]: {got[i]} elements, expected {sizes[i]}")
+        if tensors[0].get_device() != self.params[0].get_device():
+            raise ValueError("all tensors of a call must be on one device")
+        self._table[column::8] = ptrs
+        return ptrs
+
+    def step(self, grads, *, max_norm=None, pre_scale=None, grad_scale=None, lr=None):
+        """One step with `grads` (contiguous, one of fp16 / bf16 / fp32, in the parameters'
+        order). max_norm and / or pre_scale: the gradients are multiplied by pre_scale (say 1 /
+        loss scale) and clipped to the global norm max_norm, and fp32 [2] (norm, factor) is
+        returned; a norm that is not finite leaves parameters and states as they were.
+        grad_scale: instead, an fp32 device tensor whose first element multiplies the
+        gradients (the factor of a norm taken over several ranks). lr replaces the
+        optimiser's for this step and the following ones."""
+        torch = _b._torch()
+        grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+        for entry in self._lists:  # storage may have moved since the last step
+            self._enter(*entry)
+        ptrs = self._enter("grads", 1, grads, self._sizes,
+                           (torch.float16, torch.bfloat16, torch.float32))
+        if lr is not None:
+            self.lr = lr
+        norm = None
+        if max_norm is not None or pre_scale is not None:
+            if grad_scale is not None:
+                raise ValueError("grad_scale replaces max_norm and pre_scale")
+            norm = _b._grad_norm(ptrs, self._sizes, grads[0], max_norm,
+                                 1.0 if pre_scale is None else pre_scale)
+            grad_scale = norm[1:]
+        hp = _b.AdamwParams(self.lr, *self.betas, self.eps, self.weight_decay, self.steps + 1,
+                            self.seed)
+        _b._adamw(self._table, grads[0], self.weights[0] if self.weights else None,
+                  self.state_bits, hp, grad_scale)
+        self.steps += 1
+        return norm
+
+    def state(self):
+        """What a checkpoint keeps, as the constructor takes it: the state tensors themselves
+        and the step count."""
+        return dict(exp_avg=self.exp_avg, exp_avg_sq=self.exp_avg_sq, scales=self.scales,
+                    step=self.steps, seed=self.seed, state_bits=self.state_bits)
