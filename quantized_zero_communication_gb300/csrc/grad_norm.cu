@@ -30,8 +30,12 @@ __device__ __forceinline__ T block_sum(T v) {  // valid in thread 0; blockDim.x 
   return v;
 }
 
+// One chunk per CTA. A full chunk is kNormChunk / kThreads = 64 elements per thread, all of
+// whose 32-byte vectors are loaded before the first product (no loop, so the most loads in
+// flight); a tensor's last, shorter chunk is read element by element.
+template <int KIND, bool V8>
 __global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant__ NormTable tab,
-                                                           int kind, float* __restrict__ partial) {
+                                                           float* __restrict__ partial) {
   int lo = 0, hi = tab.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -39,11 +43,36 @@ __global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant
     else hi = mid;
   }
   const int64_t begin = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kNormChunk;
-  const int64_t end = min(tab.n[lo], begin + kNormChunk);
+  const int64_t left = tab.n[lo] - begin;
   float sum = 0.0f;
-  for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
-    const float g = load_as_f32(tab.ptr[lo], i, kind);
-    sum = __fmaf_rn(g, g, sum);
+  if (left >= kNormChunk) {
+    constexpr int PER = KIND == 2 ? 8 : 16;  // elements in 32 bytes
+    constexpr int VECS = kNormChunk / kThreads / PER;
+    constexpr int BYTES = 32 / PER;
+    const char* p = static_cast<const char*>(tab.ptr[lo]) + begin * BYTES + threadIdx.x * 32;
+    U8x32 w[VECS];
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) w[u] = ld_vec32<V8>(p + u * kThreads * 32);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < VECS; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (KIND == 2) {
+          const float g = __uint_as_float(w[u].w[k]);
+          acc[k & 3] = __fmaf_rn(g, g, acc[k & 3]);
+        } else {
+          const float2 g = KIND == 0 ? unpack2(w[u].w[k], F16()) : unpack2(w[u].w[k], BF16());
+          acc[(2 * k) & 3] = __fmaf_rn(g.x, g.x, acc[(2 * k) & 3]);
+          acc[(2 * k + 1) & 3] = __fmaf_rn(g.y, g.y, acc[(2 * k + 1) & 3]);
+        }
+      }
+    sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  } else {
+    for (int64_t i = begin + threadIdx.x; i < begin + left; i += kThreads) {
+      const float g = load_as_f32(tab.ptr[lo], i, KIND);
+      sum = __fmaf_rn(g, g, sum);
+    }
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -67,7 +96,14 @@ cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, 
                              float* workspace, float* out, cudaStream_t s) {
   const int chunks = tab.first[tab.count];
   if (chunks > 0) {
-    k_norm_partial<<<chunks, kThreads, 0, s>>>(tab, g_kind, workspace);
+    uintptr_t bits = 0;
+    for (int i = 0; i < tab.count; ++i)
+      if (tab.n[i] > 0) bits |= reinterpret_cast<uintptr_t>(tab.ptr[i]);
+    const bool v8 = (bits & 31) == 0;
+    auto kern = g_kind == 2   ? (v8 ? k_norm_partial<2, true> : k_norm_partial<2, false>)
+                : g_kind == 1 ? (v8 ? k_norm_partial<1, true> : k_norm_partial<1, false>)
+                              : (v8 ? k_norm_partial<0, true> : k_norm_partial<0, false>);
+    kern<<<chunks, kThreads, 0, s>>>(tab, workspace);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
