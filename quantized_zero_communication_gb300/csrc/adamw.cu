@@ -6,7 +6,9 @@
 //
 // Elementwise and memory-bound: every byte of p, m, v and g is read once and p, m, v (and
 // the 16-bit weight) written once. A warp owns 256 consecutive elements of one tensor, which
-// is one state block, so the block maximum of an 8-bit state is a warp reduction.
+// is one state block, so the block maximum of an 8-bit state is a warp reduction and the
+// states never leave registers between decoding and encoding. A lane holds 8 consecutive
+// elements: 32 bytes of p, one 256-bit access where the buffers allow it.
 #include <cuda_fp8.h>
 
 #include "zpp_device.cuh"
@@ -15,18 +17,76 @@
 namespace zpp {
 
 constexpr int kVec = kStateBlock / 32;  // elements per lane
+static_assert(kVec == 8, "the vector accesses below hold 8 elements");
 static_assert(kAdamwChunk == kWarps * kStateBlock, "one state block per warp");
+constexpr float kFltMax = 3.402823466e38f;
 
+// 32 bytes that this kernel also writes (so not through the read-only path).
+template <bool V8>
+__device__ __forceinline__ void ld_f32x8(const float* p, float f[kVec]) {
+  if constexpr (V8) {
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]),
+                   "=f"(f[6]), "=f"(f[7])
+                 : "l"(p));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(f[4 * h]), "=f"(f[4 * h + 1]), "=f"(f[4 * h + 2]), "=f"(f[4 * h + 3])
+                   : "l"(p + 4 * h));
+  }
+}
+__device__ __forceinline__ uint2 ld_b32x2(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+template <bool V8>
+__device__ __forceinline__ void st_f32x8(float* p, const float f[kVec]) {
+  U8x32 w;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) w.w[k] = __float_as_uint(f[k]);
+  st_vec32<V8>(p, w);
+}
+
+// Gradients of a lane's 8 elements: raw words first (so that every load of the block is in
+// flight before the first conversion), floats later.
+template <bool V8>
+__device__ __forceinline__ U8x32 ld_grad(const void* g, int64_t i, int kind) {
+  if (kind == 2) return ld_vec32<V8>(static_cast<const float*>(g) + i);
+  const uint4 a = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
+  U8x32 r;
+  r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+  return r;
+}
+__device__ __forceinline__ void grad_f32(const U8x32& w, int kind, float f[kVec]) {
+  if (kind == 2) {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) f[k] = __uint_as_float(w.w[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k) {
+      const float2 p = kind == 0 ? unpack2(w.w[k], F16()) : unpack2(w.w[k], BF16());
+      f[2 * k] = p.x;
+      f[2 * k + 1] = p.y;
+    }
+  }
+}
 __device__ __forceinline__ float grad_at(const void* p, int64_t i, int kind) {
   if (kind == 2) return static_cast<const float*>(p)[i];
   const uint16_t b = static_cast<const uint16_t*>(p)[i];
   return kind == 0 ? bits16_to_float(b, F16()) : bits16_to_float(b, BF16());
 }
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t b) {
-  __nv_fp8_e4m3 v;
-  v.__x = b;
-  return static_cast<float>(v);
+// Two e4m3 codes -> floats (exact).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+// Two floats that are e4m3 values (or NaN) -> codes.
+__device__ __forceinline__ uint32_t f32_to_e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // 32 bits for element number i: low 16 round m, high 16 round sqrt(v). Two multiply-xorshift
@@ -40,22 +100,22 @@ __device__ __forceinline__ uint32_t round_bits(uint64_t i, uint32_t key) {
   return x ^ (x >> 16);
 }
 
-// e4m3 code of x * inv, rounded by floor(|x inv| / h + (k + 1/2) / 65536): adding the random
-// bits below the third mantissa bit and cutting there. Below 2^-6 the grid is uniform (2^-9),
-// which is the spacing of [2^-6, 2^-5): the value is shifted there and back. A non-finite x
-// becomes NaN. KEEP: x > 0 gives at least the smallest code.
+// The e4m3 value that x * inv rounds to, floor(|x inv| / h + (k + 1/2) / 65536) h: the random
+// bits (k16, already shifted to bits 4..19) are added below the third mantissa bit and the
+// sum is cut there. Below 2^-6 the grid is uniform (2^-9), which is the spacing of [2^-6,
+// 2^-5): the value is shifted there and back. A non-finite x becomes NaN. KEEP: x > 0 gives
+// at least the smallest code.
 template <bool KEEP>
-__device__ __forceinline__ uint8_t e4m3_round(float x, float inv, uint32_t k16) {
+__device__ __forceinline__ float e4m3_round(float x, float inv, uint32_t k16) {
   const float a = fabsf(x);
   const float s = __fmul_rn(a, inv);
-  const bool low = s < 0.015625f;
-  uint32_t b = __float_as_uint(low ? __fadd_rn(s, 0.015625f) : s);
-  b = (b + (k16 * 16u + 8u)) & 0xFFF00000u;
-  float r = __uint_as_float(b);
-  if (low) r = __fadd_rn(r, -0.015625f);
-  if (KEEP && a > 0.0f && inv > 0.0f) r = fmaxf(r, 0.001953125f);
-  if (!(a <= 3.402823466e38f)) r = __int_as_float(0x7fc00000);
-  return __nv_fp8_e4m3(copysignf(r, x)).__x;
+  const float shift = s < 0.015625f ? 0.015625f : 0.0f;
+  uint32_t b = __float_as_uint(__fadd_rn(s, shift));
+  b = (b + (k16 | 8u)) & 0xFFF00000u;
+  float r = __fadd_rn(__uint_as_float(b), -shift);
+  if (KEEP && s > 0.0f) r = fmaxf(r, 0.001953125f);
+  if (!(a <= kFltMax)) r = __int_as_float(0x7fc00000);
+  return KEEP ? r : copysignf(r, x);
 }
 
 // Scale of a state block from its largest finite magnitude, and its inverse, each by one
@@ -68,10 +128,164 @@ __device__ __forceinline__ void state_scale(float amax, float& scale, float& inv
 
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.0f;
+  return a <= kFltMax ? a : 0.0f;
 }
 
+// One element: p, m, v updated in place, root = sqrt(v). For the states every operation is
+// rounded by itself (no fused multiply-add), so that codes can be reproduced bit for bit by
+// elementary fp32 arithmetic.
+__device__ __forceinline__ void update(const AdamwArgs& a, float g, float& p, float& m, float& v,
+                                       float& root) {
+  m = __fadd_rn(__fmul_rn(a.beta1, m), __fmul_rn(a.one_minus_beta1, g));
+  v = __fadd_rn(__fmul_rn(a.beta2, v), __fmul_rn(a.one_minus_beta2, __fmul_rn(g, g)));
+  root = __fsqrt_rn(v);
+  const float q = __fdiv_rn(m, __fmaf_rn(root, a.inv_root_bc2, a.eps));
+  p = __fadd_rn(p, -__fmaf_rn(a.decay, p, __fmul_rn(a.step_size, q)));
+}
+
+// One full state block by a warp, 8 consecutive elements per lane.
+template <bool FP8, bool V8>
+__device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs& a, float c,
+                                           int64_t block, int64_t number, int lane) {
+  const int64_t i = block * kStateBlock + lane * kVec;
+  float p[kVec], m[kVec], v[kVec], root[kVec], g[kVec];
+  uint2 mq, vq;
+  float ms, vs;
+  const U8x32 graw = ld_grad<V8>(t.grad, i, a.g_kind);
+  ld_f32x8<V8>(t.param + i, p);
+  if constexpr (FP8) {
+    mq = ld_b32x2(static_cast<uint8_t*>(t.m) + i);
+    vq = ld_b32x2(static_cast<uint8_t*>(t.v) + i);
+    ms = t.m_scale[block];
+    vs = t.v_scale[block];
+  } else {
+    ld_f32x8<V8>(static_cast<float*>(t.m) + i, m);
+    ld_f32x8<V8>(static_cast<float*>(t.v) + i, v);
+  }
+  grad_f32(graw, a.g_kind, g);
+  if constexpr (FP8) {
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k) {
+      const float2 x = e4m3x2_to_f32((k < 2 ? mq.x : mq.y) >> (16 * (k & 1)) & 0xffffu);
+      const float2 y = e4m3x2_to_f32((k < 2 ? vq.x : vq.y) >> (16 * (k & 1)) & 0xffffu);
+      m[2 * k] = __fmul_rn(x.x, ms);
+      m[2 * k + 1] = __fmul_rn(x.y, ms);
+      const float r0 = __fmul_rn(y.x, vs), r1 = __fmul_rn(y.y, vs);
+      v[2 * k] = __fmul_rn(r0, r0);
+      v[2 * k + 1] = __fmul_rn(r1, r1);
+    }
+  }
+  float amax_m = 0.0f, amax_r = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    update(a, __fmul_rn(g[k], c), p[k], m[k], v[k], root[k]);
+    if constexpr (FP8) {
+      amax_m = fmaxf(amax_m, finite_abs(m[k]));
+      amax_r = fmaxf(amax_r, finite_abs(root[k]));
+    }
+  }
+  st_f32x8<V8>(t.param + i, p);
+  if (t.weight) {
+    uint32_t w[kVec / 2];
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k)
+      w[k] = a.w_kind == 0 ? pack2(p[2 * k], p[2 * k + 1], F16())
+                           : pack2(p[2 * k], p[2 * k + 1], BF16());
+    st_v4(static_cast<uint16_t*>(t.weight) + i, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  if constexpr (FP8) {
+    float inv_m, inv_r;
+    // magnitudes order as their bit patterns
+    state_scale(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(amax_m))), ms, inv_m);
+    state_scale(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(amax_r))), vs, inv_r);
+    uint32_t cm[kVec / 2], cr[kVec / 2];
+#pragma unroll
+    for (int k = 0; k < kVec / 2; ++k) {
+      float x[2], y[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t bits = round_bits(number + lane * kVec + 2 * k + j, a.key);
+        x[j] = e4m3_round<false>(m[2 * k + j], inv_m, bits << 4 & 0xffff0u);
+        y[j] = e4m3_round<true>(root[2 * k + j], inv_r, bits >> 12 & 0xffff0u);
+      }
+      cm[k] = f32_to_e4m3x2(x[0], x[1]);
+      cr[k] = f32_to_e4m3x2(y[0], y[1]);
+    }
+    st_v2(static_cast<uint8_t*>(t.m) + i, make_uint2(cm[0] | cm[1] << 16, cm[2] | cm[3] << 16));
+    st_v2(static_cast<uint8_t*>(t.v) + i, make_uint2(cr[0] | cr[1] << 16, cr[2] | cr[3] << 16));
+    if (lane == 0) {
+      t.m_scale[block] = ms;
+      t.v_scale[block] = vs;
+    }
+  } else {
+    st_f32x8<V8>(static_cast<float*>(t.m) + i, m);
+    st_f32x8<V8>(static_cast<float*>(t.v) + i, v);
+  }
+}
+
+// A tensor's last, shorter block: element by element.
 template <bool FP8>
+__device__ __forceinline__ void part_block(const AdamwTensor& t, const AdamwArgs& a, float c,
+                                           int64_t block, int64_t number, int valid, int lane) {
+  float ms = 1.0f, vs = 1.0f;
+  if constexpr (FP8) {
+    ms = t.m_scale[block];
+    vs = t.v_scale[block];
+  }
+  float m[kVec], root[kVec], amax_m = 0.0f, amax_r = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    const int o = k * 32 + lane;
+    const int64_t i = block * kStateBlock + o;
+    m[k] = root[k] = 0.0f;
+    if (o >= valid) continue;
+    float p = t.param[i], v;
+    if constexpr (FP8) {
+      m[k] = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(t.m)[i]).x, ms);
+      const float r0 = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(t.v)[i]).x, vs);
+      v = __fmul_rn(r0, r0);
+    } else {
+      m[k] = static_cast<float*>(t.m)[i];
+      v = static_cast<float*>(t.v)[i];
+    }
+    update(a, __fmul_rn(grad_at(t.grad, i, a.g_kind), c), p, m[k], v, root[k]);
+    t.param[i] = p;
+    if (t.weight) {
+      if (a.w_kind == 0) static_cast<__half*>(t.weight)[i] = __float2half_rn(p);
+      else static_cast<__nv_bfloat16*>(t.weight)[i] = __float2bfloat16_rn(p);
+    }
+    if constexpr (FP8) {
+      amax_m = fmaxf(amax_m, finite_abs(m[k]));
+      amax_r = fmaxf(amax_r, finite_abs(root[k]));
+    } else {
+      static_cast<float*>(t.m)[i] = m[k];
+      static_cast<float*>(t.v)[i] = v;
+    }
+  }
+  if constexpr (FP8) {
+    float inv_m, inv_r;
+    state_scale(warp_max(amax_m, 32), ms, inv_m);
+    state_scale(warp_max(amax_r, 32), vs, inv_r);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const int o = k * 32 + lane;
+      if (o >= valid) continue;
+      const uint32_t bits = round_bits(number + o, a.key);
+      const int64_t i = block * kStateBlock + o;
+      static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(
+          f32_to_e4m3x2(e4m3_round<false>(m[k], inv_m, bits << 4 & 0xffff0u), 0.0f));
+      static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(
+          f32_to_e4m3x2(e4m3_round<true>(root[k], inv_r, bits >> 12 & 0xffff0u), 0.0f));
+    }
+    if (lane == 0) {
+      t.m_scale[block] = ms;
+      t.v_scale[block] = vs;
+    }
+  }
+}
+
+// V8: p, fp32 states and fp32 gradients of every tensor start 32-byte aligned.
+template <bool FP8, bool V8>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamwTable tab) {
   const AdamwArgs& a = tab.a;
   const float c = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
@@ -86,82 +300,30 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
   const int lane = threadIdx.x & 31;
   const int64_t block =
       static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kWarps + (threadIdx.x >> 5);
-  if (block * kStateBlock >= t.n) return;
-  const int valid = static_cast<int>(min(static_cast<int64_t>(kStateBlock), t.n - block * kStateBlock));
-
-  float ms = 1.0f, vs = 1.0f;
-  if (FP8) {
-    ms = t.m_scale[block];
-    vs = t.v_scale[block];
-  }
-  float m[kVec], r[kVec], amax_m = 0.0f, amax_r = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const int o = k * 32 + lane;
-    const int64_t i = block * kStateBlock + o;
-    m[k] = r[k] = 0.0f;
-    if (o >= valid) continue;
-    const float g = __fmul_rn(grad_at(t.grad, i, a.g_kind), c);
-    float m0, v0;
-    if (FP8) {
-      m0 = __fmul_rn(e4m3_to_f32(static_cast<uint8_t*>(t.m)[i]), ms);
-      const float r0 = __fmul_rn(e4m3_to_f32(static_cast<uint8_t*>(t.v)[i]), vs);
-      v0 = __fmul_rn(r0, r0);
-    } else {
-      m0 = static_cast<float*>(t.m)[i];
-      v0 = static_cast<float*>(t.v)[i];
-    }
-    // States: every operation rounded by itself, so that the codes can be reproduced bit for
-    // bit by elementary fp32 arithmetic.
-    m0 = __fadd_rn(__fmul_rn(a.beta1, m0), __fmul_rn(a.one_minus_beta1, g));
-    v0 = __fadd_rn(__fmul_rn(a.beta2, v0), __fmul_rn(a.one_minus_beta2, __fmul_rn(g, g)));
-    const float root = __fsqrt_rn(v0);
-    const float p0 = t.param[i];
-    const float step = __fmul_rn(a.step_size, __fdiv_rn(m0, __fmaf_rn(root, a.inv_root_bc2, a.eps)));
-    const float p = __fadd_rn(p0, -__fmaf_rn(a.decay, p0, step));
-    t.param[i] = p;
-    if (t.weight) {
-      if (a.w_kind == 0) static_cast<__half*>(t.weight)[i] = __float2half_rn(p);
-      else static_cast<__nv_bfloat16*>(t.weight)[i] = __float2bfloat16_rn(p);
-    }
-    if (FP8) {
-      m[k] = m0;
-      r[k] = root;
-      amax_m = fmaxf(amax_m, finite_abs(m0));
-      amax_r = fmaxf(amax_r, finite_abs(root));
-    } else {
-      static_cast<float*>(t.m)[i] = m0;
-      static_cast<float*>(t.v)[i] = v0;
-    }
-  }
-  if (FP8) {
-    float inv_m, inv_r;
-    state_scale(warp_max(amax_m, 32), ms, inv_m);
-    state_scale(warp_max(amax_r, 32), vs, inv_r);
-    // element number in the list: the blocks of earlier tensors (whole chunks are not
-    // blocks, so they are counted tensor by tensor) come first
-    int64_t before = tab.first_block;
-    for (int j = 0; j < lo; ++j) before += (tab.t[j].n + kStateBlock - 1) / kStateBlock;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const int o = k * 32 + lane;
-      if (o >= valid) continue;
-      const uint32_t bits = round_bits(static_cast<uint64_t>((before + block) * kStateBlock + o), a.key);
-      const int64_t i = block * kStateBlock + o;
-      static_cast<uint8_t*>(t.m)[i] = e4m3_round<false>(m[k], inv_m, bits & 0xffffu);
-      static_cast<uint8_t*>(t.v)[i] = e4m3_round<true>(r[k], inv_r, bits >> 16);
-    }
-    if (lane == 0) {
-      t.m_scale[block] = ms;
-      t.v_scale[block] = vs;
-    }
-  }
+  const int64_t left = t.n - block * kStateBlock;
+  if (left <= 0) return;
+  const int64_t number = (tab.first_block + tab.block0[lo] + block) * kStateBlock;
+  if (left >= kStateBlock) full_block<FP8, V8>(t, a, c, block, number, lane);
+  else part_block<FP8>(t, a, c, block, number, static_cast<int>(left), lane);
 }
 
 cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s) {
   const int grid = tab.first[tab.count];
-  if (state_bits == 8) k_adamw<true><<<grid, kThreads, 0, s>>>(tab);
-  else k_adamw<false><<<grid, kThreads, 0, s>>>(tab);
+  uintptr_t bits = 0;
+  for (int i = 0; i < tab.count; ++i) {
+    const AdamwTensor& t = tab.t[i];
+    bits |= reinterpret_cast<uintptr_t>(t.param);
+    if (tab.a.g_kind == 2) bits |= reinterpret_cast<uintptr_t>(t.grad);
+    if (state_bits == 32) bits |= reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v);
+  }
+  const bool v8 = (bits & 31) == 0;
+  if (state_bits == 8) {
+    if (v8) k_adamw<true, true><<<grid, kThreads, 0, s>>>(tab);
+    else k_adamw<true, false><<<grid, kThreads, 0, s>>>(tab);
+  } else {
+    if (v8) k_adamw<false, true><<<grid, kThreads, 0, s>>>(tab);
+    else k_adamw<false, false><<<grid, kThreads, 0, s>>>(tab);
+  }
   return cudaGetLastError();
 }
 

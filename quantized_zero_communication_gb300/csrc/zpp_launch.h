@@ -114,10 +114,12 @@ struct AdamwArgs {
 struct AdamwTable {
   AdamwTensor t[kAdamwTensors];
   int32_t first[kAdamwTensors + 1];  // chunks of the tensors before this one
+  int32_t block0[kAdamwTensors];     // state blocks of the tensors before this one
   int32_t count;
   int64_t first_block;               // state blocks of the tensors of earlier launches
   AdamwArgs a;
 };
+static_assert(sizeof(AdamwTable) <= 32764, "kernel parameter space");
 inline int64_t adamw_chunks(int64_t n) { return (n + kAdamwChunk - 1) / kAdamwChunk; }
 cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s);
 
