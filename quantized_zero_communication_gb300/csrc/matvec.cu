@@ -22,13 +22,15 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v, int kind) {
 
 // ---------------------------------------------------------------------------------
 // A word of codes -> pairs of exact 16-bit floats. Pair p of an INT4 word holds codes (p, p + 4),
-// of an INT8 word (p, p + 2): the two halves of a 32-bit word, so masks serve both at once.
-// The logic operation puts the code, its sign bit flipped (q + 8 or q + 128), into the low
-// mantissa bits of a power of two whose spacing is 1, and the subtraction is exact.
+// of an INT8 word (p, p + 2): the two halves of a 32-bit word, so a mask serves both at once.
+// One logic operation, (w & mask) ^ flip, puts a code with its sign bit flipped (q + 8 or
+// q + 128) into mantissa bits of a power of two; a half-precision operation, exact too, leaves q.
+// (Leaving the offset in and starting the fp32 sums at -offset sum(x) saves that operation,
+// but not time: these run on another pipe than the logic.)
 // ---------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
-  return (w & mask) ^ flip;
-}
+struct Masks {
+  uint32_t k[4];
+};
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b, F16) {
   const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -38,23 +40,27 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b, BF16) {
       __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// The constants come as kernel arguments: as immediates the compiler rebuilds one of them in a
+// register before every use.
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(mask), "r"(flip));
+  return r;
+}
 
 template <typename TT, int BITS>
 struct Codes;
-
 template <>
 struct Codes<F16, 4> {
-  static __device__ __forceinline__ void pairs(uint32_t w, uint32_t p[4]) {
-    const uint32_t one = 0x64086408u;                          // 1024 ^ 8
-    const uint32_t off = 0x64086408u;                          // 1032
+  static constexpr Masks kMasks{{0x000F000Fu, 0x64086408u, 0x00F000F0u, 0x64806480u}};
+  static __device__ __forceinline__ void pairs(uint32_t w, const Masks& m, uint32_t p[4]) {
     const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));  // 2^-4
     const __half2 m72 = __half2half2(__ushort_as_half(0xD480));        // -(64 + 8)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t v = w >> (8 * h);
-      p[2 * h] = sub2(and_xor(v, 0x000F000Fu, one), off, F16());
-      // 1024 + 16 (q + 8), so / 16 - 72
-      const uint32_t b = and_xor(v, 0x00F000F0u, 0x64806480u);
+      p[2 * h] = sub2(and_xor(v, m.k[0], m.k[1]), m.k[1], F16());  // 1024 + (q + 8) - 1032
+      const uint32_t b = and_xor(v, m.k[2], m.k[3]);               // 1024 + 16 (q + 8)
       const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&b), sixteenth, m72);
       p[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&r);
     }
@@ -62,201 +68,265 @@ struct Codes<F16, 4> {
 };
 template <>
 struct Codes<BF16, 4> {
-  static __device__ __forceinline__ void pairs(uint32_t w, uint32_t p[4]) {
+  static constexpr Masks kMasks{{0x000F000Fu, 0x43084308u, 0u, 0u}};
+  static __device__ __forceinline__ void pairs(uint32_t w, const Masks& m, uint32_t p[4]) {
 #pragma unroll
     for (int h = 0; h < 4; ++h)  // 128 + (q + 8) - 136
-      p[h] = sub2(and_xor(w >> (4 * h), 0x000F000Fu, 0x43084308u), 0x43084308u, BF16());
+      p[h] = sub2(and_xor(w >> (4 * h), m.k[0], m.k[1]), m.k[1], BF16());
   }
 };
 template <>
 struct Codes<F16, 8> {
-  static __device__ __forceinline__ void pairs(uint32_t w, uint32_t p[2]) {
+  static constexpr Masks kMasks{{0x00FF00FFu, 0x64806480u, 0u, 0u}};
+  static __device__ __forceinline__ void pairs(uint32_t w, const Masks& m, uint32_t p[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)  // 1024 + (q + 128) - 1152
-      p[h] = sub2(and_xor(w >> (8 * h), 0x00FF00FFu, 0x64806480u), 0x64806480u, F16());
+      p[h] = sub2(and_xor(w >> (8 * h), m.k[0], m.k[1]), m.k[1], F16());
   }
 };
 template <>
 struct Codes<BF16, 8> {  // bf16 holds 7 bits after the leading one: the sign bit goes apart
-  static __device__ __forceinline__ void pairs(uint32_t w, uint32_t p[2]) {
+  static constexpr Masks kMasks{{0x007F007Fu, 0x43004300u, 0x00800080u, 0u}};
+  static __device__ __forceinline__ void pairs(uint32_t w, const Masks& m, uint32_t p[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t v = w >> (8 * h);
       // (128 + low seven bits) - (128, or 256 for a negative code)
-      p[h] = sub2(and_xor(v, 0x007F007Fu, 0x43004300u), and_xor(v, 0x00800080u, 0x43004300u), BF16());
+      p[h] = sub2(and_xor(v, m.k[0], m.k[1]), and_xor(v, m.k[2], m.k[1]), BF16());
     }
   }
 };
 
+// c = A B + d, 16 x 8 x 16, fp32 sums.
+#define ZPP_MMA(TYPE)                                                                          \
+  asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE ".f32 {%0,%1,%2,%3}, "            \
+      "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"                                             \
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                         \
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(d[0]), "f"(d[1]),    \
+        "f"(d[2]), "f"(d[3]))
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1,
-                                         F16) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                                         const float d[4], F16) {
+  ZPP_MMA("f16");
 }
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1,
-                                         BF16) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                                         const float d[4], BF16) {
+  ZPP_MMA("bf16");
 }
-
-// WORDS consecutive 32-bit code words of a lane.
-template <int WORDS>
-__device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t w[WORDS]) {
-  if constexpr (WORDS == 4) {
-    const uint4 v = ld_stream_v4(p);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    const uint2 v = ld_stream_v2(p);
-    w[0] = v.x, w[1] = v.y;
-  }
-}
+#undef ZPP_MMA
 
 // ---------------------------------------------------------------------------------
-// The kernel for cols a multiple of block. A warp takes segments of SEG columns of 16 MT
-// rows. In a segment lane (g, t) (g = lane / 4, t = lane % 4) holds SEG / 4 consecutive columns,
-// starting at t SEG / 4, of the rows g and g + 8 of each fragment, and the same columns of
-// vector g: the order of the columns inside a matrix product is free as long as both
-// operands agree. A segment lies in one block, so its fp32 sum is multiplied by the row's scale
-// and added to the running one. Segments are dealt round robin to the warps of a CTA and to
-// the CTAs of a cluster; their sums are joined in a fixed order through shared memory.
+// The kernel for cols a multiple of block. A segment is the columns that 16 code bytes per
+// lane cover: 128 of INT4, 64 of INT8. In a segment lane (g, t) (g = lane / 4, t = lane % 4)
+// holds a quarter, the columns from t SEG / 4 on, of the rows g and g + 8 of each 16-row
+// fragment, and the same columns of the vector in column g of the other operand: the order of
+// the columns inside a matrix product is free as long as both operands agree.
+//
+// The other operand has 8 columns. With fewer vectors (NV = 1, 2, 4) its columns hold them for
+// 8 / NV segments at once, so that x costs no more registers, loads and permutations per
+// segment than there are vectors; each segment's product is wanted in its own columns only
+// (the rest is dropped by a select). A block of 64 is half a segment: then a segment takes
+// two columns per vector, each zero in the half that is not its own (SP = 2). A column's
+// result is a sum over one block, so it is multiplied by the row's scale and added up in fp32.
+//
+// A warp loads U segments of its rows before it works on the first. A row's batches of U segments
+// are dealt round robin to the warps that share its tile (wk of a CTA's, times `split` CTAs of a
+// cluster); their sums are joined in a fixed order through shared memory.
 // ---------------------------------------------------------------------------------
-template <typename TT, int BITS, int SEG, int MT, int NT>
-struct Seg {
-  static constexpr int COLS = SEG / 4;          // columns per lane
-  static constexpr int WORDS = COLS * BITS / 32;
-  static constexpr int PAIRS = COLS / 2;
-  uint32_t w[MT][2][WORDS];
-  float s[MT][2];
-  __device__ __forceinline__ void load(const uint8_t* const (&row)[MT][2],
-                                       const int64_t (&first)[MT][2],
-                                       const float* __restrict__ scales, int log2b, int64_t seg) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ld_words<WORDS>(row[m][h] + seg * (SEG * BITS / 8), w[m][h]);
-        s[m][h] = __ldg(scales + ((first[m][h] + seg * SEG) >> log2b));
-      }
-  }
-  // x: this lane's columns of the segment in vector g of the first tile (tiles are 8 vectors
-  // apart); use[n]: whether that vector exists.
-  __device__ __forceinline__ void add(const uint16_t* x, int64_t tile_stride, const bool (&use)[NT],
-                                      float (&y)[MT][NT][4]) const {
-    uint32_t xw[NT][PAIRS];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < PAIRS / 4; ++k) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (use[n]) v = __ldg(reinterpret_cast<const uint4*>(x + n * tile_stride) + k);
-        xw[n][4 * k] = v.x, xw[n][4 * k + 1] = v.y, xw[n][4 * k + 2] = v.z, xw[n][4 * k + 3] = v.w;
-      }
-    float c[MT][NT][4] = {};
-    constexpr int PW = 16 / BITS;  // pairs per word: 4 (INT4), 2 (INT8)
-#pragma unroll
-    for (int j = 0; j < WORDS; ++j) {
-      uint32_t b[NT][PW];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int p = 0; p < PW; p += 2) {  // pairs (p, p + PW) and (p + 1, p + 1 + PW)
-          const uint32_t lo = xw[n][j * PW + p / 2], hi = xw[n][j * PW + (p + PW) / 2];
-          b[n][p] = __byte_perm(lo, hi, 0x5410u);
-          b[n][p + 1] = __byte_perm(lo, hi, 0x7632u);
-        }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t q[2][PW];
-        Codes<TT, BITS>::pairs(w[m][0][j], q[0]);
-        Codes<TT, BITS>::pairs(w[m][1][j], q[1]);
-#pragma unroll
-        for (int p = 0; p < PW; p += 2) {
-          const uint32_t f[4] = {q[0][p], q[1][p], q[0][p + 1], q[1][p + 1]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(c[m][n], f, b[n][p], b[n][p + 1], TT());
-        }
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        y[m][n][0] = __fmaf_rn(c[m][n][0], s[m][0], y[m][n][0]);
-        y[m][n][1] = __fmaf_rn(c[m][n][1], s[m][0], y[m][n][1]);
-        y[m][n][2] = __fmaf_rn(c[m][n][2], s[m][1], y[m][n][2]);
-        y[m][n][3] = __fmaf_rn(c[m][n][3], s[m][1], y[m][n][3]);
-      }
-  }
+template <int BITS, int MT, int NV, int SP, int NT>
+struct MvShape {
+  static constexpr int SEG = BITS == 4 ? 128 : 64;
+  static constexpr int ROWS = 16 * MT, VECS = NV == 8 ? 8 * NT : NV;
+  static constexpr int COLS = SEG / 4;                         // columns per lane
+  static constexpr int TJ = COLS / 8;                          // 16-byte chunks of x per lane
+  static constexpr int PW = 16 / BITS;                         // pairs per word
+  static constexpr int SG = NV * SP >= 8 ? 1 : 8 / (NV * SP);  // segments per set of columns
+  static constexpr int TILES = NV * SP > 8 ? NT * SP : NT;     // sets of 8 columns
+  static_assert(NT == 1 || NV == 8, "more than one set of vectors only when they fill it");
 };
 
-template <typename TT, int BITS, int SEG, int MT, int NT>
-__global__ void __launch_bounds__(kThreads) k_matvec_mma(const MatvecArgs a, int log2b, int split) {
-  constexpr int ROWS = 16 * MT, VECS = 8 * NT;
-  extern __shared__ float part[];  // [warps][VECS][ROWS]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+template <typename TT, int BITS, int MT, int NV, int SP, int NT, int U>
+__global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, int log2b, int wk,
+                                                            int split, const Masks masks) {
+  using S = MvShape<BITS, MT, NV, SP, NT>;
+  constexpr int SEG = S::SEG, T = S::TILES, NS = NV * SP;
+  static_assert(U % S::SG == 0, "whole sets of columns per batch");
+  extern __shared__ float part[];  // [kWarps][VECS * ROWS]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % split;  // = the CTA's rank in its cluster
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / split) * ROWS;
-  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * VECS;
-  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(VECS)));
+  const int wr = kWarps / wk;                             // row tiles of a CTA
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x / split) * wr + warp / wk) * S::ROWS;
+  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * S::VECS;
+  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(S::VECS)));
+  const int segs = static_cast<int>(a.cols / SEG), batches = (segs + U - 1) / U;
+  const int step = wk * split;
 
-  const uint8_t* row[MT][2];
-  int64_t first[MT][2];
+  // Rows past the end read the last one, vectors past the end the last one: not stored.
+  const uint8_t* codes[MT][2];
+  const float* scale[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // rows past the end read the last one; not stored
+    for (int h = 0; h < 2; ++h) {
       const int64_t r = min(row0 + 16 * m + 8 * h + g, a.rows - 1);
-      first[m][h] = r * a.cols;
-      row[m][h] = a.codes + r * a.cols * BITS / 8 + t * (SEG / 4) * BITS / 8;
+      codes[m][h] = a.codes + r * (a.cols * BITS / 8) + t * 16;
+      scale[m][h] = a.scales + r * (a.cols >> log2b);
     }
-  bool use[NT];
+  // Column g of set i: vector, and which segment of its group and half of it.
+  const uint16_t* x[T];
+  int col_seg = 0;
+  bool col_on[T];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) use[n] = 8 * n + g < vecs;
-  const uint16_t* x = a.x + (vec0 + g) * a.x_stride + t * (SEG / 4);
+  for (int i = 0; i < T; ++i) {
+    const int slot = NS > 8 ? i % SP : g / NV;  // (segment, half)
+    const int v = NS > 8 ? i / SP * 8 + g : NV == 8 ? i * 8 + g : g % NV;
+    col_seg = NS > 8 ? 0 : slot / SP;
+    col_on[i] = SP == 1 || (t >> 1) == slot % SP;
+    x[i] = a.x + (vec0 + min(v, vecs - 1)) * a.x_stride + col_seg * SEG + t * S::COLS;
+  }
+  const int my_seg = NS >= 8 ? 0 : 2 * t / NS;  // segment of this lane's result columns 2t ..
 
-  float y[MT][NT][4] = {};
-  const int64_t segs = a.cols / SEG, step = static_cast<int64_t>(warps) * split;
-  int64_t i = static_cast<int64_t>(rank) * warps + warp;
-  if (i < segs) {
-    Seg<TT, BITS, SEG, MT, NT> now, next;
-    now.load(row, first, a.scales, log2b, i);
-    for (; i + step < segs; i += step) {
-      next.load(row, first, a.scales, log2b, i + step);
-      now.add(x + i * SEG, 8 * a.x_stride, use, y);
-      now = next;
+  float y[MT][T][4] = {};
+  for (int b = rank * wk + warp % wk; b < batches; b += step) {
+    const int seg0 = b * U, left = segs - seg0;
+    uint32_t w[U][MT][2][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < left)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = ld_stream_v4(codes[m][h] + static_cast<int64_t>(seg0) * 64 + u * 64);
+            w[u][m][h][0] = v.x, w[u][m][h][1] = v.y, w[u][m][h][2] = v.z, w[u][m][h][3] = v.w;
+          }
+#pragma unroll
+    for (int u0 = 0; u0 < U; u0 += S::SG) {  // one set of columns at a time
+      if (u0 >= left) break;
+      uint32_t f[T][S::TJ][4];  // fragments of x: the pairs that go with the code pairs
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TJ; ++j) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (col_on[i] && u0 + col_seg < left)
+            v = __ldg(reinterpret_cast<const uint4*>(x[i] + static_cast<int64_t>(seg0 + u0) * SEG) + j);
+          if constexpr (BITS == 4) {  // pairs (p, p + 4)
+            f[i][j][0] = __byte_perm(v.x, v.z, 0x5410u), f[i][j][1] = __byte_perm(v.x, v.z, 0x7632u);
+            f[i][j][2] = __byte_perm(v.y, v.w, 0x5410u), f[i][j][3] = __byte_perm(v.y, v.w, 0x7632u);
+          } else {  // pairs (p, p + 2) of each four
+            f[i][j][0] = __byte_perm(v.x, v.y, 0x5410u), f[i][j][1] = __byte_perm(v.x, v.y, 0x7632u);
+            f[i][j][2] = __byte_perm(v.z, v.w, 0x5410u), f[i][j][3] = __byte_perm(v.z, v.w, 0x7632u);
+          }
+        }
+      // scales of this lane's result columns 2t and 2t + 1 (with two vectors or more they lie
+      // in one block)
+      float sc[MT][2][T][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int e = 0; e < (NV == 1 ? 2 : 1); ++e) {
+              const int slot = NS > 8 ? i % SP : (2 * t + e) / NV;
+              const int at = seg0 + u0 + (NS > 8 ? 0 : slot / SP);
+              const int64_t col = static_cast<int64_t>(min(at, segs - 1)) * SEG + slot % SP * 64;
+              sc[m][h][i][e] = __ldg(scale[m][h] + (col >> log2b));
+              if (NV > 1) sc[m][h][i][1] = sc[m][h][i][0];
+            }
+      float r[MT][T][4] = {};
+#pragma unroll
+      for (int s = 0; s < S::SG; ++s) {
+        if (s > 0 && u0 + s >= left) break;
+        float c[MT][T][4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t q[2][S::PW];
+            Codes<TT, BITS>::pairs(w[u0 + s][m][0][j], masks, q[0]);
+            Codes<TT, BITS>::pairs(w[u0 + s][m][1][j], masks, q[1]);
+#pragma unroll
+            for (int p = 0; p < S::PW; p += 2) {
+              const uint32_t fa[4] = {q[0][p], q[1][p], q[0][p + 1], q[1][p + 1]};
+              const int fj = j * S::PW / 4, fp = j * S::PW % 4 + p;
+#pragma unroll
+              for (int i = 0; i < T; ++i)
+                mma16816(c[m][i], fa, f[i][fj][fp], f[i][fj][fp + 1], c[m][i], TT());
+            }
+          }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (S::SG == 1) r[m][i][k] = c[m][i][k];
+              else if (NS == 1) { if ((k & 1) == (s & 1) && t == s >> 1) r[m][i][k] = c[m][i][k]; }
+              else if (my_seg == s) r[m][i][k] = c[m][i][k];
+            }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[m][i][k] = __fmaf_rn(r[m][i][k], sc[m][k >> 1][i][k & 1], y[m][i][k]);
     }
-    now.add(x + i * SEG, 8 * a.x_stride, use, y);
   }
 
+  // Join: the columns of a vector, the warps of a tile, the CTAs of a cluster.
+  constexpr int OUTS = S::VECS * S::ROWS;
+  float* mine = part + warp * OUTS;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int h = 0; h < 2; ++h) {
+      float* at = mine + 16 * m + 8 * h + g;
+      if constexpr (NS > 8) {  // both halves of the segments
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int v = 8 * n + 2 * t + (k & 1);
-        if (v < vecs) part[(warp * VECS + v) * ROWS + 16 * m + 8 * (k >> 1) + g] = y[m][n][k];
+        for (int i = 0; i < T; i += 2)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            at[(i / 2 * 8 + 2 * t + e) * S::ROWS] = y[m][i][2 * h + e] + y[m][i + 1][2 * h + e];
+      } else if constexpr (NV == 8) {
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) at[(i * 8 + 2 * t + e) * S::ROWS] = y[m][i][2 * h + e];
+      } else {
+        float v[2] = {y[m][0][2 * h], y[m][0][2 * h + 1]};
+        if (NV == 1) v[0] += v[1];
+#pragma unroll
+        for (int e = 0; e < (NV == 1 ? 1 : 2); ++e) {
+          if (NV < 4) v[e] += __shfl_xor_sync(~0u, v[e], 1);
+          v[e] += __shfl_xor_sync(~0u, v[e], 2);
+          if (t < (NV + 1) / 2) at[(2 * t + e) * S::ROWS] = v[e];
+        }
       }
+    }
   __syncthreads();
-  for (int o = threadIdx.x; o < vecs * ROWS; o += blockDim.x) {
-    float sum = part[o];
-    for (int w = 1; w < warps; ++w) sum += part[w * VECS * ROWS + o];
-    part[o] = sum;  // read and written by this thread only
+  const int outs = wr * OUTS;
+  for (int o = threadIdx.x; o < outs; o += kThreads) {
+    float* p = part + o / OUTS * wk * OUTS + o % OUTS;
+    float sum = *p;
+    for (int k = 1; k < wk; ++k) sum += p[k * OUTS];
+    *p = sum;  // read and written by this thread only
   }
   if (split > 1) cg::this_cluster().sync();
   if (rank == 0) {
-    for (int o = threadIdx.x; o < vecs * ROWS; o += blockDim.x) {
-      float sum = part[o];
-      for (int r = 1; r < split; ++r) sum += cg::this_cluster().map_shared_rank(part, r)[o];
-      const int64_t r = row0 + o % ROWS;
-      if (r < a.rows) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x / split) * wr * S::ROWS;
+    for (int o = threadIdx.x; o < outs; o += kThreads) {
+      const int at = o / OUTS * wk * OUTS + o % OUTS, v = o % OUTS / S::ROWS;
+      const int64_t r = first + o / OUTS * S::ROWS + o % S::ROWS;
+      float sum = part[at];
+      for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(part, k)[at];
+      if (r < a.rows && v < vecs) {
         if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
-        store_y(a.y, (vec0 + o / ROWS) * a.y_stride + r, sum, a.y_kind);
+        store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
       }
     }
   }
@@ -287,54 +357,55 @@ __global__ void __launch_bounds__(kThreads) k_matvec(const MatvecArgs a, int log
   }
 }
 
-template <typename TT, int BITS, int SEG, int MT, int NT>
-static cudaError_t run_mma(const MatvecArgs& a, int log2b, int warps, int split, cudaStream_t s) {
-  constexpr int ROWS = 16 * MT, VECS = 8 * NT;
+// How a launch splits a product: row fragments and segments in flight per warp, warps of a CTA and
+// CTAs that share a row tile.
+struct MvPlan {
+  int mt, wk, split;
+};
+
+template <typename TT, int BITS, int MT, int NV, int SP, int NT, int U>
+static cudaError_t run_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
+  using S = MvShape<BITS, MT, NV, SP, NT>;
+  const int64_t rows = static_cast<int64_t>(S::ROWS) * (kWarps / p.wk);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + ROWS - 1) / ROWS * split),
-                     static_cast<unsigned>((a.vecs + VECS - 1) / VECS));
-  cfg.blockDim = dim3(32 * warps);
-  cfg.dynamicSmemBytes = static_cast<size_t>(warps) * ROWS * VECS * sizeof(float);
+  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + rows - 1) / rows * p.split),
+                     static_cast<unsigned>((a.vecs + S::VECS - 1) / S::VECS));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kWarps * S::VECS * S::ROWS * sizeof(float);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.x = p.split;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_matvec_mma<TT, BITS, SEG, MT, NT>, a, log2b, split);
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_matvec_mma<TT, BITS, MT, NV, SP, NT, U>, a, log2b, p.wk, p.split,
+                            Codes<TT, BITS>::kMasks);
 }
 
-template <typename TT, int BITS, int SEG, int MT>
-static cudaError_t by_vecs(const MatvecArgs& a, int log2b, int warps, int split, cudaStream_t s) {
-  if (a.vecs <= 8) return run_mma<TT, BITS, SEG, MT, 1>(a, log2b, warps, split, s);
-  if (a.vecs <= 16) return run_mma<TT, BITS, SEG, MT, 2>(a, log2b, warps, split, s);
-  return run_mma<TT, BITS, SEG, MT, 4>(a, log2b, warps, split, s);
+template <typename TT, int BITS, int SP>
+static cudaError_t by_vecs(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
+  if (a.vecs == 1) return run_mma<TT, BITS, 1, 1, SP, 1, 8>(a, log2b, p, s);
+  if (a.vecs == 2) return p.mt == 2 ? run_mma<TT, BITS, 2, 2, SP, 1, 4>(a, log2b, p, s) : run_mma<TT, BITS, 1, 2, SP, 1, 8>(a, log2b, p, s);
+  if (a.vecs <= 4) return p.mt == 2 ? run_mma<TT, BITS, 2, 4, SP, 1, 4>(a, log2b, p, s) : run_mma<TT, BITS, 1, 4, SP, 1, 8>(a, log2b, p, s);
+  if (a.vecs <= 8) return p.mt == 2 ? run_mma<TT, BITS, 2, 8, SP, 1, 4>(a, log2b, p, s) : run_mma<TT, BITS, 1, 8, SP, 1, 4>(a, log2b, p, s);
+  return p.mt == 2 ? run_mma<TT, BITS, 2, 8, SP, 2, 2>(a, log2b, p, s) : run_mma<TT, BITS, 1, 8, SP, 2, 4>(a, log2b, p, s);
 }
 
-template <typename TT, int MT>
-static cudaError_t by_codes(const MatvecArgs& a, int log2b, int warps, int split, cudaStream_t s) {
-  if (a.bits == 8) return by_vecs<TT, 8, 64, MT>(a, log2b, warps, split, s);
-  if (a.block == 64) return by_vecs<TT, 4, 64, MT>(a, log2b, warps, split, s);
-  return by_vecs<TT, 4, 128, MT>(a, log2b, warps, split, s);
+template <typename TT>
+static cudaError_t by_codes(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
+  if (a.bits == 8) return by_vecs<TT, 8, 1>(a, log2b, p, s);
+  return a.block == 64 ? by_vecs<TT, 4, 2>(a, log2b, p, s) : by_vecs<TT, 4, 1>(a, log2b, p, s);
 }
 
-static cudaError_t launch_mma(const MatvecArgs& a, int log2b, int mt, int warps, int split,
-                              cudaStream_t s) {
-  if (a.x_bf16)
-    return mt == 2 ? by_codes<BF16, 2>(a, log2b, warps, split, s)
-                   : by_codes<BF16, 1>(a, log2b, warps, split, s);
-  return mt == 2 ? by_codes<F16, 2>(a, log2b, warps, split, s)
-                 : by_codes<F16, 1>(a, log2b, warps, split, s);
+static cudaError_t launch_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
+  return a.x_bf16 ? by_codes<BF16>(a, log2b, p, s) : by_codes<F16>(a, log2b, p, s);
 }
 
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s) {
   const int log2b = __builtin_ctz(static_cast<unsigned>(a.block));
-  if (a.cols % a.block == 0 && a.x_stride % 8 == 0) {
-    const int64_t tiles = (a.rows + 15) / 16;
-    int split = 1;
-    while (split < 8 && tiles * split < 2 * 152) split *= 2;
-    return launch_mma(a, log2b, 1, 8, split, s);
+  if (a.cols % a.block == 0 && a.x_stride % 8 == 0 && (a.bits == 8 || a.cols % 128 == 0)) {
+    return launch_mma(a, log2b, MvPlan{a.vecs == 1 ? 1 : 2, 8, 1}, s);
   }
   const dim3 grid(tile_grid(a.rows, kWarps), static_cast<unsigned>(a.vecs));
   if (a.x_bf16) k_matvec<BF16><<<grid, kThreads, 0, s>>>(a, log2b);
