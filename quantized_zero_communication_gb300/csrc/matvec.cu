@@ -128,9 +128,11 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
 // two columns per vector, each zero in the half that is not its own (SP = 2). A column's
 // result is a sum over one block, so it is multiplied by the row's scale and added up in fp32.
 //
-// A warp loads U segments of its rows before it works on the first. A row's batches of U segments
-// are dealt round robin to the warps that share its tile (wk of a CTA's, times `split` CTAs of a
-// cluster); their sums are joined in a fixed order through shared memory.
+// A row's units of kUnit segments are dealt round robin to the warps that share its tile (wk of a
+// CTA's, times `split` CTAs of a cluster); their sums are joined in a fixed order through shared
+// memory. The code bytes of the next U segments are always on their way into shared memory
+// (cp.async, so they hold no registers); a lane reads back only what it copied itself, so the
+// loop has no barrier.
 // ---------------------------------------------------------------------------------
 template <int BITS, int MT, int NV, int SP, int NT>
 struct MvShape {
@@ -141,16 +143,27 @@ struct MvShape {
   static constexpr int PW = 16 / BITS;                         // pairs per word
   static constexpr int SG = NV * SP >= 8 ? 1 : 8 / (NV * SP);  // segments per set of columns
   static constexpr int TILES = NV * SP > 8 ? NT * SP : NT;     // sets of 8 columns
+  static constexpr int UNIT = 8 / MT;                          // segments dealt at a time
+  static constexpr int SEG_BYTES = 2 * MT * 32 * 16;           // code bytes of a warp's segment
   static_assert(NT == 1 || NV == 8, "more than one set of vectors only when they fill it");
+  static_assert(UNIT % SG == 0, "whole sets of columns per unit");
 };
 
+__device__ __forceinline__ uint4 ld_shared_v4(unsigned p) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(p));
+  return r;
+}
+
 template <typename TT, int BITS, int MT, int NV, int SP, int NT, int U>
-__global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, int log2b, int wk,
-                                                            int split, const Masks masks) {
+__global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
+    k_matvec_mma(const MatvecArgs a, int log2b, int wk, int split, const Masks masks) {
   using S = MvShape<BITS, MT, NV, SP, NT>;
-  constexpr int SEG = S::SEG, T = S::TILES, NS = NV * SP;
-  static_assert(U % S::SG == 0, "whole sets of columns per batch");
-  extern __shared__ float part[];  // [kWarps][VECS * ROWS]
+  constexpr int SEG = S::SEG, T = S::TILES, NS = NV * SP, UNIT = S::UNIT;
+  static_assert(UNIT % U == 0, "a segment's place in the ring is known at compile time");
+  extern __shared__ __align__(16) uint8_t smem[];  // [kWarps][U segments]; later the sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % split;  // = the CTA's rank in its cluster
@@ -158,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x / split) * wr + warp / wk) * S::ROWS;
   const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * S::VECS;
   const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(S::VECS)));
-  const int segs = static_cast<int>(a.cols / SEG), batches = (segs + U - 1) / U;
-  const int step = wk * split;
+  const int segs = static_cast<int>(a.cols / SEG), units = (segs + UNIT - 1) / UNIT;
+  const int step = wk * split, unit0 = rank * wk + warp % wk;
 
   // Rows past the end read the last one, vectors past the end the last one: not stored.
   const uint8_t* codes[MT][2];
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t r = min(row0 + 16 * m + 8 * h + g, a.rows - 1);
-      codes[m][h] = a.codes + r * (a.cols * BITS / 8) + t * 16;
+      codes[m][h] = a.codes + r * (a.cols * BITS / 8) + static_cast<int64_t>(unit0) * (UNIT * 64) + t * 16;
       scale[m][h] = a.scales + r * (a.cols >> log2b);
     }
   // Column g of set i: vector, and which segment of its group and half of it.
@@ -186,22 +199,29 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
   }
   const int my_seg = NS >= 8 ? 0 : 2 * t / NS;  // segment of this lane's result columns 2t ..
 
+  const unsigned ring = smem_addr(smem) + warp * (U * S::SEG_BYTES) + lane * 16;
+  // Segment `at` of this warp's unit number n, into its place.
+  auto fill = [&](int n, int at) {
+    const int seg = (unit0 + n * step) * UNIT + at;
+    if (seg < segs)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           ring + at % U * S::SEG_BYTES + (2 * m + h) * 512),
+                       "l"(codes[m][h] + static_cast<int64_t>(n) * step * (UNIT * 64) + at * 64)
+                       : "memory");
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) fill(0, u);
+
   float y[MT][T][4] = {};
-  for (int b = rank * wk + warp % wk; b < batches; b += step) {
-    const int seg0 = b * U, left = segs - seg0;
-    uint32_t w[U][MT][2][4];
+  for (int n = 0; unit0 + n * step < units; ++n) {
+    const int seg0 = (unit0 + n * step) * UNIT, left = segs - seg0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 v = ld_stream_v4(codes[m][h] + static_cast<int64_t>(seg0) * 64 + u * 64);
-            w[u][m][h][0] = v.x, w[u][m][h][1] = v.y, w[u][m][h][2] = v.z, w[u][m][h][3] = v.w;
-          }
-#pragma unroll
-    for (int u0 = 0; u0 < U; u0 += S::SG) {  // one set of columns at a time
+    for (int u0 = 0; u0 < UNIT; u0 += S::SG) {  // one set of columns at a time
       if (u0 >= left) break;
       uint32_t f[T][S::TJ][4];  // fragments of x: the pairs that go with the code pairs
 #pragma unroll
@@ -240,14 +260,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
 #pragma unroll
       for (int s = 0; s < S::SG; ++s) {
         if (s > 0 && u0 + s >= left) break;
+        cp_async_wait<U - 1>();
+        uint32_t w[MT][2][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = ld_shared_v4(ring + (u0 + s) % U * S::SEG_BYTES + (2 * m + h) * 512);
+            w[m][h][0] = v.x, w[m][h][1] = v.y, w[m][h][2] = v.z, w[m][h][3] = v.w;
+          }
         float c[MT][T][4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             uint32_t q[2][S::PW];
-            Codes<TT, BITS>::pairs(w[u0 + s][m][0][j], masks, q[0]);
-            Codes<TT, BITS>::pairs(w[u0 + s][m][1][j], masks, q[1]);
+            Codes<TT, BITS>::pairs(w[m][0][j], masks, q[0]);
+            Codes<TT, BITS>::pairs(w[m][1][j], masks, q[1]);
 #pragma unroll
             for (int p = 0; p < S::PW; p += 2) {
               const uint32_t fa[4] = {q[0][p], q[1][p], q[0][p + 1], q[1][p + 1]};
@@ -267,6 +296,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
               else if (NS == 1) { if ((k & 1) == (s & 1) && t == s >> 1) r[m][i][k] = c[m][i][k]; }
               else if (my_seg == s) r[m][i][k] = c[m][i][k];
             }
+        // the segment's place is free (its codes have been used)
+        if (u0 + s + U < UNIT) fill(n, u0 + s + U);
+        else fill(n + 1, u0 + s + U - UNIT);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -278,9 +310,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
     }
   }
 
-  // Join: the columns of a vector, the warps of a tile, the CTAs of a cluster.
-  constexpr int OUTS = S::VECS * S::ROWS;
-  float* mine = part + warp * OUTS;
+  // Join: the columns of a vector, the warps of a tile, the CTAs of a cluster. The warp's sums
+  // replace its codes, all of which have landed and been used.
+  cp_async_wait<0>();
+  __syncwarp();
+  constexpr int OUTS = S::VECS * S::ROWS, STRIDE = U * S::SEG_BYTES / 4;
+  static_assert(OUTS <= STRIDE, "the sums fit into the ring");
+  float* part = reinterpret_cast<float*>(smem);
+  float* mine = part + warp * STRIDE;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -311,16 +348,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
   __syncthreads();
   const int outs = wr * OUTS;
   for (int o = threadIdx.x; o < outs; o += kThreads) {
-    float* p = part + o / OUTS * wk * OUTS + o % OUTS;
+    float* p = part + o / OUTS * wk * STRIDE + o % OUTS;
     float sum = *p;
-    for (int k = 1; k < wk; ++k) sum += p[k * OUTS];
+    for (int k = 1; k < wk; ++k) sum += p[k * STRIDE];
     *p = sum;  // read and written by this thread only
   }
   if (split > 1) cg::this_cluster().sync();
   if (rank == 0) {
     const int64_t first = static_cast<int64_t>(blockIdx.x / split) * wr * S::ROWS;
     for (int o = threadIdx.x; o < outs; o += kThreads) {
-      const int at = o / OUTS * wk * OUTS + o % OUTS, v = o % OUTS / S::ROWS;
+      const int at = o / OUTS * wk * STRIDE + o % OUTS, v = o % OUTS / S::ROWS;
       const int64_t r = first + o / OUTS * S::ROWS + o % S::ROWS;
       float sum = part[at];
       for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(part, k)[at];
@@ -333,63 +370,242 @@ __global__ void __launch_bounds__(kThreads, 2) k_matvec_mma(const MatvecArgs a, 
   if (split > 1) cg::this_cluster().sync();  // a CTA's sums outlive their readers
 }
 
-// Any width: a warp per row and vector, lanes striding over the row's codes.
-template <typename TT>
-__global__ void __launch_bounds__(kThreads) k_matvec(const MatvecArgs a, int log2b) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (r >= a.rows) return;
-  for (int64_t j = blockIdx.y; j < a.vecs; j += gridDim.y) {
-    const uint16_t* x = a.x + j * a.x_stride;
-    float sum = 0.0f;
-    for (int64_t c = lane; c < a.cols; c += 32) {
-      const int64_t e = r * a.cols + c;
-      const int q = a.bits == 8 ? static_cast<int>(static_cast<int8_t>(__ldg(a.codes + e)))
-                                : code_int4(__ldg(a.codes + (e >> 1)), static_cast<int>(e & 1));
-      const float w = __fmul_rn(static_cast<float>(q), __ldg(a.scales + (e >> log2b)));
-      sum = __fmaf_rn(w, bits16_to_float(__ldg(x + c), TT()), sum);
+// ---------------------------------------------------------------------------------
+// Any width, any stride of x: rows start inside a block, a word, a byte, so a matrix fragment has
+// no common scale and the products are fp32 ones. The codes are read by aligned octets (8
+// codes, one block each); a row whose first code is number s of its octet meets x shifted by s
+// columns, with zeros beyond both ends for the codes of its neighbours. Rows 8 apart have the
+// same s, so a warp takes RPW of them and reads its part of x once for all: without that the
+// shared-memory loads of x, one per code and vector, would cost more than the products.
+// ---------------------------------------------------------------------------------
+constexpr int kAnyOctets = 1024;  // of a row per pass over x, over all vectors: 36 KB
+
+// Octets of a row per CTA and per pass of it over x.
+struct AnyShape {
+  int per, chunk, pitch;  // pitch: floats of a vector's part of x, 9 for every 8 columns
+};
+__host__ __device__ inline AnyShape any_shape(int64_t cols, int split, int nvp) {
+  AnyShape s;
+  s.per = static_cast<int>(((cols + 14) / 8 + split - 1) / split);
+  s.chunk = s.per < kAnyOctets / nvp ? s.per : kAnyOctets / nvp;
+  s.pitch = (s.chunk + 3) * 9;
+  return s;
+}
+
+// Octet number o of the n codes: two words (INT8) or one. The last one may end early.
+template <int BITS>
+__device__ __forceinline__ uint2 ld_octet(const uint8_t* codes, int64_t o, int64_t n) {
+  const uint8_t* p = codes + o * BITS;
+  if ((o + 1) * 8 <= n)
+    return BITS == 8 ? ld_stream_v2(p) : make_uint2(ld_stream_b32(p), 0u);
+  uint32_t w[2] = {0u, 0u};
+  const int bytes = static_cast<int>((n - o * 8) * BITS + 7) / 8;
+  for (int i = 0; i < bytes; ++i) w[i >> 2] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+template <typename TT, int BITS, int RPW, int NVP>
+__global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int log2b, int split) {
+  const AnyShape shape = any_shape(a.cols, split, NVP);
+  extern __shared__ float xs[];  // [NVP][pitch], then [kWarps * RPW][NVP] sums
+  float* sums = xs + NVP * shape.pitch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(blockIdx.x) % split;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / split) * (kWarps * RPW) + warp;
+  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * NVP;
+  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(NVP)));
+  const int64_t n = a.rows * a.cols;
+  const int shift = static_cast<int>(row0 * a.cols & 7);  // the same for rows 8 apart
+  // Octets of a row, and this CTA's range of them (the same numbers for every row).
+  const int octets = static_cast<int>((a.cols + shift + 7) / 8);
+  const int last = (rank + 1) * shape.per;
+
+  int64_t first[RPW];       // octet that holds the row's first code
+  const float* scale[RPW];  // of its block
+  int in_block[RPW];        // its number in the block
+  const int sh = log2b - 3;
+#pragma unroll
+  for (int i = 0; i < RPW; ++i) {
+    const int64_t r = row0 + 8 * i < a.rows ? row0 + 8 * i : 0;  // (rows past the end: not read)
+    first[i] = r * a.cols / 8;
+    scale[i] = a.scales + (first[i] >> sh);
+    in_block[i] = static_cast<int>(first[i] & ((1 << sh) - 1));
+  }
+
+  float acc[RPW][NVP] = {};
+  for (int k0 = rank * shape.per; k0 < last; k0 += shape.chunk) {
+    const int k1 = min(k0 + shape.chunk, last);
+    // columns 8 k0 - 8 .. 8 k1 + 7 of x, zero outside the row; column c at c + c / 8 from there
+    __syncthreads();
+    for (int v = 0; v < vecs; ++v)
+      for (int i = threadIdx.x; i < (k1 - k0 + 2) * 8; i += kThreads) {
+        const int64_t c = static_cast<int64_t>(k0) * 8 - 8 + i;
+        xs[v * shape.pitch + i + i / 8] =
+            c >= 0 && c < a.cols ? bits16_to_float(__ldg(a.x + (vec0 + v) * a.x_stride + c), TT()) : 0.0f;
+      }
+    __syncthreads();
+    // octet k, code e: column 8 k + e - shift, at 9 (k - k0) + (8 + e - shift) of xs, one more
+    // from 8 on
+    int at[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) at[e] = 8 + e - shift + (8 + e - shift) / 8;
+    const int end = min(k1, octets);
+    constexpr int STEPS = 2;  // octets per lane and row whose codes are loaded ahead
+    for (int k = k0 + lane; k < end; k += 32 * STEPS) {
+      uint2 w[STEPS][RPW];
+      float sc[STEPS][RPW];
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+          w[j][i] = make_uint2(0u, 0u);
+          sc[j][i] = 0.0f;
+          if (k + 32 * j < end && row0 + 8 * i < a.rows) {
+            w[j][i] = ld_octet<BITS>(a.codes, first[i] + k + 32 * j, n);
+            sc[j][i] = __ldg(scale[i] + ((in_block[i] + k + 32 * j) >> sh));
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        if (k + 32 * j >= end) break;
+        const float* xk = xs + 9 * (k + 32 * j - k0);
+        f32x2 xp[NVP][4];  // in the order of the converted codes
+#pragma unroll
+        for (int v = 0; v < NVP; ++v) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = v < vecs ? xk[v * shape.pitch + at[e]] : 0.0f;
+          if constexpr (BITS == 4) {
+            xp[v][0] = f2(f[0], f[2]), xp[v][1] = f2(f[4], f[6]);
+            xp[v][2] = f2(f[1], f[3]), xp[v][3] = f2(f[5], f[7]);
+          } else {
+            xp[v][0] = f2(f[0], f[1]), xp[v][1] = f2(f[2], f[3]);
+            xp[v][2] = f2(f[4], f[5]), xp[v][3] = f2(f[6], f[7]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+          f32x2 q[4];
+          if constexpr (BITS == 4) {
+            int4x8_to_f2_eo(w[j][i].x, q, q + 2);
+          } else {
+            int8x4_to_f2(w[j][i].x, q);
+            int8x4_to_f2(w[j][i].y, q + 2);
+          }
+#pragma unroll
+          for (int v = 0; v < NVP; ++v) {
+            f32x2 d = f2_mul(q[0], xp[v][0]);
+            d = f2_fma(q[1], xp[v][1], d);
+            d = f2_fma(q[2], xp[v][2], d);
+            d = f2_fma(q[3], xp[v][3], d);
+            float lo, hi;
+            f2_split(d, lo, hi);
+            acc[i][v] = __fmaf_rn(__fadd_rn(lo, hi), sc[j][i], acc[i][v]);
+          }
+        }
+      }
     }
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) {
-      if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
-      store_y(a.y, j * a.y_stride + r, sum, a.y_kind);
+  }
+#pragma unroll
+  for (int i = 0; i < RPW; ++i)
+#pragma unroll
+    for (int v = 0; v < NVP; ++v) {
+      float sum = acc[i][v];
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == 0) sums[(8 * i + warp) * NVP + v] = sum;
     }
+  __syncthreads();
+  if (split > 1) cg::this_cluster().sync();
+  if (rank == 0) {
+    for (int o = threadIdx.x; o < kWarps * RPW * NVP; o += kThreads) {
+      const int v = o / (kWarps * RPW), i = o % (kWarps * RPW);
+      float sum = sums[i * NVP + v];
+      for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(sums, k)[i * NVP + v];
+      const int64_t r = static_cast<int64_t>(blockIdx.x / split) * (kWarps * RPW) + i;
+      if (r < a.rows && v < vecs) {
+        if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+        store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
+      }
+    }
+  }
+  if (split > 1) cg::this_cluster().sync();  // a CTA's sums outlive their readers
+}
+
+// One launch with `split` CTAs of a cluster along each row.
+template <typename... Params, typename... Args>
+static cudaError_t launch_split(void (*kern)(Params...), int64_t tiles, int64_t vec_groups, int split,
+                                size_t bytes, cudaStream_t s, Args... args) {
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(vec_groups));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(split);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
+template <typename TT, int BITS, int RPW, int NVP>
+static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  const int64_t octets = (a.cols + 14) / 8, tiles = (a.rows + kWarps * RPW - 1) / (kWarps * RPW);
+  int split = 1;  // until every SM has two CTAs, as long as a CTA has a step for every lane
+  while (split < 8 && tiles * split < 304 && octets >= split * 2 * 64) split *= 2;
+  const size_t bytes =
+      (static_cast<size_t>(NVP) * any_shape(a.cols, split, NVP).pitch + kWarps * RPW * NVP) * sizeof(float);
+  return launch_split(k_matvec_any<TT, BITS, RPW, NVP>, tiles, (a.vecs + NVP - 1) / NVP, split, bytes, s,
+                      a, log2b, split);
+}
+
+template <typename TT, int BITS, int RPW>
+static cudaError_t any_by_vecs(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  switch (a.vecs) {
+    case 1: return run_any<TT, BITS, RPW, 1>(a, log2b, s);
+    case 2: return run_any<TT, BITS, RPW, 2>(a, log2b, s);
+    case 3: return run_any<TT, BITS, RPW, 3>(a, log2b, s);
+    default: return run_any<TT, BITS, RPW, 4>(a, log2b, s);
   }
 }
 
-// How a launch splits a product: row fragments and segments in flight per warp, warps of a CTA and
-// CTAs that share a row tile.
+template <typename TT>
+static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  const bool few = a.rows < 4 * 8 * 152;  // rows for one CTA per SM
+  if (a.bits == 8) return few ? any_by_vecs<TT, 8, 1>(a, log2b, s) : any_by_vecs<TT, 8, 4>(a, log2b, s);
+  return few ? any_by_vecs<TT, 4, 1>(a, log2b, s) : any_by_vecs<TT, 4, 4>(a, log2b, s);
+}
+
+// How a launch splits a row: over wk warps of a CTA and `split` CTAs.
 struct MvPlan {
-  int mt, wk, split;
+  int wk, split;
 };
 
 template <typename TT, int BITS, int MT, int NV, int SP, int NT, int U>
 static cudaError_t run_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
   using S = MvShape<BITS, MT, NV, SP, NT>;
+  constexpr size_t kBytes = kWarps * U * S::SEG_BYTES;
+  static_assert(kBytes <= 48 * 1024, "no opt-in shared memory");
   const int64_t rows = static_cast<int64_t>(S::ROWS) * (kWarps / p.wk);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + rows - 1) / rows * p.split),
-                     static_cast<unsigned>((a.vecs + S::VECS - 1) / S::VECS));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kWarps * S::VECS * S::ROWS * sizeof(float);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = p.split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_matvec_mma<TT, BITS, MT, NV, SP, NT, U>, a, log2b, p.wk, p.split,
-                            Codes<TT, BITS>::kMasks);
+  return launch_split(k_matvec_mma<TT, BITS, MT, NV, SP, NT, U>, (a.rows + rows - 1) / rows,
+                      (a.vecs + S::VECS - 1) / S::VECS, p.split, kBytes, s, a, log2b, p.wk, p.split,
+                      Codes<TT, BITS>::kMasks);
 }
 
+// U: 4 KB of codes on their way per warp.
 template <typename TT, int BITS, int SP>
 static cudaError_t by_vecs(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
-  if (a.vecs == 1) return run_mma<TT, BITS, 1, 1, SP, 1, 8>(a, log2b, p, s);
-  if (a.vecs == 2) return p.mt == 2 ? run_mma<TT, BITS, 2, 2, SP, 1, 4>(a, log2b, p, s) : run_mma<TT, BITS, 1, 2, SP, 1, 8>(a, log2b, p, s);
-  if (a.vecs <= 4) return p.mt == 2 ? run_mma<TT, BITS, 2, 4, SP, 1, 4>(a, log2b, p, s) : run_mma<TT, BITS, 1, 4, SP, 1, 8>(a, log2b, p, s);
-  if (a.vecs <= 8) return p.mt == 2 ? run_mma<TT, BITS, 2, 8, SP, 1, 4>(a, log2b, p, s) : run_mma<TT, BITS, 1, 8, SP, 1, 4>(a, log2b, p, s);
-  return p.mt == 2 ? run_mma<TT, BITS, 2, 8, SP, 2, 2>(a, log2b, p, s) : run_mma<TT, BITS, 1, 8, SP, 2, 4>(a, log2b, p, s);
+  if (a.vecs == 1) return run_mma<TT, BITS, 1, 1, SP, 1, 4>(a, log2b, p, s);
+  if (a.vecs == 2) return run_mma<TT, BITS, 2, 2, SP, 1, 2>(a, log2b, p, s);
+  if (a.vecs <= 4) return run_mma<TT, BITS, 2, 4, SP, 1, 2>(a, log2b, p, s);
+  if (a.vecs <= 8) return run_mma<TT, BITS, 2, 8, SP, 1, 2>(a, log2b, p, s);
+  return run_mma<TT, BITS, SP == 1 ? 2 : 1, 8, SP, 2, SP == 1 ? 2 : 4>(a, log2b, p, s);
 }
 
 template <typename TT>
@@ -398,19 +614,27 @@ static cudaError_t by_codes(const MatvecArgs& a, int log2b, const MvPlan& p, cud
   return a.block == 64 ? by_vecs<TT, 4, 2>(a, log2b, p, s) : by_vecs<TT, 4, 1>(a, log2b, p, s);
 }
 
-static cudaError_t launch_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
-  return a.x_bf16 ? by_codes<BF16>(a, log2b, p, s) : by_codes<F16>(a, log2b, p, s);
+// Four warps a row where it has as many units, then more warps and CTAs until some 13 warps per
+// SM have work, never more than units. (8192 x 8192 INT4, one vector: 2 / 4 / 8 warps 15.4 / 12.3
+// / 14.7 us; 1024 x 16384, 8 warps: 1 / 2 / 4 CTAs 9.4 / 8.2 / 10.2 us; 32768 x 1024, one unit
+// a row: 1 / 2 warps 8.2 / 10.3 us.)
+static MvPlan mv_plan(int64_t tiles, int64_t units) {
+  MvPlan p{1, 1};
+  constexpr int64_t kBusy = 2000;
+  while (p.wk < kWarps && 2 * p.wk <= units && (p.wk < 4 || tiles * p.wk < kBusy)) p.wk *= 2;
+  while (p.split < 8 && 2 * p.split * p.wk <= units && tiles * p.wk * p.split < kBusy) p.split *= 2;
+  return p;
 }
 
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s) {
   const int log2b = __builtin_ctz(static_cast<unsigned>(a.block));
-  if (a.cols % a.block == 0 && a.x_stride % 8 == 0 && (a.bits == 8 || a.cols % 128 == 0)) {
-    return launch_mma(a, log2b, MvPlan{a.vecs == 1 ? 1 : 2, 8, 1}, s);
+  const int seg = a.bits == 8 ? 64 : 128;
+  if (a.cols % a.block == 0 && a.cols % seg == 0 && a.x_stride % 8 == 0) {
+    const int rows = a.vecs == 1 ? 16 : 32, unit = a.vecs == 1 ? 8 : 4;
+    const MvPlan p = mv_plan((a.rows + rows - 1) / rows, (a.cols / seg + unit - 1) / unit);
+    return a.x_bf16 ? by_codes<BF16>(a, log2b, p, s) : by_codes<F16>(a, log2b, p, s);
   }
-  const dim3 grid(tile_grid(a.rows, kWarps), static_cast<unsigned>(a.vecs));
-  if (a.x_bf16) k_matvec<BF16><<<grid, kThreads, 0, s>>>(a, log2b);
-  else k_matvec<F16><<<grid, kThreads, 0, s>>>(a, log2b);
-  return cudaGetLastError();
+  return a.x_bf16 ? launch_any<BF16>(a, log2b, s) : launch_any<F16>(a, log2b, s);
 }
 
 }  // namespace zpp
