@@ -251,14 +251,25 @@ def zpp_status_string(status):
 # reads or writes, then that all tensors are contiguous CUDA tensors on one device, and
 # raise ValueError before calling into libzpp. Sizes that the C ABI itself rejects (bad
 # bits, block or topology) are left to it and raise ZppError with its status.
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_kinds = {}  # torch dtype -> zpp_dtype, filled on first use
 
 
 def _dt(t):
-    torch = _torch()
-    return {torch.float16: ZPP_F16, torch.bfloat16: ZPP_BF16, torch.float32: ZPP_F32}[t]
+    if not _kinds:
+        torch = _torch()
+        _kinds.update({torch.float16: ZPP_F16, torch.bfloat16: ZPP_BF16, torch.float32: ZPP_F32})
+    return _kinds[t]
 
 
 def _bytes_dtypes():
@@ -286,6 +297,14 @@ def _cuda(*ts):
 
 def _stream(t):
     return _torch().cuda.current_stream(t.device).cuda_stream
+
+
+def _raw_stream(device):
+    """The current stream's handle of a device index, without building a Stream object where
+    torch offers that (a few microseconds of every call)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _check(status, where):
@@ -585,13 +604,17 @@ def _grad_norm(ptrs, sizes, like, max_norm, pre_scale, out=None):
         _need(out, "out", 2, (torch.float32,))
         _cuda(like, out)
     else:
-        out = torch.empty(2, dtype=torch.float32, device=like.device)
-    work = torch.empty(zpp_grad_norm_workspace(sum(sizes), len(sizes)), dtype=torch.float32,
-                       device=like.device)
-    _check(zpp_grad_norm(ptrs, sizes, _dt(like.dtype), float(pre_scale),
-                         math.inf if max_norm is None else float(max_norm), work.data_ptr(),
-                         out.data_ptr(), _stream(like)), "zpp_grad_norm")
+        out = like.new_empty(2, dtype=torch.float32)
+    work = like.new_empty(zpp_grad_norm_workspace(sum(sizes), len(sizes)), dtype=torch.float32)
+    _norm_call(ptrs, array.array("q", sizes), like, max_norm, pre_scale, work, out)
     return out
+
+
+def _norm_call(ptrs, lens, like, max_norm, pre_scale, work, out):
+    _check(lib().zpp_grad_norm(ptrs.buffer_info()[0], lens.buffer_info()[0], len(lens),
+                               _dt(like.dtype), pre_scale,
+                               math.inf if max_norm is None else max_norm, work.data_ptr(),
+                               out.data_ptr(), _raw_stream(like.get_device())), "zpp_grad_norm")
 
 
 def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -641,19 +664,24 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
     tab[7::8] = array.array("q", ptrs["n"])
     hp = AdamwParams(lr, betas[0], betas[1], eps, weight_decay, step, seed)
     _adamw(tab, grads[0], lists[-1][1][0] if weights is not None else None,
-           32 if scales is None else 8, hp, grad_scale)
+           32 if scales is None else 8, hp, _scale_address(grads[0], grad_scale))
 
 
-def _adamw(tab, grad, weight, state_bits, hp, grad_scale):
-    torch = _torch()
-    if grad_scale is not None:
-        _need(grad_scale, "grad_scale", dtypes=(torch.float32,))
-        if grad_scale.numel() < 1:
-            raise ValueError("grad_scale: at least one element")
-        _cuda(grad, grad_scale)
-    _check(zpp_adamw_step(tab, _dt(grad.dtype), ZPP_BF16 if weight is None else _dt(weight.dtype),
-                          state_bits, hp, 0 if grad_scale is None else grad_scale.data_ptr(),
-                          _stream(grad)), "zpp_adamw_step")
+def _scale_address(grad, grad_scale):
+    if grad_scale is None:
+        return 0
+    _need(grad_scale, "grad_scale", dtypes=(_torch().float32,))
+    if grad_scale.numel() < 1:
+        raise ValueError("grad_scale: at least one element")
+    _cuda(grad, grad_scale)
+    return grad_scale.data_ptr()
+
+
+def _adamw(tab, grad, weight, state_bits, hp, scale):
+    _check(lib().zpp_adamw_step(tab.buffer_info()[0], len(tab) // 8, _dt(grad.dtype),
+                                ZPP_BF16 if weight is None else _dt(weight.dtype), state_bits,
+                                ctypes.addressof(hp), scale, _raw_stream(grad.get_device())),
+           "zpp_adamw_step")
 
 
 def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None, y=None):
@@ -661,31 +689,42 @@ def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None,
     transposed [rows][cols] matrix that quant_blockwise gave (codes, scales) for -> y [..., rows]
     of `dtype` (default: x's). bias: [rows] of x's dtype. y: an output buffer, same form as x."""
     torch = _torch()
-    _need(x, "x", dtypes=(torch.float16, torch.bfloat16))
-    if x.dim() < 1 or x.shape[-1] < 1 or rows < 0:
+    dt, shape = x.dtype, x.shape
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        _need(x, "x", dtypes=(torch.float16, torch.bfloat16))
+    if not shape or shape[-1] < 1 or rows < 0:
         raise ValueError("x: [..., cols] with cols >= 1, and rows >= 0")
-    cols = x.shape[-1]
-    n, ok = rows * cols, _sizes_ok(rows * cols, block, bits)
-    _need(codes, "codes", zpp_code_bytes(n, bits) if ok else None, _bytes_dtypes())
-    _need(scales, "scales", zpp_num_scales(n, block) if ok else None, (torch.float32,))
-    if bias is not None:
-        _need(bias, "bias", rows, (x.dtype,))
-    vecs, x_stride = _rows(x, "x")
+    cols = shape[-1]
+    n = rows * cols
+    if _sizes_ok(n, block, bits):
+        if codes.numel() != (n if bits == 8 else (n + 1) // 2) or scales.numel() != -(-n // block):
+            _need(codes, "codes", zpp_code_bytes(n, bits))
+            _need(scales, "scales", zpp_num_scales(n, block))
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
+        _need(codes, "codes", dtypes=_bytes_dtypes())
+        _need(scales, "scales", dtypes=(torch.float32,))
+    if bias is not None and (bias.dtype is not dt or bias.numel() != rows):
+        _need(bias, "bias", rows, (dt,))
+    vecs, x_stride = (1, cols) if len(shape) == 1 and x.is_contiguous() else _rows(x, "x")
+    device = x.get_device()
     if y is None:
-        y = torch.empty(x.shape[:-1] + (rows,), dtype=dtype or x.dtype, device=x.device)
+        if device >= 0:
+            y = x.new_empty((*shape[:-1], rows), dtype=dtype or dt)
         y_stride = rows
     else:
         _need(y, "y", vecs * rows, (torch.float16, torch.bfloat16, torch.float32))
-        if y.shape != x.shape[:-1] + (rows,) or (dtype is not None and y.dtype != dtype):
+        if y.shape != (*shape[:-1], rows) or (dtype is not None and y.dtype != dtype):
             raise ValueError(f"y: {tuple(y.shape)} of {y.dtype} does not fit the call")
         y_stride = _rows(y, "y")[1]
-    _cuda(codes, scales, *(t for t in (bias,) if t is not None))
-    if not x.is_cuda or any(t.device != x.device for t in (codes, y)):
+    if (device < 0 or codes.get_device() != device or scales.get_device() != device
+            or y.get_device() != device or not codes.is_contiguous() or not scales.is_contiguous()
+            or (bias is not None and (bias.get_device() != device or not bias.is_contiguous()))):
+        _cuda(codes, scales, *(t for t in (bias,) if t is not None))
         raise ValueError("all tensors of a call must be on one CUDA device")
-    _check(zpp_matvec_blockwise(codes.data_ptr(), scales.data_ptr(), rows, cols, block, bits,
-                                x.data_ptr(), _dt(x.dtype), vecs, x_stride,
-                                0 if bias is None else bias.data_ptr(), y.data_ptr(),
-                                _dt(y.dtype), y_stride, _stream(x)), "zpp_matvec_blockwise")
+    _check(lib().zpp_matvec_blockwise(
+        codes.data_ptr(), scales.data_ptr(), rows, cols, block, bits, x.data_ptr(), _dt(dt), vecs,
+        x_stride, 0 if bias is None else bias.data_ptr(), y.data_ptr(), _dt(y.dtype), y_stride,
+        _raw_stream(device)), "zpp_matvec_blockwise")
     return y
 
 
@@ -694,7 +733,7 @@ def _rows(t, name):
     cols = t.shape[-1]
     if t.is_contiguous():
         return (t.numel() // cols if cols else 0), cols
-    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < cols:
+    if t.dim() != 2 or (t.stride(1) != 1 and cols > 1) or t.stride(0) < cols:
         raise ValueError(f"{name}: rows must be contiguous and at least a row apart")
     return t.shape[0], t.stride(0)
 

@@ -285,8 +285,8 @@ __device__ __forceinline__ void part_block(const AdamwTensor& t, const AdamwArgs
 }
 
 // V8: p, fp32 states and fp32 gradients of every tensor start 32-byte aligned.
-template <bool FP8, bool V8>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamwTable tab) {
+template <bool FP8, bool V8, int CAP>
+__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamwTableOf<CAP> tab) {
   const AdamwArgs& a = tab.a;
   const float c = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
   if (!isfinite(c)) return;  // overflowed gradients: the step is skipped
@@ -307,8 +307,16 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
   else part_block<FP8>(t, a, c, block, number, static_cast<int>(left), lane);
 }
 
-cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s) {
+template <int CAP>
+static cudaError_t run_adamw(const AdamwTableOf<CAP>& tab, int state_bits, bool v8, cudaStream_t s) {
   const int grid = tab.first[tab.count];
+  auto kern = state_bits == 8 ? (v8 ? k_adamw<true, true, CAP> : k_adamw<true, false, CAP>)
+                              : (v8 ? k_adamw<false, true, CAP> : k_adamw<false, false, CAP>);
+  kern<<<grid, kThreads, 0, s>>>(tab);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s) {
   uintptr_t bits = 0;
   for (int i = 0; i < tab.count; ++i) {
     const AdamwTensor& t = tab.t[i];
@@ -317,14 +325,18 @@ cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s) 
     if (state_bits == 32) bits |= reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v);
   }
   const bool v8 = (bits & 31) == 0;
-  if (state_bits == 8) {
-    if (v8) k_adamw<true, true><<<grid, kThreads, 0, s>>>(tab);
-    else k_adamw<true, false><<<grid, kThreads, 0, s>>>(tab);
-  } else {
-    if (v8) k_adamw<false, true><<<grid, kThreads, 0, s>>>(tab);
-    else k_adamw<false, false><<<grid, kThreads, 0, s>>>(tab);
+  if (tab.count > kFewTensors) return run_adamw(tab, state_bits, v8, s);
+  AdamwTableOf<kFewTensors> few;
+  for (int i = 0; i < tab.count; ++i) {
+    few.t[i] = tab.t[i];
+    few.first[i] = tab.first[i];
+    few.block0[i] = tab.block0[i];
   }
-  return cudaGetLastError();
+  few.first[tab.count] = tab.first[tab.count];
+  few.count = tab.count;
+  few.first_block = tab.first_block;
+  few.a = tab.a;
+  return run_adamw(few, state_bits, v8, s);
 }
 
 }  // namespace zpp

@@ -33,9 +33,9 @@ __device__ __forceinline__ T block_sum(T v) {  // valid in thread 0; blockDim.x 
 // One chunk per CTA. A full chunk is kNormChunk / kThreads = 64 elements per thread, all of
 // whose 32-byte vectors are loaded before the first product (no loop, so the most loads in
 // flight); a tensor's last, shorter chunk is read element by element.
-template <int KIND, bool V8>
-__global__ void __launch_bounds__(kThreads) k_norm_partial(const __grid_constant__ NormTable tab,
-                                                           float* __restrict__ partial) {
+template <int KIND, bool V8, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    k_norm_partial(const __grid_constant__ NormTableOf<CAP> tab, float* __restrict__ partial) {
   int lo = 0, hi = tab.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -92,6 +92,16 @@ __global__ void __launch_bounds__(1024) k_norm_finish(const float* __restrict__ 
   }
 }
 
+template <int CAP>
+static cudaError_t run_partial(const NormTableOf<CAP>& tab, int g_kind, bool v8, float* workspace,
+                               cudaStream_t s) {
+  auto kern = g_kind == 2   ? (v8 ? k_norm_partial<2, true, CAP> : k_norm_partial<2, false, CAP>)
+              : g_kind == 1 ? (v8 ? k_norm_partial<1, true, CAP> : k_norm_partial<1, false, CAP>)
+                            : (v8 ? k_norm_partial<0, true, CAP> : k_norm_partial<0, false, CAP>);
+  kern<<<tab.first[tab.count], kThreads, 0, s>>>(tab, workspace);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
                              float* workspace, float* out, cudaStream_t s) {
   const int chunks = tab.first[tab.count];
@@ -100,11 +110,20 @@ cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, 
     for (int i = 0; i < tab.count; ++i)
       if (tab.n[i] > 0) bits |= reinterpret_cast<uintptr_t>(tab.ptr[i]);
     const bool v8 = (bits & 31) == 0;
-    auto kern = g_kind == 2   ? (v8 ? k_norm_partial<2, true> : k_norm_partial<2, false>)
-                : g_kind == 1 ? (v8 ? k_norm_partial<1, true> : k_norm_partial<1, false>)
-                              : (v8 ? k_norm_partial<0, true> : k_norm_partial<0, false>);
-    kern<<<chunks, kThreads, 0, s>>>(tab, workspace);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (tab.count > kFewTensors) {
+      e = run_partial(tab, g_kind, v8, workspace, s);
+    } else {
+      NormTableOf<kFewTensors> few;
+      for (int i = 0; i < tab.count; ++i) {
+        few.ptr[i] = tab.ptr[i];
+        few.n[i] = tab.n[i];
+        few.first[i] = tab.first[i];
+      }
+      few.first[tab.count] = chunks;
+      few.count = tab.count;
+      e = run_partial(few, g_kind, v8, workspace, s);
+    }
     if (e != cudaSuccess) return e;
   }
   k_norm_finish<<<1, 1024, 0, s>>>(workspace, chunks, pre_scale, max_norm, out);

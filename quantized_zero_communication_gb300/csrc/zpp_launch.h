@@ -77,12 +77,17 @@ cudaError_t launch_copy(const void* src, void* dst, int64_t bytes, cudaStream_t 
 // K7: sums of squares over a list of tensors (one partial per CTA into `workspace`), then
 // norm and clip factor. The list travels in the kernel's parameter space.
 constexpr int kNormChunk = 16384;  // elements per CTA
-struct NormTable {
-  const void* ptr[kMaxTensors];
-  int64_t n[kMaxTensors];
-  int32_t first[kMaxTensors + 1];  // CTAs of the tensors before this one
+template <int CAP>
+struct NormTableOf {
+  const void* ptr[CAP];
+  int64_t n[CAP];
+  int32_t first[CAP + 1];  // CTAs of the tensors before this one
   int32_t count;
 };
+using NormTable = NormTableOf<kMaxTensors>;
+// A launch's parameters are copied by the driver: up to this many tensors travel in a small
+// table (a call with one tensor costs the host 3 us less than with the full one).
+constexpr int kFewTensors = 16;
 inline int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
 cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
                              float* workspace, float* out, cudaStream_t s);
@@ -111,14 +116,16 @@ struct AdamwArgs {
   const float* grad_scale;
   int32_t g_kind, w_kind;  // zpp_dtype of grad and weight
 };
-struct AdamwTable {
-  AdamwTensor t[kAdamwTensors];
-  int32_t first[kAdamwTensors + 1];  // chunks of the tensors before this one
-  int32_t block0[kAdamwTensors];     // state blocks of the tensors before this one
+template <int CAP>
+struct AdamwTableOf {
+  AdamwTensor t[CAP];
+  int32_t first[CAP + 1];  // chunks of the tensors before this one
+  int32_t block0[CAP];     // state blocks of the tensors before this one
   int32_t count;
-  int64_t first_block;               // state blocks of the tensors of earlier launches
+  int64_t first_block;     // state blocks of the tensors of earlier launches
   AdamwArgs a;
 };
+using AdamwTable = AdamwTableOf<kAdamwTensors>;
 static_assert(sizeof(AdamwTable) <= 32764, "kernel parameter space");
 inline int64_t adamw_chunks(int64_t n) { return (n + kAdamwChunk - 1) / kAdamwChunk; }
 cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s);

@@ -17,7 +17,8 @@ class AdamW:
     with one fp32 scale per 256 elements, rounded stochastically from `seed` and the step
     (see include/zpp.h). weights: fp16 or bf16 tensors of the parameters' sizes that each
     step fills, or None. exp_avg, exp_avg_sq, scales and step resume from a saved state()
-    (the tensors are taken over, not copied); by default the states start at zero.
+    (the tensors are taken over, not copied); by default the states start at zero. One
+    optimiser's steps belong on one stream at a time (they share a workspace).
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *,
@@ -43,8 +44,8 @@ class AdamW:
         code = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
 
         def states(given, sizes, dtype):
-            if given is not None:
-                return list(given)
+            if given is not None:  # (aliases, which keep the memory alive)
+                return [t.detach() for t in given]
             # one buffer, every tensor's part 256 elements aligned
             at, end = [], 0
             for n in sizes:
@@ -73,8 +74,10 @@ class AdamW:
                                 (torch.float16, torch.bfloat16)))
         self._table = array.array("q", bytes(64 * len(self.params)))
         self._table[7::8] = array.array("q", self._sizes)
-        for entry in self._lists:
-            self._enter(*entry)
+        self._hp = _b.AdamwParams(lr, *self.betas, eps, weight_decay, step, seed)
+        self._ptrs = {entry[0]: self._enter(*entry) for entry in self._lists}
+        self._lens = array.array("q", self._sizes)
+        self._work = None
 
     def _enter(self, name, column, tensors, sizes, dtypes):
         """Checks a list and writes its addresses into the call's table."""
@@ -99,23 +102,35 @@ class AdamW:
         optimiser's for this step and the following ones."""
         torch = _b._torch()
         grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
-        for entry in self._lists:  # storage may have moved since the last step
-            self._enter(*entry)
+        address = torch.Tensor.data_ptr
+        for entry in self._lists:  # the caller's tensors may have other storage by now
+            if entry[0] in ("params", "weights") and \
+                    array.array("q", map(address, entry[2])) != self._ptrs[entry[0]]:
+                self._ptrs[entry[0]] = self._enter(*entry)
         ptrs = self._enter("grads", 1, grads, self._sizes,
                            (torch.float16, torch.bfloat16, torch.float32))
         if lr is not None:
             self.lr = lr
-        norm = None
+        norm, scale = None, 0
         if max_norm is not None or pre_scale is not None:
             if grad_scale is not None:
                 raise ValueError("grad_scale replaces max_norm and pre_scale")
-            norm = _b._grad_norm(ptrs, self._sizes, grads[0], max_norm,
-                                 1.0 if pre_scale is None else pre_scale)
-            grad_scale = norm[1:]
-        hp = _b.AdamwParams(self.lr, *self.betas, self.eps, self.weight_decay, self.steps + 1,
-                            self.seed)
+            if self._work is None:
+                self._work = grads[0].new_empty(
+                    _b.zpp_grad_norm_workspace(sum(self._sizes), len(self._sizes)),
+                    dtype=torch.float32)
+            norm = grads[0].new_empty(2, dtype=torch.float32)
+            _b._norm_call(ptrs, self._lens, grads[0], max_norm,
+                          1.0 if pre_scale is None else pre_scale, self._work, norm)
+            scale = norm.data_ptr() + 4  # its second element
+        elif grad_scale is not None:
+            scale = _b._scale_address(grads[0], grad_scale)
+        hp = self._hp
+        hp.lr, hp.step = self.lr, self.steps + 1
+        hp.beta1, hp.beta2 = self.betas
+        hp.eps, hp.weight_decay = self.eps, self.weight_decay
         _b._adamw(self._table, grads[0], self.weights[0] if self.weights else None,
-                  self.state_bits, hp, grad_scale)
+                  self.state_bits, hp, scale)
         self.steps += 1
         return norm
 
