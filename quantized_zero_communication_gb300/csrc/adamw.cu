@@ -91,30 +91,34 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x2(float a, float b) {
 
 // 32 bits for element number i: low 16 round m, high 16 round sqrt(v). Two multiply-xorshift
 // rounds over a Weyl sequence; the odd constants are fractional bits of the golden ratio and of
-// the square roots of 3, 7 and 13.
-__device__ __forceinline__ uint32_t round_bits(uint64_t i, uint32_t key) {
-  uint32_t x = static_cast<uint32_t>(i) * 0x9E3779B9u +
-               static_cast<uint32_t>(i >> 32) * 0xA54FF53Bu + key;
-  x = (x ^ (x >> 16)) * 0xBB67AE85u + key;
-  x = (x ^ (x >> 15)) * 0x9B05688Du;
-  return x ^ (x >> 16);
+// the square roots of 3, 7 and 13. A block's numbers start at a multiple of 256, so they share
+// their high word: hash_start gives the sequence at the block's first number, hash_at the bits
+// of the o-th after it, the last xorshift left to the two users (it changes the low half only).
+__device__ __forceinline__ uint32_t hash_start(uint64_t i, uint32_t key) {
+  return static_cast<uint32_t>(i) * 0x9E3779B9u + static_cast<uint32_t>(i >> 32) * 0xA54FF53Bu + key;
 }
+__device__ __forceinline__ uint32_t hash_at(uint32_t start, uint32_t o, uint32_t key) {
+  uint32_t x = start + o * 0x9E3779B9u;
+  x = (x ^ (x >> 16)) * 0xBB67AE85u + key;
+  return (x ^ (x >> 15)) * 0x9B05688Du;
+}
+// k + 1/2 in units of 2^-20 of a step, k the 16 bits for m or for sqrt(v).
+__device__ __forceinline__ uint32_t bits_m(uint32_t x) { return ((x ^ (x >> 16)) << 4 & 0xFFFF0u) | 8u; }
+__device__ __forceinline__ uint32_t bits_r(uint32_t x) { return (x >> 12 & 0xFFFF0u) | 8u; }
 
 // The e4m3 value that x * inv rounds to, floor(|x inv| / h + (k + 1/2) / 65536) h: the random
-// bits (k16, already shifted to bits 4..19) are added below the third mantissa bit and the
-// sum is cut there. Below 2^-6 the grid is uniform (2^-9), which is the spacing of [2^-6,
-// 2^-5): the value is shifted there and back. A non-finite x becomes NaN. KEEP: x > 0 gives
-// at least the smallest code.
-template <bool KEEP>
-__device__ __forceinline__ float e4m3_round(float x, float inv, uint32_t k16) {
-  const float a = fabsf(x);
-  const float s = __fmul_rn(a, inv);
+// bits are added below the third mantissa bit and the sum is cut there. Below 2^-6 the grid
+// is uniform (2^-9), which is the spacing of [2^-6, 2^-5): the value is shifted there and
+// back. KEEP (x >= 0): x > 0 gives at least the smallest code. GUARD: a non-finite x becomes
+// NaN (without it x has to be finite).
+template <bool KEEP, bool GUARD>
+__device__ __forceinline__ float e4m3_round(float x, float inv, uint32_t k) {
+  const float s = __fmul_rn(fabsf(x), inv);
   const float shift = s < 0.015625f ? 0.015625f : 0.0f;
-  uint32_t b = __float_as_uint(__fadd_rn(s, shift));
-  b = (b + (k16 | 8u)) & 0xFFF00000u;
+  const uint32_t b = (__float_as_uint(__fadd_rn(s, shift)) + k) & 0xFFF00000u;
   float r = __fadd_rn(__uint_as_float(b), -shift);
   if (KEEP && s > 0.0f) r = fmaxf(r, 0.001953125f);
-  if (!(a <= kFltMax)) r = __int_as_float(0x7fc00000);
+  if (GUARD && !(fabsf(x) <= kFltMax)) r = __int_as_float(0x7fc00000);
   return KEEP ? r : copysignf(r, x);
 }
 
@@ -130,17 +134,56 @@ __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a <= kFltMax ? a : 0.0f;
 }
+// max(a, |x|), NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(x)));
+  return r;
+}
+// Magnitudes order as their bit patterns, NaN above infinity.
+__device__ __forceinline__ float warp_max_bits(float a) {
+  return __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(a) & 0x7FFFFFFFu));
+}
+// 1 / x to one ulp; 0 for x above 2^126 and infinity for x below 2^-126.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // One element: p, m, v updated in place, root = sqrt(v). For the states every operation is
 // rounded by itself (no fused multiply-add), so that codes can be reproduced bit for bit by
-// elementary fp32 arithmetic.
+// elementary fp32 arithmetic. The quotient needs no such care: a reciprocal within one ulp.
 __device__ __forceinline__ void update(const AdamwArgs& a, float g, float& p, float& m, float& v,
                                        float& root) {
   m = __fadd_rn(__fmul_rn(a.beta1, m), __fmul_rn(a.one_minus_beta1, g));
   v = __fadd_rn(__fmul_rn(a.beta2, v), __fmul_rn(a.one_minus_beta2, __fmul_rn(g, g)));
   root = __fsqrt_rn(v);
-  const float q = __fdiv_rn(m, __fmaf_rn(root, a.inv_root_bc2, a.eps));
+  const float q = __fmul_rn(m, rcp_approx(__fmaf_rn(root, a.inv_root_bc2, a.eps)));
   p = __fadd_rn(p, -__fmaf_rn(a.decay, p, __fmul_rn(a.step_size, q)));
+}
+
+// The codes of a lane's 8 consecutive elements. start: hash_start of the block; o: the first
+// element's place in it.
+template <bool GUARD>
+__device__ __forceinline__ void encode8(const float m[kVec], const float root[kVec], float inv_m,
+                                        float inv_r, uint32_t start, uint32_t o, uint32_t key,
+                                        uint2& cm, uint2& cr) {
+  uint32_t wm[kVec / 2], wr[kVec / 2];
+#pragma unroll
+  for (int k = 0; k < kVec / 2; ++k) {
+    float x[2], y[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t h = hash_at(start, o + 2 * k + j, key);
+      x[j] = e4m3_round<false, GUARD>(m[2 * k + j], inv_m, bits_m(h));
+      y[j] = e4m3_round<true, GUARD>(root[2 * k + j], inv_r, bits_r(h));
+    }
+    wm[k] = f32_to_e4m3x2(x[0], x[1]);
+    wr[k] = f32_to_e4m3x2(y[0], y[1]);
+  }
+  cm = make_uint2(wm[0] | wm[1] << 16, wm[2] | wm[3] << 16);
+  cr = make_uint2(wr[0] | wr[1] << 16, wr[2] | wr[3] << 16);
 }
 
 // One full state block by a warp, 8 consecutive elements per lane.
@@ -180,8 +223,8 @@ __device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs
   for (int k = 0; k < kVec; ++k) {
     update(a, __fmul_rn(g[k], c), p[k], m[k], v[k], root[k]);
     if constexpr (FP8) {
-      amax_m = fmaxf(amax_m, finite_abs(m[k]));
-      amax_r = fmaxf(amax_r, finite_abs(root[k]));
+      amax_m = max_abs_nan(amax_m, m[k]);
+      amax_r = max_abs_nan(amax_r, root[k]);
     }
   }
   st_f32x8<V8>(t.param + i, p);
@@ -194,25 +237,28 @@ __device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs
     st_v4(static_cast<uint16_t*>(t.weight) + i, make_uint4(w[0], w[1], w[2], w[3]));
   }
   if constexpr (FP8) {
-    float inv_m, inv_r;
-    // magnitudes order as their bit patterns
-    state_scale(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(amax_m))), ms, inv_m);
-    state_scale(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(amax_r))), vs, inv_r);
-    uint32_t cm[kVec / 2], cr[kVec / 2];
+    amax_m = warp_max_bits(amax_m);
+    amax_r = warp_max_bits(amax_r);
+    const bool finite = amax_m <= kFltMax && amax_r <= kFltMax;  // the same in all lanes
+    if (!finite) {  // scales over the finite values
+      amax_m = amax_r = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kVec / 2; ++k) {
-      float x[2], y[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t bits = round_bits(number + lane * kVec + 2 * k + j, a.key);
-        x[j] = e4m3_round<false>(m[2 * k + j], inv_m, bits << 4 & 0xffff0u);
-        y[j] = e4m3_round<true>(root[2 * k + j], inv_r, bits >> 12 & 0xffff0u);
+      for (int k = 0; k < kVec; ++k) {
+        amax_m = fmaxf(amax_m, finite_abs(m[k]));
+        amax_r = fmaxf(amax_r, finite_abs(root[k]));
       }
-      cm[k] = f32_to_e4m3x2(x[0], x[1]);
-      cr[k] = f32_to_e4m3x2(y[0], y[1]);
+      amax_m = warp_max_bits(amax_m);
+      amax_r = warp_max_bits(amax_r);
     }
-    st_v2(static_cast<uint8_t*>(t.m) + i, make_uint2(cm[0] | cm[1] << 16, cm[2] | cm[3] << 16));
-    st_v2(static_cast<uint8_t*>(t.v) + i, make_uint2(cr[0] | cr[1] << 16, cr[2] | cr[3] << 16));
+    float inv_m, inv_r;
+    state_scale(amax_m, ms, inv_m);
+    state_scale(amax_r, vs, inv_r);
+    const uint32_t start = hash_start(number, a.key);
+    uint2 cm, cr;
+    if (finite) encode8<false>(m, root, inv_m, inv_r, start, lane * kVec, a.key, cm, cr);
+    else encode8<true>(m, root, inv_m, inv_r, start, lane * kVec, a.key, cm, cr);
+    st_v2(static_cast<uint8_t*>(t.m) + i, cm);
+    st_v2(static_cast<uint8_t*>(t.v) + i, cr);
     if (lane == 0) {
       t.m_scale[block] = ms;
       t.v_scale[block] = vs;
@@ -270,12 +316,12 @@ __device__ __forceinline__ void part_block(const AdamwTensor& t, const AdamwArgs
     for (int k = 0; k < kVec; ++k) {
       const int o = k * 32 + lane;
       if (o >= valid) continue;
-      const uint32_t bits = round_bits(number + o, a.key);
+      const uint32_t h = hash_at(hash_start(number, a.key), o, a.key);
       const int64_t i = block * kStateBlock + o;
       static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(
-          f32_to_e4m3x2(e4m3_round<false>(m[k], inv_m, bits << 4 & 0xffff0u), 0.0f));
+          f32_to_e4m3x2(e4m3_round<false, true>(m[k], inv_m, bits_m(h)), 0.0f));
       static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(
-          f32_to_e4m3x2(e4m3_round<true>(root[k], inv_r, bits >> 12 & 0xffff0u), 0.0f));
+          f32_to_e4m3x2(e4m3_round<true, true>(root[k], inv_r, bits_r(h)), 0.0f));
     }
     if (lane == 0) {
       t.m_scale[block] = ms;
