@@ -340,15 +340,17 @@ typedef struct zpp_adamw_params {
  * state_bits 8: m and r = sqrt(v) are held as e4m3 codes with one fp32 scale per
  * ZPP_STATE_BLOCK consecutive elements of a tensor (the last block may be shorter; amax over
  * its finite values),
- *   scale = amax * fl(1/448), value = code * scale  (448 * fl(1/amax) not finite: scale 0, codes 0)
- * The step itself uses the unrounded m and v. Rounding is stochastic: with x = value * (448 * fl(1/amax))
- * and h the e4m3 spacing at |x|, the code is floor(|x| / h + u) h with u = (k + 1/2) / 65536,
- * k 16 bits of a hash of (seed, step, element number): the low ones for m, the high ones for
- * r. So a running average moves in expectation even where its change is far below h (round
- * to nearest would freeze it), and equal inputs give equal bits. r > 0 keeps at least the
- * smallest code, so a denominator never collapses. Element numbers count blocks through
- * the list: tensor t's element i has ZPP_STATE_BLOCK * (blocks of tensors 0..t-1) + i. An Inf
- * or NaN gradient makes its own element's states NaN, no other's.
+ *   scale = amax * fl(1/448), inv = 448 * fl(1/amax), value = code * scale
+ *   (inv not finite: scale 0, codes 0)
+ * The step itself uses the unrounded m and v. Rounding is stochastic: with x = value * inv and
+ * h the e4m3 spacing at |x|, the code is floor(|x| / h + u) h with u = (k + 1/2) / 65536, k 16
+ * bits of a hash of (seed, step, element number): the low ones for m, the high ones for r. So a
+ * running average moves in expectation even where its change is far below h (round to
+ * nearest would freeze it), and equal inputs give equal bits. r > 0 keeps at least the
+ * smallest code, so a denominator never collapses. Element numbers count blocks through the
+ * list: tensor t's element i has ZPP_STATE_BLOCK * (blocks of tensors 0..t-1) + i. An Inf or NaN
+ * gradient, or one whose square overflows, makes its own element NaN, no other's. A v below
+ * 2^-126 (|grad| below some 1e-18) may count as smaller than it is.
  *   hash: all mod 2^32, key = (seed * 0x9E3779B9) ^ (step * 0x510E527F), i split in lo, hi:
  *     x = lo * 0x9E3779B9 + hi * 0xA54FF53B + key;  x = (x ^ x >> 16) * 0xBB67AE85 + key
  *     x = (x ^ x >> 15) * 0x9B05688D;               bits = x ^ x >> 16

@@ -18,7 +18,7 @@ namespace zpp {
 
 constexpr int kVec = kStateBlock / 32;  // elements per lane
 static_assert(kVec == 8, "the vector accesses below hold 8 elements");
-static_assert(kAdamwChunk == kWarps * kStateBlock, "one state block per warp");
+static_assert(adamw_chunk(32) == kWarps * kStateBlock, "one state block per warp");
 constexpr float kFltMax = 3.402823466e38f;
 
 // 32 bytes that this kernel also writes (so not through the read-only path).
@@ -151,14 +151,29 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
+// sqrt(v) for v = 0 and for normal v by one Newton step from the approximate reciprocal root y:
+// s = v y, then s + (v - s^2) y / 2, whose residual is exact in a fused multiply-add. The error
+// before the last rounding is the square of y's, 2^-44, so the result is the correctly rounded
+// root but for about two values in a million. It costs 7 instructions where the correctly
+// rounded one, with its range checks, costs about 13: 10 % of the whole step with 8-bit states.
+// v below 2^-126 gives a root below 2^-63, too small by up to a factor of 2000; an infinite v
+// gives NaN.
+__device__ __forceinline__ float sqrt_newton(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 1.17549435e-38f)));
+  const float s = __fmul_rn(v, y);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), __fmul_rn(0.5f, y), s);
+}
+
 // One element: p, m, v updated in place, root = sqrt(v). For the states every operation is
 // rounded by itself (no fused multiply-add), so that codes can be reproduced bit for bit by
 // elementary fp32 arithmetic. The quotient needs no such care: a reciprocal within one ulp.
+template <bool FP8>
 __device__ __forceinline__ void update(const AdamwArgs& a, float g, float& p, float& m, float& v,
                                        float& root) {
   m = __fadd_rn(__fmul_rn(a.beta1, m), __fmul_rn(a.one_minus_beta1, g));
   v = __fadd_rn(__fmul_rn(a.beta2, v), __fmul_rn(a.one_minus_beta2, __fmul_rn(g, g)));
-  root = __fsqrt_rn(v);
+  root = FP8 ? sqrt_newton(v) : __fsqrt_rn(v);
   const float q = __fmul_rn(m, rcp_approx(__fmaf_rn(root, a.inv_root_bc2, a.eps)));
   p = __fadd_rn(p, -__fmaf_rn(a.decay, p, __fmul_rn(a.step_size, q)));
 }
@@ -186,26 +201,49 @@ __device__ __forceinline__ void encode8(const float m[kVec], const float root[kV
   cr = make_uint2(wr[0] | wr[1] << 16, wr[2] | wr[3] << 16);
 }
 
-// One full state block by a warp, 8 consecutive elements per lane.
-template <bool FP8, bool V8>
-__device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs& a, float c,
-                                           int64_t block, int64_t number, int lane) {
-  const int64_t i = block * kStateBlock + lane * kVec;
-  float p[kVec], m[kVec], v[kVec], root[kVec], g[kVec];
+// What a lane reads of a full state block: 8 consecutive elements.
+template <bool FP8>
+struct Loaded {
+  U8x32 g;
+  float p[kVec], m[FP8 ? 1 : kVec], v[FP8 ? 1 : kVec];
   uint2 mq, vq;
   float ms, vs;
-  const U8x32 graw = ld_grad<V8>(t.grad, i, a.g_kind);
-  ld_f32x8<V8>(t.param + i, p);
+};
+template <bool FP8, bool V8>
+__device__ __forceinline__ void load_block(const AdamwTensor& t, const AdamwArgs& a, int64_t block,
+                                           int lane, Loaded<FP8>& l) {
+  const int64_t i = block * kStateBlock + lane * kVec;
+  l.g = ld_grad<V8>(t.grad, i, a.g_kind);
+  ld_f32x8<V8>(t.param + i, l.p);
   if constexpr (FP8) {
-    mq = ld_b32x2(static_cast<uint8_t*>(t.m) + i);
-    vq = ld_b32x2(static_cast<uint8_t*>(t.v) + i);
-    ms = t.m_scale[block];
-    vs = t.v_scale[block];
+    l.mq = ld_b32x2(static_cast<uint8_t*>(t.m) + i);
+    l.vq = ld_b32x2(static_cast<uint8_t*>(t.v) + i);
+    l.ms = t.m_scale[block];
+    l.vs = t.v_scale[block];
   } else {
-    ld_f32x8<V8>(static_cast<float*>(t.m) + i, m);
-    ld_f32x8<V8>(static_cast<float*>(t.v) + i, v);
+    ld_f32x8<V8>(static_cast<float*>(t.m) + i, l.m);
+    ld_f32x8<V8>(static_cast<float*>(t.v) + i, l.v);
   }
-  grad_f32(graw, a.g_kind, g);
+}
+
+// One full state block by a warp.
+template <bool FP8, bool V8>
+__device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs& a, float c,
+                                           int64_t block, int64_t number, int lane,
+                                           const Loaded<FP8>& l) {
+  const int64_t i = block * kStateBlock + lane * kVec;
+  float p[kVec], m[kVec], v[kVec], root[kVec], g[kVec];
+  float ms = l.ms, vs = l.vs;
+  const uint2 mq = l.mq, vq = l.vq;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    p[k] = l.p[k];
+    if constexpr (!FP8) {
+      m[k] = l.m[k];
+      v[k] = l.v[k];
+    }
+  }
+  grad_f32(l.g, a.g_kind, g);
   if constexpr (FP8) {
 #pragma unroll
     for (int k = 0; k < kVec / 2; ++k) {
@@ -221,7 +259,7 @@ __device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs
   float amax_m = 0.0f, amax_r = 0.0f;
 #pragma unroll
   for (int k = 0; k < kVec; ++k) {
-    update(a, __fmul_rn(g[k], c), p[k], m[k], v[k], root[k]);
+    update<FP8>(a, __fmul_rn(g[k], c), p[k], m[k], v[k], root[k]);
     if constexpr (FP8) {
       amax_m = max_abs_nan(amax_m, m[k]);
       amax_r = max_abs_nan(amax_r, root[k]);
@@ -294,7 +332,7 @@ __device__ __forceinline__ void part_block(const AdamwTensor& t, const AdamwArgs
       m[k] = static_cast<float*>(t.m)[i];
       v = static_cast<float*>(t.v)[i];
     }
-    update(a, __fmul_rn(grad_at(t.grad, i, a.g_kind), c), p, m[k], v, root[k]);
+    update<FP8>(a, __fmul_rn(grad_at(t.grad, i, a.g_kind), c), p, m[k], v, root[k]);
     t.param[i] = p;
     if (t.weight) {
       if (a.w_kind == 0) static_cast<__half*>(t.weight)[i] = __float2half_rn(p);
@@ -344,13 +382,23 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
   }
   const AdamwTensor& t = tab.t[lo];
   const int lane = threadIdx.x & 31;
-  const int64_t block =
-      static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kWarps + (threadIdx.x >> 5);
+  constexpr int NB = adamw_warp_blocks(FP8 ? 8 : 32);
+  const int64_t block = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * (kWarps * NB) + (threadIdx.x >> 5) * NB;
   const int64_t left = t.n - block * kStateBlock;
   if (left <= 0) return;
   const int64_t number = (tab.first_block + tab.block0[lo] + block) * kStateBlock;
-  if (left >= kStateBlock) full_block<FP8, V8>(t, a, c, block, number, lane);
-  else part_block<FP8>(t, a, c, block, number, static_cast<int>(left), lane);
+  if (left >= NB * kStateBlock) {
+    Loaded<FP8> l[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) load_block<FP8, V8>(t, a, block + b, lane, l[b]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      full_block<FP8, V8>(t, a, c, block + b, number + b * kStateBlock, lane, l[b]);
+  } else {
+    for (int b = 0; b < NB && left > b * kStateBlock; ++b)
+      part_block<FP8>(t, a, c, block + b, number + b * kStateBlock,
+                      static_cast<int>(min(left - b * kStateBlock, static_cast<int64_t>(kStateBlock))), lane);
+  }
 }
 
 template <int CAP>

@@ -405,7 +405,7 @@ zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, 
       const int32_t c = tab.count++;
       tab.t[c] = zpp::AdamwTensor{s.param,         s.grad,             s.exp_avg, s.exp_avg_sq,
                                   s.exp_avg_scale, s.exp_avg_sq_scale, s.weight,  s.n};
-      tab.first[c + 1] = tab.first[c] + static_cast<int32_t>(zpp::adamw_chunks(s.n));
+      tab.first[c + 1] = tab.first[c] + static_cast<int32_t>(zpp::adamw_chunks(s.n, state_bits));
       tab.block0[c] = static_cast<int32_t>(blocks - tab.first_block);
       blocks += (s.n + ZPP_STATE_BLOCK - 1) / ZPP_STATE_BLOCK;
     }

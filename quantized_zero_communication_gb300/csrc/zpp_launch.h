@@ -95,7 +95,6 @@ cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, 
 // K8: one AdamW step over a list of tensors; at most kAdamwTensors per launch (their
 // descriptors travel in the kernel's parameter space, which holds 32,764 bytes).
 constexpr int kAdamwTensors = 448;
-constexpr int kAdamwChunk = 2048;  // elements per CTA
 constexpr int kStateBlock = 256;   // = ZPP_STATE_BLOCK
 struct AdamwTensor {
   float* param;
@@ -127,7 +126,13 @@ struct AdamwTableOf {
 };
 using AdamwTable = AdamwTableOf<kAdamwTensors>;
 static_assert(sizeof(AdamwTable) <= 32764, "kernel parameter space");
-inline int64_t adamw_chunks(int64_t n) { return (n + kAdamwChunk - 1) / kAdamwChunk; }
+constexpr int adamw_warp_blocks(int state_bits) { return state_bits == 8 ? 2 : 1; }
+constexpr int adamw_chunk(int state_bits) {  // elements per CTA of 8 warps
+  return 8 * adamw_warp_blocks(state_bits) * kStateBlock;
+}
+inline int64_t adamw_chunks(int64_t n, int state_bits) {
+  return (n + adamw_chunk(state_bits) - 1) / adamw_chunk(state_bits);
+}
 cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s);
 
 // K9: y = x W^T (+ bias) from block-quantised codes. x_bf16: x and bias are bf16, else fp16;
