@@ -570,19 +570,36 @@ def dequant_reduce_local(codes, scales, slice_len, block, bits, sources, post_sc
 
 
 # ------------------------------------------------------------- the weights' other operators
-def _dev_list(ts, name, dtypes):
-    """Checks a list of tensors that one call reads or writes: one dtype of `dtypes`,
-    contiguous CUDA tensors on one device. Returns (addresses, element counts)."""
-    torch = _torch()
-    T = torch.Tensor
-    kinds = {t.dtype for t in ts}
-    if len(kinds) != 1 or kinds.pop() not in dtypes:
-        raise ValueError(f"{name}: every tensor needs one dtype of {tuple(dtypes)}")
-    if len(set(map(T.get_device, ts))) != 1:
-        raise ValueError("all tensors of a call must be on one device")
-    if not all(map(T.is_contiguous, ts)) or not ts[0].is_cuda:
+_tensors_module = None
+_KIND_NAMES = ("float16", "bfloat16", "float32", "uint8 / int8", "float8_e4m3fn")
+
+
+def _tensors():
+    """The extension that reads tensors' addresses, counts, types and devices."""
+    global _tensors_module
+    if _tensors_module is None:
+        _torch()
+        if not os.path.exists(_build.EXT):
+            raise RuntimeError(f"{_build.EXT} is missing: build it with __graft_entry__.build() "
+                               "(there is no fallback path)")
+        from . import _tensors as module
+        _tensors_module = module
+    return _tensors_module
+
+
+def _dev_list(ts, name, kinds):
+    """Checks a list of tensors that one call reads or writes: one dtype among `kinds` (indices
+    into _KIND_NAMES), contiguous CUDA tensors on one device. Returns (addresses, element
+    counts, kind, device)."""
+    ptrs = array.array("q", bytes(8 * len(ts)))
+    sizes = array.array("q", ptrs)
+    kind, device = _tensors().scan(ts, ptrs, sizes)
+    if kind not in kinds:
+        raise ValueError(f"{name}: every tensor needs one dtype of "
+                         f"{tuple(_KIND_NAMES[k] for k in kinds)}")
+    if device < 0:
         _cuda(*ts)
-    return array.array("q", map(T.data_ptr, ts)), list(map(T.numel, ts))
+    return ptrs, sizes, kind, device
 
 
 def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
@@ -594,27 +611,22 @@ def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if not grads:
         raise ValueError("grad_norm needs at least one tensor")
-    ptrs, sizes = _dev_list(grads, "grads", (torch.float16, torch.bfloat16, torch.float32))
-    return _grad_norm(ptrs, sizes, grads[0], max_norm, pre_scale, out)
-
-
-def _grad_norm(ptrs, sizes, like, max_norm, pre_scale, out=None):
-    torch = _torch()
+    ptrs, sizes, kind, device = _dev_list(grads, "grads", (ZPP_F16, ZPP_BF16, ZPP_F32))
     if out is not None:
         _need(out, "out", 2, (torch.float32,))
-        _cuda(like, out)
+        _cuda(grads[0], out)
     else:
-        out = like.new_empty(2, dtype=torch.float32)
-    work = like.new_empty(zpp_grad_norm_workspace(sum(sizes), len(sizes)), dtype=torch.float32)
-    _norm_call(ptrs, array.array("q", sizes), like, max_norm, pre_scale, work, out)
+        out = grads[0].new_empty(2, dtype=torch.float32)
+    work = grads[0].new_empty(zpp_grad_norm_workspace(sum(sizes), len(sizes)),
+                              dtype=torch.float32)
+    _norm_call(ptrs, sizes, kind, device, max_norm, pre_scale, work.data_ptr(), out.data_ptr())
     return out
 
 
-def _norm_call(ptrs, lens, like, max_norm, pre_scale, work, out):
-    _check(lib().zpp_grad_norm(ptrs.buffer_info()[0], lens.buffer_info()[0], len(lens),
-                               _dt(like.dtype), pre_scale,
-                               math.inf if max_norm is None else max_norm, work.data_ptr(),
-                               out.data_ptr(), _raw_stream(like.get_device())), "zpp_grad_norm")
+def _norm_call(ptrs, sizes, kind, device, max_norm, pre_scale, work, out):
+    _check(lib().zpp_grad_norm(ptrs.buffer_info()[0], sizes.buffer_info()[0], len(sizes), kind,
+                               pre_scale, math.inf if max_norm is None else max_norm, work, out,
+                               _raw_stream(device)), "zpp_grad_norm")
 
 
 def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -629,42 +641,53 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
     1; seed (0 .. 2^32 - 1) is that of the 8-bit states' stochastic rounding."""
     torch = _torch()
     aslist = lambda v: [v] if isinstance(v, torch.Tensor) else list(v)  # noqa: E731
-    f32 = (torch.float32,)
+    f32 = (ZPP_F32,)
     params, grads = aslist(params), aslist(grads)
-    lists = [("params", params, f32), ("grads", grads, (torch.float16, torch.bfloat16) + f32)]
-    state = f32 if scales is None else (torch.float8_e4m3fn,)
+    lists = [("params", params, f32), ("grads", grads, (ZPP_F16, ZPP_BF16, ZPP_F32))]
+    state = f32 if scales is None else (_E4M3,)
     lists += [("exp_avg", aslist(exp_avg), state), ("exp_avg_sq", aslist(exp_avg_sq), state)]
     if scales is not None:
         lists += [("scales[0]", aslist(scales[0]), f32), ("scales[1]", aslist(scales[1]), f32)]
     if weights is not None:
-        lists.append(("weights", aslist(weights), (torch.float16, torch.bfloat16)))
+        lists.append(("weights", aslist(weights), (ZPP_F16, ZPP_BF16)))
     if not params:
         raise ValueError("adamw_step needs at least one tensor")
     if not 0 <= seed < 1 << 32:
         raise ValueError("seed: 0 .. 2^32 - 1")
-    ptrs, device = {}, params[0].get_device()
-    for name, ts, dtypes in lists:
+    tab = array.array("q", bytes(64 * len(params)))
+    want, at, kinds = None, None, {}
+    for column, (name, ts, allowed) in zip(_columns(scales is not None), lists):
         if len(ts) != len(params):
             raise ValueError(f"{name}: {len(ts)} tensors, expected {len(params)}")
-        ptrs[name], sizes = _dev_list(ts, name, dtypes)
-        if ts[0].get_device() != device:
+        ptrs, sizes, kinds[name], device = _dev_list(ts, name, allowed)
+        if want is None:
+            want, at, blocks = sizes, device, _state_blocks(sizes)
+        _same_sizes(name, sizes, blocks if name.startswith("scales") else want)
+        if device != at:
             raise ValueError("all tensors of a call must be on one device")
-        want = ptrs.setdefault("n", sizes)
-        if name.startswith("scales"):
-            want = [-(-n // ZPP_STATE_BLOCK) for n in want]
-        if sizes != want:
-            i = next(i for i, (a, b) in enumerate(zip(sizes, want)) if a != b)
-            raise ValueError(f"{name}[{i}]: {sizes[i]} elements, expected {want[i]}")
-    T = len(params)
-    tab = array.array("q", bytes(64 * T))
-    for k, name in enumerate(("params", "grads", "exp_avg", "exp_avg_sq", "scales[0]",
-                              "scales[1]", "weights")):
-        if name in ptrs:
-            tab[k::8] = ptrs[name]
-    tab[7::8] = array.array("q", ptrs["n"])
+        tab[column::8] = ptrs
+    tab[7::8] = want
     hp = AdamwParams(lr, betas[0], betas[1], eps, weight_decay, step, seed)
-    _adamw(tab, grads[0], lists[-1][1][0] if weights is not None else None,
-           32 if scales is None else 8, hp, _scale_address(grads[0], grad_scale))
+    _adamw(tab, kinds["grads"], kinds.get("weights", ZPP_BF16), 32 if scales is None else 8, hp,
+           _scale_address(grads[0], grad_scale), at)
+
+
+_E4M3 = _KIND_NAMES.index("float8_e4m3fn")
+
+
+def _columns(scaled):
+    """Fields of AdamwTensor that params, grads, the states, the scales and weights go to."""
+    return (0, 1, 2, 3, 4, 5, 6) if scaled else (0, 1, 2, 3, 6)
+
+
+def _state_blocks(sizes):
+    return array.array("q", [-(-n // ZPP_STATE_BLOCK) for n in sizes])
+
+
+def _same_sizes(name, sizes, want):
+    if sizes != want:
+        i = next(i for i, (a, b) in enumerate(zip(sizes, want)) if a != b)
+        raise ValueError(f"{name}[{i}]: {sizes[i]} elements, expected {want[i]}")
 
 
 def _scale_address(grad, grad_scale):
@@ -677,10 +700,9 @@ def _scale_address(grad, grad_scale):
     return grad_scale.data_ptr()
 
 
-def _adamw(tab, grad, weight, state_bits, hp, scale):
-    _check(lib().zpp_adamw_step(tab.buffer_info()[0], len(tab) // 8, _dt(grad.dtype),
-                                ZPP_BF16 if weight is None else _dt(weight.dtype), state_bits,
-                                ctypes.addressof(hp), scale, _raw_stream(grad.get_device())),
+def _adamw(tab, g_kind, w_kind, state_bits, hp, scale, device):
+    _check(lib().zpp_adamw_step(tab.buffer_info()[0], len(tab) // 8, g_kind, w_kind, state_bits,
+                                ctypes.addressof(hp), scale, _raw_stream(device)),
            "zpp_adamw_step")
 
 
@@ -688,43 +710,50 @@ def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None,
     """x [..., cols] (fp16 / bf16; rows of cols contiguous elements, any row stride) times the
     transposed [rows][cols] matrix that quant_blockwise gave (codes, scales) for -> y [..., rows]
     of `dtype` (default: x's). bias: [rows] of x's dtype. y: an output buffer, same form as x."""
-    torch = _torch()
-    dt, shape = x.dtype, x.shape
-    if dt is not torch.float16 and dt is not torch.bfloat16:
-        _need(x, "x", dtypes=(torch.float16, torch.bfloat16))
+    probe, shape = _tensors().probe, x.shape
+    x_at, x_n, x_kind, device, x_whole = probe(x)
+    if x_kind not in (ZPP_F16, ZPP_BF16):
+        _need(x, "x", dtypes=(_torch().float16, _torch().bfloat16))
     if not shape or shape[-1] < 1 or rows < 0:
         raise ValueError("x: [..., cols] with cols >= 1, and rows >= 0")
     cols = shape[-1]
     n = rows * cols
-    if _sizes_ok(n, block, bits):
-        if codes.numel() != (n if bits == 8 else (n + 1) // 2) or scales.numel() != -(-n // block):
-            _need(codes, "codes", zpp_code_bytes(n, bits))
-            _need(scales, "scales", zpp_num_scales(n, block))
-    if codes.dtype is not torch.uint8 or scales.dtype is not torch.float32:
+    c_at, c_n, c_kind, c_dev, c_whole = probe(codes)
+    s_at, s_n, s_kind, s_dev, s_whole = probe(scales)
+    if _sizes_ok(n, block, bits) and (c_n != (n if bits == 8 else (n + 1) // 2)
+                                      or s_n != -(-n // block)):
+        _need(codes, "codes", zpp_code_bytes(n, bits))
+        _need(scales, "scales", zpp_num_scales(n, block))
+    if c_kind != 3 or s_kind != ZPP_F32:
         _need(codes, "codes", dtypes=_bytes_dtypes())
-        _need(scales, "scales", dtypes=(torch.float32,))
-    if bias is not None and (bias.dtype is not dt or bias.numel() != rows):
-        _need(bias, "bias", rows, (dt,))
-    vecs, x_stride = (1, cols) if len(shape) == 1 and x.is_contiguous() else _rows(x, "x")
-    device = x.get_device()
+        _need(scales, "scales", dtypes=(_torch().float32,))
+    b_at, b_ok = 0, True
+    if bias is not None:
+        b_at, b_n, b_kind, b_dev, b_whole = probe(bias)
+        if b_kind != x_kind or b_n != rows:
+            _need(bias, "bias", rows, (x.dtype,))
+        b_ok = b_dev == device and b_whole
+    vecs, x_stride = (x_n // cols, cols) if x_whole else _rows(x, "x")
     if y is None:
         if device >= 0:
-            y = x.new_empty((*shape[:-1], rows), dtype=dtype or dt)
+            y = x.new_empty((*shape[:-1], rows), dtype=dtype)
+            y_at, _, y_kind, y_dev, _ = probe(y)
         y_stride = rows
     else:
+        torch = _torch()
         _need(y, "y", vecs * rows, (torch.float16, torch.bfloat16, torch.float32))
         if y.shape != (*shape[:-1], rows) or (dtype is not None and y.dtype != dtype):
             raise ValueError(f"y: {tuple(y.shape)} of {y.dtype} does not fit the call")
         y_stride = _rows(y, "y")[1]
-    if (device < 0 or codes.get_device() != device or scales.get_device() != device
-            or y.get_device() != device or not codes.is_contiguous() or not scales.is_contiguous()
-            or (bias is not None and (bias.get_device() != device or not bias.is_contiguous()))):
+        y_at, _, y_kind, y_dev, _ = probe(y)
+    if device < 0 or not (c_dev == s_dev == y_dev == device and c_whole and s_whole and b_ok):
         _cuda(codes, scales, *(t for t in (bias,) if t is not None))
         raise ValueError("all tensors of a call must be on one CUDA device")
-    _check(lib().zpp_matvec_blockwise(
-        codes.data_ptr(), scales.data_ptr(), rows, cols, block, bits, x.data_ptr(), _dt(dt), vecs,
-        x_stride, 0 if bias is None else bias.data_ptr(), y.data_ptr(), _dt(y.dtype), y_stride,
-        _raw_stream(device)), "zpp_matvec_blockwise")
+    status = lib().zpp_matvec_blockwise(c_at, s_at, rows, cols, block, bits, x_at, x_kind, vecs,
+                                        x_stride, b_at, y_at, y_kind, y_stride,
+                                        _raw_stream(device))
+    if status != ZPP_OK:
+        raise ZppError(status, "zpp_matvec_blockwise")
     return y
 
 

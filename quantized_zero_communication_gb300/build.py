@@ -1,4 +1,5 @@
-"""Build ``libzpp.so`` in-tree with nvcc for sm_103a (no torch extension machinery).
+"""Build ``libzpp.so`` in-tree with nvcc for sm_103a, and the Python extension ``_tensors`` with
+the host compiler against torch's headers (no torch extension machinery).
 
 Each translation unit compiles in parallel into ``_build/``; the objects link into one
 shared library (CUDA runtime linked statically). Numerics flags: -fmad=false (no FMA
@@ -8,6 +9,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzpp.so")
+EXT = os.path.join(PKG, "_tensors.so")
 SOURCES = ["zpp_abi.cu", "quant.cu", "reorder_quant.cu", "reorder_tensors_f16.cu",
            "reorder_tensors_bf16.cu", "dequant.cu", "qgz.cu", "adamw.cu", "grad_norm.cu",
            "matvec.cu"]
@@ -37,10 +40,26 @@ def _inputs():
 
 
 def _stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _build_ext():
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "tensor_access.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + os.path.join(root, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling tensor_access.cpp failed:\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -60,8 +79,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        ext = ex.submit(_build_ext)
         results = list(ex.map(compile_one, SOURCES))
+        ext.result()
     objs = [o for o, _ in results]
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]

@@ -13,6 +13,7 @@
 
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
+#include "zpp_overlap.cuh"
 
 namespace zpp {
 
@@ -21,25 +22,18 @@ static_assert(kVec == 8, "the vector accesses below hold 8 elements");
 static_assert(adamw_chunk(32) == kWarps * kStateBlock, "one state block per warp");
 constexpr float kFltMax = 3.402823466e38f;
 
-// 32 bytes that this kernel also writes (so not through the read-only path).
 template <bool V8>
 __device__ __forceinline__ void ld_f32x8(const float* p, float f[kVec]) {
-  if constexpr (V8) {
-    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]),
-                   "=f"(f[6]), "=f"(f[7])
-                 : "l"(p));
-  } else {
+  const U8x32 w = ld_after_vec32<V8>(p);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(f[4 * h]), "=f"(f[4 * h + 1]), "=f"(f[4 * h + 2]), "=f"(f[4 * h + 3])
-                   : "l"(p + 4 * h));
-  }
+  for (int k = 0; k < kVec; ++k) f[k] = __uint_as_float(w.w[k]);
 }
 __device__ __forceinline__ uint2 ld_b32x2(const void* p) {
   uint2 r;
-  asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
+               : "=r"(r.x), "=r"(r.y)
+               : "l"(p)
+               : "memory");
   return r;
 }
 template <bool V8>
@@ -54,8 +48,8 @@ __device__ __forceinline__ void st_f32x8(float* p, const float f[kVec]) {
 // flight before the first conversion), floats later.
 template <bool V8>
 __device__ __forceinline__ U8x32 ld_grad(const void* g, int64_t i, int kind) {
-  if (kind == 2) return ld_vec32<V8>(static_cast<const float*>(g) + i);
-  const uint4 a = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
+  if (kind == 2) return ld_after_vec32<V8>(static_cast<const float*>(g) + i);
+  const uint4 a = ld_after_v4(static_cast<const uint16_t*>(g) + i);
   U8x32 r;
   r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
   return r;
@@ -73,12 +67,6 @@ __device__ __forceinline__ void grad_f32(const U8x32& w, int kind, float f[kVec]
     }
   }
 }
-__device__ __forceinline__ float grad_at(const void* p, int64_t i, int kind) {
-  if (kind == 2) return static_cast<const float*>(p)[i];
-  const uint16_t b = static_cast<const uint16_t*>(p)[i];
-  return kind == 0 ? bits16_to_float(b, F16()) : bits16_to_float(b, BF16());
-}
-
 // Two e4m3 codes -> floats (exact).
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
@@ -201,7 +189,9 @@ __device__ __forceinline__ void encode8(const float m[kVec], const float root[kV
   cr = make_uint2(wr[0] | wr[1] << 16, wr[2] | wr[3] << 16);
 }
 
-// What a lane reads of a full state block: 8 consecutive elements.
+// What a lane reads of a state block: 8 consecutive elements, the first `cnt` of them in the
+// tensor. Every load is issued before the first use, also in a tensor's last, shorter block
+// (PART): its warp would otherwise finish some 10 us after all others.
 template <bool FP8>
 struct Loaded {
   U8x32 g;
@@ -209,32 +199,60 @@ struct Loaded {
   uint2 mq, vq;
   float ms, vs;
 };
-template <bool FP8, bool V8>
+template <bool FP8, bool V8, bool PART>
 __device__ __forceinline__ void load_block(const AdamwTensor& t, const AdamwArgs& a, int64_t block,
-                                           int lane, Loaded<FP8>& l) {
+                                           int lane, int cnt, Loaded<FP8>& l) {
   const int64_t i = block * kStateBlock + lane * kVec;
-  l.g = ld_grad<V8>(t.grad, i, a.g_kind);
-  ld_f32x8<V8>(t.param + i, l.p);
   if constexpr (FP8) {
-    l.mq = ld_b32x2(static_cast<uint8_t*>(t.m) + i);
-    l.vq = ld_b32x2(static_cast<uint8_t*>(t.v) + i);
     l.ms = t.m_scale[block];
     l.vs = t.v_scale[block];
-  } else {
-    ld_f32x8<V8>(static_cast<float*>(t.m) + i, l.m);
-    ld_f32x8<V8>(static_cast<float*>(t.v) + i, l.v);
   }
+  if (!PART || cnt == kVec) {
+    l.g = ld_grad<V8>(t.grad, i, a.g_kind);
+    ld_f32x8<V8>(t.param + i, l.p);
+    if constexpr (FP8) {
+      l.mq = ld_b32x2(static_cast<uint8_t*>(t.m) + i);
+      l.vq = ld_b32x2(static_cast<uint8_t*>(t.v) + i);
+    } else {
+      ld_f32x8<V8>(static_cast<float*>(t.m) + i, l.m);
+      ld_f32x8<V8>(static_cast<float*>(t.v) + i, l.v);
+    }
+    return;
+  }
+  uint32_t mq[2] = {0u, 0u}, vq[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    l.p[k] = 0.0f;
+    l.g.w[k] = 0u;
+    if constexpr (!FP8) l.m[k] = l.v[k] = 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    if (k >= cnt) continue;
+    l.p[k] = t.param[i + k];
+    if (a.g_kind == 2) l.g.w[k] = __float_as_uint(static_cast<const float*>(t.grad)[i + k]);
+    else
+      l.g.w[k / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(t.grad)[i + k]) << (16 * (k & 1));
+    if constexpr (FP8) {
+      mq[k / 4] |= static_cast<uint32_t>(static_cast<uint8_t*>(t.m)[i + k]) << (8 * (k & 3));
+      vq[k / 4] |= static_cast<uint32_t>(static_cast<uint8_t*>(t.v)[i + k]) << (8 * (k & 3));
+    } else {
+      l.m[k] = static_cast<float*>(t.m)[i + k];
+      l.v[k] = static_cast<float*>(t.v)[i + k];
+    }
+  }
+  l.mq = make_uint2(mq[0], mq[1]);
+  l.vq = make_uint2(vq[0], vq[1]);
 }
 
-// One full state block by a warp.
-template <bool FP8, bool V8>
-__device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs& a, float c,
-                                           int64_t block, int64_t number, int lane,
+// One state block by a warp. number: the block's first element number in the list.
+template <bool FP8, bool V8, bool PART>
+__device__ __forceinline__ void step_block(const AdamwTensor& t, const AdamwArgs& a, float c,
+                                           int64_t block, int64_t number, int lane, int cnt,
                                            const Loaded<FP8>& l) {
   const int64_t i = block * kStateBlock + lane * kVec;
   float p[kVec], m[kVec], v[kVec], root[kVec], g[kVec];
   float ms = l.ms, vs = l.vs;
-  const uint2 mq = l.mq, vq = l.vq;
 #pragma unroll
   for (int k = 0; k < kVec; ++k) {
     p[k] = l.p[k];
@@ -247,8 +265,8 @@ __device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs
   if constexpr (FP8) {
 #pragma unroll
     for (int k = 0; k < kVec / 2; ++k) {
-      const float2 x = e4m3x2_to_f32((k < 2 ? mq.x : mq.y) >> (16 * (k & 1)) & 0xffffu);
-      const float2 y = e4m3x2_to_f32((k < 2 ? vq.x : vq.y) >> (16 * (k & 1)) & 0xffffu);
+      const float2 x = e4m3x2_to_f32((k < 2 ? l.mq.x : l.mq.y) >> (16 * (k & 1)) & 0xffffu);
+      const float2 y = e4m3x2_to_f32((k < 2 ? l.vq.x : l.vq.y) >> (16 * (k & 1)) & 0xffffu);
       m[2 * k] = __fmul_rn(x.x, ms);
       m[2 * k + 1] = __fmul_rn(x.y, ms);
       const float r0 = __fmul_rn(y.x, vs), r1 = __fmul_rn(y.y, vs);
@@ -261,18 +279,25 @@ __device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs
   for (int k = 0; k < kVec; ++k) {
     update<FP8>(a, __fmul_rn(g[k], c), p[k], m[k], v[k], root[k]);
     if constexpr (FP8) {
+      if (PART && k >= cnt) m[k] = root[k] = 0.0f;
       amax_m = max_abs_nan(amax_m, m[k]);
       amax_r = max_abs_nan(amax_r, root[k]);
     }
   }
-  st_f32x8<V8>(t.param + i, p);
+  const bool whole = !PART || cnt == kVec;
+  if (whole) st_f32x8<V8>(t.param + i, p);
+  else
+    for (int k = 0; k < cnt; ++k) t.param[i + k] = p[k];
   if (t.weight) {
     uint32_t w[kVec / 2];
 #pragma unroll
     for (int k = 0; k < kVec / 2; ++k)
       w[k] = a.w_kind == 0 ? pack2(p[2 * k], p[2 * k + 1], F16())
                            : pack2(p[2 * k], p[2 * k + 1], BF16());
-    st_v4(static_cast<uint16_t*>(t.weight) + i, make_uint4(w[0], w[1], w[2], w[3]));
+    uint16_t* to = static_cast<uint16_t*>(t.weight) + i;
+    if (whole) st_v4(to, make_uint4(w[0], w[1], w[2], w[3]));
+    else
+      for (int k = 0; k < cnt; ++k) to[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
   }
   if constexpr (FP8) {
     amax_m = warp_max_bits(amax_m);
@@ -295,75 +320,32 @@ __device__ __forceinline__ void full_block(const AdamwTensor& t, const AdamwArgs
     uint2 cm, cr;
     if (finite) encode8<false>(m, root, inv_m, inv_r, start, lane * kVec, a.key, cm, cr);
     else encode8<true>(m, root, inv_m, inv_r, start, lane * kVec, a.key, cm, cr);
-    st_v2(static_cast<uint8_t*>(t.m) + i, cm);
-    st_v2(static_cast<uint8_t*>(t.v) + i, cr);
+    uint8_t *tm = static_cast<uint8_t*>(t.m) + i, *tv = static_cast<uint8_t*>(t.v) + i;
+    if (whole) {
+      st_v2(tm, cm);
+      st_v2(tv, cr);
+    } else {
+      for (int k = 0; k < cnt; ++k) {
+        tm[k] = static_cast<uint8_t>((k < 4 ? cm.x : cm.y) >> (8 * (k & 3)));
+        tv[k] = static_cast<uint8_t>((k < 4 ? cr.x : cr.y) >> (8 * (k & 3)));
+      }
+    }
     if (lane == 0) {
       t.m_scale[block] = ms;
       t.v_scale[block] = vs;
     }
   } else {
-    st_f32x8<V8>(static_cast<float*>(t.m) + i, m);
-    st_f32x8<V8>(static_cast<float*>(t.v) + i, v);
-  }
-}
-
-// A tensor's last, shorter block: element by element.
-template <bool FP8>
-__device__ __forceinline__ void part_block(const AdamwTensor& t, const AdamwArgs& a, float c,
-                                           int64_t block, int64_t number, int valid, int lane) {
-  float ms = 1.0f, vs = 1.0f;
-  if constexpr (FP8) {
-    ms = t.m_scale[block];
-    vs = t.v_scale[block];
-  }
-  float m[kVec], root[kVec], amax_m = 0.0f, amax_r = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const int o = k * 32 + lane;
-    const int64_t i = block * kStateBlock + o;
-    m[k] = root[k] = 0.0f;
-    if (o >= valid) continue;
-    float p = t.param[i], v;
-    if constexpr (FP8) {
-      m[k] = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(t.m)[i]).x, ms);
-      const float r0 = __fmul_rn(e4m3x2_to_f32(static_cast<uint8_t*>(t.v)[i]).x, vs);
-      v = __fmul_rn(r0, r0);
+    float *tm = static_cast<float*>(t.m) + i, *tv = static_cast<float*>(t.v) + i;
+    if (whole) {
+      st_f32x8<V8>(tm, m);
+      st_f32x8<V8>(tv, v);
     } else {
-      m[k] = static_cast<float*>(t.m)[i];
-      v = static_cast<float*>(t.v)[i];
-    }
-    update<FP8>(a, __fmul_rn(grad_at(t.grad, i, a.g_kind), c), p, m[k], v, root[k]);
-    t.param[i] = p;
-    if (t.weight) {
-      if (a.w_kind == 0) static_cast<__half*>(t.weight)[i] = __float2half_rn(p);
-      else static_cast<__nv_bfloat16*>(t.weight)[i] = __float2bfloat16_rn(p);
-    }
-    if constexpr (FP8) {
-      amax_m = fmaxf(amax_m, finite_abs(m[k]));
-      amax_r = fmaxf(amax_r, finite_abs(root[k]));
-    } else {
-      static_cast<float*>(t.m)[i] = m[k];
-      static_cast<float*>(t.v)[i] = v;
-    }
-  }
-  if constexpr (FP8) {
-    float inv_m, inv_r;
-    state_scale(warp_max(amax_m, 32), ms, inv_m);
-    state_scale(warp_max(amax_r, 32), vs, inv_r);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const int o = k * 32 + lane;
-      if (o >= valid) continue;
-      const uint32_t h = hash_at(hash_start(number, a.key), o, a.key);
-      const int64_t i = block * kStateBlock + o;
-      static_cast<uint8_t*>(t.m)[i] = static_cast<uint8_t>(
-          f32_to_e4m3x2(e4m3_round<false, true>(m[k], inv_m, bits_m(h)), 0.0f));
-      static_cast<uint8_t*>(t.v)[i] = static_cast<uint8_t>(
-          f32_to_e4m3x2(e4m3_round<true, true>(root[k], inv_r, bits_r(h)), 0.0f));
-    }
-    if (lane == 0) {
-      t.m_scale[block] = ms;
-      t.v_scale[block] = vs;
+      for (int k = 0; k < kVec; ++k)
+        if (k < cnt) {
+          tm[k] = m[k];
+          tv[k] = v[k];
+        }
     }
   }
 }
@@ -372,7 +354,8 @@ __device__ __forceinline__ void part_block(const AdamwTensor& t, const AdamwArgs
 template <bool FP8, bool V8, int CAP>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamwTableOf<CAP> tab) {
   const AdamwArgs& a = tab.a;
-  const float c = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
+  grid_wait();  // everything before this launch is done and visible
+  const float c = a.grad_scale ? *static_cast<const volatile float*>(a.grad_scale) : 1.0f;
   if (!isfinite(c)) return;  // overflowed gradients: the step is skipped
   int lo = 0, hi = tab.count;
   while (hi - lo > 1) {
@@ -390,14 +373,17 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
   if (left >= NB * kStateBlock) {
     Loaded<FP8> l[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) load_block<FP8, V8>(t, a, block + b, lane, l[b]);
+    for (int b = 0; b < NB; ++b) load_block<FP8, V8, false>(t, a, block + b, lane, kVec, l[b]);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      full_block<FP8, V8>(t, a, c, block + b, number + b * kStateBlock, lane, l[b]);
+      step_block<FP8, V8, false>(t, a, c, block + b, number + b * kStateBlock, lane, kVec, l[b]);
   } else {
-    for (int b = 0; b < NB && left > b * kStateBlock; ++b)
-      part_block<FP8>(t, a, c, block + b, number + b * kStateBlock,
-                      static_cast<int>(min(left - b * kStateBlock, static_cast<int64_t>(kStateBlock))), lane);
+    for (int b = 0; b < NB && left > b * kStateBlock; ++b) {
+      const int cnt = static_cast<int>(min(left - b * kStateBlock - lane * kVec, static_cast<int64_t>(kVec)));
+      Loaded<FP8> l;
+      load_block<FP8, V8, true>(t, a, block + b, lane, max(cnt, 0), l);
+      step_block<FP8, V8, true>(t, a, c, block + b, number + b * kStateBlock, lane, max(cnt, 0), l);
+    }
   }
 }
 
@@ -406,8 +392,7 @@ static cudaError_t run_adamw(const AdamwTableOf<CAP>& tab, int state_bits, bool 
   const int grid = tab.first[tab.count];
   auto kern = state_bits == 8 ? (v8 ? k_adamw<true, true, CAP> : k_adamw<true, false, CAP>)
                               : (v8 ? k_adamw<false, true, CAP> : k_adamw<false, false, CAP>);
-  kern<<<grid, kThreads, 0, s>>>(tab);
-  return cudaGetLastError();
+  return launch_overlapped(kern, grid, kThreads, s, tab);
 }
 
 cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s) {

@@ -8,6 +8,7 @@
 // partial, a single CTA adds the partials (in fp64) in a fixed order.
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
+#include "zpp_overlap.cuh"
 
 namespace zpp {
 
@@ -36,6 +37,8 @@ __device__ __forceinline__ T block_sum(T v) {  // valid in thread 0; blockDim.x 
 template <int KIND, bool V8, int CAP>
 __global__ void __launch_bounds__(kThreads)
     k_norm_partial(const __grid_constant__ NormTableOf<CAP> tab, float* __restrict__ partial) {
+  grid_wait();
+  grid_release();
   int lo = 0, hi = tab.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -52,7 +55,7 @@ __global__ void __launch_bounds__(kThreads)
     const char* p = static_cast<const char*>(tab.ptr[lo]) + begin * BYTES + threadIdx.x * 32;
     U8x32 w[VECS];
 #pragma unroll
-    for (int u = 0; u < VECS; ++u) w[u] = ld_vec32<V8>(p + u * kThreads * 32);
+    for (int u = 0; u < VECS; ++u) w[u] = ld_after_vec32<V8>(p + u * kThreads * 32);
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < VECS; ++u)
@@ -68,11 +71,37 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-  } else {
-    for (int64_t i = begin + threadIdx.x; i < begin + left; i += kThreads) {
-      const float g = load_as_f32(tab.ptr[lo], i, KIND);
-      sum = __fmaf_rn(g, g, sum);
+  } else {  // whole vectors first, all loaded ahead too, then the last few elements
+    constexpr int PER = KIND == 2 ? 8 : 16;
+    constexpr int VECS = kNormChunk / kThreads / PER;
+    const int vecs = static_cast<int>(left) / PER;
+    const char* p = static_cast<const char*>(tab.ptr[lo]) + begin * (32 / PER);
+    U8x32 w[VECS];
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) {
+      const int at = u * kThreads + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[u].w[k] = 0u;
+      if (at < vecs) w[u] = ld_after_vec32<V8>(p + static_cast<int64_t>(at) * 32);
     }
+    const int64_t i = begin + vecs * PER + threadIdx.x;
+    if (i < begin + left) {  // fewer than PER elements
+      const float g = load_as_f32(tab.ptr[lo], i, KIND);
+      sum = __fmul_rn(g, g);
+    }
+#pragma unroll
+    for (int u = 0; u < VECS; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (KIND == 2) {
+          const float g = __uint_as_float(w[u].w[k]);
+          sum = __fmaf_rn(g, g, sum);
+        } else {
+          const float2 g = KIND == 0 ? unpack2(w[u].w[k], F16()) : unpack2(w[u].w[k], BF16());
+          sum = __fmaf_rn(g.x, g.x, sum);
+          sum = __fmaf_rn(g.y, g.y, sum);
+        }
+      }
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -81,8 +110,11 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(1024) k_norm_finish(const float* __restrict__ partial, int count,
                                                       float pre_scale, float max_norm,
                                                       float* __restrict__ out) {
+  grid_wait();
+  grid_release();
   double sum = 0.0;
-  for (int i = threadIdx.x; i < count; i += 1024) sum += static_cast<double>(partial[i]);
+  for (int i = threadIdx.x; i < count; i += 1024)
+    sum += static_cast<double>(*static_cast<const volatile float*>(partial + i));
   sum = block_sum(sum);
   if (threadIdx.x == 0) {
     const float norm = static_cast<float>(sqrt(sum)) * fabsf(pre_scale);
@@ -98,8 +130,7 @@ static cudaError_t run_partial(const NormTableOf<CAP>& tab, int g_kind, bool v8,
   auto kern = g_kind == 2   ? (v8 ? k_norm_partial<2, true, CAP> : k_norm_partial<2, false, CAP>)
               : g_kind == 1 ? (v8 ? k_norm_partial<1, true, CAP> : k_norm_partial<1, false, CAP>)
                             : (v8 ? k_norm_partial<0, true, CAP> : k_norm_partial<0, false, CAP>);
-  kern<<<tab.first[tab.count], kThreads, 0, s>>>(tab, workspace);
-  return cudaGetLastError();
+  return launch_overlapped(kern, tab.first[tab.count], kThreads, s, tab, workspace);
 }
 
 cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
@@ -126,8 +157,8 @@ cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, 
     }
     if (e != cudaSuccess) return e;
   }
-  k_norm_finish<<<1, 1024, 0, s>>>(workspace, chunks, pre_scale, max_norm, out);
-  return cudaGetLastError();
+  return launch_overlapped(k_norm_finish, 1, 1024, s, static_cast<const float*>(workspace), chunks,
+                           pre_scale, max_norm, out);
 }
 
 }  // namespace zpp

@@ -25,7 +25,7 @@ class AdamW:
                  state_bits=32, weights=None, seed=0, exp_avg=None, exp_avg_sq=None, scales=None,
                  step=0):
         torch = _b._torch()
-        f32 = (torch.float32,)
+        f32 = (_b.ZPP_F32,)
         self.params = list(params)
         if not self.params:
             raise ValueError("AdamW needs at least one tensor")
@@ -39,13 +39,13 @@ class AdamW:
             raise ValueError("seed: 0 .. 2^32 - 1")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.state_bits, self.seed, self.steps = state_bits, seed, step
-        self._sizes = [p.numel() for p in self.params]
-        self._blocks = [-(-n // _b.ZPP_STATE_BLOCK) for n in self._sizes]
+        self._sizes = array.array("q", [p.numel() for p in self.params])
+        self._blocks = _b._state_blocks(self._sizes)
         code = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
 
         def states(given, sizes, dtype):
-            if given is not None:  # (aliases, which keep the memory alive)
-                return [t.detach() for t in given]
+            if given is not None:
+                return list(given)
             # one buffer, every tensor's part 256 elements aligned
             at, end = [], 0
             for n in sizes:
@@ -63,34 +63,42 @@ class AdamW:
             self.scales = tuple(states(s, self._blocks, torch.float32)
                                 for s in (scales or (None, None)))
         self.weights = None if weights is None else list(weights)
+        state = f32 if state_bits == 32 else (_b._E4M3,)
         self._lists = [("params", 0, self.params, self._sizes, f32),
-                       ("exp_avg", 2, self.exp_avg, self._sizes, (code,)),
-                       ("exp_avg_sq", 3, self.exp_avg_sq, self._sizes, (code,))]
+                       ("exp_avg", 2, self.exp_avg, self._sizes, state),
+                       ("exp_avg_sq", 3, self.exp_avg_sq, self._sizes, state)]
         if state_bits == 8:
             self._lists += [(f"scales[{k}]", 4 + k, self.scales[k], self._blocks, f32)
                             for k in (0, 1)]
         if self.weights is not None:
             self._lists.append(("weights", 6, self.weights, self._sizes,
-                                (torch.float16, torch.bfloat16)))
+                                (_b.ZPP_F16, _b.ZPP_BF16)))
+        self._device = None
         self._table = array.array("q", bytes(64 * len(self.params)))
-        self._table[7::8] = array.array("q", self._sizes)
+        self._table[7::8] = self._sizes
         self._hp = _b.AdamwParams(lr, *self.betas, eps, weight_decay, step, seed)
-        self._ptrs = {entry[0]: self._enter(*entry) for entry in self._lists}
-        self._lens = array.array("q", self._sizes)
-        self._work = None
+        self._w_kind, self._work = _b.ZPP_BF16, None
+        self._gather()
 
-    def _enter(self, name, column, tensors, sizes, dtypes):
-        """Checks a list and writes its addresses into the call's table."""
+    def _enter(self, name, column, tensors, sizes, kinds):
+        """Checks a list and writes its addresses into the call's table; their dtype's kind."""
         if len(tensors) != len(sizes):
             raise ValueError(f"{name}: {len(tensors)} tensors, expected {len(sizes)}")
-        ptrs, got = _b._dev_list(tensors, name, dtypes)
-        if got != sizes:
-            i = next(i for i, (a, b) in enumerate(zip(got, sizes)) if a != b)
-            raise ValueError(f"{name}[{i}]: {got[i]} elements, expected {sizes[i]}")
-        if tensors[0].get_device() != self.params[0].get_device():
+        ptrs, got, kind, device = _b._dev_list(tensors, name, kinds)
+        _b._same_sizes(name, got, sizes)
+        if self._device is None:
+            self._device = device
+        if device != self._device:
             raise ValueError("all tensors of a call must be on one device")
         self._table[column::8] = ptrs
-        return ptrs
+        return ptrs, kind
+
+    def _gather(self):
+        """Every tensor that the optimiser holds, as it is now (storage may have moved)."""
+        for entry in self._lists:
+            kind = self._enter(*entry)[1]
+            if entry[0] == "weights":
+                self._w_kind = kind
 
     def step(self, grads, *, max_norm=None, pre_scale=None, grad_scale=None, lr=None):
         """One step with `grads` (contiguous, one of fp16 / bf16 / fp32, in the parameters'
@@ -102,13 +110,9 @@ class AdamW:
         optimiser's for this step and the following ones."""
         torch = _b._torch()
         grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
-        address = torch.Tensor.data_ptr
-        for entry in self._lists:  # the caller's tensors may have other storage by now
-            if entry[0] in ("params", "weights") and \
-                    array.array("q", map(address, entry[2])) != self._ptrs[entry[0]]:
-                self._ptrs[entry[0]] = self._enter(*entry)
-        ptrs = self._enter("grads", 1, grads, self._sizes,
-                           (torch.float16, torch.bfloat16, torch.float32))
+        self._gather()
+        ptrs, kind = self._enter("grads", 1, grads, self._sizes,
+                                 (_b.ZPP_F16, _b.ZPP_BF16, _b.ZPP_F32))
         if lr is not None:
             self.lr = lr
         norm, scale = None, 0
@@ -120,17 +124,17 @@ class AdamW:
                     _b.zpp_grad_norm_workspace(sum(self._sizes), len(self._sizes)),
                     dtype=torch.float32)
             norm = grads[0].new_empty(2, dtype=torch.float32)
-            _b._norm_call(ptrs, self._lens, grads[0], max_norm,
-                          1.0 if pre_scale is None else pre_scale, self._work, norm)
-            scale = norm.data_ptr() + 4  # its second element
+            at = norm.data_ptr()
+            _b._norm_call(ptrs, self._sizes, kind, self._device, max_norm,
+                          1.0 if pre_scale is None else pre_scale, self._work.data_ptr(), at)
+            scale = at + 4  # its second element
         elif grad_scale is not None:
             scale = _b._scale_address(grads[0], grad_scale)
         hp = self._hp
         hp.lr, hp.step = self.lr, self.steps + 1
         hp.beta1, hp.beta2 = self.betas
         hp.eps, hp.weight_decay = self.eps, self.weight_decay
-        _b._adamw(self._table, grads[0], self.weights[0] if self.weights else None,
-                  self.state_bits, hp, scale)
+        _b._adamw(self._table, kind, self._w_kind, self.state_bits, hp, scale, self._device)
         self.steps += 1
         return norm
 
