@@ -706,11 +706,25 @@ def _adamw(tab, g_kind, w_kind, state_bits, hp, scale, device):
            "zpp_adamw_step")
 
 
+_matvec_address = None
+
+
 def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None, y=None):
     """x [..., cols] (fp16 / bf16; rows of cols contiguous elements, any row stride) times the
     transposed [rows][cols] matrix that quant_blockwise gave (codes, scales) for -> y [..., rows]
     of `dtype` (default: x's). bias: [rows] of x's dtype. y: an output buffer, same form as x."""
-    probe, shape = _tensors().probe, x.shape
+    global _matvec_address
+    if _matvec_address is None:
+        _matvec_address = ctypes.cast(lib().zpp_matvec_blockwise, ctypes.c_void_p).value
+    native = _tensors()
+    if y is None:
+        y = native.matvec(_matvec_address, codes, scales, x, rows, block, bits, bias,
+                          -1 if dtype is None else _dt(dtype))
+        if y is not None:
+            if type(y) is int:
+                raise ZppError(y, "zpp_matvec_blockwise")
+            return y
+    probe, shape = native.probe, x.shape
     x_at, x_n, x_kind, device, x_whole = probe(x)
     if x_kind not in (ZPP_F16, ZPP_BF16):
         _need(x, "x", dtypes=(_torch().float16, _torch().bfloat16))

@@ -1,13 +1,19 @@
-// tensor_access.cpp -- Python extension `_tensors`: address, element count, type, device and
-// contiguity of torch tensors in one call. The optimiser step takes lists of hundreds of
-// tensors; asking each for these five things from Python costs the host some 0.4 us a tensor
-// (60 us for 150 tensors, more than the step itself takes on the GPU), here some 10 ns.
+// tensor_access.cpp -- Python extension `_tensors`: what the wrappers ask of torch tensors, in one
+// call. The optimiser step takes lists of hundreds of tensors; asking each for its address,
+// element count, type, device and contiguity from Python costs the host some 0.4 us a tensor
+// (60 us for 150 tensors, more than the step itself takes on the GPU), here some 10 ns. And a
+// product for one token takes the GPU 4 us: its wrapper's common case (plain contiguous
+// tensors, a new output) is one call here too, 14 us of host time otherwise.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <zpp.h>
 
 #include <cstdint>
+#include <vector>
 
 namespace {
 
@@ -23,7 +29,7 @@ long kind_of(const at::Tensor& t) {
     default: return -1;
   }
 }
-long device_of(const at::Tensor& t) { return t.is_cuda() ? t.get_device() : -1; }
+long gpu_of(const at::Tensor& t) { return t.is_cuda() ? t.get_device() : -1; }
 int64_t address_of(const at::Tensor& t) {
   return t.numel() ? reinterpret_cast<int64_t>(t.data_ptr()) : 0;
 }
@@ -67,10 +73,10 @@ PyObject* scan(PyObject*, PyObject* const* args, Py_ssize_t n) {
         contiguous = contiguous && t.is_contiguous();
         if (i == 0) {
           kind = kind_of(t);
-          device = device_of(t);
+          device = gpu_of(t);
         } else {
           if (kind_of(t) != kind) kind = -1;
-          if (device_of(t) != device) device = -1;
+          if (gpu_of(t) != device) device = -1;
         }
       }
     } catch (const std::exception& e) {
@@ -93,8 +99,70 @@ PyObject* probe(PyObject*, PyObject* o) {
   try {
     const at::Tensor& t = THPVariable_Unpack(o);
     return Py_BuildValue("LLlli", static_cast<long long>(address_of(t)),
-                         static_cast<long long>(t.numel()), kind_of(t), device_of(t),
+                         static_cast<long long>(t.numel()), kind_of(t), gpu_of(t),
                          t.is_contiguous() ? 1 : 0);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+// matvec(address of zpp_matvec_blockwise, codes, scales, x, rows, block, bits, bias or None, out
+// kind or -1): the product in a new tensor, a status other than ZPP_OK as an int, or None where
+// something is not the plain case (the Python wrapper then finds out what).
+PyObject* matvec(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "matvec: 9 arguments");
+    return nullptr;
+  }
+  if (!plain(args[1]) || !plain(args[2]) || !plain(args[3])) Py_RETURN_NONE;
+  const bool has_bias = args[7] != Py_None;
+  if (has_bias && !plain(args[7])) Py_RETURN_NONE;
+  const long long rows = PyLong_AsLongLong(args[4]), block = PyLong_AsLongLong(args[5]),
+                  bits = PyLong_AsLongLong(args[6]), out = PyLong_AsLongLong(args[8]);
+  void* fn = PyLong_AsVoidPtr(args[0]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  try {
+    const at::Tensor &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]),
+                     &x = THPVariable_Unpack(args[3]);
+    const long kind = kind_of(x), device = gpu_of(x);
+    if (device < 0 || (kind != ZPP_F16 && kind != ZPP_BF16) || x.dim() < 1 || !x.is_contiguous())
+      Py_RETURN_NONE;
+    const int64_t cols = x.size(-1);
+    if (cols < 1 || rows < 0 || rows > ZPP_MAX_ELEMS / cols) Py_RETURN_NONE;
+    if ((bits != 4 && bits != 8) || block < ZPP_MIN_BLOCK || block > ZPP_MAX_BLOCK) Py_RETURN_NONE;
+    const int64_t total = rows * cols;
+    if (kind_of(codes) != 3 || kind_of(scales) != ZPP_F32 || gpu_of(codes) != device ||
+        gpu_of(scales) != device || !codes.is_contiguous() || !scales.is_contiguous() ||
+        codes.numel() != (bits == 8 ? total : (total + 1) / 2) ||
+        scales.numel() != (total + block - 1) / block)
+      Py_RETURN_NONE;
+    const void* bias = nullptr;
+    if (has_bias) {
+      const at::Tensor& b = THPVariable_Unpack(args[7]);
+      if (kind_of(b) != kind || b.numel() != rows || gpu_of(b) != device || !b.is_contiguous())
+        Py_RETURN_NONE;
+      bias = reinterpret_cast<const void*>(address_of(b));
+    }
+    const long y_kind = out < 0 ? kind : static_cast<long>(out);
+    if (y_kind > ZPP_F32) Py_RETURN_NONE;
+    std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = rows;
+    at::Tensor y = at::empty(shape, x.options().dtype(y_kind == ZPP_F16    ? at::kHalf
+                                                      : y_kind == ZPP_BF16 ? at::kBFloat16
+                                                                           : at::kFloat));
+    const zpp_status st = reinterpret_cast<decltype(&zpp_matvec_blockwise)>(fn)(
+        reinterpret_cast<const void*>(address_of(codes)),
+        reinterpret_cast<const float*>(address_of(scales)), rows, cols, static_cast<int32_t>(block),
+        static_cast<int32_t>(bits), reinterpret_cast<const void*>(address_of(x)),
+        static_cast<zpp_dtype>(kind), x.numel() / cols, cols, bias,
+        reinterpret_cast<void*>(address_of(y)), static_cast<zpp_dtype>(y_kind), rows,
+        c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream());
+    if (st != ZPP_OK) return PyLong_FromLong(st);
+    return THPVariable_Wrap(std::move(y));
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
@@ -104,6 +172,8 @@ PyObject* probe(PyObject*, PyObject* o) {
 PyMethodDef methods[] = {
     {"scan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scan)), METH_FASTCALL,
      "addresses and element counts of a list of tensors; (kind, device)"},
+    {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matvec)), METH_FASTCALL,
+     "the product with a quantised matrix, plain case"},
     {"probe", probe, METH_O, "(address, elements, kind, device, contiguous) of a tensor"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
