@@ -285,9 +285,13 @@ __device__ __forceinline__ void step_block(const AdamwTensor& t, const AdamwArgs
     }
   }
   const bool whole = !PART || cnt == kVec;
-  if (whole) st_f32x8<V8>(t.param + i, p);
-  else
-    for (int k = 0; k < cnt; ++k) t.param[i + k] = p[k];
+  if (whole) {
+    st_f32x8<V8>(t.param + i, p);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k)
+      if (k < cnt) t.param[i + k] = p[k];
+  }
   if (t.weight) {
     uint32_t w[kVec / 2];
 #pragma unroll
@@ -295,9 +299,13 @@ __device__ __forceinline__ void step_block(const AdamwTensor& t, const AdamwArgs
       w[k] = a.w_kind == 0 ? pack2(p[2 * k], p[2 * k + 1], F16())
                            : pack2(p[2 * k], p[2 * k + 1], BF16());
     uint16_t* to = static_cast<uint16_t*>(t.weight) + i;
-    if (whole) st_v4(to, make_uint4(w[0], w[1], w[2], w[3]));
-    else
-      for (int k = 0; k < cnt; ++k) to[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+    if (whole) {
+      st_v4(to, make_uint4(w[0], w[1], w[2], w[3]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (k < cnt) to[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+    }
   }
   if constexpr (FP8) {
     amax_m = warp_max_bits(amax_m);
@@ -325,10 +333,12 @@ __device__ __forceinline__ void step_block(const AdamwTensor& t, const AdamwArgs
       st_v2(tm, cm);
       st_v2(tv, cr);
     } else {
-      for (int k = 0; k < cnt; ++k) {
-        tm[k] = static_cast<uint8_t>((k < 4 ? cm.x : cm.y) >> (8 * (k & 3)));
-        tv[k] = static_cast<uint8_t>((k < 4 ? cr.x : cr.y) >> (8 * (k & 3)));
-      }
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (k < cnt) {
+          tm[k] = static_cast<uint8_t>((k < 4 ? cm.x : cm.y) >> (8 * (k & 3)));
+          tv[k] = static_cast<uint8_t>((k < 4 ? cr.x : cr.y) >> (8 * (k & 3)));
+        }
     }
     if (lane == 0) {
       t.m_scale[block] = ms;

@@ -8,6 +8,8 @@
 // fragment of 16 rows meets 8 vectors, and products (exact) and sums are fp32.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
 
@@ -380,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
 // ---------------------------------------------------------------------------------
 constexpr int kAnyOctets = 1024;  // of a row per pass over x, over all vectors: 36 KB
 
+constexpr int kAnyCtas = 152 * 4;
+
 // Octets of a row per CTA and per pass of it over x.
 struct AnyShape {
   int per, chunk, pitch;  // pitch: floats of a vector's part of x, 9 for every 8 columns
@@ -405,126 +409,137 @@ __device__ __forceinline__ uint2 ld_octet(const uint8_t* codes, int64_t o, int64
 }
 
 template <typename TT, int BITS, int RPW, int NVP>
-__global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int log2b, int split) {
+__global__ void __launch_bounds__(kThreads, 2) k_matvec_any(const MatvecArgs a, int log2b, int split) {
   const AnyShape shape = any_shape(a.cols, split, NVP);
-  extern __shared__ float xs[];  // [NVP][pitch], then [kWarps * RPW][NVP] sums
-  float* sums = xs + NVP * shape.pitch;
+  constexpr int ROWS = kWarps * RPW, OUTS = ROWS * NVP;
+  extern __shared__ float xs[];  // [NVP][pitch], then two sets of [ROWS][NVP] sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(blockIdx.x) % split;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / split) * (kWarps * RPW) + warp;
+  const int64_t tiles = (a.rows + ROWS - 1) / ROWS;
   const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * NVP;
   const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(NVP)));
   const int64_t n = a.rows * a.cols;
-  const int shift = static_cast<int>(row0 * a.cols & 7);  // the same for rows 8 apart
+  const int shift = static_cast<int>(warp * a.cols & 7);  // the same for rows 8 apart
   // Octets of a row, and this CTA's range of them (the same numbers for every row).
   const int octets = static_cast<int>((a.cols + shift + 7) / 8);
-  const int last = (rank + 1) * shape.per;
-
-  int64_t first[RPW];       // octet that holds the row's first code
-  const float* scale[RPW];  // of its block
-  int in_block[RPW];        // its number in the block
+  const int begin = rank * shape.per, last = begin + shape.per;
   const int sh = log2b - 3;
+  // octet k, code e: column 8 k + e - shift, at 9 (k - k0) + (8 + e - shift) of xs, one more from
+  // 8 on
+  int at[8];
 #pragma unroll
-  for (int i = 0; i < RPW; ++i) {
-    const int64_t r = row0 + 8 * i < a.rows ? row0 + 8 * i : 0;  // (rows past the end: not read)
-    first[i] = r * a.cols / 8;
-    scale[i] = a.scales + (first[i] >> sh);
-    in_block[i] = static_cast<int>(first[i] & ((1 << sh) - 1));
-  }
+  for (int e = 0; e < 8; ++e) at[e] = 8 + e - shift + (8 + e - shift) / 8;
 
-  float acc[RPW][NVP] = {};
-  for (int k0 = rank * shape.per; k0 < last; k0 += shape.chunk) {
-    const int k1 = min(k0 + shape.chunk, last);
-    // columns 8 k0 - 8 .. 8 k1 + 7 of x, zero outside the row; column c at c + c / 8 from there
-    __syncthreads();
-    for (int v = 0; v < vecs; ++v)
-      for (int i = threadIdx.x; i < (k1 - k0 + 2) * 8; i += kThreads) {
-        const int64_t c = static_cast<int64_t>(k0) * 8 - 8 + i;
-        xs[v * shape.pitch + i + i / 8] =
-            c >= 0 && c < a.cols ? bits16_to_float(__ldg(a.x + (vec0 + v) * a.x_stride + c), TT()) : 0.0f;
+  int buf = 0;
+  for (int64_t tile = blockIdx.x / split; tile < tiles; tile += gridDim.x / split, buf ^= 1) {
+    const int64_t row0 = tile * ROWS + warp;
+    int64_t first[RPW];       // octet that holds the row's first code
+    const float* scale[RPW];  // of its block
+    int in_block[RPW];        // its number in the block
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      const int64_t r = row0 + 8 * i < a.rows ? row0 + 8 * i : 0;  // (rows past the end: not read)
+      first[i] = r * a.cols / 8;
+      scale[i] = a.scales + (first[i] >> sh);
+      in_block[i] = static_cast<int>(first[i] & ((1 << sh) - 1));
+    }
+
+    float acc[RPW][NVP] = {};
+    for (int k0 = begin; k0 < last; k0 += shape.chunk) {
+      const int k1 = min(k0 + shape.chunk, last);
+      if (shape.chunk < shape.per || tile == blockIdx.x / split) {
+        // columns 8 k0 - 8 .. 8 k1 + 7 of x, zero outside the row; column c at c + c / 8 from there
+        __syncthreads();
+        for (int v = 0; v < vecs; ++v) {
+          const uint16_t* x = a.x + (vec0 + v) * a.x_stride;
+#pragma unroll 4
+          for (int i = threadIdx.x; i < (k1 - k0 + 2) * 8; i += kThreads) {
+            const int64_t c = static_cast<int64_t>(k0) * 8 - 8 + i;
+            xs[v * shape.pitch + i + i / 8] =
+                c >= 0 && c < a.cols ? bits16_to_float(__ldg(x + c), TT()) : 0.0f;
+          }
+        }
+        __syncthreads();
       }
-    __syncthreads();
-    // octet k, code e: column 8 k + e - shift, at 9 (k - k0) + (8 + e - shift) of xs, one more
-    // from 8 on
-    int at[8];
+      const int end = min(k1, octets);
+      constexpr int STEPS = 2;  // octets per lane and row whose codes are loaded ahead
+      for (int k = k0 + lane; k < end; k += 32 * STEPS) {
+        uint2 w[STEPS][RPW];
+        float sc[STEPS][RPW];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) at[e] = 8 + e - shift + (8 + e - shift) / 8;
-    const int end = min(k1, octets);
-    constexpr int STEPS = 2;  // octets per lane and row whose codes are loaded ahead
-    for (int k = k0 + lane; k < end; k += 32 * STEPS) {
-      uint2 w[STEPS][RPW];
-      float sc[STEPS][RPW];
+        for (int j = 0; j < STEPS; ++j)
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j)
-#pragma unroll
-        for (int i = 0; i < RPW; ++i) {
-          w[j][i] = make_uint2(0u, 0u);
-          sc[j][i] = 0.0f;
-          if (k + 32 * j < end && row0 + 8 * i < a.rows) {
-            w[j][i] = ld_octet<BITS>(a.codes, first[i] + k + 32 * j, n);
-            sc[j][i] = __ldg(scale[i] + ((in_block[i] + k + 32 * j) >> sh));
+          for (int i = 0; i < RPW; ++i) {
+            w[j][i] = make_uint2(0u, 0u);
+            sc[j][i] = 0.0f;
+            if (k + 32 * j < end && row0 + 8 * i < a.rows) {
+              w[j][i] = ld_octet<BITS>(a.codes, first[i] + k + 32 * j, n);
+              sc[j][i] = __ldg(scale[i] + ((in_block[i] + k + 32 * j) >> sh));
+            }
           }
-        }
 #pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        if (k + 32 * j >= end) break;
-        const float* xk = xs + 9 * (k + 32 * j - k0);
-        f32x2 xp[NVP][4];  // in the order of the converted codes
-#pragma unroll
-        for (int v = 0; v < NVP; ++v) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = v < vecs ? xk[v * shape.pitch + at[e]] : 0.0f;
-          if constexpr (BITS == 4) {
-            xp[v][0] = f2(f[0], f[2]), xp[v][1] = f2(f[4], f[6]);
-            xp[v][2] = f2(f[1], f[3]), xp[v][3] = f2(f[5], f[7]);
-          } else {
-            xp[v][0] = f2(f[0], f[1]), xp[v][1] = f2(f[2], f[3]);
-            xp[v][2] = f2(f[4], f[5]), xp[v][3] = f2(f[6], f[7]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < RPW; ++i) {
-          f32x2 q[4];
-          if constexpr (BITS == 4) {
-            int4x8_to_f2_eo(w[j][i].x, q, q + 2);
-          } else {
-            int8x4_to_f2(w[j][i].x, q);
-            int8x4_to_f2(w[j][i].y, q + 2);
-          }
+        for (int j = 0; j < STEPS; ++j) {
+          if (k + 32 * j >= end) break;
+          const float* xk = xs + 9 * (k + 32 * j - k0);
+          f32x2 xp[NVP][4];  // in the order of the converted codes
 #pragma unroll
           for (int v = 0; v < NVP; ++v) {
-            f32x2 d = f2_mul(q[0], xp[v][0]);
-            d = f2_fma(q[1], xp[v][1], d);
-            d = f2_fma(q[2], xp[v][2], d);
-            d = f2_fma(q[3], xp[v][3], d);
-            float lo, hi;
-            f2_split(d, lo, hi);
-            acc[i][v] = __fmaf_rn(__fadd_rn(lo, hi), sc[j][i], acc[i][v]);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = v < vecs ? xk[v * shape.pitch + at[e]] : 0.0f;
+            if constexpr (BITS == 4) {
+              xp[v][0] = f2(f[0], f[2]), xp[v][1] = f2(f[4], f[6]);
+              xp[v][2] = f2(f[1], f[3]), xp[v][3] = f2(f[5], f[7]);
+            } else {
+              xp[v][0] = f2(f[0], f[1]), xp[v][1] = f2(f[2], f[3]);
+              xp[v][2] = f2(f[4], f[5]), xp[v][3] = f2(f[6], f[7]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < RPW; ++i) {
+            f32x2 q[4];
+            if constexpr (BITS == 4) {
+              int4x8_to_f2_eo(w[j][i].x, q, q + 2);
+            } else {
+              int8x4_to_f2(w[j][i].x, q);
+              int8x4_to_f2(w[j][i].y, q + 2);
+            }
+#pragma unroll
+            for (int v = 0; v < NVP; ++v) {
+              f32x2 d = f2_mul(q[0], xp[v][0]);
+              d = f2_fma(q[1], xp[v][1], d);
+              d = f2_fma(q[2], xp[v][2], d);
+              d = f2_fma(q[3], xp[v][3], d);
+              float lo, hi;
+              f2_split(d, lo, hi);
+              acc[i][v] = __fmaf_rn(__fadd_rn(lo, hi), sc[j][i], acc[i][v]);
+            }
           }
         }
       }
     }
-  }
+    float* sums = xs + NVP * shape.pitch + buf * OUTS;
 #pragma unroll
-  for (int i = 0; i < RPW; ++i)
+    for (int i = 0; i < RPW; ++i)
 #pragma unroll
-    for (int v = 0; v < NVP; ++v) {
-      float sum = acc[i][v];
-      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      if (lane == 0) sums[(8 * i + warp) * NVP + v] = sum;
-    }
-  __syncthreads();
-  if (split > 1) cg::this_cluster().sync();
-  if (rank == 0) {
-    for (int o = threadIdx.x; o < kWarps * RPW * NVP; o += kThreads) {
-      const int v = o / (kWarps * RPW), i = o % (kWarps * RPW);
-      float sum = sums[i * NVP + v];
-      for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(sums, k)[i * NVP + v];
-      const int64_t r = static_cast<int64_t>(blockIdx.x / split) * (kWarps * RPW) + i;
-      if (r < a.rows && v < vecs) {
-        if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
-        store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
+      for (int v = 0; v < NVP; ++v) {
+        float sum = acc[i][v];
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) sums[(8 * i + warp) * NVP + v] = sum;
+      }
+    // (the two sets take turns: one is written again only after the next tile's barrier)
+    __syncthreads();
+    if (split > 1) cg::this_cluster().sync();
+    if (rank == 0) {
+      for (int o = threadIdx.x; o < OUTS; o += kThreads) {
+        const int v = o / ROWS, i = o % ROWS;
+        float sum = sums[i * NVP + v];
+        for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(sums, k)[i * NVP + v];
+        const int64_t r = tile * ROWS + i;
+        if (r < a.rows && v < vecs) {
+          if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+          store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
+        }
       }
     }
   }
@@ -560,9 +575,10 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
   int split = 1;  // until every SM has two CTAs, as long as a CTA has a step for every lane
   while (split < 8 && tiles * split < 304 && octets >= split * 2 * 64) split *= 2;
   const size_t bytes =
-      (static_cast<size_t>(NVP) * any_shape(a.cols, split, NVP).pitch + kWarps * RPW * NVP) * sizeof(float);
-  return launch_split(k_matvec_any<TT, BITS, RPW, NVP>, tiles, (a.vecs + NVP - 1) / NVP, split, bytes, s,
-                      a, log2b, split);
+      (static_cast<size_t>(NVP) * any_shape(a.cols, split, NVP).pitch + 2 * kWarps * RPW * NVP) * sizeof(float);
+  // the CTAs stay on their SMs and keep x, where all of it fits
+  return launch_split(k_matvec_any<TT, BITS, RPW, NVP>, std::min<int64_t>(tiles, kAnyCtas / split),
+                      (a.vecs + NVP - 1) / NVP, split, bytes, s, a, log2b, split);
 }
 
 template <typename TT, int BITS, int RPW>
