@@ -373,177 +373,210 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
 }
 
 // ---------------------------------------------------------------------------------
-// Any width, any stride of x: rows start inside a block, a word, a byte, so a matrix fragment has
-// no common scale and the products are fp32 ones. The codes are read by aligned octets (8
-// codes, one block each); a row whose first code is number s of its octet meets x shifted by s
-// columns, with zeros beyond both ends for the codes of its neighbours. Rows 8 apart have the
-// same s, so a warp takes RPW of them and reads its part of x once for all: without that the
-// shared-memory loads of x, one per code and vector, would cost more than the products.
+// Any width, any stride of x: rows start inside a block, a word, a byte. The codes are read by
+// aligned chunks of 16 bytes (32 or 16 codes, one block each). A row whose first code is number s
+// of its chunk meets x shifted by s columns, with zeros beyond both ends for its neighbours'
+// codes; rows CH apart (CH codes a chunk) have the same s. So a CTA takes rows of one s only, a
+// fragment is 16 of them CH apart, and x lies in shared memory shifted, as fragments. Blocks begin
+// at other columns in every row, so a product covers one chunk and is scaled per row and chunk;
+// lane (g, t) takes word t of the chunks of rows g and g + 8.
+//
+// A stage is four chunks of a warp's 16 rows; a lane copies chunk t of its two rows, and its
+// scales, but reads word t of all four (the copies are swapped so that this is free of bank
+// conflicts). Stages are dealt round robin as in k_matvec_mma.
 // ---------------------------------------------------------------------------------
-constexpr int kAnyOctets = 1024;  // of a row per pass over x, over all vectors: 36 KB
-
-constexpr int kAnyCtas = 152 * 4;
-
-// Octets of a row per CTA and per pass of it over x.
-struct AnyShape {
-  int per, chunk, pitch;  // pitch: floats of a vector's part of x, 9 for every 8 columns
-};
-__host__ __device__ inline AnyShape any_shape(int64_t cols, int split, int nvp) {
-  AnyShape s;
-  s.per = static_cast<int>(((cols + 14) / 8 + split - 1) / split);
-  s.chunk = s.per < kAnyOctets / nvp ? s.per : kAnyOctets / nvp;
-  s.pitch = (s.chunk + 3) * 9;
-  return s;
-}
-
-// Octet number o of the n codes: two words (INT8) or one. The last one may end early.
 template <int BITS>
-__device__ __forceinline__ uint2 ld_octet(const uint8_t* codes, int64_t o, int64_t n) {
-  const uint8_t* p = codes + o * BITS;
-  if ((o + 1) * 8 <= n)
-    return BITS == 8 ? ld_stream_v2(p) : make_uint2(ld_stream_b32(p), 0u);
-  uint32_t w[2] = {0u, 0u};
-  const int bytes = static_cast<int>((n - o * 8) * BITS + 7) / 8;
-  for (int i = 0; i < bytes; ++i) w[i >> 2] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+struct AnyShape {
+  static constexpr int CH = 128 / BITS;      // codes per chunk, rows apart with one shift
+  static constexpr int WC = 32 / BITS;       // codes (columns) per word
+  static constexpr int PW = 16 / BITS;       // pairs per word
+  static constexpr int XB = WC * 2;          // bytes of a word's columns of x
+  static constexpr int STAGE = 2 * 512 + 2 * 128;  // codes, scales
+  static constexpr int DEPTH = 4;            // stages on their way
+  static constexpr int RING = DEPTH * STAGE;
+};
+// Stages of a row and a CTA's share of them (at most, over its warps and ranks).
+__host__ __device__ inline int any_stages(int64_t cols, int ch) {
+  return static_cast<int>(((cols + 2 * ch - 2) / ch + 3) / 4);
+}
+__host__ __device__ inline int any_share(int64_t cols, int ch, int wk, int split) {
+  const int step = wk * split;
+  return (any_stages(cols, ch) + step - 1) / step * wk;
 }
 
-template <typename TT, int BITS, int RPW, int NVP>
-__global__ void __launch_bounds__(kThreads, 2) k_matvec_any(const MatvecArgs a, int log2b, int split) {
-  const AnyShape shape = any_shape(a.cols, split, NVP);
-  constexpr int ROWS = kWarps * RPW, OUTS = ROWS * NVP;
-  extern __shared__ float xs[];  // [NVP][pitch], then two sets of [ROWS][NVP] sums
+template <typename TT, int BITS>
+__global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int log2b, int wk, int split,
+                                                         const Masks masks) {
+  using S = AnyShape<BITS>;
+  constexpr int CH = S::CH;
+  extern __shared__ __align__(16) uint8_t smem[];  // [kWarps] rings (later sums), then x
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(blockIdx.x) % split;
-  const int64_t tiles = (a.rows + ROWS - 1) / ROWS;
-  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * NVP;
-  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(NVP)));
-  const int64_t n = a.rows * a.cols;
-  const int shift = static_cast<int>(warp * a.cols & 7);  // the same for rows 8 apart
-  // Octets of a row, and this CTA's range of them (the same numbers for every row).
-  const int octets = static_cast<int>((a.cols + shift + 7) / 8);
-  const int begin = rank * shape.per, last = begin + shape.per;
-  const int sh = log2b - 3;
-  // octet k, code e: column 8 k + e - shift, at 9 (k - k0) + (8 + e - shift) of xs, one more from
-  // 8 on
-  int at[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) at[e] = 8 + e - shift + (8 + e - shift) / 8;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(blockIdx.x) % split, cta = static_cast<int>(blockIdx.x) / split;
+  const int wr = kWarps / wk;  // row tiles of a CTA
+  // Rows rho + CH i of this CTA, 16 i per tile.
+  const int rho = cta % CH;
+  const int64_t tile = static_cast<int64_t>(cta / CH) * wr + warp / wk;
+  const int64_t row0 = rho + tile * (16 * CH);
+  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * 8;
+  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(8)));
+  const int shift = static_cast<int>(rho * a.cols % CH);
+  const int chunks = static_cast<int>((a.cols + shift + CH - 1) / CH), stages = (chunks + 3) / 4;
+  const int step = wk * split, first = rank * wk + warp % wk;
+  const int64_t bytes = (a.rows * a.cols * BITS + 7) / 8;  // of all codes
+  const int sh = log2b - (BITS == 4 ? 5 : 4);               // chunks per block
 
-  int buf = 0;
-  for (int64_t tile = blockIdx.x / split; tile < tiles; tile += gridDim.x / split, buf ^= 1) {
-    const int64_t row0 = tile * ROWS + warp;
-    int64_t first[RPW];       // octet that holds the row's first code
-    const float* scale[RPW];  // of its block
-    int in_block[RPW];        // its number in the block
+  int64_t at[2];  // chunk of all codes that holds the row's first code
 #pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int64_t r = row0 + 8 * i < a.rows ? row0 + 8 * i : 0;  // (rows past the end: not read)
-      first[i] = r * a.cols / 8;
-      scale[i] = a.scales + (first[i] >> sh);
-      in_block[i] = static_cast<int>(first[i] & ((1 << sh) - 1));
-    }
-
-    float acc[RPW][NVP] = {};
-    for (int k0 = begin; k0 < last; k0 += shape.chunk) {
-      const int k1 = min(k0 + shape.chunk, last);
-      if (shape.chunk < shape.per || tile == blockIdx.x / split) {
-        // columns 8 k0 - 8 .. 8 k1 + 7 of x, zero outside the row; column c at c + c / 8 from there
-        __syncthreads();
-        for (int v = 0; v < vecs; ++v) {
-          const uint16_t* x = a.x + (vec0 + v) * a.x_stride;
-#pragma unroll 4
-          for (int i = threadIdx.x; i < (k1 - k0 + 2) * 8; i += kThreads) {
-            const int64_t c = static_cast<int64_t>(k0) * 8 - 8 + i;
-            xs[v * shape.pitch + i + i / 8] =
-                c >= 0 && c < a.cols ? bits16_to_float(__ldg(x + c), TT()) : 0.0f;
-          }
-        }
-        __syncthreads();
-      }
-      const int end = min(k1, octets);
-      constexpr int STEPS = 2;  // octets per lane and row whose codes are loaded ahead
-      for (int k = k0 + lane; k < end; k += 32 * STEPS) {
-        uint2 w[STEPS][RPW];
-        float sc[STEPS][RPW];
+  for (int h = 0; h < 2; ++h) {  // rows past the end read the first one of this shift; not stored
+    int64_t r = row0 + (8 * h + g) * CH;
+    if (r >= a.rows) r = min(static_cast<int64_t>(rho), a.rows - 1);
+    at[h] = r * a.cols / CH;
+  }
+  const bool live = rho < a.rows;  // (a CTA without rows writes nothing)
+  const unsigned ring = smem_addr(smem) + warp * S::RING;
+  const unsigned put = ring + g * 64 + ((t ^ ((g >> 1) & 3)) * 16);
+  auto fill = [&](int n) {  // stage number n of this warp
+    const int c = (first + n * step) * 4 + t;
+    if (live && c < chunks) {
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j)
-#pragma unroll
-          for (int i = 0; i < RPW; ++i) {
-            w[j][i] = make_uint2(0u, 0u);
-            sc[j][i] = 0.0f;
-            if (k + 32 * j < end && row0 + 8 * i < a.rows) {
-              w[j][i] = ld_octet<BITS>(a.codes, first[i] + k + 32 * j, n);
-              sc[j][i] = __ldg(scale[i] + ((in_block[i] + k + 32 * j) >> sh));
-            }
-          }
-#pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-          if (k + 32 * j >= end) break;
-          const float* xk = xs + 9 * (k + 32 * j - k0);
-          f32x2 xp[NVP][4];  // in the order of the converted codes
-#pragma unroll
-          for (int v = 0; v < NVP; ++v) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = v < vecs ? xk[v * shape.pitch + at[e]] : 0.0f;
-            if constexpr (BITS == 4) {
-              xp[v][0] = f2(f[0], f[2]), xp[v][1] = f2(f[4], f[6]);
-              xp[v][2] = f2(f[1], f[3]), xp[v][3] = f2(f[5], f[7]);
-            } else {
-              xp[v][0] = f2(f[0], f[1]), xp[v][1] = f2(f[2], f[3]);
-              xp[v][2] = f2(f[4], f[5]), xp[v][3] = f2(f[6], f[7]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < RPW; ++i) {
-            f32x2 q[4];
-            if constexpr (BITS == 4) {
-              int4x8_to_f2_eo(w[j][i].x, q, q + 2);
-            } else {
-              int8x4_to_f2(w[j][i].x, q);
-              int8x4_to_f2(w[j][i].y, q + 2);
-            }
-#pragma unroll
-            for (int v = 0; v < NVP; ++v) {
-              f32x2 d = f2_mul(q[0], xp[v][0]);
-              d = f2_fma(q[1], xp[v][1], d);
-              d = f2_fma(q[2], xp[v][2], d);
-              d = f2_fma(q[3], xp[v][3], d);
-              float lo, hi;
-              f2_split(d, lo, hi);
-              acc[i][v] = __fmaf_rn(__fadd_rn(lo, hi), sc[j][i], acc[i][v]);
-            }
-          }
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int64_t o = at[h] + c;
+        const int64_t left = bytes - o * 16;  // the last chunk of all may end early
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         put + n % S::DEPTH * S::STAGE + h * 512),
+                     "l"(a.codes + o * 16), "r"(static_cast<int>(min(left, static_cast<int64_t>(16))))
+                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                         ring + n % S::DEPTH * S::STAGE + 1024 + h * 128 + lane * 4),
+                     "l"(a.scales + (o >> sh))
+                     : "memory");
       }
     }
-    float* sums = xs + NVP * shape.pitch + buf * OUTS;
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int i = 0; i < RPW; ++i)
+  for (int n = 0; n < S::DEPTH - 1; ++n) fill(n);
+
+  // x as fragments: unit (stage l of the CTA's share, chunk c of it, vector v, t) holds the pairs of
+  // columns that go with the code pairs of word t.
+  const int share = any_share(a.cols, CH, wk, split);
+  uint8_t* const frag = smem + kWarps * S::RING;
+  for (int v = 0; v < vecs; ++v) {
+    const uint16_t* x = a.x + (vec0 + v) * a.x_stride;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < share * 16; i += kThreads) {
+      const int l = i >> 4, c = i >> 2 & 3;
+      const int64_t stage = rank * wk + static_cast<int64_t>(l / wk) * step + l % wk;
+      const int64_t col = (stage * 4 + c) * CH + (i & 3) * S::WC - shift;
+      uint32_t e[S::WC];
 #pragma unroll
-      for (int v = 0; v < NVP; ++v) {
-        float sum = acc[i][v];
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) sums[(8 * i + warp) * NVP + v] = sum;
+      for (int k = 0; k < S::WC; ++k)
+        e[k] = col + k >= 0 && col + k < a.cols ? __ldg(x + col + k) : 0u;
+      uint32_t* to = reinterpret_cast<uint32_t*>(frag + (((l * 4 + c) * vecs + v) * 4 + (i & 3)) * S::XB);
+#pragma unroll
+      for (int p = 0; p < S::PW; ++p) to[p] = e[p] | e[p + S::PW] << 16;
+    }
+  }
+  __syncthreads();
+
+  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const unsigned get = ring + g * 64 + t * 4;
+  unsigned xs = smem_addr(frag) + (warp % wk) * (16 * vecs * S::XB) + (min(g, vecs - 1) * 4 + t) * S::XB;
+  for (int n = 0; first + n * step < stages; ++n) {
+    cp_async_wait<S::DEPTH - 2>();
+    __syncwarp();  // all lanes' copies of this stage have landed, the one before is free
+    fill(n + S::DEPTH - 1);
+    const unsigned base = n % S::DEPTH * S::STAGE;
+    const int left = chunks - (first + n * step) * 4;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c >= left) break;
+      uint32_t q[2][S::PW], b[S::PW];
+      float sc[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(get + base + h * 512 + ((c ^ ((g >> 1) & 3)) * 16)));
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(sc[h])
+                     : "r"(ring + base + 1024 + h * 128 + (g * 4 + c) * 4));
+        Codes<TT, BITS>::pairs(w, masks, q[h]);
       }
-    // (the two sets take turns: one is written again only after the next tile's barrier)
-    __syncthreads();
-    if (split > 1) cg::this_cluster().sync();
-    if (rank == 0) {
-      for (int o = threadIdx.x; o < OUTS; o += kThreads) {
-        const int v = o / ROWS, i = o % ROWS;
-        float sum = sums[i * NVP + v];
-        for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(sums, k)[i * NVP + v];
-        const int64_t r = tile * ROWS + i;
-        if (r < a.rows && v < vecs) {
-          if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
-          store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
-        }
+      if constexpr (BITS == 4) {
+        const uint4 v = ld_shared_v4(xs + c * (vecs * 4 * S::XB));
+        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+      } else {
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                     : "=r"(b[0]), "=r"(b[1])
+                     : "r"(xs + c * (vecs * 4 * S::XB)));
+      }
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p < S::PW; p += 2) {
+        const uint32_t f[4] = {q[0][p], q[1][p], q[0][p + 1], q[1][p + 1]};
+        mma16816(d, f, b[p], b[p + 1], d, TT());
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = __fmaf_rn(d[k], sc[k >> 1], y[k]);
+    }
+    xs += wk * (16 * vecs * S::XB);
+  }
+
+  cp_async_wait<0>();
+  __syncwarp();
+  constexpr int STRIDE = S::RING / 4;
+  float* part = reinterpret_cast<float*>(smem);  // a warp's [8][16] sums over its ring
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    part[warp * STRIDE + (2 * t + (k & 1)) * 16 + 8 * (k >> 1) + g] = y[k];
+  __syncthreads();
+  const int outs = wr * 128;
+  for (int o = threadIdx.x; o < outs; o += kThreads) {
+    float* p = part + o / 128 * wk * STRIDE + o % 128;
+    float sum = *p;
+    for (int k = 1; k < wk; ++k) sum += p[k * STRIDE];
+    *p = sum;  // read and written by this thread only
+  }
+  if (split > 1) cg::this_cluster().sync();
+  if (rank == 0) {
+    for (int o = threadIdx.x; o < outs; o += kThreads) {
+      const int from = o / 128 * wk * STRIDE + o % 128, v = o % 128 / 16;
+      const int64_t r =
+          rho + ((static_cast<int64_t>(cta / CH) * wr + o / 128) * 16 + o % 16) * CH;
+      float sum = part[from];
+      for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(part, k)[from];
+      if (r < a.rows && v < vecs) {
+        if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+        store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
       }
     }
   }
   if (split > 1) cg::this_cluster().sync();  // a CTA's sums outlive their readers
+}
+
+// Rows so long that a cluster's shared memory cannot hold x (beyond some 700,000 columns): one warp
+// per row and vector, x from global memory.
+template <typename TT>
+__global__ void __launch_bounds__(kThreads) k_matvec_long(const MatvecArgs a, int log2b) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), j = blockIdx.y;
+  if (r >= a.rows) return;
+  const uint16_t* x = a.x + j * a.x_stride;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int64_t c = lane; c < a.cols; c += 32) {
+    const int64_t e = r * a.cols + c;
+    const int q = a.bits == 8 ? static_cast<int>(static_cast<int8_t>(__ldg(a.codes + e)))
+                              : code_int4(__ldg(a.codes + (e >> 1)), static_cast<int>(e & 1));
+    const float w = __fmul_rn(static_cast<float>(q), __ldg(a.scales + (e >> log2b)));
+    sum = __fmaf_rn(w, bits16_to_float(__ldg(x + c), TT()), sum);
+  }
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) {
+    if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+    store_y(a.y, j * a.y_stride + r, sum, a.y_kind);
+  }
 }
 
 // One launch with `split` CTAs of a cluster along each row.
@@ -569,34 +602,8 @@ static cudaError_t launch_split(void (*kern)(Params...), int64_t tiles, int64_t 
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
-template <typename TT, int BITS, int RPW, int NVP>
-static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  const int64_t octets = (a.cols + 14) / 8, tiles = (a.rows + kWarps * RPW - 1) / (kWarps * RPW);
-  int split = 1;  // until every SM has two CTAs, as long as a CTA has a step for every lane
-  while (split < 8 && tiles * split < 304 && octets >= split * 2 * 64) split *= 2;
-  const size_t bytes =
-      (static_cast<size_t>(NVP) * any_shape(a.cols, split, NVP).pitch + 2 * kWarps * RPW * NVP) * sizeof(float);
-  // the CTAs stay on their SMs and keep x, where all of it fits
-  return launch_split(k_matvec_any<TT, BITS, RPW, NVP>, std::min<int64_t>(tiles, kAnyCtas / split),
-                      (a.vecs + NVP - 1) / NVP, split, bytes, s, a, log2b, split);
-}
-
-template <typename TT, int BITS, int RPW>
-static cudaError_t any_by_vecs(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  switch (a.vecs) {
-    case 1: return run_any<TT, BITS, RPW, 1>(a, log2b, s);
-    case 2: return run_any<TT, BITS, RPW, 2>(a, log2b, s);
-    case 3: return run_any<TT, BITS, RPW, 3>(a, log2b, s);
-    default: return run_any<TT, BITS, RPW, 4>(a, log2b, s);
-  }
-}
-
-template <typename TT>
-static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  const bool few = a.rows < 4 * 8 * 152;  // rows for one CTA per SM
-  if (a.bits == 8) return few ? any_by_vecs<TT, 8, 1>(a, log2b, s) : any_by_vecs<TT, 8, 4>(a, log2b, s);
-  return few ? any_by_vecs<TT, 4, 1>(a, log2b, s) : any_by_vecs<TT, 4, 4>(a, log2b, s);
-}
+// Bytes of x per CTA of k_matvec_any: two CTAs per SM; what one can hold.
+constexpr int64_t kAnyX = 64 * 1024, kAnyMaxX = 180 * 1024;
 
 // How a launch splits a row: over wk warps of a CTA and `split` CTAs.
 struct MvPlan {
@@ -640,6 +647,44 @@ static MvPlan mv_plan(int64_t tiles, int64_t units) {
   while (p.wk < kWarps && 2 * p.wk <= units && (p.wk < 4 || tiles * p.wk < kBusy)) p.wk *= 2;
   while (p.split < 8 && 2 * p.split * p.wk <= units && tiles * p.wk * p.split < kBusy) p.split *= 2;
   return p;
+}
+
+template <typename TT, int BITS>
+static cudaError_t run_any(MatvecArgs a, int log2b, cudaStream_t s) {
+  using S = AnyShape<BITS>;
+  const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;  // tiles of one shift
+  MvPlan p = mv_plan(groups * S::CH, any_stages(a.cols, S::CH));
+  // x of a CTA's share lies in shared memory: more CTAs along a row, then fewer vectors at a time
+  const auto x_bytes = [&](int64_t vecs) {
+    return static_cast<int64_t>(any_share(a.cols, S::CH, p.wk, p.split)) * 16 * vecs * S::XB;
+  };
+  int64_t vecs = a.vecs < 8 ? a.vecs : 8;
+  while (p.split < 8 && x_bytes(vecs) > kAnyX) p.split *= 2;
+  while (vecs > 1 && x_bytes(vecs) > kAnyMaxX) vecs /= 2;
+  if (x_bytes(vecs) > kAnyMaxX) {
+    const dim3 grid(tile_grid(a.rows, kWarps), static_cast<unsigned>(a.vecs));
+    k_matvec_long<TT><<<grid, kThreads, 0, s>>>(a, log2b);
+    return cudaGetLastError();
+  }
+  const int wr = kWarps / p.wk;
+  const int64_t at_once = vecs < 8 ? vecs : a.vecs;  // of one launch
+  for (int64_t v = 0; v < a.vecs; v += at_once) {
+    MatvecArgs part = a;
+    part.x = a.x + v * a.x_stride;
+    part.y = static_cast<uint8_t*>(a.y) + v * a.y_stride * (a.y_kind == 2 ? 4 : 2);
+    part.vecs = std::min(at_once, a.vecs - v);
+    const cudaError_t e = launch_split(
+        k_matvec_any<TT, BITS>, (groups + wr - 1) / wr * S::CH, (part.vecs + 7) / 8, p.split,
+        kWarps * S::RING + static_cast<size_t>(x_bytes(std::min<int64_t>(part.vecs, 8))), s, part, log2b,
+        p.wk, p.split, Codes<TT, BITS>::kMasks);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename TT>
+static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  return a.bits == 8 ? run_any<TT, 8>(a, log2b, s) : run_any<TT, 4>(a, log2b, s);
 }
 
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s) {

@@ -93,6 +93,23 @@ def test_long_and_tall(rows, cols, block, bits):
     check_exact(rows, cols, block, bits, 9, torch.bfloat16)
 
 
+@pytest.mark.parametrize("rows,cols,vecs", [
+    (3, 100_001, 5),    # x over a whole cluster's shared memory
+    (2, 300_001, 8),    # and a few vectors at a time
+    (2, 800_003, 2)])   # and beyond it
+@pytest.mark.parametrize("bits", [4, 8])
+def test_very_long_rows(rows, cols, vecs, bits):
+    check_exact(rows, cols, 128, bits, vecs, torch.float16, bias=True)
+
+
+@pytest.mark.parametrize("rows", [1, 15, 31, 32, 33, 511, 512, 513, 2500])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_odd_width_row_counts(rows, bits):
+    """Rows are gathered by the place of their first code in a 16-byte chunk."""
+    for cols in (5, 333, 1001):
+        check_exact(rows, cols, 64, bits, 2, torch.float16, seed=rows)
+
+
 @pytest.mark.parametrize("rows,cols,block,bits,vecs,dtype,out", [
     (1000, 4096, 128, 4, 1, torch.bfloat16, torch.bfloat16),
     (1000, 4096, 64, 4, 8, torch.float16, torch.float32),
