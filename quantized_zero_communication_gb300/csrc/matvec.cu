@@ -12,6 +12,7 @@
 
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
+#include "zpp_overlap.cuh"
 
 namespace zpp {
 namespace cg = cooperative_groups;
@@ -216,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
                        : "memory");
     cp_async_commit();
   };
+  grid_wait();
+  grid_release();
 #pragma unroll
   for (int u = 0; u < U; ++u) fill(0, u);
 
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
         for (int j = 0; j < S::TJ; ++j) {
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (col_on[i] && u0 + col_seg < left)
-            v = __ldg(reinterpret_cast<const uint4*>(x[i] + static_cast<int64_t>(seg0 + u0) * SEG) + j);
+            v = ld_after_shared_v4(x[i] + static_cast<int64_t>(seg0 + u0) * SEG + 8 * j);
           if constexpr (BITS == 4) {  // pairs (p, p + 4)
             f[i][j][0] = __byte_perm(v.x, v.z, 0x5410u), f[i][j][1] = __byte_perm(v.x, v.z, 0x7632u);
             f[i][j][2] = __byte_perm(v.y, v.w, 0x5410u), f[i][j][3] = __byte_perm(v.y, v.w, 0x7632u);
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
               const int slot = NS > 8 ? i % SP : (2 * t + e) / NV;
               const int at = seg0 + u0 + (NS > 8 ? 0 : slot / SP);
               const int64_t col = static_cast<int64_t>(min(at, segs - 1)) * SEG + slot % SP * 64;
-              sc[m][h][i][e] = __ldg(scale[m][h] + (col >> log2b));
+              sc[m][h][i][e] = ld_after_f32(scale[m][h] + (col >> log2b));
               if (NV > 1) sc[m][h][i][1] = sc[m][h][i][0];
             }
       float r[MT][T][4] = {};
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
       float sum = part[at];
       for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(part, k)[at];
       if (r < a.rows && v < vecs) {
-        if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+        if (a.bias) sum += bits16_to_float(ld_after_u16(a.bias + r), TT());
         store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
       }
     }
@@ -455,6 +458,8 @@ __global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int
     }
     cp_async_commit();
   };
+  grid_wait();
+  grid_release();
 #pragma unroll
   for (int n = 0; n < S::DEPTH - 1; ++n) fill(n);
 
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int
       uint32_t e[S::WC];
 #pragma unroll
       for (int k = 0; k < S::WC; ++k)
-        e[k] = col + k >= 0 && col + k < a.cols ? __ldg(x + col + k) : 0u;
+        e[k] = col + k >= 0 && col + k < a.cols ? ld_after_u16(x + col + k) : 0u;
       uint32_t* to = reinterpret_cast<uint32_t*>(frag + (((l * 4 + c) * vecs + v) * 4 + (i & 3)) * S::XB);
 #pragma unroll
       for (int p = 0; p < S::PW; ++p) to[p] = e[p] | e[p + S::PW] << 16;
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int
       float sum = part[from];
       for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(part, k)[from];
       if (r < a.rows && v < vecs) {
-        if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+        if (a.bias) sum += bits16_to_float(ld_after_u16(a.bias + r), TT());
         store_y(a.y, (vec0 + v) * a.y_stride + r, sum, a.y_kind);
       }
     }
@@ -561,7 +566,7 @@ template <typename TT>
 __global__ void __launch_bounds__(kThreads) k_matvec_long(const MatvecArgs a, int log2b) {
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), j = blockIdx.y;
-  if (r >= a.rows) return;
+  if (r >= a.rows) return;  // (an ordinary launch: no overlap)
   const uint16_t* x = a.x + j * a.x_stride;
   float sum = 0.0f;
 #pragma unroll 8
@@ -574,12 +579,12 @@ __global__ void __launch_bounds__(kThreads) k_matvec_long(const MatvecArgs a, in
   }
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane == 0) {
-    if (a.bias) sum += bits16_to_float(__ldg(a.bias + r), TT());
+    if (a.bias) sum += bits16_to_float(ld_after_u16(a.bias + r), TT());
     store_y(a.y, j * a.y_stride + r, sum, a.y_kind);
   }
 }
 
-// One launch with `split` CTAs of a cluster along each row.
+// One overlapped launch (zpp_overlap.cuh) with `split` CTAs of a cluster along each row.
 template <typename... Params, typename... Args>
 static cudaError_t launch_split(void (*kern)(Params...), int64_t tiles, int64_t vec_groups, int split,
                                 size_t bytes, cudaStream_t s, Args... args) {
@@ -593,12 +598,14 @@ static cudaError_t launch_split(void (*kern)(Params...), int64_t tiles, int64_t 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(split);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
 
@@ -637,23 +644,22 @@ static cudaError_t by_codes(const MatvecArgs& a, int log2b, const MvPlan& p, cud
   return a.block == 64 ? by_vecs<TT, 4, 2>(a, log2b, p, s) : by_vecs<TT, 4, 1>(a, log2b, p, s);
 }
 
-// Four warps a row where it has as many units, then more warps and CTAs until some 13 warps per
-// SM have work, never more than units. (8192 x 8192 INT4, one vector: 2 / 4 / 8 warps 15.4 / 12.3
-// / 14.7 us; 1024 x 16384, 8 warps: 1 / 2 / 4 CTAs 9.4 / 8.2 / 10.2 us; 32768 x 1024, one unit
-// a row: 1 / 2 warps 8.2 / 10.3 us.)
-static MvPlan mv_plan(int64_t tiles, int64_t units) {
+// `base` warps a row where it has as many units, then more warps and CTAs until some 13 warps per
+// SM have work, never more than units. (8192 x 8192 INT4, one vector, base 4: 2 / 4 / 8 warps
+// 15.4 / 12.3 / 14.7 us; 1024 x 16384, 8 warps: 1 / 2 / 4 CTAs 9.4 / 8.2 / 10.2 us; 32768 x 1024,
+// one unit a row: 1 / 2 warps 8.2 / 10.3 us.)
+static MvPlan mv_plan(int64_t tiles, int64_t units, int base) {
   MvPlan p{1, 1};
   constexpr int64_t kBusy = 2000;
-  while (p.wk < kWarps && 2 * p.wk <= units && (p.wk < 4 || tiles * p.wk < kBusy)) p.wk *= 2;
+  while (p.wk < kWarps && 2 * p.wk <= units && (p.wk < base || tiles * p.wk < kBusy)) p.wk *= 2;
   while (p.split < 8 && 2 * p.split * p.wk <= units && tiles * p.wk * p.split < kBusy) p.split *= 2;
   return p;
 }
 
 template <typename TT, int BITS>
-static cudaError_t run_any(MatvecArgs a, int log2b, cudaStream_t s) {
+static cudaError_t run_any(const MatvecArgs& a, int log2b, MvPlan p, cudaStream_t s) {
   using S = AnyShape<BITS>;
   const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;  // tiles of one shift
-  MvPlan p = mv_plan(groups * S::CH, any_stages(a.cols, S::CH));
   // x of a CTA's share lies in shared memory: more CTAs along a row, then fewer vectors at a time
   const auto x_bytes = [&](int64_t vecs) {
     return static_cast<int64_t>(any_share(a.cols, S::CH, p.wk, p.split)) * 16 * vecs * S::XB;
@@ -682,9 +688,22 @@ static cudaError_t run_any(MatvecArgs a, int log2b, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// A CTA lays x out for all its tiles, so more tiles and fewer warps a row where that is much
+// work or the rows are short (9000 x 20016, 16 vectors: 1 / 4 warps 161 / 221 us; 50001 x 1003, 9
+// stages a row: 1 / 2 / 4 warps 18.2 / 16.4 / 17.9 us; 30000 x 6001: 2 / 4 / 8 warps 41.8 / 38.9 /
+// 41.0 us).
+template <int BITS>
+static MvPlan any_plan(const MatvecArgs& a) {
+  using S = AnyShape<BITS>;
+  const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;
+  const int stages = any_stages(a.cols, S::CH);
+  return mv_plan(groups * S::CH, stages, a.vecs > 8 ? 1 : stages < 16 ? 2 : 4);
+}
+
 template <typename TT>
 static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  return a.bits == 8 ? run_any<TT, 8>(a, log2b, s) : run_any<TT, 4>(a, log2b, s);
+  return a.bits == 8 ? run_any<TT, 8>(a, log2b, any_plan<8>(a), s)
+                     : run_any<TT, 4>(a, log2b, any_plan<4>(a), s);
 }
 
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s) {
@@ -692,7 +711,7 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s) {
   const int seg = a.bits == 8 ? 64 : 128;
   if (a.cols % a.block == 0 && a.cols % seg == 0 && a.x_stride % 8 == 0) {
     const int rows = a.vecs == 1 ? 16 : 32, unit = a.vecs == 1 ? 8 : 4;
-    const MvPlan p = mv_plan((a.rows + rows - 1) / rows, (a.cols / seg + unit - 1) / unit);
+    const MvPlan p = mv_plan((a.rows + rows - 1) / rows, (a.cols / seg + unit - 1) / unit, 4);
     return a.x_bf16 ? by_codes<BF16>(a, log2b, p, s) : by_codes<F16>(a, log2b, p, s);
   }
   return a.x_bf16 ? launch_any<BF16>(a, log2b, s) : launch_any<F16>(a, log2b, s);

@@ -29,6 +29,25 @@ __device__ __forceinline__ uint4 ld_after_v4(const void* p) {
                : "memory");
   return r;
 }
+// The same through L1, for data that several warps read.
+__device__ __forceinline__ uint4 ld_after_shared_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ float ld_after_f32(const float* p) {
+  float r;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint16_t ld_after_u16(const uint16_t* p) {
+  uint16_t r;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(r) : "l"(p) : "memory");
+  return r;
+}
 template <bool V8>
 __device__ __forceinline__ U8x32 ld_after_vec32(const void* p) {
   U8x32 r;
