@@ -146,7 +146,7 @@ struct MvShape {
   static constexpr int PW = 16 / BITS;                         // pairs per word
   static constexpr int SG = NV * SP >= 8 ? 1 : 8 / (NV * SP);  // segments per set of columns
   static constexpr int TILES = NV * SP > 8 ? NT * SP : NT;     // sets of 8 columns
-  static constexpr int UNIT = 8 / MT;                          // segments dealt at a time
+  static constexpr int UNIT = SG > 8 / MT ? SG : 8 / MT;       // segments dealt at a time
   static constexpr int SEG_BYTES = 2 * MT * 32 * 16;           // code bytes of a warp's segment
   static_assert(NT == 1 || NV == 8, "more than one set of vectors only when they fill it");
   static_assert(UNIT % SG == 0, "whole sets of columns per unit");
@@ -628,22 +628,6 @@ static cudaError_t run_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cuda
                       Codes<TT, BITS>::kMasks);
 }
 
-// U: 4 KB of codes on their way per warp.
-template <typename TT, int BITS, int SP>
-static cudaError_t by_vecs(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
-  if (a.vecs == 1) return run_mma<TT, BITS, 1, 1, SP, 1, 4>(a, log2b, p, s);
-  if (a.vecs == 2) return run_mma<TT, BITS, 2, 2, SP, 1, 2>(a, log2b, p, s);
-  if (a.vecs <= 4) return run_mma<TT, BITS, 2, 4, SP, 1, 2>(a, log2b, p, s);
-  if (a.vecs <= 8) return run_mma<TT, BITS, 2, 8, SP, 1, 2>(a, log2b, p, s);
-  return run_mma<TT, BITS, SP == 1 ? 2 : 1, 8, SP, 2, SP == 1 ? 2 : 4>(a, log2b, p, s);
-}
-
-template <typename TT>
-static cudaError_t by_codes(const MatvecArgs& a, int log2b, const MvPlan& p, cudaStream_t s) {
-  if (a.bits == 8) return by_vecs<TT, 8, 1>(a, log2b, p, s);
-  return a.block == 64 ? by_vecs<TT, 4, 2>(a, log2b, p, s) : by_vecs<TT, 4, 1>(a, log2b, p, s);
-}
-
 // `base` warps a row where it has as many units, then more warps and CTAs until some 13 warps per
 // SM have work, never more than units. (8192 x 8192 INT4, one vector, base 4: 2 / 4 / 8 warps
 // 15.4 / 12.3 / 14.7 us; 1024 x 16384, 8 warps: 1 / 2 / 4 CTAs 9.4 / 8.2 / 10.2 us; 32768 x 1024,
@@ -706,15 +690,45 @@ static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
                      : run_any<TT, 4>(a, log2b, any_plan<4>(a), s);
 }
 
+template <typename TT, int BITS, int SP, int MT, int NV, int NT>
+static cudaError_t run_planned(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  using S = MvShape<BITS, MT, NV, SP, NT>;
+  const int64_t segs = a.cols / S::SEG;
+  const MvPlan p = mv_plan((a.rows + S::ROWS - 1) / S::ROWS, (segs + S::UNIT - 1) / S::UNIT, 4);
+  return run_mma<TT, BITS, MT, NV, SP, NT, 4 / MT>(a, log2b, p, s);  // 4 KB on their way per warp
+}
+
+// Two fragments of rows per warp share every load and permutation of x. One vector has little of
+// those, so there the second fragment pays only once some seven warps per SM have a unit to do.
+// (One vector, one / two fragments: 24576 x 8192 25.0 / 23.9 us, 8192 x 8192 12.4 / 9.7; but 4096
+// x 4096 5.0 / 5.9, 2048 x 2048 INT8 4.0 / 5.9 us. Four vectors: 2048 x 2048 INT8 6.3 / 4.0, 4096 x
+// 4096 6.2 / 5.2.) More than eight vectors of blocks of 64 take one: four sets of results of 32
+// rows do not fit the registers.
+template <typename TT, int BITS, int SP>
+static cudaError_t by_vecs(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  if (a.vecs == 1) {
+    using S = MvShape<BITS, 2, 1, SP, 1>;
+    const int64_t units = (a.rows + S::ROWS - 1) / S::ROWS * ((a.cols / S::SEG + S::UNIT - 1) / S::UNIT);
+    return units >= 1000 ? run_planned<TT, BITS, SP, 2, 1, 1>(a, log2b, s)
+                         : run_planned<TT, BITS, SP, 1, 1, 1>(a, log2b, s);
+  }
+  if (a.vecs == 2) return run_planned<TT, BITS, SP, 2, 2, 1>(a, log2b, s);
+  if (a.vecs <= 4) return run_planned<TT, BITS, SP, 2, 4, 1>(a, log2b, s);
+  if (a.vecs <= 8) return run_planned<TT, BITS, SP, 2, 8, 1>(a, log2b, s);
+  return run_planned<TT, BITS, SP, SP == 1 ? 2 : 1, 8, 2>(a, log2b, s);
+}
+
+template <typename TT>
+static cudaError_t launch_type(const MatvecArgs& a, int log2b, cudaStream_t s) {
+  if (a.cols % a.block != 0 || a.cols % (a.bits == 8 ? 64 : 128) != 0 || a.x_stride % 8 != 0)
+    return launch_any<TT>(a, log2b, s);
+  if (a.bits == 8) return by_vecs<TT, 8, 1>(a, log2b, s);
+  return a.block == 64 ? by_vecs<TT, 4, 2>(a, log2b, s) : by_vecs<TT, 4, 1>(a, log2b, s);
+}
+
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s) {
   const int log2b = __builtin_ctz(static_cast<unsigned>(a.block));
-  const int seg = a.bits == 8 ? 64 : 128;
-  if (a.cols % a.block == 0 && a.cols % seg == 0 && a.x_stride % 8 == 0) {
-    const int rows = a.vecs == 1 ? 16 : 32, unit = a.vecs == 1 ? 8 : 4;
-    const MvPlan p = mv_plan((a.rows + rows - 1) / rows, (a.cols / seg + unit - 1) / unit, 4);
-    return a.x_bf16 ? by_codes<BF16>(a, log2b, p, s) : by_codes<F16>(a, log2b, p, s);
-  }
-  return a.x_bf16 ? launch_any<BF16>(a, log2b, s) : launch_any<F16>(a, log2b, s);
+  return a.x_bf16 ? launch_type<BF16>(a, log2b, s) : launch_type<F16>(a, log2b, s);
 }
 
 }  // namespace zpp
