@@ -385,3 +385,104 @@ def test_overflowed_step_is_skipped_end_to_end():
     g[7] = math.inf
     opt.step(g, max_norm=1.0)
     assert bool((p == 1).all()) and bool((opt.exp_avg[0] == 0).all())
+
+
+def test_offsets_beyond_32_bits():
+    """A shard of more than 2^32 elements: the first and the last of them."""
+    n, g_ = (1 << 32) + 1003, gen(12)
+    p = torch.ones(n, device=DEV)
+    g = torch.zeros(n, device=DEV, dtype=torch.bfloat16)
+    m, v = (torch.zeros(n, device=DEV, dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
+    a, b = (torch.zeros(-(-n // BLOCK), device=DEV) for _ in range(2))
+    ends = (slice(0, 1024), slice(n - 1003 - 768, n))  # whole blocks, from multiples of 256 on
+    for e in ends:
+        g[e] = normal(e.stop - e.start, 1e-3, g_).bfloat16()
+    zpp.adamw_step(p, g, m, v, step=1, scales=([a], [b]), seed=3, **HP)
+    for e in ends:
+        k = e.stop - e.start
+        zero = torch.zeros(k, device=DEV)
+        want = reference(torch.ones(k, device=DEV), g[e], zero, zero, 1)
+        within(p[e], want[0], want[3], "p")
+        for codes, scale, x, draw in ((m, a, want[1], 0), (v, b, want[2].sqrt(), 16)):
+            s = scale[e.start // BLOCK:].double().repeat_interleave(BLOCK)[:k]
+            bits = bits_of(torch.arange(e.start, e.stop, device=DEV), 3, 1) >> draw & 65535
+            y = x.abs() / s
+            h = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -6))) - 3)
+            q = (torch.floor(y / h + (bits.double() + 0.5) / 65536) * h).clamp(max=448.0)
+            q = torch.where(y > 0, q, q) if draw == 0 else torch.where(y > 0, q.clamp(min=2.0 ** -9), q)
+            off = codes[e].double().abs() != q
+            assert int(off.sum()) <= 2  # (a value within fp32's error of the next grid point)
+    middle = slice(n // 2, n // 2 + 1000)
+    assert bool((v[middle].float() == 0).all()) and float(p[middle].max()) < 1.0
+    del p, g, m, v
+    total = torch.full(((1 << 32) + 77,), 0.5, device=DEV, dtype=torch.float16)
+    norm = zpp.grad_norm(total)
+    assert abs(float(norm[0]) / (0.5 * math.sqrt(total.numel())) - 1) < 1e-5
+
+
+def test_in_a_cuda_graph():
+    """Norm, clip factor and step captured once (the step's number is captured with it)."""
+    n, g_ = 10_007, gen(13)
+    p, m, v = torch.ones(n, device=DEV), torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    g = normal(n, 1.0, g_).bfloat16()
+    out = torch.empty(2, device=DEV)
+
+    def work():
+        zpp.grad_norm(g, max_norm=1.0, out=out)
+        zpp.adamw_step(p, g, m, v, step=1, grad_scale=out[1:], **HP)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for seed in (1, 2):
+        for t, value in ((p, 1.0), (m, 0.0), (v, 0.0)):
+            t.fill_(value)
+        g.copy_(normal(n, 1.0, gen(seed)))
+        graph.replay()
+        got = [t.clone() for t in (out, p, m, v)]
+        for t, value in ((p, 1.0), (m, 0.0), (v, 0.0)):
+            t.fill_(value)
+        work()
+        assert all(torch.equal(x, y) for x, y in zip(got, (out, p, m, v)))
+
+
+def test_steps_back_to_back_wait_for_each_other():
+    """Fifty clipped steps without a synchronisation equal fifty with one after each."""
+    n, g_ = 3_000_001, gen(14)
+    G = [normal(n, 1.0, g_).half() for _ in range(3)]
+    out = []
+    for sync in (False, True):
+        p = torch.ones(n, device=DEV)
+        opt = zpp.AdamW([p], state_bits=8, seed=2, **HP)
+        for t in range(50):
+            norm = opt.step([G[t % 3]], max_norm=1.0)
+            if sync:
+                torch.cuda.synchronize()
+        out.append((p, norm, opt.exp_avg[0].float(), opt.exp_avg_sq[0].float(), *opt.scales[0]))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_empty_list_through_the_c_interface():
+    out, work = torch.full((2,), 7.0, device=DEV), torch.empty(1, device=DEV)
+    assert zb.zpp_grad_norm([], [], zb.ZPP_F32, 0.25, 1.0, work.data_ptr(), out.data_ptr()) == zb.ZPP_OK
+    assert out.tolist() == [0.0, 0.25]
+
+
+def test_moved_storage_is_seen_by_the_next_step():
+    """A parameter given new storage between two steps."""
+    p = torch.ones(1000, device=DEV)
+    opt = zpp.AdamW([p], **HP)
+    g = torch.ones(1000, device=DEV)
+    opt.step(g)
+    old = p.data
+    p.data = torch.full((1000,), 5.0, device=DEV)
+    keep = old.clone()
+    opt.step(g)
+    assert torch.equal(old, keep) and float((p - 5.0).abs().max()) > 1e-3
+    p.data = torch.ones(999, device=DEV)
+    with pytest.raises(ValueError, match="999 elements, expected 1000"):
+        opt.step(g)

@@ -196,3 +196,65 @@ def test_another_stream():
         y = zpp.matvec_blockwise(codes, scales, x, 512, 64, 4)
     s.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("cols", [8192, 8191])
+def test_offsets_beyond_32_bits(cols):
+    """Code bytes and element numbers past 2^32: the first and the last rows of 4.9 GB."""
+    g, rows, block = gen(8), 600_000, 4096
+    n = rows * cols
+    codes = torch.randint(0, 256, (n,), generator=g, device=DEV, dtype=torch.uint8)
+    codes[codes == 128] = 0  # -128 is no code
+    scales = torch.exp2(torch.randint(-1, 2, (-(-n // block),), generator=g, device=DEV).float())
+    x = torch.randint(-1, 2, (2, cols), generator=g, device=DEV).half()
+    y = zpp.matvec_blockwise(codes, scales, x, rows, block, 8, dtype=torch.float32)
+    for lo in (0, rows - 64):
+        part = slice(lo * cols, (lo + 64) * cols)
+        at = torch.arange(part.start, part.stop, device=DEV) // block
+        w = (codes[part].view(torch.int8).double() * scales[at].double()).view(64, cols)
+        assert torch.equal(y[:, lo:lo + 64], (x.double() @ w.T).float())
+
+
+def test_in_a_cuda_graph():
+    """Captured calls (overlapped launches among them) replay on new inputs."""
+    g, rows, cols = gen(9), 320, 1024
+    w = torch.randn(rows * cols, generator=g, device=DEV).half()
+    codes, scales = zpp.quant_blockwise(w, 128, 4)
+    x = torch.randn(1, cols, generator=g, device=DEV).half()
+    a, b = torch.empty(1, rows, device=DEV).half(), torch.empty(1, rows, device=DEV).half()
+
+    def work():
+        zpp.matvec_blockwise(codes, scales, x, rows, 128, 4, y=a)
+        zpp.matvec_blockwise(codes, scales, x[:, :], rows, 128, 4, y=b)
+        b.add_(a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for seed in (1, 2):
+        x.copy_(torch.randn(1, cols, generator=gen(seed), device=DEV))
+        graph.replay()
+        want = zpp.matvec_blockwise(codes, scales, x, rows, 128, 4)
+        assert torch.equal(a, want) and torch.equal(b, want + want)
+
+
+def test_chains_of_calls_see_each_others_results():
+    """Each call's input is the output of the one before, back to back on one stream: an
+    overlapped launch must not read it early."""
+    g, d = gen(10), 512
+    mats = [zpp.quant_blockwise(torch.randn(d * d, generator=g, device=DEV).half() / d ** 0.5, 128, 4)
+            for _ in range(4)]
+    x = torch.randn(1, d, generator=g, device=DEV).half()
+    want = x
+    for codes, scales in mats * 8:
+        want = zpp.matvec_blockwise(codes, scales, want, d, 128, 4)
+        torch.cuda.synchronize()
+    for _ in range(20):
+        got = x
+        for codes, scales in mats * 8:
+            got = zpp.matvec_blockwise(codes, scales, got, d, 128, 4)
+        assert torch.equal(got, want)
