@@ -257,8 +257,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
             for (int e = 0; e < (NV == 1 ? 2 : 1); ++e) {
               const int slot = NS > 8 ? i % SP : (2 * t + e) / NV;
               const int at = seg0 + u0 + (NS > 8 ? 0 : slot / SP);
-              const int64_t col = static_cast<int64_t>(min(at, segs - 1)) * SEG + slot % SP * 64;
-              sc[m][h][i][e] = ld_after_f32(scale[m][h] + (col >> log2b));
+              const int64_t col = static_cast<int64_t>(at) * SEG + slot % SP * 64;
+              // beyond the row 0, not another block's scale: that may be infinite
+              sc[m][h][i][e] = at < segs ? ld_after_f32(scale[m][h] + (col >> log2b)) : 0.0f;
               if (NV > 1) sc[m][h][i][1] = sc[m][h][i][0];
             }
       float r[MT][T][4] = {};

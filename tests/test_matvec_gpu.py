@@ -258,3 +258,19 @@ def test_chains_of_calls_see_each_others_results():
         for codes, scales in mats * 8:
             got = zpp.matvec_blockwise(codes, scales, got, d, 128, 4)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("vecs", [1, 2, 3, 5])
+@pytest.mark.parametrize("bits, block, segments", [(4, 64, 3), (4, 128, 5), (4, 128, 11), (8, 64, 5)])
+def test_infinite_scale_of_a_rows_last_block_gives_infinity(bits, block, segments, vecs):
+    # rows of fewer segments than a warp takes at a time, or of a part more
+    cols, rows = segments * (128 if bits == 4 else 64), 40
+    n = rows * cols
+    codes = torch.full((n * bits // 8,), 0x11 if bits == 4 else 1, dtype=torch.uint8, device=DEV)
+    scales = torch.ones(rows, cols // block, device=DEV)
+    scales[7, -1] = scales[20, -1] = float("inf")
+    x = torch.ones(vecs, cols, device=DEV, dtype=torch.bfloat16)
+    y = zpp.matvec_blockwise(codes, scales.view(-1), x, rows, block, bits, dtype=torch.float32)
+    want = torch.full((vecs, rows), float(cols), device=DEV)
+    want[:, 7] = want[:, 20] = float("inf")
+    assert torch.equal(y, want)
