@@ -396,7 +396,7 @@ struct AnyShape {
   static constexpr int PW = 16 / BITS;       // pairs per word
   static constexpr int XB = WC * 2;          // bytes of a word's columns of x
   static constexpr int STAGE = 2 * 512 + 2 * 128;  // codes, scales
-  static constexpr int DEPTH = 4;            // stages on their way
+  static constexpr int DEPTH = 3;            // stages on their way (with 4: 50001 x 1003 16.5 us, not 16.0)
   static constexpr int RING = DEPTH * STAGE;
 };
 // Stages of a row and a CTA's share of them (at most, over its warps and ranks).
