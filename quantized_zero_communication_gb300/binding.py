@@ -8,6 +8,7 @@ is an error.
 """
 import array
 import ctypes
+import functools
 import math
 import os
 import re
@@ -611,6 +612,13 @@ def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if not grads:
         raise ValueError("grad_norm needs at least one tensor")
+    if out is None:
+        found = _tensors().grad_norm(_address("zpp_grad_norm"), _address("zpp_grad_norm_workspace"),
+                                     grads, math.inf if max_norm is None else max_norm, pre_scale)
+        if found is not None:
+            if type(found) is int:
+                raise ZppError(found, "zpp_grad_norm")
+            return found
     ptrs, sizes, kind, device = _dev_list(grads, "grads", (ZPP_F16, ZPP_BF16, ZPP_F32))
     if out is not None:
         _need(out, "out", 2, (torch.float32,))
@@ -706,19 +714,19 @@ def _adamw(tab, g_kind, w_kind, state_bits, hp, scale, device):
            "zpp_adamw_step")
 
 
-_matvec_address = None
+@functools.cache
+def _address(name):
+    """The address of a library function, as the extension takes it."""
+    return ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
 
 
 def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None, y=None):
     """x [..., cols] (fp16 / bf16; rows of cols contiguous elements, any row stride) times the
     transposed [rows][cols] matrix that quant_blockwise gave (codes, scales) for -> y [..., rows]
     of `dtype` (default: x's). bias: [rows] of x's dtype. y: an output buffer, same form as x."""
-    global _matvec_address
-    if _matvec_address is None:
-        _matvec_address = ctypes.cast(lib().zpp_matvec_blockwise, ctypes.c_void_p).value
     native = _tensors()
     if y is None:
-        y = native.matvec(_matvec_address, codes, scales, x, rows, block, bits, bias,
+        y = native.matvec(_address("zpp_matvec_blockwise"), codes, scales, x, rows, block, bits, bias,
                           -1 if dtype is None else _dt(dtype))
         if y is not None:
             if type(y) is int:

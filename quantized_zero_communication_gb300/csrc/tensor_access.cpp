@@ -3,7 +3,8 @@
 // element count, type, device and contiguity from Python costs the host some 0.4 us a tensor
 // (60 us for 150 tensors, more than the step itself takes on the GPU), here some 10 ns. And a
 // product for one token takes the GPU 4 us: its wrapper's common case (plain contiguous
-// tensors, a new output) is one call here too, 14 us of host time otherwise.
+// tensors, a new output) is one call here too, 14 us of host time otherwise. The norm of 40
+// gradients takes it 6 us, and 22 us through Python.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -169,7 +170,64 @@ PyObject* matvec(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
+// grad_norm(address of zpp_grad_norm, address of zpp_grad_norm_workspace, list of gradients,
+// max_norm, pre_scale): (norm, factor) in a new tensor, a status other than ZPP_OK as an int, or
+// None where something is not the plain case.
+PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 5) {
+    PyErr_SetString(PyExc_TypeError, "grad_norm: 5 arguments");
+    return nullptr;
+  }
+  const auto number = [](PyObject* o) { return PyFloat_Check(o) || PyLong_Check(o); };
+  if (!PyList_Check(args[2]) || !number(args[3]) || !number(args[4])) Py_RETURN_NONE;
+  void* fn = PyLong_AsVoidPtr(args[0]);
+  void* workspace = PyLong_AsVoidPtr(args[1]);
+  const double max_norm = PyFloat_AsDouble(args[3]), pre_scale = PyFloat_AsDouble(args[4]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  const Py_ssize_t count = PyList_GET_SIZE(args[2]);
+  if (count < 1 || count > INT32_MAX) Py_RETURN_NONE;
+  try {
+    std::vector<const void*> at(count);
+    std::vector<int64_t> counts(count);
+    long kind = -1, device = -1;
+    int64_t total = 0;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      PyObject* o = PyList_GET_ITEM(args[2], i);
+      if (!plain(o)) Py_RETURN_NONE;
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (i == 0) kind = kind_of(t), device = gpu_of(t);
+      if (kind < 0 || kind > ZPP_F32 || device < 0 || kind_of(t) != kind || gpu_of(t) != device ||
+          !t.is_contiguous())
+        Py_RETURN_NONE;
+      at[i] = reinterpret_cast<const void*>(address_of(t));
+      counts[i] = t.numel();
+      total += counts[i];
+    }
+    const int64_t floats = reinterpret_cast<decltype(&zpp_grad_norm_workspace)>(workspace)(
+        total, static_cast<int32_t>(count));
+    if (floats < 0) Py_RETURN_NONE;
+    const auto options = THPVariable_Unpack(PyList_GET_ITEM(args[2], 0)).options().dtype(at::kFloat);
+    at::Tensor out = at::empty({2}, options);
+    const at::Tensor work = at::empty({floats}, options);
+    const zpp_status st = reinterpret_cast<decltype(&zpp_grad_norm)>(fn)(
+        at.data(), counts.data(), static_cast<int32_t>(count), static_cast<zpp_dtype>(kind),
+        static_cast<float>(pre_scale), static_cast<float>(max_norm),
+        reinterpret_cast<float*>(address_of(work)), reinterpret_cast<float*>(address_of(out)),
+        c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream());
+    if (st != ZPP_OK) return PyLong_FromLong(st);
+    return THPVariable_Wrap(std::move(out));
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
 PyMethodDef methods[] = {
+    {"grad_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grad_norm)),
+     METH_FASTCALL, "the norm of a list of gradients, plain case"},
     {"scan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scan)), METH_FASTCALL,
      "addresses and element counts of a list of tensors; (kind, device)"},
     {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matvec)), METH_FASTCALL,
