@@ -9,6 +9,12 @@
 // is one state block, so the block maximum of an 8-bit state is a warp reduction and the
 // states never leave registers between decoding and encoding. A lane holds 8 consecutive
 // elements: 32 bytes of p, one 256-bit access where the buffers allow it.
+//
+// fp32 states are bound by DRAM: 201,326,592 elements with bf16 gradients and weights 801 us, 7.04
+// TB/s over 28 bytes each. 8-bit states (16.06 bytes) are bound by instruction issue, some 80 per
+// element: 268,435,456 elements 680 us, 6.34 TB/s, issue slots 79 % busy; a warp takes two blocks
+// there so that the loads of one cover the arithmetic of the other. A short list is bound by the
+// launch: 1024 elements 9 us, most of it on the host.
 #include <cuda_fp8.h>
 
 #include "zpp_device.cuh"
@@ -376,7 +382,8 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
   const AdamwTensor& t = tab.t[lo];
   const int lane = threadIdx.x & 31;
   constexpr int NB = adamw_warp_blocks(FP8 ? 8 : 32);
-  const int64_t block = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * (kWarps * NB) + (threadIdx.x >> 5) * NB;
+  const int64_t block =
+      static_cast<int64_t>(blockIdx.x - tab.first[lo]) * (kWarps * NB) + (threadIdx.x >> 5) * NB;
   const int64_t left = t.n - block * kStateBlock;
   if (left <= 0) return;
   const int64_t number = (tab.first_block + tab.block0[lo] + block) * kStateBlock;
@@ -389,7 +396,8 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
       step_block<FP8, V8, false>(t, a, c, block + b, number + b * kStateBlock, lane, kVec, l[b]);
   } else {
     for (int b = 0; b < NB && left > b * kStateBlock; ++b) {
-      const int cnt = static_cast<int>(min(left - b * kStateBlock - lane * kVec, static_cast<int64_t>(kVec)));
+      const int cnt =
+          static_cast<int>(min(left - b * kStateBlock - lane * kVec, static_cast<int64_t>(kVec)));
       Loaded<FP8> l;
       load_block<FP8, V8, true>(t, a, block + b, lane, max(cnt, 0), l);
       step_block<FP8, V8, true>(t, a, c, block + b, number + b * kStateBlock, lane, max(cnt, 0), l);
