@@ -603,6 +603,9 @@ def _dev_list(ts, name, kinds):
     return ptrs, sizes, kind, device
 
 
+_GRAD_KINDS = (ZPP_F16, ZPP_BF16, ZPP_F32)
+
+
 def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
     """The global norm of a list of gradient tensors (one fp16 / bf16 / fp32 dtype) times
     |pre_scale|, and the factor that clips it to `max_norm` (None: no clipping) with
@@ -619,7 +622,7 @@ def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
             if type(found) is int:
                 raise ZppError(found, "zpp_grad_norm")
             return found
-    ptrs, sizes, kind, device = _dev_list(grads, "grads", (ZPP_F16, ZPP_BF16, ZPP_F32))
+    ptrs, sizes, kind, device = _dev_list(grads, "grads", _GRAD_KINDS)
     if out is not None:
         _need(out, "out", 2, (torch.float32,))
         _cuda(grads[0], out)
@@ -651,7 +654,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
     aslist = lambda v: [v] if isinstance(v, torch.Tensor) else list(v)  # noqa: E731
     f32 = (ZPP_F32,)
     params, grads = aslist(params), aslist(grads)
-    lists = [("params", params, f32), ("grads", grads, (ZPP_F16, ZPP_BF16, ZPP_F32))]
+    lists = [("params", params, f32), ("grads", grads, _GRAD_KINDS)]
     state = f32 if scales is None else (_E4M3,)
     lists += [("exp_avg", aslist(exp_avg), state), ("exp_avg_sq", aslist(exp_avg_sq), state)]
     if scales is not None:

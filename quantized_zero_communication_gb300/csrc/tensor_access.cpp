@@ -39,6 +39,37 @@ bool plain(PyObject* o) {
   return THPVariable_Check(o) && THPVariable_Unpack(o).layout() == at::kStrided;
 }
 
+// What a list's tensors have in common.
+struct Seen {
+  long kind = -1, device = -1;  // -1 unless the same for all
+  bool contiguous = true;
+  long place() const { return device >= 0 && !contiguous ? -2 : device; }
+};
+// Calls each(i, tensor) for the list's tensors; false with an error set.
+template <typename F>
+bool look(PyObject* list, Seen& seen, const F& each) {
+  const Py_ssize_t count = PyList_GET_SIZE(list);
+  try {
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      PyObject* o = PyList_GET_ITEM(list, i);
+      if (!plain(o)) {
+        PyErr_Format(PyExc_TypeError, "expected a tensor, got %s", Py_TYPE(o)->tp_name);
+        return false;
+      }
+      const at::Tensor& t = THPVariable_Unpack(o);
+      const long kind = kind_of(t), device = gpu_of(t);
+      seen.contiguous = seen.contiguous && t.is_contiguous();
+      seen.kind = i == 0 || kind == seen.kind ? kind : -1;
+      seen.device = i == 0 || device == seen.device ? device : -1;
+      each(i, t);
+    }
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return false;
+  }
+  return true;
+}
+
 // scan(tensors, addresses, counts): writes every tensor's address and element count into the two
 // writable int64 buffers and returns (kind, device), each -1 unless it is the same for all;
 // device -2: a tensor is not contiguous.
@@ -58,36 +89,48 @@ PyObject* scan(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (at.len < count * 8 || counts.len < count * 8) {
     PyErr_SetString(PyExc_ValueError, "scan: buffers too small");
   } else {
-    long kind = -1, device = -1;
-    bool contiguous = true, ok = true;
-    try {
-      for (Py_ssize_t i = 0; i < count; ++i) {
-        PyObject* o = PyList_GET_ITEM(args[0], i);
-        if (!plain(o)) {
-          PyErr_Format(PyExc_TypeError, "expected a tensor, got %s", Py_TYPE(o)->tp_name);
-          ok = false;
-          break;
-        }
-        const at::Tensor& t = THPVariable_Unpack(o);
-        static_cast<int64_t*>(at.buf)[i] = address_of(t);
-        static_cast<int64_t*>(counts.buf)[i] = t.numel();
-        contiguous = contiguous && t.is_contiguous();
-        if (i == 0) {
-          kind = kind_of(t);
-          device = gpu_of(t);
-        } else {
-          if (kind_of(t) != kind) kind = -1;
-          if (gpu_of(t) != device) device = -1;
-        }
-      }
-    } catch (const std::exception& e) {
-      PyErr_SetString(PyExc_RuntimeError, e.what());
-      ok = false;
-    }
-    if (ok) result = Py_BuildValue("ll", kind, device >= 0 && !contiguous ? -2 : device);
+    Seen seen;
+    if (look(args[0], seen, [&](Py_ssize_t i, const at::Tensor& t) {
+          static_cast<int64_t*>(at.buf)[i] = address_of(t);
+          static_cast<int64_t*>(counts.buf)[i] = t.numel();
+        }))
+      result = Py_BuildValue("ll", seen.kind, seen.place());
   }
   PyBuffer_Release(&at);
   PyBuffer_Release(&counts);
+  return result;
+}
+
+// enter(tensors, table, column, sizes): writes every tensor's address into its row of the
+// writable int64 table [.][8], at `column`; (kind, device, same), kind and device as of scan,
+// same: every element count equals that in the int64 buffer `sizes`.
+PyObject* enter(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  const long column = n == 4 ? PyLong_AsLong(args[2]) : -1;
+  if (n != 4 || !PyList_Check(args[0]) || column < 0 || column > 7) {
+    PyErr_SetString(PyExc_TypeError, "enter(list of tensors, int64 table, column, int64 buffer)");
+    return nullptr;
+  }
+  const Py_ssize_t count = PyList_GET_SIZE(args[0]);
+  Py_buffer table, sizes;
+  if (PyObject_GetBuffer(args[1], &table, PyBUF_WRITABLE) != 0) return nullptr;
+  if (PyObject_GetBuffer(args[3], &sizes, PyBUF_SIMPLE) != 0) {
+    PyBuffer_Release(&table);
+    return nullptr;
+  }
+  PyObject* result = nullptr;
+  if (table.len < count * 64 || sizes.len < count * 8) {
+    PyErr_SetString(PyExc_ValueError, "enter: buffers too small");
+  } else {
+    Seen seen;
+    bool same = true;
+    if (look(args[0], seen, [&](Py_ssize_t i, const at::Tensor& t) {
+          static_cast<int64_t*>(table.buf)[8 * i + column] = address_of(t);
+          same = same && t.numel() == static_cast<const int64_t*>(sizes.buf)[i];
+        }))
+      result = Py_BuildValue("lli", seen.kind, seen.place(), same ? 1 : 0);
+  }
+  PyBuffer_Release(&table);
+  PyBuffer_Release(&sizes);
   return result;
 }
 
@@ -230,6 +273,8 @@ PyMethodDef methods[] = {
      METH_FASTCALL, "the norm of a list of gradients, plain case"},
     {"scan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scan)), METH_FASTCALL,
      "addresses and element counts of a list of tensors; (kind, device)"},
+    {"enter", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(enter)), METH_FASTCALL,
+     "addresses of a list of tensors into a column of a table; (kind, device, same sizes)"},
     {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matvec)), METH_FASTCALL,
      "the product with a quantised matrix, plain case"},
     {"probe", probe, METH_O, "(address, elements, kind, device, contiguous) of a tensor"},

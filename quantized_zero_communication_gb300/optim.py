@@ -84,19 +84,19 @@ class AdamW:
         """Checks a list and writes its addresses into the call's table; their dtype's kind."""
         if len(tensors) != len(sizes):
             raise ValueError(f"{name}: {len(tensors)} tensors, expected {len(sizes)}")
-        ptrs, got, kind, device = _b._dev_list(tensors, name, kinds)
-        _b._same_sizes(name, got, sizes)
+        kind, device, same = _b._tensors().enter(tensors, self._table, column, sizes)
+        if kind not in kinds or device < 0 or not same:
+            _b._same_sizes(name, _b._dev_list(tensors, name, kinds)[1], sizes)
         if self._device is None:
             self._device = device
         if device != self._device:
             raise ValueError("all tensors of a call must be on one device")
-        self._table[column::8] = ptrs
-        return ptrs, kind
+        return kind
 
     def _gather(self):
         """Every tensor that the optimiser holds, as it is now (storage may have moved)."""
         for entry in self._lists:
-            kind = self._enter(*entry)[1]
+            kind = self._enter(*entry)
             if entry[0] == "weights":
                 self._w_kind = kind
 
@@ -111,8 +111,7 @@ class AdamW:
         torch = _b._torch()
         grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
         self._gather()
-        ptrs, kind = self._enter("grads", 1, grads, self._sizes,
-                                 (_b.ZPP_F16, _b.ZPP_BF16, _b.ZPP_F32))
+        kind = self._enter("grads", 1, grads, self._sizes, _b._GRAD_KINDS)
         if lr is not None:
             self.lr = lr
         norm, scale = None, 0
@@ -125,7 +124,7 @@ class AdamW:
                     dtype=torch.float32)
             norm = grads[0].new_empty(2, dtype=torch.float32)
             at = norm.data_ptr()
-            _b._norm_call(ptrs, self._sizes, kind, self._device, max_norm,
+            _b._norm_call(self._table[1::8], self._sizes, kind, self._device, max_norm,
                           1.0 if pre_scale is None else pre_scale, self._work.data_ptr(), at)
             scale = at + 4  # its second element
         elif grad_scale is not None:
