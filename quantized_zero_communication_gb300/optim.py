@@ -18,7 +18,7 @@ class AdamW:
     (see include/zpp.h). weights: fp16 or bf16 tensors of the parameters' sizes that each
     step fills, or None. exp_avg, exp_avg_sq, scales and step resume from a saved state()
     (the tensors are taken over, not copied); by default the states start at zero. One
-    optimiser's steps belong on one stream at a time (they share a workspace).
+    optimiser's steps belong on one stream at a time.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *,
@@ -77,7 +77,7 @@ class AdamW:
         self._table = array.array("q", bytes(64 * len(self.params)))
         self._table[7::8] = self._sizes
         self._hp = _b.AdamwParams(lr, *self.betas, eps, weight_decay, step, seed)
-        self._w_kind, self._work = _b.ZPP_BF16, None
+        self._w_kind = _b.ZPP_BF16
         self._gather()
 
     def _enter(self, name, column, tensors, sizes, kinds):
@@ -118,15 +118,8 @@ class AdamW:
         if max_norm is not None or pre_scale is not None:
             if grad_scale is not None:
                 raise ValueError("grad_scale replaces max_norm and pre_scale")
-            if self._work is None:
-                self._work = grads[0].new_empty(
-                    _b.zpp_grad_norm_workspace(sum(self._sizes), len(self._sizes)),
-                    dtype=torch.float32)
-            norm = grads[0].new_empty(2, dtype=torch.float32)
-            at = norm.data_ptr()
-            _b._norm_call(self._table[1::8], self._sizes, kind, self._device, max_norm,
-                          1.0 if pre_scale is None else pre_scale, self._work.data_ptr(), at)
-            scale = at + 4  # its second element
+            norm = _b.grad_norm(grads, max_norm, 1.0 if pre_scale is None else pre_scale)
+            scale = norm.data_ptr() + 4  # its second element
         elif grad_scale is not None:
             scale = _b._scale_address(grads[0], grad_scale)
         hp = self._hp
