@@ -387,8 +387,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
 // Any width, any stride of x: rows start inside a block, a word, a byte. The codes are read by
 // aligned chunks of 16 bytes (32 or 16 codes, one block each). A row whose first code is number s
 // of its chunk meets x shifted by s columns, with zeros beyond both ends for its neighbours'
-// codes; rows CH apart (CH codes a chunk) have the same s. So a CTA takes rows of one s only, a
-// fragment is 16 of them CH apart, and x lies in shared memory shifted, as fragments. Blocks begin
+// codes; rows CH apart (CH codes a chunk) have the same s. So a CTA takes rows of one s only and a
+// fragment is 16 of them CH apart. Where rows start at words (WORDS: the width and x's stride are
+// multiples of 8 INT4, 4 INT8 columns) a lane reads its words of x where they are; else x is laid
+// out in shared memory, shifted, as fragments, by each CTA, which costs more than the products from
+// four vectors on. (24576 x 8224 INT4, 1 / 8 vectors: in place 43 / 45 us, laid out 40 / 98; 2861 x
+// 20896: 22 / 23 and 22 / 62; 5120 x 1280 INT8: 6.3 / 6.6 and 6.6 / 11.) Blocks begin
 // at other columns in every row, so a product covers one chunk and is scaled per row and chunk;
 // lane (g, t) takes word t of the chunks of rows g and g + 8.
 //
@@ -415,114 +419,154 @@ __host__ __device__ inline int any_share(int64_t cols, int ch, int wk, int split
   return (any_stages(cols, ch) + step - 1) / step * wk;
 }
 
-template <typename TT, int BITS>
-__global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int log2b, int wk, int split,
-                                                         const Masks masks) {
+template <typename TT, int BITS, bool WORDS>
+__global__ void __launch_bounds__(kThreads, 4)
+    k_matvec_any(const MatvecArgs a, int log2b, int wk, int split, const Masks masks) {
   using S = AnyShape<BITS>;
   constexpr int CH = S::CH;
   extern __shared__ __align__(16) uint8_t smem[];  // [kWarps] rings (later sums), then x
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int rank = static_cast<int>(blockIdx.x) % split, cta = static_cast<int>(blockIdx.x) / split;
-  const int wr = kWarps / wk;  // row tiles of a CTA
+  const int log2wk = __popc(wk - 1), log2split = __popc(split - 1);  // both powers of two
+  const int rank = static_cast<int>(blockIdx.x) & (split - 1);
+  const int cta = static_cast<int>(blockIdx.x) >> log2split, wr = kWarps >> log2wk;  // wr: row tiles of a CTA
   // Rows rho + CH i of this CTA, 16 i per tile.
   const int rho = cta % CH;
-  const int64_t tile = static_cast<int64_t>(cta / CH) * wr + warp / wk;
+  const int64_t tile = static_cast<int64_t>(cta / CH) * wr + (warp >> log2wk);
   const int64_t row0 = rho + tile * (16 * CH);
   const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * 8;
   const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(8)));
+  const unsigned cols = static_cast<unsigned>(a.cols);  // less than 2^31
   const int shift = static_cast<int>(rho * a.cols % CH);
   const int chunks = static_cast<int>((a.cols + shift + CH - 1) / CH), stages = (chunks + 3) / 4;
-  const int step = wk * split, first = rank * wk + warp % wk;
+  const int step = wk * split, first = rank * wk + (warp & (wk - 1));
   const int64_t bytes = (a.rows * a.cols * BITS + 7) / 8;  // of all codes
-  const int sh = log2b - (BITS == 4 ? 5 : 4);               // chunks per block
+  const int sh = log2b - (BITS == 4 ? 5 : 4);               // log2 of chunks per block
+  const bool live = rho < a.rows;                           // (a CTA without rows writes nothing)
 
-  int64_t at[2];  // chunk of all codes that holds the row's first code
+  // The next stage to copy: chunk number `to` (in its rows) of this lane's two rows.
+  const unsigned ring = smem_addr(smem) + warp * S::RING;
+  const unsigned put = ring + g * 64 + ((t ^ ((g >> 1) & 3)) * 16);
+  const uint8_t* codes[2];
+  const float* scales[2];
+  int in_block[2], short_at[2];  // the last chunk of all may end early
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // rows past the end read the first one of this shift; not stored
     int64_t r = row0 + (8 * h + g) * CH;
     if (r >= a.rows) r = min(static_cast<int64_t>(rho), a.rows - 1);
-    at[h] = r * a.cols / CH;
+    const int64_t at = r * a.cols / CH;  // chunk of all codes that holds the row's first code
+    codes[h] = a.codes + (at + first * 4 + t) * 16;
+    scales[h] = a.scales + (at >> sh);
+    in_block[h] = static_cast<int>(at & ((1 << sh) - 1));
+    short_at[h] = static_cast<int>(min(bytes / 16 - at, static_cast<int64_t>(chunks)));
   }
-  const bool live = rho < a.rows;  // (a CTA without rows writes nothing)
-  const unsigned ring = smem_addr(smem) + warp * S::RING;
-  const unsigned put = ring + g * 64 + ((t ^ ((g >> 1) & 3)) * 16);
-  auto fill = [&](int n) {  // stage number n of this warp
-    const int c = (first + n * step) * 4 + t;
-    if (live && c < chunks) {
+  const int short_bytes = static_cast<int>(bytes % 16);
+  int to = first * 4 + t;
+  unsigned to_slot = 0;
+  auto fill = [&] {
+    const bool on = live && to < chunks;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t o = at[h] + c;
-        const int64_t left = bytes - o * 16;  // the last chunk of all may end early
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         put + n % S::DEPTH * S::STAGE + h * 512),
-                     "l"(a.codes + o * 16), "r"(static_cast<int>(min(left, static_cast<int64_t>(16))))
-                     : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                         ring + n % S::DEPTH * S::STAGE + 1024 + h * 128 + lane * 4),
-                     "l"(a.scales + (o >> sh))
-                     : "memory");
-      }
+    for (int h = 0; h < 2; ++h) {
+      // (zeros for what is not there; of those nothing is read)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(put + to_slot + h * 512),
+                   "l"(codes[h]), "r"(on ? (to == short_at[h] ? short_bytes : 16) : 0)
+                   : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                       ring + to_slot + 1024 + h * 128 + lane * 4),
+                   "l"(scales[h] + (on ? (in_block[h] + to) >> sh : 0)), "r"(on ? 4 : 0)
+                   : "memory");
+      codes[h] += step * 64;
     }
+    to += step * 4;
+    to_slot = to_slot == (S::DEPTH - 1) * S::STAGE ? 0 : to_slot + S::STAGE;
     cp_async_commit();
   };
   grid_wait();
   grid_release();
 #pragma unroll
-  for (int n = 0; n < S::DEPTH - 1; ++n) fill(n);
+  for (int n = 0; n < S::DEPTH - 1; ++n) fill();
 
   // x as fragments: unit (stage l of the CTA's share, chunk c of it, vector v, t) holds the pairs of
   // columns that go with the code pairs of word t.
-  const int share = any_share(a.cols, CH, wk, split);
   uint8_t* const frag = smem + kWarps * S::RING;
-  for (int v = 0; v < vecs; ++v) {
-    const uint16_t* x = a.x + (vec0 + v) * a.x_stride;
-#pragma unroll 2
-    for (int i = threadIdx.x; i < share * 16; i += kThreads) {
-      const int l = i >> 4, c = i >> 2 & 3;
-      const int64_t stage = rank * wk + static_cast<int64_t>(l / wk) * step + l % wk;
-      const int64_t col = (stage * 4 + c) * CH + (i & 3) * S::WC - shift;
+  if constexpr (!WORDS) {
+    const int units = ((stages + step - 1) >> (log2wk + log2split) << log2wk) * 16;
+    int i = threadIdx.x, v = 0;
+    auto settle = [&] {
+      while (i >= units) i -= units, ++v;
+    };
+    settle();
+    while (v < vecs) {
+      const unsigned l = i >> 4, c = i >> 2 & 3;
+      const unsigned stage = rank * wk + (l >> log2wk) * step + (l & (wk - 1));
+      const unsigned col = (stage * 4 + c) * CH + (i & 3) * S::WC - shift;  // below 0: above cols
+      const uint16_t* x = a.x + (vec0 + v) * a.x_stride;
       uint32_t e[S::WC];
 #pragma unroll
-      for (int k = 0; k < S::WC; ++k)
-        e[k] = col + k >= 0 && col + k < a.cols ? ld_after_u16(x + col + k) : 0u;
-      uint32_t* to = reinterpret_cast<uint32_t*>(frag + (((l * 4 + c) * vecs + v) * 4 + (i & 3)) * S::XB);
+      for (int j = 0; j < S::WC; ++j) e[j] = col + j < cols ? ld_after_u16(x + (col + j)) : 0u;
+      uint32_t* to_x = reinterpret_cast<uint32_t*>(frag + ((i >> 2) * vecs + v) * (4 * S::XB)) +
+                       (i & 3) * (S::XB / 4);
 #pragma unroll
-      for (int p = 0; p < S::PW; ++p) to[p] = e[p] | e[p + S::PW] << 16;
+      for (int p = 0; p < S::PW; ++p) to_x[p] = e[p] | e[p + S::PW] << 16;
+      i += kThreads;
+      settle();
     }
+    __syncthreads();
   }
-  __syncthreads();
+
+  // Where this lane reads: word t of the chunks of rows g and g + 8, the scales of row g, x.
+  const uint8_t* const mine = smem + warp * S::RING + g * 64 + t * 4;
+  int word[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) word[c] = (c ^ ((g >> 1) & 3)) * 16;
+  const uint8_t* xs = frag + (warp & (wk - 1)) * (16 * vecs * S::XB) + (min(g, vecs - 1) * 4 + t) * S::XB;
+  const bool has_x = g < vecs;
+  unsigned col = first * 4 * CH + t * S::WC - shift;
+  const uint16_t* xg = a.x + (vec0 + min(g, vecs - 1)) * a.x_stride + static_cast<int>(col);
 
   float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const unsigned get = ring + g * 64 + t * 4;
-  unsigned xs = smem_addr(frag) + (warp % wk) * (16 * vecs * S::XB) + (min(g, vecs - 1) * 4 + t) * S::XB;
-  for (int n = 0; first + n * step < stages; ++n) {
+  int slot = 0;
+  for (int stage = first; stage < stages; stage += step) {
+    uint4 xw[4];
+    if constexpr (WORDS) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool on = has_x && col + c * CH < cols;
+        xw[c] = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (BITS == 4) ld_after_shared_v4_if(on, xg + c * CH, xw[c]);
+        else ld_after_shared_v2_if(on, xg + c * CH, xw[c]);
+      }
+      col += step * 4 * CH;
+      xg += step * 4 * CH;
+    }
     cp_async_wait<S::DEPTH - 2>();
     __syncwarp();  // all lanes' copies of this stage have landed, the one before is free
-    fill(n + S::DEPTH - 1);
-    const unsigned base = n % S::DEPTH * S::STAGE;
-    const int left = chunks - (first + n * step) * 4;
+    fill();
+    float sc[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(smem + warp * S::RING + slot + 1024 + h * 128 + g * 16);
+      sc[h][0] = v.x, sc[h][1] = v.y, sc[h][2] = v.z, sc[h][3] = v.w;
+    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (c >= left) break;
       uint32_t q[2][S::PW], b[S::PW];
-      float sc[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(get + base + h * 512 + ((c ^ ((g >> 1) & 3)) * 16)));
-        asm volatile("ld.shared.f32 %0, [%1];"
-                     : "=f"(sc[h])
-                     : "r"(ring + base + 1024 + h * 128 + (g * 4 + c) * 4));
-        Codes<TT, BITS>::pairs(w, masks, q[h]);
-      }
-      if constexpr (BITS == 4) {
-        const uint4 v = ld_shared_v4(xs + c * (vecs * 4 * S::XB));
-        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+      for (int h = 0; h < 2; ++h)
+        Codes<TT, BITS>::pairs(*reinterpret_cast<const uint32_t*>(mine + slot + word[c] + h * 512), masks, q[h]);
+      if constexpr (!WORDS) {
+        if constexpr (BITS == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(xs + c * (vecs * 4 * S::XB));
+          b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(xs + c * (vecs * 4 * S::XB));
+          b[0] = v.x, b[1] = v.y;
+        }
+      } else if constexpr (BITS == 4) {
+        b[0] = __byte_perm(xw[c].x, xw[c].z, 0x5410u), b[1] = __byte_perm(xw[c].x, xw[c].z, 0x7632u);
+        b[2] = __byte_perm(xw[c].y, xw[c].w, 0x5410u), b[3] = __byte_perm(xw[c].y, xw[c].w, 0x7632u);
       } else {
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                     : "=r"(b[0]), "=r"(b[1])
-                     : "r"(xs + c * (vecs * 4 * S::XB)));
+        b[0] = __byte_perm(xw[c].x, xw[c].y, 0x5410u), b[1] = __byte_perm(xw[c].x, xw[c].y, 0x7632u);
       }
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -531,9 +575,10 @@ __global__ void __launch_bounds__(kThreads) k_matvec_any(const MatvecArgs a, int
         mma16816(d, f, b[p], b[p + 1], d, TT());
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = __fmaf_rn(d[k], sc[k >> 1], y[k]);
+      for (int k = 0; k < 4; ++k) y[k] = __fmaf_rn(d[k], sc[k >> 1][c], y[k]);
     }
     xs += wk * (16 * vecs * S::XB);
+    slot = slot == (S::DEPTH - 1) * S::STAGE ? 0 : slot + S::STAGE;
   }
 
   cp_async_wait<0>();
@@ -649,9 +694,21 @@ static MvPlan mv_plan(int64_t tiles, int64_t units, int base) {
 }
 
 template <typename TT, int BITS>
-static cudaError_t run_any(const MatvecArgs& a, int log2b, MvPlan p, cudaStream_t s) {
+static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
   using S = AnyShape<BITS>;
   const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;  // tiles of one shift
+  const bool words = a.cols % S::WC == 0 && a.x_stride % S::WC == 0;
+  // Where a CTA lays x out it does so for all its tiles, so more tiles and fewer warps a row where
+  // that is much work; fewer warps too where rows are short. (9000 x 20015, 16 vectors: 1 / 4 warps
+  // 161 / 221 us; 50001 x 1003, 9 stages a row: 1 / 2 / 4 warps 18.2 / 16.4 / 17.9 us; 30000 x 6001:
+  // 2 / 4 / 8 warps 41.8 / 38.9 / 41.0 us; taken some steps before the times above.)
+  const int stages = any_stages(a.cols, S::CH);
+  MvPlan p = mv_plan(groups * S::CH, stages, !words && a.vecs > 8 ? 1 : stages < 16 ? 2 : 4);
+  const int wr = kWarps / p.wk;
+  const int64_t ctas = (groups + wr - 1) / wr * S::CH;
+  if (words)
+    return launch_split(k_matvec_any<TT, BITS, true>, ctas, (a.vecs + 7) / 8, p.split, kWarps * S::RING, s, a,
+                        log2b, p.wk, p.split, Codes<TT, BITS>::kMasks);
   // x of a CTA's share lies in shared memory: more CTAs along a row, then fewer vectors at a time
   const auto x_bytes = [&](int64_t vecs) {
     return static_cast<int64_t>(any_share(a.cols, S::CH, p.wk, p.split)) * 16 * vecs * S::XB;
@@ -664,7 +721,6 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, MvPlan p, cudaStream_
     k_matvec_long<TT><<<grid, kThreads, 0, s>>>(a, log2b);
     return cudaGetLastError();
   }
-  const int wr = kWarps / p.wk;
   const int64_t at_once = vecs < 8 ? vecs : a.vecs;  // of one launch
   for (int64_t v = 0; v < a.vecs; v += at_once) {
     MatvecArgs part = a;
@@ -672,7 +728,7 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, MvPlan p, cudaStream_
     part.y = static_cast<uint8_t*>(a.y) + v * a.y_stride * (a.y_kind == 2 ? 4 : 2);
     part.vecs = std::min(at_once, a.vecs - v);
     const cudaError_t e = launch_split(
-        k_matvec_any<TT, BITS>, (groups + wr - 1) / wr * S::CH, (part.vecs + 7) / 8, p.split,
+        k_matvec_any<TT, BITS, false>, ctas, (part.vecs + 7) / 8, p.split,
         kWarps * S::RING + static_cast<size_t>(x_bytes(std::min<int64_t>(part.vecs, 8))), s, part, log2b,
         p.wk, p.split, Codes<TT, BITS>::kMasks);
     if (e != cudaSuccess) return e;
@@ -680,22 +736,9 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, MvPlan p, cudaStream_
   return cudaSuccess;
 }
 
-// A CTA lays x out for all its tiles, so more tiles and fewer warps a row where that is much
-// work or the rows are short (9000 x 20016, 16 vectors: 1 / 4 warps 161 / 221 us; 50001 x 1003, 9
-// stages a row: 1 / 2 / 4 warps 18.2 / 16.4 / 17.9 us; 30000 x 6001: 2 / 4 / 8 warps 41.8 / 38.9 /
-// 41.0 us).
-template <int BITS>
-static MvPlan any_plan(const MatvecArgs& a) {
-  using S = AnyShape<BITS>;
-  const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;
-  const int stages = any_stages(a.cols, S::CH);
-  return mv_plan(groups * S::CH, stages, a.vecs > 8 ? 1 : stages < 16 ? 2 : 4);
-}
-
 template <typename TT>
 static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  return a.bits == 8 ? run_any<TT, 8>(a, log2b, any_plan<8>(a), s)
-                     : run_any<TT, 4>(a, log2b, any_plan<4>(a), s);
+  return a.bits == 8 ? run_any<TT, 8>(a, log2b, s) : run_any<TT, 4>(a, log2b, s);
 }
 
 template <typename TT, int BITS, int SP, int MT, int NV, int NT>

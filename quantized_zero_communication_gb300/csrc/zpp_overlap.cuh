@@ -38,6 +38,20 @@ __device__ __forceinline__ uint4 ld_after_shared_v4(const void* p) {
                : "memory");
   return r;
 }
+// Predicated, without a branch: r keeps its value where not `on`.
+__device__ __forceinline__ void ld_after_shared_v4_if(bool on, const void* p, uint4& r) {
+  asm volatile(
+      "{.reg .pred q; setp.ne.b32 q, %5, 0; @q ld.global.v4.b32 {%0,%1,%2,%3}, [%4];}"
+      : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+      : "l"(p), "r"(static_cast<int>(on))
+      : "memory");
+}
+__device__ __forceinline__ void ld_after_shared_v2_if(bool on, const void* p, uint4& r) {
+  asm volatile("{.reg .pred q; setp.ne.b32 q, %3, 0; @q ld.global.v2.b32 {%0,%1}, [%2];}"
+               : "+r"(r.x), "+r"(r.y)
+               : "l"(p), "r"(static_cast<int>(on))
+               : "memory");
+}
 __device__ __forceinline__ float ld_after_f32(const float* p) {
   float r;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p) : "memory");

@@ -274,3 +274,35 @@ def test_infinite_scale_of_a_rows_last_block_gives_infinity(bits, block, segment
     want = torch.full((vecs, rows), float(cols), device=DEV)
     want[:, 7] = want[:, 20] = float("inf")
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("rows, cols", [(1, 8), (3, 24), (33, 40), (1027, 136), (515, 1032), (64, 8200),
+                                        (2, 800_008)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("vecs", [1, 8, 13])
+def test_exact_rows_that_start_at_words(rows, cols, bits, vecs):
+    check_exact(rows, cols, 64, bits, vecs, torch.bfloat16, seed=rows + vecs)
+    check_exact(rows, cols - cols % 8 + 4, 2048, bits, vecs, torch.float16, seed=rows + vecs, bias=True)
+
+
+def test_words_with_strides_of_x():
+    """The width allows whole words, the stride of x does or does not."""
+    rows, cols, g = 100, 1000, gen(21)
+    codes = random_codes(rows * cols, 4, g)
+    scales = torch.exp2(torch.randint(-1, 2, (-(-rows * cols // 128),), generator=g, device=DEV).float())
+    want = weights(codes, scales, rows, cols, 128, 4)
+    for stride in (1000, 1001, 1004, 1008):
+        x = torch.randint(-3, 4, (5, stride), generator=g, device=DEV).half()[:, :cols]
+        y = zpp.matvec_blockwise(codes, scales, x, rows, 128, 4, dtype=torch.float32)
+        assert torch.equal(y.double(), x.double() @ want.T)
+
+
+def test_stale_shared_memory_stays_out():
+    """Chunks past a row's end meet what an earlier call left in shared memory: infinite scales."""
+    g = gen(22)
+    big = 4096 * 1000
+    codes = random_codes(big, 4, g)
+    x = torch.ones(3, 1000, device=DEV).half()
+    zpp.matvec_blockwise(codes, torch.full((big // 64,), float("inf"), device=DEV), x, 4096, 64, 4)
+    for cols in (40, 72, 1000, 1003):
+        check_exact(600, cols, 64, 4, 3, torch.float16, seed=cols)
