@@ -125,8 +125,8 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
 #undef ZPP_MMA
 
 // ---------------------------------------------------------------------------------
-// The kernel for cols a multiple of block. A segment is the columns that 16 code bytes per
-// lane cover: 128 of INT4, 64 of INT8. In a segment lane (g, t) (g = lane / 4, t = lane % 4)
+// The kernel for cols a multiple of a segment, the columns that 16 code bytes per lane cover: 128
+// of INT4, 64 of INT8 (so that a segment lies in one block, or is two of 64). In a segment lane (g, t) (g = lane / 4, t = lane % 4)
 // holds a quarter, the columns from t SEG / 4 on, of the rows g and g + 8 of each 16-row
 // fragment, and the same columns of the vector in column g of the other operand: the order of
 // the columns inside a matrix product is free as long as both operands agree.
@@ -187,13 +187,15 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
   // Rows past the end read the last one, vectors past the end the last one: not stored.
   const uint8_t* codes[MT][2];
   const float* scale[MT][2];
+  unsigned in_block[MT][2];  // where in its block a row begins (blocks of 64, SP = 2: at 0)
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t r = min(row0 + 16 * m + 8 * h + g, a.rows - 1);
       codes[m][h] = a.codes + r * (a.cols * BITS / 8) + static_cast<int64_t>(unit0) * (UNIT * 64) + t * 16;
-      scale[m][h] = a.scales + r * (a.cols >> log2b);
+      scale[m][h] = a.scales + (r * a.cols >> log2b);
+      in_block[m][h] = static_cast<unsigned>(r * a.cols) & ((1u << log2b) - 1);
     }
   // Column g of set i: vector, and which segment of its group and half of it.
   const uint16_t* x[T];
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
             for (int e = 0; e < (NV == 1 ? 2 : 1); ++e) {
               const int slot = NS > 8 ? i % SP : (2 * t + e) / NV;
               const int at = seg0 + u0 + (NS > 8 ? 0 : slot / SP);
-              const int64_t col = static_cast<int64_t>(at) * SEG + slot % SP * 64;
+              const unsigned col = static_cast<unsigned>(at) * SEG + slot % SP * 64 + (SP == 1 ? in_block[m][h] : 0u);
               // beyond the row 0, not another block's scale: that may be infinite
               sc[m][h][i][e] = at < segs ? ld_after_f32(scale[m][h] + (col >> log2b)) : 0.0f;
               if (NV > 1) sc[m][h][i][1] = sc[m][h][i][0];
@@ -771,7 +773,7 @@ static cudaError_t by_vecs(const MatvecArgs& a, int log2b, cudaStream_t s) {
 
 template <typename TT>
 static cudaError_t launch_type(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  if (a.cols % a.block != 0 || a.cols % (a.bits == 8 ? 64 : 128) != 0 || a.x_stride % 8 != 0)
+  if (a.cols % (a.bits == 8 ? 64 : 128) != 0 || a.x_stride % 8 != 0)
     return launch_any<TT>(a, log2b, s);
   if (a.bits == 8) return by_vecs<TT, 8, 1>(a, log2b, s);
   return a.block == 64 ? by_vecs<TT, 4, 2>(a, log2b, s) : by_vecs<TT, 4, 1>(a, log2b, s);

@@ -306,3 +306,11 @@ def test_stale_shared_memory_stays_out():
     zpp.matvec_blockwise(codes, torch.full((big // 64,), float("inf"), device=DEV), x, 4096, 64, 4)
     for cols in (40, 72, 1000, 1003):
         check_exact(600, cols, 64, 4, 3, torch.float16, seed=cols)
+
+
+@pytest.mark.parametrize("rows, cols", [(5, 128), (70, 384), (600, 1280), (33, 8320)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("block", [64, 256, 512, 2048, 4096])
+def test_exact_whole_segments_in_blocks_across_rows(rows, cols, bits, block):
+    for vecs in (1, 2, 3, 8, 17):
+        check_exact(rows, cols, block, bits, vecs, torch.bfloat16, seed=rows + vecs)
