@@ -373,12 +373,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
   grid_wait();  // everything before this launch is done and visible
   const float c = a.grad_scale ? *static_cast<const volatile float*>(a.grad_scale) : 1.0f;
   if (!isfinite(c)) return;  // overflowed gradients: the step is skipped
-  int lo = 0, hi = tab.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tab.first[mid] <= static_cast<int>(blockIdx.x)) lo = mid;
-    else hi = mid;
-  }
+  const int lo = tensor_of(tab.hints, tab.first, static_cast<int>(blockIdx.x));
   const AdamwTensor& t = tab.t[lo];
   const int lane = threadIdx.x & 31;
   constexpr int NB = adamw_warp_blocks(FP8 ? 8 : 32);
@@ -406,14 +401,15 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
 }
 
 template <int CAP>
-static cudaError_t run_adamw(const AdamwTableOf<CAP>& tab, int state_bits, bool v8, cudaStream_t s) {
+static cudaError_t run_adamw(AdamwTableOf<CAP>& tab, int state_bits, bool v8, cudaStream_t s) {
   const int grid = tab.first[tab.count];
+  tab.hints.fill(tab.first, tab.count);
   auto kern = state_bits == 8 ? (v8 ? k_adamw<true, true, CAP> : k_adamw<true, false, CAP>)
                               : (v8 ? k_adamw<false, true, CAP> : k_adamw<false, false, CAP>);
   return launch_overlapped(kern, grid, kThreads, s, tab);
 }
 
-cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s) {
+cudaError_t launch_adamw(AdamwTable& tab, int state_bits, cudaStream_t s) {
   uintptr_t bits = 0;
   for (int i = 0; i < tab.count; ++i) {
     const AdamwTensor& t = tab.t[i];

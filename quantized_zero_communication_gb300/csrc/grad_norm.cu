@@ -42,12 +42,7 @@ __global__ void __launch_bounds__(kThreads)
     k_norm_partial(const __grid_constant__ NormTableOf<CAP> tab, float* __restrict__ partial) {
   grid_wait();
   grid_release();
-  int lo = 0, hi = tab.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tab.first[mid] <= static_cast<int>(blockIdx.x)) lo = mid;
-    else hi = mid;
-  }
+  const int lo = tensor_of(tab.hints, tab.first, static_cast<int>(blockIdx.x));
   const int64_t begin = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kNormChunk;
   const int64_t left = tab.n[lo] - begin;
   float sum = 0.0f;
@@ -128,15 +123,16 @@ __global__ void __launch_bounds__(1024) k_norm_finish(const float* __restrict__ 
 }
 
 template <int CAP>
-static cudaError_t run_partial(const NormTableOf<CAP>& tab, int g_kind, bool v8, float* workspace,
+static cudaError_t run_partial(NormTableOf<CAP>& tab, int g_kind, bool v8, float* workspace,
                                cudaStream_t s) {
   auto kern = g_kind == 2   ? (v8 ? k_norm_partial<2, true, CAP> : k_norm_partial<2, false, CAP>)
               : g_kind == 1 ? (v8 ? k_norm_partial<1, true, CAP> : k_norm_partial<1, false, CAP>)
                             : (v8 ? k_norm_partial<0, true, CAP> : k_norm_partial<0, false, CAP>);
+  tab.hints.fill(tab.first, tab.count);
   return launch_overlapped(kern, tab.first[tab.count], kThreads, s, tab, workspace);
 }
 
-cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
+cudaError_t launch_grad_norm(NormTable& tab, int g_kind, float pre_scale, float max_norm,
                              float* workspace, float* out, cudaStream_t s) {
   const int chunks = tab.first[tab.count];
   if (chunks > 0) {

@@ -74,6 +74,35 @@ cudaError_t launch_wait_selftest(unsigned long long limit_ns, cudaStream_t s);
 // K6: 256-bit device copy (the same-run HBM reference).
 cudaError_t launch_copy(const void* src, void* dst, int64_t bytes, cudaStream_t s);
 
+// Which tensor of a list a CTA belongs to: the tensors of a launch have first[0] .. first[count]
+// CTAs before them, and every 2^shift-th CTA's tensor is written down, so that a CTA searches a
+// few entries (from kernel parameters, each step a dependent load) and not all.
+struct ChunkHints {
+  static constexpr int kBuckets = 64;
+  int32_t shift;
+  uint16_t at[kBuckets + 1];
+  void fill(const int32_t* first, int count) {  // count >= 1
+    const int32_t grid = first[count];
+    for (shift = 0; (grid - 1) >> shift >= kBuckets;) ++shift;
+    int t = 0;
+    for (int b = 0; b <= kBuckets; ++b) {
+      while (t + 1 < count && first[t + 1] <= static_cast<int64_t>(b) << shift) ++t;
+      at[b] = static_cast<uint16_t>(t);
+    }
+  }
+};
+#ifdef __CUDACC__
+__device__ __forceinline__ int tensor_of(const ChunkHints& hints, const int32_t* first, int cta) {
+  int lo = hints.at[cta >> hints.shift], hi = hints.at[(cta >> hints.shift) + 1] + 1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= cta) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+#endif
+
 // K7: sums of squares over a list of tensors (one partial per CTA into `workspace`), then
 // norm and clip factor. The list travels in the kernel's parameter space.
 constexpr int kNormChunk = 16384;  // elements per CTA
@@ -83,13 +112,14 @@ struct NormTableOf {
   int64_t n[CAP];
   int32_t first[CAP + 1];  // CTAs of the tensors before this one
   int32_t count;
+  ChunkHints hints;
 };
 using NormTable = NormTableOf<kMaxTensors>;
 // A launch's parameters are copied by the driver: up to this many tensors travel in a small
 // table (a call with one tensor costs the host 3 us less than with the full one).
 constexpr int kFewTensors = 16;
 inline int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
-cudaError_t launch_grad_norm(const NormTable& tab, int g_kind, float pre_scale, float max_norm,
+cudaError_t launch_grad_norm(NormTable& tab, int g_kind, float pre_scale, float max_norm,
                              float* workspace, float* out, cudaStream_t s);
 
 // K8: one AdamW step over a list of tensors; at most kAdamwTensors per launch (their
@@ -121,6 +151,7 @@ struct AdamwTableOf {
   int32_t first[CAP + 1];  // chunks of the tensors before this one
   int32_t block0[CAP];     // state blocks of the tensors before this one
   int32_t count;
+  ChunkHints hints;
   int64_t first_block;     // state blocks of the tensors of earlier launches
   AdamwArgs a;
 };
@@ -133,7 +164,7 @@ constexpr int adamw_chunk(int state_bits) {  // elements per CTA of 8 warps
 inline int64_t adamw_chunks(int64_t n, int state_bits) {
   return (n + adamw_chunk(state_bits) - 1) / adamw_chunk(state_bits);
 }
-cudaError_t launch_adamw(const AdamwTable& tab, int state_bits, cudaStream_t s);
+cudaError_t launch_adamw(AdamwTable& tab, int state_bits, cudaStream_t s);
 
 // K9: y = x W^T (+ bias) from block-quantised codes. x_bf16: x and bias are bf16, else fp16;
 // y_kind as a zpp_dtype.
