@@ -14,7 +14,7 @@
 // TB/s over 28 bytes each. 8-bit states (16.06 bytes) are bound by instruction issue, some 80 per
 // element: 268,435,456 elements 680 us, 6.34 TB/s, issue slots 79 % busy; a warp takes two blocks
 // there so that the loads of one cover the arithmetic of the other. A short list is bound by the
-// launch: 1024 elements 9 us, most of it on the host.
+// call: 1024 elements 6.3 us, 1.8 of them on the device.
 #include <cuda_fp8.h>
 
 #include "zpp_device.cuh"

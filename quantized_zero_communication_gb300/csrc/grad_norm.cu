@@ -8,7 +8,7 @@
 // partial, a single CTA adds the partials (in fp64) in a fixed order, so that the norm is the
 // same in every run. Bound by DRAM: 536,870,912 bf16 elements 163 us, 6.6 TB/s; 32 registers
 // leave room for 8 CTAs per SM, whose loads are all in flight at once. A short list is bound by
-// its two launches: 40 tensors, 1,000,003 fp32 elements, 6.3 us on the device.
+// its two launches: one of 1024 elements 4.1 us on the device.
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
 #include "zpp_overlap.cuh"

@@ -10,7 +10,7 @@
 //
 // Measured (us; bytes at 6.78 TB/s in brackets): 24576 x 8192 INT4, one vector 24 (15.8); 8192 x
 // 32768 INT4, 8 vectors 39 (20.4); 8192 x 8192 INT8 12.6 (9.9); 50001 x 1003 INT4, 3 vectors, rows
-// that start inside blocks 15.9 (4.2); 1024 x 1024 4, which is the launch. Loads alone, in this
+// that start inside words 15.7 (4.3); 1024 x 1024 4, which is the launch. Loads alone, in this
 // pattern, take 17 us for the first: the rest is the chain of each warp from shared memory through
 // the conversion to the matrix unit, of which registers let only four run per scheduler.
 #include <cooperative_groups.h>

@@ -4,7 +4,7 @@
 // (60 us for 150 tensors, more than the step itself takes on the GPU), here some 10 ns. And a
 // product for one token takes the GPU 4 us: its wrapper's common case (plain contiguous
 // tensors, a new output) is one call here too, 14 us of host time otherwise. The norm of 40
-// gradients takes it 6 us, and 22 us through Python.
+// small gradients takes 8 us as one call, 22 through Python.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
