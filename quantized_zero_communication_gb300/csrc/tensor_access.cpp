@@ -235,20 +235,18 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     std::vector<const void*> at(count);
     std::vector<int64_t> counts(count);
-    long kind = -1, device = -1;
     int64_t total = 0;
-    for (Py_ssize_t i = 0; i < count; ++i) {
-      PyObject* o = PyList_GET_ITEM(args[2], i);
-      if (!plain(o)) Py_RETURN_NONE;
-      const at::Tensor& t = THPVariable_Unpack(o);
-      if (i == 0) kind = kind_of(t), device = gpu_of(t);
-      if (kind < 0 || kind > ZPP_F32 || device < 0 || kind_of(t) != kind || gpu_of(t) != device ||
-          !t.is_contiguous())
-        Py_RETURN_NONE;
-      at[i] = reinterpret_cast<const void*>(address_of(t));
-      counts[i] = t.numel();
-      total += counts[i];
+    Seen seen;
+    if (!look(args[2], seen, [&](Py_ssize_t i, const at::Tensor& t) {
+          at[i] = reinterpret_cast<const void*>(address_of(t));
+          counts[i] = t.numel();
+          total += counts[i];
+        })) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
     }
+    const long kind = seen.kind, device = seen.place();
+    if (kind < 0 || kind > ZPP_F32 || device < 0) Py_RETURN_NONE;
     const int64_t floats = reinterpret_cast<decltype(&zpp_grad_norm_workspace)>(workspace)(
         total, static_cast<int32_t>(count));
     if (floats < 0) Py_RETURN_NONE;
