@@ -379,9 +379,8 @@ ZPP_API zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_t
  *   rows, cols    : 0 <= rows < 2^31, 1 <= cols < 2^31; block, bits as in zpp_quant_blockwise
  *   x             : [vecs] rows of cols elements of x_dt (ZPP_F16 or ZPP_BF16; ZPP_F32 ->
  *                   ZPP_ERR_UNSUPPORTED), row j at x + j * x_stride, x_stride >= cols
- *   vecs          : 0 .. 65535. Meant for a handful (decoding): the codes are read once for 16 vectors
- *                   (8 where cols is not a multiple of 128 INT4 / 64 INT8 codes, or
- *                   x_stride not of 8), so for many vectors dequantise and use a matrix product
+ *   vecs          : 0 .. 65535. Meant for a handful (decoding): the codes are read once for 16 vectors,
+ *                   so for many vectors dequantise and use a matrix product
  *   bias          : NULL or [rows] of x_dt
  *   y             : out, row j at y + j * y_stride, y_stride >= rows, of y_dt (any zpp_dtype)
  * x and y must be 16-byte aligned, bias 2-byte; the strides (in elements) may be any.

@@ -394,9 +394,10 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
 // multiples of 8 INT4, 4 INT8 columns) a lane reads its words of x where they are; else x is laid
 // out in shared memory, shifted, as fragments, by each CTA, which costs more than the products from
 // four vectors on. (24576 x 8224 INT4, 1 / 8 vectors: in place 43 / 45 us, laid out 40 / 98; 2861 x
-// 20896: 22 / 23 and 22 / 62; 5120 x 1280 INT8: 6.3 / 6.6 and 6.6 / 11.) Blocks begin
-// at other columns in every row, so a product covers one chunk and is scaled per row and chunk;
-// lane (g, t) takes word t of the chunks of rows g and g + 8.
+// 20896: 22 / 23 and 22 / 62; 5120 x 1288 INT8: 6.5 / 6.7 and 6.6 / 11.) Blocks begin at other
+// columns in every row, so a product covers one chunk and is scaled per row and chunk; lane (g, t)
+// takes word t of the chunks of rows g and g + 8. Two sets of 8 vectors share the codes where there
+// are more than 8 (NT = 2: 24576 x 8224, 16 vectors 61 us from 79).
 //
 // A stage is four chunks of a warp's 16 rows; a lane copies chunk t of its two rows, and its
 // scales, but reads word t of all four (the copies are swapped so that this is free of bank
@@ -421,8 +422,8 @@ __host__ __device__ inline int any_share(int64_t cols, int ch, int wk, int split
   return (any_stages(cols, ch) + step - 1) / step * wk;
 }
 
-template <typename TT, int BITS, bool WORDS>
-__global__ void __launch_bounds__(kThreads, 4)
+template <typename TT, int BITS, bool WORDS, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     k_matvec_any(const MatvecArgs a, int log2b, int wk, int split, const Masks masks) {
   using S = AnyShape<BITS>;
   constexpr int CH = S::CH;
@@ -436,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int rho = cta % CH;
   const int64_t tile = static_cast<int64_t>(cta / CH) * wr + (warp >> log2wk);
   const int64_t row0 = rho + tile * (16 * CH);
-  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * 8;
-  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(8)));
+  const int64_t vec0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
+  const int vecs = static_cast<int>(min(a.vecs - vec0, static_cast<int64_t>(8 * NT)));
   const unsigned cols = static_cast<unsigned>(a.cols);  // less than 2^31
   const int shift = static_cast<int>(rho * a.cols % CH);
   const int chunks = static_cast<int>((a.cols + shift + CH - 1) / CH), stages = (chunks + 3) / 4;
@@ -521,25 +522,33 @@ __global__ void __launch_bounds__(kThreads, 4)
   int word[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) word[c] = (c ^ ((g >> 1) & 3)) * 16;
-  const uint8_t* xs = frag + (warp & (wk - 1)) * (16 * vecs * S::XB) + (min(g, vecs - 1) * 4 + t) * S::XB;
-  const bool has_x = g < vecs;
+  const uint8_t* xs[NT];
+  const uint16_t* xg[NT];
   unsigned col = first * 4 * CH + t * S::WC - shift;
-  const uint16_t* xg = a.x + (vec0 + min(g, vecs - 1)) * a.x_stride + static_cast<int>(col);
+#pragma unroll
+  for (int k = 0; k < NT; ++k) {
+    const int v = min(8 * k + g, vecs - 1);
+    xs[k] = frag + (warp & (wk - 1)) * (16 * vecs * S::XB) + (v * 4 + t) * S::XB;
+    xg[k] = a.x + (vec0 + v) * a.x_stride + static_cast<int>(col);
+  }
 
-  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float y[NT][4] = {};
   int slot = 0;
   for (int stage = first; stage < stages; stage += step) {
-    uint4 xw[4];
+    uint4 xw[NT][4];
     if constexpr (WORDS) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool on = has_x && col + c * CH < cols;
-        xw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (BITS == 4) ld_after_shared_v4_if(on, xg + c * CH, xw[c]);
-        else ld_after_shared_v2_if(on, xg + c * CH, xw[c]);
+      for (int k = 0; k < NT; ++k) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool on = 8 * k + g < vecs && col + c * CH < cols;
+          xw[k][c] = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (BITS == 4) ld_after_shared_v4_if(on, xg[k] + c * CH, xw[k][c]);
+          else ld_after_shared_v2_if(on, xg[k] + c * CH, xw[k][c]);
+        }
+        xg[k] += step * 4 * CH;
       }
       col += step * 4 * CH;
-      xg += step * 4 * CH;
     }
     cp_async_wait<S::DEPTH - 2>();
     __syncwarp();  // all lanes' copies of this stage have landed, the one before is free
@@ -552,48 +561,57 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint32_t q[2][S::PW], b[S::PW];
+      uint32_t q[2][S::PW];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         Codes<TT, BITS>::pairs(*reinterpret_cast<const uint32_t*>(mine + slot + word[c] + h * 512), masks, q[h]);
-      if constexpr (!WORDS) {
-        if constexpr (BITS == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(xs + c * (vecs * 4 * S::XB));
-          b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        uint32_t b[S::PW];
+        const uint4& w = xw[k][c];
+        if constexpr (!WORDS) {
+          if constexpr (BITS == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xs[k] + c * (vecs * 4 * S::XB));
+            b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(xs[k] + c * (vecs * 4 * S::XB));
+            b[0] = v.x, b[1] = v.y;
+          }
+        } else if constexpr (BITS == 4) {
+          b[0] = __byte_perm(w.x, w.z, 0x5410u), b[1] = __byte_perm(w.x, w.z, 0x7632u);
+          b[2] = __byte_perm(w.y, w.w, 0x5410u), b[3] = __byte_perm(w.y, w.w, 0x7632u);
         } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(xs + c * (vecs * 4 * S::XB));
-          b[0] = v.x, b[1] = v.y;
+          b[0] = __byte_perm(w.x, w.y, 0x5410u), b[1] = __byte_perm(w.x, w.y, 0x7632u);
         }
-      } else if constexpr (BITS == 4) {
-        b[0] = __byte_perm(xw[c].x, xw[c].z, 0x5410u), b[1] = __byte_perm(xw[c].x, xw[c].z, 0x7632u);
-        b[2] = __byte_perm(xw[c].y, xw[c].w, 0x5410u), b[3] = __byte_perm(xw[c].y, xw[c].w, 0x7632u);
-      } else {
-        b[0] = __byte_perm(xw[c].x, xw[c].y, 0x5410u), b[1] = __byte_perm(xw[c].x, xw[c].y, 0x7632u);
-      }
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p < S::PW; p += 2) {
-        const uint32_t f[4] = {q[0][p], q[1][p], q[0][p + 1], q[1][p + 1]};
-        mma16816(d, f, b[p], b[p + 1], d, TT());
-      }
+        for (int p = 0; p < S::PW; p += 2) {
+          const uint32_t f[4] = {q[0][p], q[1][p], q[0][p + 1], q[1][p + 1]};
+          mma16816(d, f, b[p], b[p + 1], d, TT());
+        }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = __fmaf_rn(d[k], sc[k >> 1][c], y[k]);
+        for (int e = 0; e < 4; ++e) y[k][e] = __fmaf_rn(d[e], sc[e >> 1][c], y[k][e]);
+      }
     }
-    xs += wk * (16 * vecs * S::XB);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) xs[k] += wk * (16 * vecs * S::XB);
     slot = slot == (S::DEPTH - 1) * S::STAGE ? 0 : slot + S::STAGE;
   }
 
   cp_async_wait<0>();
   __syncwarp();
-  constexpr int STRIDE = S::RING / 4;
-  float* part = reinterpret_cast<float*>(smem);  // a warp's [8][16] sums over its ring
+  constexpr int STRIDE = S::RING / 4, OUTS = 128 * NT;
+  static_assert(OUTS <= STRIDE, "the sums fit into the ring");
+  float* part = reinterpret_cast<float*>(smem);  // a warp's [8 NT][16] sums over its ring
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    part[warp * STRIDE + (2 * t + (k & 1)) * 16 + 8 * (k >> 1) + g] = y[k];
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      part[warp * STRIDE + (8 * n + 2 * t + (k & 1)) * 16 + 8 * (k >> 1) + g] = y[n][k];
   __syncthreads();
-  const int outs = wr * 128;
+  const int outs = wr * OUTS;
   for (int o = threadIdx.x; o < outs; o += kThreads) {
-    float* p = part + o / 128 * wk * STRIDE + o % 128;
+    float* p = part + o / OUTS * wk * STRIDE + o % OUTS;
     float sum = *p;
     for (int k = 1; k < wk; ++k) sum += p[k * STRIDE];
     *p = sum;  // read and written by this thread only
@@ -601,9 +619,9 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (split > 1) cg::this_cluster().sync();
   if (rank == 0) {
     for (int o = threadIdx.x; o < outs; o += kThreads) {
-      const int from = o / 128 * wk * STRIDE + o % 128, v = o % 128 / 16;
+      const int from = o / OUTS * wk * STRIDE + o % OUTS, v = o % OUTS / 16;
       const int64_t r =
-          rho + ((static_cast<int64_t>(cta / CH) * wr + o / 128) * 16 + o % 16) * CH;
+          rho + ((static_cast<int64_t>(cta / CH) * wr + o / OUTS) * 16 + o % 16) * CH;
       float sum = part[from];
       for (int k = 1; k < split; ++k) sum += cg::this_cluster().map_shared_rank(part, k)[from];
       if (r < a.rows && v < vecs) {
@@ -687,35 +705,43 @@ static cudaError_t run_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cuda
 // SM have work, never more than units. (8192 x 8192 INT4, one vector, base 4: 2 / 4 / 8 warps
 // 15.4 / 12.3 / 14.7 us; 1024 x 16384, 8 warps: 1 / 2 / 4 CTAs 9.4 / 8.2 / 10.2 us; 32768 x 1024,
 // one unit a row: 1 / 2 warps 8.2 / 10.3 us.)
-static MvPlan mv_plan(int64_t tiles, int64_t units, int base) {
+static MvPlan mv_plan(int64_t tiles, int64_t units, int base, bool ctas_first = false) {
   MvPlan p{1, 1};
   constexpr int64_t kBusy = 2000;
-  while (p.wk < kWarps && 2 * p.wk <= units && (p.wk < base || tiles * p.wk < kBusy)) p.wk *= 2;
-  while (p.split < 8 && 2 * p.split * p.wk <= units && tiles * p.wk * p.split < kBusy) p.split *= 2;
+  const auto idle = [&] { return 2 * p.split * p.wk <= units && tiles * p.wk * p.split < kBusy; };
+  while (p.wk < base && 2 * p.wk <= units) p.wk *= 2;
+  if (ctas_first)
+    while (p.split < 8 && idle()) p.split *= 2;
+  while (p.wk < kWarps && idle()) p.wk *= 2;
+  while (p.split < 8 && idle()) p.split *= 2;
   return p;
 }
 
-template <typename TT, int BITS>
+template <typename TT, int BITS, int NT>
 static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
   using S = AnyShape<BITS>;
   const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;  // tiles of one shift
   const bool words = a.cols % S::WC == 0 && a.x_stride % S::WC == 0;
-  // Where a CTA lays x out it does so for all its tiles, so more tiles and fewer warps a row where
-  // that is much work; fewer warps too where rows are short. (9000 x 20015, 16 vectors: 1 / 4 warps
-  // 161 / 221 us; 50001 x 1003, 9 stages a row: 1 / 2 / 4 warps 18.2 / 16.4 / 17.9 us; 30000 x 6001:
-  // 2 / 4 / 8 warps 41.8 / 38.9 / 41.0 us; taken some steps before the times above.)
+  // A CTA that lays x out does so for all its tiles: with four vectors or more fewer warps share a
+  // row, so that a CTA has more tiles, and CTAs come before warps. (30000 x 6001, 8 vectors: 1 / 2 /
+  // 4 warps 54 / 65 / 90 us; 2861 x 20897, 8 vectors: CTAs first 39, warps first 66; but 4 vectors of
+  // the first 54 / 47 / 56, and one vector, with an earlier kernel, 2 / 4 / 8 warps 41.8 / 38.9 / 41.0;
+  // and 5121 x 1283 INT8, 13 vectors, CTAs first 14.7, warps first 12.8.) Short rows: 50001 x 1003, 9
+  // stages a row, 4 vectors 1 / 2 warps 17.8 / 17.0 us, 13 vectors 20.8 / 26.7.
   const int stages = any_stages(a.cols, S::CH);
-  MvPlan p = mv_plan(groups * S::CH, stages, !words && a.vecs > 8 ? 1 : stages < 16 ? 2 : 4);
+  const bool lay_out = !words && a.vecs > 3;
+  const int base = stages < 16 ? (!words && a.vecs > 8 ? 1 : 2) : !lay_out ? 4 : a.vecs > 4 ? 1 : 2;
+  MvPlan p = mv_plan(groups * S::CH, stages, base, lay_out && stages >= 16);
   const int wr = kWarps / p.wk;
   const int64_t ctas = (groups + wr - 1) / wr * S::CH;
   if (words)
-    return launch_split(k_matvec_any<TT, BITS, true>, ctas, (a.vecs + 7) / 8, p.split, kWarps * S::RING, s, a,
+    return launch_split(k_matvec_any<TT, BITS, true, NT>, ctas, (a.vecs + 8 * NT - 1) / (8 * NT), p.split, kWarps * S::RING, s, a,
                         log2b, p.wk, p.split, Codes<TT, BITS>::kMasks);
   // x of a CTA's share lies in shared memory: more CTAs along a row, then fewer vectors at a time
   const auto x_bytes = [&](int64_t vecs) {
     return static_cast<int64_t>(any_share(a.cols, S::CH, p.wk, p.split)) * 16 * vecs * S::XB;
   };
-  int64_t vecs = a.vecs < 8 ? a.vecs : 8;
+  int64_t vecs = a.vecs < 8 * NT ? a.vecs : 8 * NT;
   while (p.split < 8 && x_bytes(vecs) > kAnyX) p.split *= 2;
   while (vecs > 1 && x_bytes(vecs) > kAnyMaxX) vecs /= 2;
   if (x_bytes(vecs) > kAnyMaxX) {
@@ -723,15 +749,15 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
     k_matvec_long<TT><<<grid, kThreads, 0, s>>>(a, log2b);
     return cudaGetLastError();
   }
-  const int64_t at_once = vecs < 8 ? vecs : a.vecs;  // of one launch
+  const int64_t at_once = vecs < 8 * NT ? vecs : a.vecs;  // of one launch
   for (int64_t v = 0; v < a.vecs; v += at_once) {
     MatvecArgs part = a;
     part.x = a.x + v * a.x_stride;
     part.y = static_cast<uint8_t*>(a.y) + v * a.y_stride * (a.y_kind == 2 ? 4 : 2);
     part.vecs = std::min(at_once, a.vecs - v);
     const cudaError_t e = launch_split(
-        k_matvec_any<TT, BITS, false>, ctas, (part.vecs + 7) / 8, p.split,
-        kWarps * S::RING + static_cast<size_t>(x_bytes(std::min<int64_t>(part.vecs, 8))), s, part, log2b,
+        k_matvec_any<TT, BITS, false, NT>, ctas, (part.vecs + 8 * NT - 1) / (8 * NT), p.split,
+        kWarps * S::RING + static_cast<size_t>(x_bytes(std::min<int64_t>(part.vecs, 8 * NT))), s, part, log2b,
         p.wk, p.split, Codes<TT, BITS>::kMasks);
     if (e != cudaSuccess) return e;
   }
@@ -740,7 +766,8 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
 
 template <typename TT>
 static cudaError_t launch_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
-  return a.bits == 8 ? run_any<TT, 8>(a, log2b, s) : run_any<TT, 4>(a, log2b, s);
+  if (a.vecs > 8) return a.bits == 8 ? run_any<TT, 8, 2>(a, log2b, s) : run_any<TT, 4, 2>(a, log2b, s);
+  return a.bits == 8 ? run_any<TT, 8, 1>(a, log2b, s) : run_any<TT, 4, 1>(a, log2b, s);
 }
 
 template <typename TT, int BITS, int SP, int MT, int NV, int NT>
