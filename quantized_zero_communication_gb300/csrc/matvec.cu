@@ -126,10 +126,10 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
 
 // ---------------------------------------------------------------------------------
 // The kernel for cols a multiple of a segment, the columns that 16 code bytes per lane cover: 128
-// of INT4, 64 of INT8 (so that a segment lies in one block, or is two of 64). In a segment lane (g, t) (g = lane / 4, t = lane % 4)
-// holds a quarter, the columns from t SEG / 4 on, of the rows g and g + 8 of each 16-row
-// fragment, and the same columns of the vector in column g of the other operand: the order of
-// the columns inside a matrix product is free as long as both operands agree.
+// of INT4, 64 of INT8 (so that a segment lies in one block, or is two of 64). In a segment lane (g,
+// t) (g = lane / 4, t = lane % 4) holds a quarter, the columns from t SEG / 4 on, of the rows g and
+// g + 8 of each 16-row fragment, and the same columns of the vector in column g of the other
+// operand: the order of the columns inside a matrix product is free as long as both operands agree.
 //
 // The other operand has 8 columns. With fewer vectors (NV = 1, 2, 4) its columns hold them for
 // 8 / NV segments at once, so that x costs no more registers, loads and permutations per
@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
             for (int e = 0; e < (NV == 1 ? 2 : 1); ++e) {
               const int slot = NS > 8 ? i % SP : (2 * t + e) / NV;
               const int at = seg0 + u0 + (NS > 8 ? 0 : slot / SP);
-              const unsigned col = static_cast<unsigned>(at) * SEG + slot % SP * 64 + (SP == 1 ? in_block[m][h] : 0u);
+              const unsigned col =
+                  static_cast<unsigned>(at) * SEG + slot % SP * 64 + (SP == 1 ? in_block[m][h] : 0u);
               // beyond the row 0, not another block's scale: that may be infinite
               sc[m][h][i][e] = at < segs ? ld_after_f32(scale[m][h] + (col >> log2b)) : 0.0f;
               if (NV > 1) sc[m][h][i][1] = sc[m][h][i][0];
@@ -432,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   const int g = lane >> 2, t = lane & 3;
   const int log2wk = __popc(wk - 1), log2split = __popc(split - 1);  // both powers of two
   const int rank = static_cast<int>(blockIdx.x) & (split - 1);
-  const int cta = static_cast<int>(blockIdx.x) >> log2split, wr = kWarps >> log2wk;  // wr: row tiles of a CTA
+  const int cta = static_cast<int>(blockIdx.x) >> log2split;
+  const int wr = kWarps >> log2wk;  // row tiles of a CTA
   // Rows rho + CH i of this CTA, 16 i per tile.
   const int rho = cta % CH;
   const int64_t tile = static_cast<int64_t>(cta / CH) * wr + (warp >> log2wk);
@@ -556,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     float sc[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float4 v = *reinterpret_cast<const float4*>(smem + warp * S::RING + slot + 1024 + h * 128 + g * 16);
+      const float4 v = *reinterpret_cast<const float4*>(smem + warp * S::RING + slot + 1024 + h * 128 +
+                                                        g * 16);
       sc[h][0] = v.x, sc[h][1] = v.y, sc[h][2] = v.z, sc[h][3] = v.w;
     }
 #pragma unroll
@@ -564,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       uint32_t q[2][S::PW];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        Codes<TT, BITS>::pairs(*reinterpret_cast<const uint32_t*>(mine + slot + word[c] + h * 512), masks, q[h]);
+        Codes<TT, BITS>::pairs(*reinterpret_cast<const uint32_t*>(mine + slot + word[c] + h * 512), masks,
+                               q[h]);
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
         uint32_t b[S::PW];
@@ -735,8 +739,8 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
   const int wr = kWarps / p.wk;
   const int64_t ctas = (groups + wr - 1) / wr * S::CH;
   if (words)
-    return launch_split(k_matvec_any<TT, BITS, true, NT>, ctas, (a.vecs + 8 * NT - 1) / (8 * NT), p.split, kWarps * S::RING, s, a,
-                        log2b, p.wk, p.split, Codes<TT, BITS>::kMasks);
+    return launch_split(k_matvec_any<TT, BITS, true, NT>, ctas, (a.vecs + 8 * NT - 1) / (8 * NT), p.split,
+                        kWarps * S::RING, s, a, log2b, p.wk, p.split, Codes<TT, BITS>::kMasks);
   // x of a CTA's share lies in shared memory: more CTAs along a row, then fewer vectors at a time
   const auto x_bytes = [&](int64_t vecs) {
     return static_cast<int64_t>(any_share(a.cols, S::CH, p.wk, p.split)) * 16 * vecs * S::XB;
