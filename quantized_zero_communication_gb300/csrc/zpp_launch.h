@@ -123,8 +123,8 @@ cudaError_t launch_grad_norm(NormTable& tab, int g_kind, float pre_scale, float 
                              float* workspace, float* out, cudaStream_t s);
 
 // K8: one AdamW step over a list of tensors; at most kAdamwTensors per launch (their
-// descriptors travel in the kernel's parameter space, which holds 32,764 bytes).
-constexpr int kAdamwTensors = 448;
+// descriptors travel in the kernel's parameter space).
+constexpr int kAdamwTensors = 432;
 constexpr int kStateBlock = 256;   // = ZPP_STATE_BLOCK
 struct AdamwTensor {
   float* param;
@@ -147,16 +147,19 @@ struct AdamwArgs {
 };
 template <int CAP>
 struct AdamwTableOf {
-  AdamwTensor t[CAP];
+  AdamwArgs a;
+  int64_t first_block;     // state blocks of the tensors of earlier launches
+  ChunkHints hints;
+  int32_t count;
   int32_t first[CAP + 1];  // chunks of the tensors before this one
   int32_t block0[CAP];     // state blocks of the tensors before this one
-  int32_t count;
-  ChunkHints hints;
-  int64_t first_block;     // state blocks of the tensors of earlier launches
-  AdamwArgs a;
+  AdamwTensor t[CAP];
 };
 using AdamwTable = AdamwTableOf<kAdamwTensors>;
-static_assert(sizeof(AdamwTable) <= 32764, "kernel parameter space");
+// The parameter space is said to hold 32,764 bytes, but a build of k_adamw whose hints lay at its
+// byte 32,264 (behind 448 tensors, with fp32 states) found zeros there, and so the first tensor only.
+// So the table, with the 1 KB that precede the parameters, ends before 32 KB, the tensors last.
+static_assert(sizeof(AdamwTable) <= 31 * 1024, "kernel parameter space");
 constexpr int adamw_warp_blocks(int state_bits) { return state_bits == 8 ? 2 : 1; }
 constexpr int adamw_chunk(int state_bits) {  // elements per CTA of 8 warps
   return 8 * adamw_warp_blocks(state_bits) * kStateBlock;
