@@ -370,6 +370,42 @@ ZPP_API zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_t
                                   const zpp_adamw_params* hp, const float* grad_scale,
                                   cudaStream_t stream);
 
+/* A run's step count on the device, 16-byte aligned. The caller sets `step` (0 for a new run) and
+ * zeroes the rest, which zpp_adamw_step_counted keeps: the factors of the step in hand, and
+ * beta^step, so that the next step's power is one product. */
+typedef struct zpp_adamw_record {
+  int64_t step; /* number of the last step that was taken */
+  int64_t reserved;
+  float factor, step_size, inv_root_bc2;
+  uint32_t key;
+  double beta[2], power[2]; /* power[k] = beta[k]^step, for beta1 and beta2 */
+} zpp_adamw_record;
+
+/* Clipping by the norm of the step's own gradients, as zpp_grad_norm. */
+typedef struct zpp_adamw_clip {
+  float pre_scale, max_norm;
+  float* workspace; /* zpp_grad_norm_workspace(sum of n, num_tensors) floats */
+  float* out;       /* (norm, factor) */
+} zpp_adamw_clip;
+
+/*
+ * zpp_adamw_step, counted: a step that a non-finite factor skips has no number, so bias
+ * corrections and rounding bits go on from the last step that was taken. Nobody on the host
+ * needs to know which ones were, and a captured step is the next one each time it is replayed.
+ *   hp->step    : 0: this step is number record->step + 1 (nothing has to be in flight to it but
+ *                 work on `stream`); >= 1: its number, where the caller knows it
+ *   grad_scale  : as above; clip: NULL, or the factor comes from the norm of the gradients, left
+ *                 in clip->out (HOST struct, read during the call; then grad_scale is NULL)
+ *   record      : device; afterwards record->step is this step's number, or one less if it was
+ *                 skipped
+ * Every argument is checked before the first launch. The rest as zpp_adamw_step.
+ */
+ZPP_API zpp_status zpp_adamw_step_counted(const zpp_adamw_tensor* tensors, int32_t num_tensors,
+                                          zpp_dtype g_dt, zpp_dtype w_dt, int32_t state_bits,
+                                          const zpp_adamw_params* hp, const float* grad_scale,
+                                          const zpp_adamw_clip* clip, zpp_adamw_record* record,
+                                          cudaStream_t stream);
+
 /*
  * y = x W^T (+ bias) for a few vectors x, straight from the codes of a [rows][cols] matrix
  * quantised row-major by zpp_quant_blockwise (blocks may run across rows):

@@ -43,6 +43,11 @@ class AdamwParams(ctypes.Structure):
         ("step", ctypes.c_int64), ("seed", ctypes.c_uint32)]
 
 
+class AdamwClip(ctypes.Structure):
+    _fields_ = [("pre_scale", ctypes.c_float), ("max_norm", ctypes.c_float),
+                ("workspace", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
 class ZppError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -89,6 +94,7 @@ def lib():
         "zpp_wait_selftest": [ctypes.c_uint64, vp],
         "zpp_grad_norm": [vp, vp, i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, vp],
         "zpp_adamw_step": [vp, i32, i32, i32, i32, vp, vp, vp],
+        "zpp_adamw_step_counted": [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp],
         "zpp_matvec_blockwise": [vp, vp, i64, i64, i32, i32, vp, i32, i64, i64, vp, vp, i32, i64,
                                  vp],
     }
@@ -219,14 +225,25 @@ def zpp_grad_norm_workspace(total_elems, num_tensors):
 def zpp_adamw_step(tensors, g_dt, w_dt, state_bits, hp, grad_scale=0, stream=0):
     """tensors: a sequence of AdamwTensor, or an array('q') with their fields one after the
     other; hp: an AdamwParams."""
-    if isinstance(tensors, array.array):
-        num, at = len(tensors) // 8, tensors.buffer_info()[0]
-    else:
-        num = len(tensors)
-        tensors = (AdamwTensor * max(num, 1))(*tensors)
-        at = ctypes.addressof(tensors)
+    num, at, keep = _adamw_table(tensors)
     return lib().zpp_adamw_step(at, num, g_dt, w_dt, state_bits, ctypes.addressof(hp),
                                 grad_scale, stream)
+
+
+def zpp_adamw_step_counted(tensors, g_dt, w_dt, state_bits, hp, grad_scale, clip, record, stream=0):
+    """clip: an AdamwClip or None; the rest as zpp_adamw_step."""
+    num, at, keep = _adamw_table(tensors)
+    return lib().zpp_adamw_step_counted(at, num, g_dt, w_dt, state_bits, ctypes.addressof(hp),
+                                        grad_scale, ctypes.addressof(clip) if clip else 0, record,
+                                        stream)
+
+
+def _adamw_table(tensors):
+    """(number of tensors, address of their fields, what keeps it alive)."""
+    if isinstance(tensors, array.array):
+        return len(tensors) // 8, tensors.buffer_info()[0], tensors
+    fields = (AdamwTensor * max(len(tensors), 1))(*tensors)
+    return len(tensors), ctypes.addressof(fields), fields
 
 
 def zpp_matvec_blockwise(codes, scales, rows, cols, block, bits, x, x_dt, vecs, x_stride, bias, y,

@@ -12,6 +12,7 @@
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
 #include "zpp_overlap.cuh"
+#include "zpp_step_count.cuh"
 
 namespace zpp {
 
@@ -105,11 +106,19 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+// COUNTED: also the record of the optimiser step by this factor, by the last warp, which makes the
+// step's factors while the others wait for their partials.
+template <bool COUNTED>
 __global__ void __launch_bounds__(1024) k_norm_finish(const float* __restrict__ partial, int count,
                                                       float pre_scale, float max_norm,
-                                                      float* __restrict__ out) {
+                                                      float* __restrict__ out, const StepCount c) {
   grid_wait();
   grid_release();
+  const int lane = static_cast<int>(threadIdx.x) - (1024 - 32);
+  StepFactor f{};
+  if constexpr (COUNTED)
+    if (lane == 0 || lane == 1) f = step_factor(c, lane);
+  __shared__ float taken_by;
   double sum = 0.0;
   for (int i = threadIdx.x; i < count; i += 1024)
     sum += static_cast<double>(*static_cast<const volatile float*>(partial + i));
@@ -117,8 +126,15 @@ __global__ void __launch_bounds__(1024) k_norm_finish(const float* __restrict__ 
   if (threadIdx.x == 0) {
     const float norm = static_cast<float>(sqrt(sum)) * fabsf(pre_scale);
     out[0] = norm;
-    out[1] = !isfinite(norm) ? __int_as_float(0x7fc00000)
-                             : pre_scale * (norm > max_norm ? max_norm / norm : 1.0f);
+    const float factor = !isfinite(norm) ? __int_as_float(0x7fc00000)
+                                         : pre_scale * (norm > max_norm ? max_norm / norm : 1.0f);
+    out[1] = factor;
+    if constexpr (COUNTED) taken_by = factor;
+  }
+  if constexpr (COUNTED) {
+    __syncthreads();
+    const float inv_root_bc2 = __shfl_sync(~0u, f.made, 1);
+    if (lane == 0 || lane == 1) write_record(c, f, lane, taken_by, inv_root_bc2);
   }
 }
 
@@ -133,7 +149,7 @@ static cudaError_t run_partial(NormTableOf<CAP>& tab, int g_kind, bool v8, float
 }
 
 cudaError_t launch_grad_norm(NormTable& tab, int g_kind, float pre_scale, float max_norm,
-                             float* workspace, float* out, cudaStream_t s) {
+                             float* workspace, float* out, const StepCount& count, cudaStream_t s) {
   const int chunks = tab.first[tab.count];
   if (chunks > 0) {
     uintptr_t bits = 0;
@@ -156,8 +172,8 @@ cudaError_t launch_grad_norm(NormTable& tab, int g_kind, float pre_scale, float 
     }
     if (e != cudaSuccess) return e;
   }
-  return launch_overlapped(k_norm_finish, 1, 1024, s, static_cast<const float*>(workspace), chunks,
-                           pre_scale, max_norm, out);
+  return launch_overlapped(count.record ? k_norm_finish<true> : k_norm_finish<false>, 1, 1024, s,
+                           static_cast<const float*>(workspace), chunks, pre_scale, max_norm, out, count);
 }
 
 }  // namespace zpp

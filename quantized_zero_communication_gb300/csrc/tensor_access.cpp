@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <zpp.h>
@@ -266,7 +267,67 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
+// step(address of zpp_adamw_step_counted, int64 table [tensors][8], gradients' kind, weights' kind,
+// state bits, address of the zpp_adamw_params, address of the gradients' scale or 0, None or (max_norm,
+// pre_scale, floats of workspace), address of the record, device): one counted step on the device's
+// current stream; (norm, factor) in a new tensor, None without clipping, or a status other than
+// ZPP_OK as an int. While the stream is captured the number of the step is left to the device,
+// whose count a replay moves on: hp->step is set to 0.
+PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 10) {
+    PyErr_SetString(PyExc_TypeError, "step: 10 arguments");
+    return nullptr;
+  }
+  const auto fn = reinterpret_cast<decltype(&zpp_adamw_step_counted)>(PyLong_AsVoidPtr(args[0]));
+  const long g_kind = PyLong_AsLong(args[2]), w_kind = PyLong_AsLong(args[3]),
+             bits = PyLong_AsLong(args[4]), device = PyLong_AsLong(args[9]);
+  auto* hp = static_cast<zpp_adamw_params*>(PyLong_AsVoidPtr(args[5]));
+  const void* scale = PyLong_AsVoidPtr(args[6]);
+  void* record = PyLong_AsVoidPtr(args[8]);
+  double max_norm = 0.0, pre_scale = 0.0;
+  long long floats = 0;
+  const bool clipped = args[7] != Py_None;
+  if (PyErr_Occurred() || (clipped && !PyArg_ParseTuple(args[7], "ddL", &max_norm, &pre_scale, &floats)))
+    return nullptr;
+  Py_buffer table;
+  if (PyObject_GetBuffer(args[1], &table, PyBUF_SIMPLE) != 0) return nullptr;
+  PyObject* result = nullptr;
+  try {
+    const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device));
+    if (hp->step > 0 &&
+        c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+      hp->step = 0;
+    at::Tensor norm, work;
+    zpp_adamw_clip clip{};
+    if (clipped) {
+      const auto options = at::TensorOptions().dtype(at::kFloat).device(
+          at::kCUDA, static_cast<c10::DeviceIndex>(device));
+      norm = at::empty({2}, options);
+      work = at::empty({floats}, options);
+      clip.max_norm = static_cast<float>(max_norm);
+      clip.pre_scale = static_cast<float>(pre_scale);
+      clip.workspace = reinterpret_cast<float*>(address_of(work));
+      clip.out = reinterpret_cast<float*>(address_of(norm));
+    }
+    const zpp_status st =
+        fn(static_cast<const zpp_adamw_tensor*>(table.buf),
+           static_cast<int32_t>(table.len / static_cast<Py_ssize_t>(sizeof(zpp_adamw_tensor))),
+           static_cast<zpp_dtype>(g_kind), static_cast<zpp_dtype>(w_kind), static_cast<int32_t>(bits), hp,
+           static_cast<const float*>(scale), clipped ? &clip : nullptr,
+           static_cast<zpp_adamw_record*>(record), stream.stream());
+    if (st != ZPP_OK) result = PyLong_FromLong(st);
+    else if (clipped) result = THPVariable_Wrap(std::move(norm));
+    else result = Py_NewRef(Py_None);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  PyBuffer_Release(&table);
+  return result;
+}
+
 PyMethodDef methods[] = {
+    {"step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(step)), METH_FASTCALL,
+     "one counted AdamW step from a table of addresses"},
     {"grad_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grad_norm)),
      METH_FASTCALL, "the norm of a list of gradients, plain case"},
     {"scan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scan)), METH_FASTCALL,

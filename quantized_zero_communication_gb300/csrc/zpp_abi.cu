@@ -3,6 +3,7 @@
 #include <zpp.h>
 
 #include <cmath>
+#include <cstddef>
 
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
@@ -338,12 +339,15 @@ zpp_status zpp_grad_norm(const void* const* grads, const int64_t* sizes, int32_t
     tab.first[t + 1] = tab.first[t] + static_cast<int32_t>(zpp::norm_chunks(sizes[t]));
   }
   return from_cuda(zpp::launch_grad_norm(tab, static_cast<int>(g_dt), pre_scale, max_norm,
-                                         workspace, out, stream));
+                                         workspace, out, zpp::StepCount{}, stream));
 }
 
-zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, zpp_dtype g_dt,
-                          zpp_dtype w_dt, int32_t state_bits, const zpp_adamw_params* hp,
-                          const float* grad_scale, cudaStream_t stream) {
+namespace {
+
+// The arguments that both forms of the step share. step_min: the smallest number of a step.
+zpp_status check_adamw(const zpp_adamw_tensor* tensors, int32_t num_tensors, zpp_dtype g_dt,
+                       zpp_dtype w_dt, int32_t state_bits, const zpp_adamw_params* hp,
+                       int64_t step_min, const float* grad_scale) {
   static_assert(zpp::kStateBlock == ZPP_STATE_BLOCK, "state block");
   if (num_tensors < 0 || num_tensors > ZPP_MAX_TENSORS || (num_tensors > 0 && !tensors) || !hp)
     return ZPP_ERR_INVALID_ARG;
@@ -351,7 +355,7 @@ zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, 
     return ZPP_ERR_INVALID_ARG;
   if (!is_finite(hp->lr) || !is_finite(hp->weight_decay) || !is_finite(hp->eps) || hp->eps < 0.0 ||
       !(hp->beta1 >= 0.0 && hp->beta1 < 1.0) || !(hp->beta2 >= 0.0 && hp->beta2 < 1.0) ||
-      hp->step < 1)
+      hp->step < step_min)
     return ZPP_ERR_INVALID_ARG;
   int64_t total = 0;
   bool any_weight = false;
@@ -375,22 +379,43 @@ zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, 
     if (state_bits == 8 && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4)))
       return ZPP_ERR_MISALIGNED;
   }
-  if (!aligned(grad_scale, 4)) return ZPP_ERR_MISALIGNED;
+  return aligned(grad_scale, 4) ? ZPP_OK : ZPP_ERR_MISALIGNED;
+}
 
+// beta^step and the factors made from it, in 64 bits, rounded once.
+struct StepFactors {
+  double power[2];
+  float step_size, inv_root_bc2;
+  explicit StepFactors(const zpp_adamw_params& hp) {
+    const double t = static_cast<double>(hp.step);
+    power[0] = std::pow(hp.beta1, t);
+    power[1] = std::pow(hp.beta2, t);
+    step_size = static_cast<float>(hp.lr / (1.0 - power[0]));
+    inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - power[1]));
+  }
+};
+
+// record: null, or the step's record: told hp->step where that is known, read where it is 0.
+zpp_status run_adamw(const zpp_adamw_tensor* tensors, int32_t num_tensors, zpp_dtype g_dt,
+                     zpp_dtype w_dt, int32_t state_bits, const zpp_adamw_params* hp,
+                     const float* grad_scale, zpp_adamw_record* record, cudaStream_t stream) {
   zpp::AdamwTable tab;
-  const double t = static_cast<double>(hp->step);
-  const double bc1 = 1.0 - std::pow(hp->beta1, t), bc2 = 1.0 - std::pow(hp->beta2, t);
   zpp::AdamwArgs& a = tab.a;
   a.beta1 = static_cast<float>(hp->beta1);
   a.one_minus_beta1 = static_cast<float>(1.0 - hp->beta1);
   a.beta2 = static_cast<float>(hp->beta2);
   a.one_minus_beta2 = static_cast<float>(1.0 - hp->beta2);
-  a.step_size = static_cast<float>(hp->lr / bc1);
-  a.inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
+  if (hp->step > 0) {
+    const StepFactors f(*hp);
+    a.step_size = f.step_size;
+    a.inv_root_bc2 = f.inv_root_bc2;
+  }
   a.eps = static_cast<float>(hp->eps);
   a.decay = static_cast<float>(hp->lr * hp->weight_decay);
   a.key = (hp->seed * 0x9E3779B9u) ^ (static_cast<uint32_t>(hp->step) * 0x510E527Fu);
   a.grad_scale = grad_scale;
+  a.record = reinterpret_cast<zpp::StepRecord*>(record);
+  a.step = hp->step;
   a.g_kind = static_cast<int32_t>(g_dt);
   a.w_kind = static_cast<int32_t>(w_dt);
   tab.first_block = 0;
@@ -414,6 +439,77 @@ zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, 
     if (st != ZPP_OK) return st;
   }
   return ZPP_OK;
+}
+
+}  // namespace
+
+zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors, zpp_dtype g_dt,
+                          zpp_dtype w_dt, int32_t state_bits, const zpp_adamw_params* hp,
+                          const float* grad_scale, cudaStream_t stream) {
+  const zpp_status st =
+      check_adamw(tensors, num_tensors, g_dt, w_dt, state_bits, hp, 1, grad_scale);
+  if (st != ZPP_OK) return st;
+  return run_adamw(tensors, num_tensors, g_dt, w_dt, state_bits, hp, grad_scale, nullptr, stream);
+}
+
+zpp_status zpp_adamw_step_counted(const zpp_adamw_tensor* tensors, int32_t num_tensors,
+                                  zpp_dtype g_dt, zpp_dtype w_dt, int32_t state_bits,
+                                  const zpp_adamw_params* hp, const float* grad_scale,
+                                  const zpp_adamw_clip* clip, zpp_adamw_record* record,
+                                  cudaStream_t stream) {
+  static_assert(sizeof(zpp_adamw_record) == sizeof(zpp::StepRecord) &&
+                    offsetof(zpp_adamw_record, factor) == offsetof(zpp::StepRecord, factor) &&
+                    offsetof(zpp_adamw_record, power) == offsetof(zpp::StepRecord, power) &&
+                    offsetof(zpp::StepRecord, factor) % 16 == 0,
+                "the record's layout");
+  zpp_status st = check_adamw(tensors, num_tensors, g_dt, w_dt, state_bits, hp, 0, grad_scale);
+  if (st != ZPP_OK) return st;
+  if (!record || (clip && grad_scale)) return ZPP_ERR_INVALID_ARG;
+  if (clip) {
+    if (!is_finite(clip->pre_scale) || !(clip->max_norm > 0.0f) || !clip->workspace || !clip->out)
+      return ZPP_ERR_INVALID_ARG;
+    if (!aligned(clip->workspace, 4) || !aligned(clip->out, 4)) return ZPP_ERR_MISALIGNED;
+  }
+  if (!aligned(record, 16)) return ZPP_ERR_MISALIGNED;
+
+  bool elements = false;
+  for (int32_t i = 0; i < num_tensors; ++i) elements |= tensors[i].n > 0;
+  // A step whose number the host knows and that cannot be skipped leaves its number as it runs.
+  if (hp->step > 0 && !clip && !grad_scale && elements)
+    return run_adamw(tensors, num_tensors, g_dt, w_dt, state_bits, hp, nullptr, record, stream);
+
+  zpp::StepCount count{};
+  count.lr = hp->lr;
+  count.beta[0] = hp->beta1;
+  count.beta[1] = hp->beta2;
+  count.known = hp->step;
+  count.seed = hp->seed;
+  count.record = reinterpret_cast<zpp::StepRecord*>(record);
+  if (hp->step > 0) {
+    const StepFactors f(*hp);
+    count.power[0] = f.power[0];
+    count.power[1] = f.power[1];
+    count.step_size = f.step_size;
+    count.inv_root_bc2 = f.inv_root_bc2;
+  }
+  if (clip) {
+    zpp::NormTable tab;
+    tab.count = num_tensors;
+    tab.first[0] = 0;
+    for (int32_t i = 0; i < num_tensors; ++i) {
+      tab.ptr[i] = tensors[i].grad;
+      tab.n[i] = tensors[i].n;
+      tab.first[i + 1] = tab.first[i] + static_cast<int32_t>(zpp::norm_chunks(tensors[i].n));
+    }
+    st = from_cuda(zpp::launch_grad_norm(tab, static_cast<int>(g_dt), clip->pre_scale, clip->max_norm,
+                                         clip->workspace, clip->out, count, stream));
+  } else {
+    st = from_cuda(zpp::launch_step_count(count, grad_scale, stream));
+  }
+  if (st != ZPP_OK) return st;
+  zpp_adamw_params recorded = *hp;
+  recorded.step = 0;
+  return run_adamw(tensors, num_tensors, g_dt, w_dt, state_bits, &recorded, nullptr, record, stream);
 }
 
 zpp_status zpp_matvec_blockwise(const void* codes, const float* scales, int64_t rows, int64_t cols,

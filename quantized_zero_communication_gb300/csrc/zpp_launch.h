@@ -119,8 +119,25 @@ using NormTable = NormTableOf<kMaxTensors>;
 // table (a call with one tensor costs the host 3 us less than with the full one).
 constexpr int kFewTensors = 16;
 inline int64_t norm_chunks(int64_t n) { return (n + kNormChunk - 1) / kNormChunk; }
+// What a counted optimiser step keeps on the device (= zpp_adamw_record), and what its factors
+// are made of.
+struct StepRecord {
+  int64_t step, reserved;
+  float factor, step_size, inv_root_bc2;
+  uint32_t key;
+  double beta[2], power[2];
+};
+struct StepCount {
+  double lr, beta[2];
+  double power[2];                // known > 0: beta^known, and
+  float step_size, inv_root_bc2;  // the factors of that step
+  int64_t known;                  // the step's number; 0: one more than the record's
+  uint32_t seed;
+  StepRecord* record;  // null: nothing is counted
+};
+// count: the factor `out[1]` is that of an optimiser step, whose record is written.
 cudaError_t launch_grad_norm(NormTable& tab, int g_kind, float pre_scale, float max_norm,
-                             float* workspace, float* out, cudaStream_t s);
+                             float* workspace, float* out, const StepCount& count, cudaStream_t s);
 
 // K8: one AdamW step over a list of tensors; at most kAdamwTensors per launch (their
 // descriptors travel in the kernel's parameter space).
@@ -143,6 +160,8 @@ struct AdamwArgs {
   float eps, decay;     // decay = lr * weight_decay
   uint32_t key;         // of the rounding hash
   const float* grad_scale;
+  StepRecord* record;      // its factors replace those above (counted), or it is told `step`
+  int64_t step;            // > 0 with a record: the step's number, known on the host
   int32_t g_kind, w_kind;  // zpp_dtype of grad and weight
 };
 template <int CAP>
@@ -168,6 +187,8 @@ inline int64_t adamw_chunks(int64_t n, int state_bits) {
   return (n + adamw_chunk(state_bits) - 1) / adamw_chunk(state_bits);
 }
 cudaError_t launch_adamw(AdamwTable& tab, int state_bits, cudaStream_t s);
+// Writes count.record for a step by the factor *grad_scale (null: 1).
+cudaError_t launch_step_count(const StepCount& count, const float* grad_scale, cudaStream_t s);
 
 // K9: y = x W^T (+ bias) from block-quantised codes. x_bf16: x and bias are bf16, else fp16;
 // y_kind as a zpp_dtype.

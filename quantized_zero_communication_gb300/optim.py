@@ -1,11 +1,13 @@
 """AdamW over the tensors of a parameter shard: fp32 master weights, states in fp32 or in
-8 bits, one library call per step (``zpp_adamw_step``), and one more when the gradient norm
-is clipped (``zpp_grad_norm``). Everything stays on the device; a step never synchronises.
+8 bits, one library call per step (``zpp_adamw_step_counted``), which also takes the gradient norm
+when it clips. Everything stays on the device; a step never synchronises.
 
 The 16-bit tensors in ``weights`` receive the updated parameters, ready for the next
 all-gather's ``quant_blockwise``.
 """
 import array
+import ctypes
+import math
 
 from . import binding as _b
 
@@ -38,7 +40,7 @@ class AdamW:
         if not 0 <= seed < 1 << 32:
             raise ValueError("seed: 0 .. 2^32 - 1")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.state_bits, self.seed, self.steps = state_bits, seed, step
+        self.state_bits, self.seed = state_bits, seed
         self._sizes = array.array("q", [p.numel() for p in self.params])
         self._blocks = _b._state_blocks(self._sizes)
         code = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
@@ -77,8 +79,27 @@ class AdamW:
         self._table = array.array("q", bytes(64 * len(self.params)))
         self._table[7::8] = self._sizes
         self._hp = _b.AdamwParams(lr, *self.betas, eps, weight_decay, step, seed)
+        self._work = _b.zpp_grad_norm_workspace(sum(self._sizes), len(self._sizes))
         self._w_kind = _b.ZPP_BF16
         self._gather()
+        # The number of the last step on the device (zpp_adamw_record), and here as long as no step
+        # may have been skipped: _known is None afterwards.
+        self._record = torch.zeros(8, dtype=torch.int64, device=self.params[0].device)
+        self._record[:1].fill_(step)
+        self._known = step
+
+    @property
+    def steps(self):
+        """The steps taken; skipped ones do not count. Once a step was clipped or scaled only the
+        device knows, and reading this waits for it. Setting it gives the next step's number, less
+        one."""
+        return self._known if self._known is not None else int(self._record[0])
+
+    @steps.setter
+    def steps(self, step):
+        self._record.zero_()
+        self._record[:1].fill_(step)
+        self._known = None
 
     def _enter(self, name, column, tensors, sizes, kinds):
         """Checks a list and writes its addresses into the call's table; their dtype's kind."""
@@ -104,8 +125,8 @@ class AdamW:
         """One step with `grads` (contiguous, one of fp16 / bf16 / fp32, in the parameters'
         order). max_norm and / or pre_scale: the gradients are multiplied by pre_scale (say 1 /
         loss scale) and clipped to the global norm max_norm, and fp32 [2] (norm, factor) is
-        returned; a norm that is not finite leaves parameters and states as they were.
-        grad_scale: instead, an fp32 device tensor whose first element multiplies the
+        returned; a norm that is not finite leaves parameters, states and the count of steps as
+        they were. grad_scale: instead, an fp32 device tensor whose first element multiplies the
         gradients (the factor of a norm taken over several ranks). lr replaces the
         optimiser's for this step and the following ones."""
         torch = _b._torch()
@@ -114,24 +135,29 @@ class AdamW:
         kind = self._enter("grads", 1, grads, self._sizes, _b._GRAD_KINDS)
         if lr is not None:
             self.lr = lr
-        norm, scale = None, 0
+        scale, clip = 0, None
         if max_norm is not None or pre_scale is not None:
             if grad_scale is not None:
                 raise ValueError("grad_scale replaces max_norm and pre_scale")
-            norm = _b.grad_norm(grads, max_norm, 1.0 if pre_scale is None else pre_scale)
-            scale = norm.data_ptr() + 4  # its second element
+            clip = (math.inf if max_norm is None else max_norm,
+                    1.0 if pre_scale is None else pre_scale, self._work)
         elif grad_scale is not None:
             scale = _b._scale_address(grads[0], grad_scale)
         hp = self._hp
-        hp.lr, hp.step = self.lr, self.steps + 1
+        hp.lr, hp.step = self.lr, 0 if self._known is None else self._known + 1
         hp.beta1, hp.beta2 = self.betas
         hp.eps, hp.weight_decay = self.eps, self.weight_decay
-        _b._adamw(self._table, kind, self._w_kind, self.state_bits, hp, scale, self._device)
-        self.steps += 1
+        norm = _b._tensors().step(_b._address("zpp_adamw_step_counted"), self._table, kind, self._w_kind,
+                                  self.state_bits, ctypes.addressof(hp), scale, clip,
+                                  self._record.data_ptr(), self._device)
+        if type(norm) is int:
+            raise _b.ZppError(norm, "zpp_adamw_step_counted")
+        # (in a captured stream hp.step is 0 now: a replay is another step, the device counts them)
+        self._known = None if clip or scale or not hp.step else hp.step
         return norm
 
     def state(self):
         """What a checkpoint keeps, as the constructor takes it: the state tensors themselves
-        and the step count."""
+        and the step count (which waits for the device once a step was clipped or scaled)."""
         return dict(exp_avg=self.exp_avg, exp_avg_sq=self.exp_avg_sq, scales=self.scales,
                     step=self.steps, seed=self.seed, state_bits=self.state_bits)
