@@ -362,7 +362,8 @@ typedef struct zpp_adamw_params {
  *                 non-NULL weight: ZPP_ERR_UNSUPPORTED)
  *   state_bits  : 32 or 8
  *   hp          : HOST, read during the call: lr and weight_decay finite, 0 <= beta1, beta2 < 1,
- *                 eps >= 0 and finite, step >= 1
+ *                 eps >= 0 and finite (one below 2^-126 counts as 2^-126; with 0 an element that
+ *                 never had a gradient is 0 / 0), step >= 1
  *   grad_scale  : device, 4-byte aligned, or NULL
  */
 ZPP_API zpp_status zpp_adamw_step(const zpp_adamw_tensor* tensors, int32_t num_tensors,

@@ -2,8 +2,10 @@
 // kernel selection, status codes, and the same-run 256-bit copy kernel.
 #include <zpp.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <limits>
 
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
@@ -410,7 +412,8 @@ zpp_status run_adamw(const zpp_adamw_tensor* tensors, int32_t num_tensors, zpp_d
     a.step_size = f.step_size;
     a.inv_root_bc2 = f.inv_root_bc2;
   }
-  a.eps = static_cast<float>(hp->eps);
+  // The denominator's reciprocal takes a subnormal for zero, and 0 / eps has to stay 0.
+  a.eps = hp->eps > 0.0 ? std::max(static_cast<float>(hp->eps), std::numeric_limits<float>::min()) : 0.0f;
   a.decay = static_cast<float>(hp->lr * hp->weight_decay);
   a.key = (hp->seed * 0x9E3779B9u) ^ (static_cast<uint32_t>(hp->step) * 0x510E527Fu);
   a.grad_scale = grad_scale;
