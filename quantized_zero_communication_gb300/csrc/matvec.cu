@@ -651,8 +651,8 @@ __global__ void __launch_bounds__(kThreads) k_matvec_long(const MatvecArgs a, in
     const int64_t e = r * a.cols + c;
     const int q = a.bits == 8 ? static_cast<int>(static_cast<int8_t>(__ldg(a.codes + e)))
                               : code_int4(__ldg(a.codes + (e >> 1)), static_cast<int>(e & 1));
-    const float w = __fmul_rn(static_cast<float>(q), __ldg(a.scales + (e >> log2b)));
-    sum = __fmaf_rn(w, bits16_to_float(__ldg(x + c), TT()), sum);
+    const float qx = __fmul_rn(static_cast<float>(q), bits16_to_float(__ldg(x + c), TT()));  // exact
+    sum = __fmaf_rn(qx, __ldg(a.scales + (e >> log2b)), sum);
   }
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (lane == 0) {
