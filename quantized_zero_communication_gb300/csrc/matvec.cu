@@ -661,13 +661,19 @@ __global__ void __launch_bounds__(kThreads) k_matvec_long(const MatvecArgs a, in
   }
 }
 
-// One overlapped launch (zpp_overlap.cuh) with `split` CTAs of a cluster along each row.
+// Bytes of x per CTA of k_matvec_any: two CTAs per SM; what one can hold.
+constexpr int64_t kAnyX = 64 * 1024, kAnyMaxX = 180 * 1024;
+constexpr int kAnyMaxBytes = static_cast<int>(kAnyMaxX) + kWarps * std::max(AnyShape<4>::RING, AnyShape<8>::RING);
+
+// One overlapped launch (zpp_overlap.cuh) with `split` CTAs of a cluster along each row. The opt-in
+// limit belongs to the kernel, which other threads launch too with layouts of other sizes, so it
+// is always set to the largest.
 template <typename... Params, typename... Args>
 static cudaError_t launch_split(void (*kern)(Params...), int64_t tiles, int64_t vec_groups, int split,
                                 size_t bytes, cudaStream_t s, Args... args) {
   if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(bytes));
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAnyMaxBytes);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -685,9 +691,6 @@ static cudaError_t launch_split(void (*kern)(Params...), int64_t tiles, int64_t 
   cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
 }
-
-// Bytes of x per CTA of k_matvec_any: two CTAs per SM; what one can hold.
-constexpr int64_t kAnyX = 64 * 1024, kAnyMaxX = 180 * 1024;
 
 // How a launch splits a row: over wk warps of a CTA and `split` CTAs.
 struct MvPlan {
