@@ -11,6 +11,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <zpp.h>
 
@@ -40,6 +41,17 @@ bool plain(PyObject* o) {
   return THPVariable_Check(o) && THPVariable_Unpack(o).layout() == at::kStrided;
 }
 
+// Python's exception for `e`: torch's own where memory ran out, as its allocations in Python raise it.
+void raise(const std::exception& e) {
+  const auto* memory = dynamic_cast<const c10::OutOfMemoryError*>(&e);
+  PyObject* torch = memory ? PyImport_ImportModule("torch") : nullptr;
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  if (type) PyErr_SetString(type, memory->what_without_backtrace());
+  else if (!memory) PyErr_SetString(PyExc_RuntimeError, e.what());
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 // What a list's tensors have in common.
 struct Seen {
   long kind = -1, device = -1;  // -1 unless the same for all
@@ -65,7 +77,7 @@ bool look(PyObject* list, Seen& seen, const F& each) {
       each(i, t);
     }
   } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    raise(e);
     return false;
   }
   return true;
@@ -147,7 +159,7 @@ PyObject* probe(PyObject*, PyObject* o) {
                          static_cast<long long>(t.numel()), kind_of(t), gpu_of(t),
                          t.is_contiguous() ? 1 : 0);
   } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    raise(e);
     return nullptr;
   }
 }
@@ -209,7 +221,7 @@ PyObject* matvec(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (st != ZPP_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(std::move(y));
   } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    raise(e);
     return nullptr;
   }
 }
@@ -262,7 +274,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (st != ZPP_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(std::move(out));
   } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    raise(e);
     return nullptr;
   }
 }
@@ -319,7 +331,7 @@ PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
     else if (clipped) result = THPVariable_Wrap(std::move(norm));
     else result = Py_NewRef(Py_None);
   } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+    raise(e);
   }
   PyBuffer_Release(&table);
   return result;
