@@ -647,14 +647,21 @@ def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
         out = grads[0].new_empty(2, dtype=torch.float32)
     work = grads[0].new_empty(zpp_grad_norm_workspace(sum(sizes), len(sizes)),
                               dtype=torch.float32)
-    _norm_call(ptrs, sizes, kind, device, max_norm, pre_scale, work.data_ptr(), out.data_ptr())
+    _launch(device, "zpp_grad_norm", ptrs.buffer_info()[0], sizes.buffer_info()[0], len(sizes), kind,
+            pre_scale, math.inf if max_norm is None else max_norm, work.data_ptr(), out.data_ptr())
     return out
 
 
-def _norm_call(ptrs, sizes, kind, device, max_norm, pre_scale, work, out):
-    _check(lib().zpp_grad_norm(ptrs.buffer_info()[0], sizes.buffer_info()[0], len(sizes), kind,
-                               pre_scale, math.inf if max_norm is None else max_norm, work, out,
-                               _raw_stream(device)), "zpp_grad_norm")
+def _launch(device, name, *args):
+    """The library function `name` on a device's current stream, with that device current: a kernel
+    starts on the current device, whatever device its stream belongs to."""
+    torch = _torch()
+    if device == torch.cuda.current_device():
+        status = getattr(lib(), name)(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), name)(*args, _raw_stream(device))
+    _check(status, name)
 
 
 def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -729,9 +736,8 @@ def _scale_address(grad, grad_scale):
 
 
 def _adamw(tab, g_kind, w_kind, state_bits, hp, scale, device):
-    _check(lib().zpp_adamw_step(tab.buffer_info()[0], len(tab) // 8, g_kind, w_kind, state_bits,
-                                ctypes.addressof(hp), scale, _raw_stream(device)),
-           "zpp_adamw_step")
+    _launch(device, "zpp_adamw_step", tab.buffer_info()[0], len(tab) // 8, g_kind, w_kind, state_bits,
+            ctypes.addressof(hp), scale)
 
 
 @functools.cache
@@ -791,11 +797,8 @@ def matvec_blockwise(codes, scales, x, rows, block, bits, bias=None, dtype=None,
     if device < 0 or not (c_dev == s_dev == y_dev == device and c_whole and s_whole and b_ok):
         _cuda(codes, scales, *(t for t in (bias,) if t is not None))
         raise ValueError("all tensors of a call must be on one CUDA device")
-    status = lib().zpp_matvec_blockwise(c_at, s_at, rows, cols, block, bits, x_at, x_kind, vecs,
-                                        x_stride, b_at, y_at, y_kind, y_stride,
-                                        _raw_stream(device))
-    if status != ZPP_OK:
-        raise ZppError(status, "zpp_matvec_blockwise")
+    _launch(device, "zpp_matvec_blockwise", c_at, s_at, rows, cols, block, bits, x_at, x_kind, vecs,
+            x_stride, b_at, y_at, y_kind, y_stride)
     return y
 
 

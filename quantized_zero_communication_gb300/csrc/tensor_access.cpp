@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
@@ -33,6 +34,8 @@ long kind_of(const at::Tensor& t) {
   }
 }
 long gpu_of(const at::Tensor& t) { return t.is_cuda() ? t.get_device() : -1; }
+// A kernel starts on the current device, whatever device its stream belongs to.
+bool current(long device) { return device >= 0 && device == c10::cuda::current_device(); }
 int64_t address_of(const at::Tensor& t) {
   return t.numel() ? reinterpret_cast<int64_t>(t.data_ptr()) : 0;
 }
@@ -42,7 +45,7 @@ bool plain(PyObject* o) {
 }
 
 // Python's exception for `e`: torch's own where memory ran out, as its allocations in Python raise it.
-void raise(const std::exception& e) {
+void set_error(const std::exception& e) {
   const auto* memory = dynamic_cast<const c10::OutOfMemoryError*>(&e);
   PyObject* torch = memory ? PyImport_ImportModule("torch") : nullptr;
   PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
@@ -77,7 +80,7 @@ bool look(PyObject* list, Seen& seen, const F& each) {
       each(i, t);
     }
   } catch (const std::exception& e) {
-    raise(e);
+    set_error(e);
     return false;
   }
   return true;
@@ -159,7 +162,7 @@ PyObject* probe(PyObject*, PyObject* o) {
                          static_cast<long long>(t.numel()), kind_of(t), gpu_of(t),
                          t.is_contiguous() ? 1 : 0);
   } catch (const std::exception& e) {
-    raise(e);
+    set_error(e);
     return nullptr;
   }
 }
@@ -186,7 +189,7 @@ PyObject* matvec(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor &codes = THPVariable_Unpack(args[1]), &scales = THPVariable_Unpack(args[2]),
                      &x = THPVariable_Unpack(args[3]);
     const long kind = kind_of(x), device = gpu_of(x);
-    if (device < 0 || (kind != ZPP_F16 && kind != ZPP_BF16) || x.dim() < 1 || !x.is_contiguous())
+    if (!current(device) || (kind != ZPP_F16 && kind != ZPP_BF16) || x.dim() < 1 || !x.is_contiguous())
       Py_RETURN_NONE;
     const int64_t cols = x.size(-1);
     if (cols < 1 || rows < 0 || rows > ZPP_MAX_ELEMS / cols) Py_RETURN_NONE;
@@ -221,7 +224,7 @@ PyObject* matvec(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (st != ZPP_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(std::move(y));
   } catch (const std::exception& e) {
-    raise(e);
+    set_error(e);
     return nullptr;
   }
 }
@@ -259,7 +262,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
       Py_RETURN_NONE;
     }
     const long kind = seen.kind, device = seen.place();
-    if (kind < 0 || kind > ZPP_F32 || device < 0) Py_RETURN_NONE;
+    if (kind < 0 || kind > ZPP_F32 || !current(device)) Py_RETURN_NONE;
     const int64_t floats = reinterpret_cast<decltype(&zpp_grad_norm_workspace)>(workspace)(
         total, static_cast<int32_t>(count));
     if (floats < 0) Py_RETURN_NONE;
@@ -274,7 +277,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (st != ZPP_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(std::move(out));
   } catch (const std::exception& e) {
-    raise(e);
+    set_error(e);
     return nullptr;
   }
 }
@@ -283,7 +286,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // state bits, address of the zpp_adamw_params, address of the gradients' scale or 0, None or (max_norm,
 // pre_scale, floats of workspace), address of the record, device): one counted step on the device's
 // current stream; (norm, factor) in a new tensor, None without clipping, or a status other than
-// ZPP_OK as an int. While the stream is captured the number of the step is left to the device,
+// ZPP_OK as an int; False, with nothing done, where the device is not the current one. While the stream is captured the number of the step is left to the device,
 // whose count a replay moves on: hp->step is set to 0.
 PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 10) {
@@ -305,6 +308,10 @@ PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (PyObject_GetBuffer(args[1], &table, PyBUF_SIMPLE) != 0) return nullptr;
   PyObject* result = nullptr;
   try {
+    if (!current(device)) {
+      PyBuffer_Release(&table);
+      Py_RETURN_FALSE;
+    }
     const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device));
     if (hp->step > 0 &&
         c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
@@ -331,7 +338,7 @@ PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
     else if (clipped) result = THPVariable_Wrap(std::move(norm));
     else result = Py_NewRef(Py_None);
   } catch (const std::exception& e) {
-    raise(e);
+    set_error(e);
   }
   PyBuffer_Release(&table);
   return result;

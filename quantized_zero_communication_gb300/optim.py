@@ -147,9 +147,12 @@ class AdamW:
         hp.lr, hp.step = self.lr, 0 if self._known is None else self._known + 1
         hp.beta1, hp.beta2 = self.betas
         hp.eps, hp.weight_decay = self.eps, self.weight_decay
-        norm = _b._tensors().step(_b._address("zpp_adamw_step_counted"), self._table, kind, self._w_kind,
-                                  self.state_bits, ctypes.addressof(hp), scale, clip,
-                                  self._record.data_ptr(), self._device)
+        args = (_b._address("zpp_adamw_step_counted"), self._table, kind, self._w_kind, self.state_bits,
+                ctypes.addressof(hp), scale, clip, self._record.data_ptr(), self._device)
+        norm = _b._tensors().step(*args)
+        if norm is False:  # another device is current
+            with torch.cuda.device(self._device):
+                norm = _b._tensors().step(*args)
         if type(norm) is int:
             raise _b.ZppError(norm, "zpp_adamw_step_counted")
         # (in a captured stream hp.step is 0 now: a replay is another step, the device counts them)
