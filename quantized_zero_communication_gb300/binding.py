@@ -17,7 +17,7 @@ from . import build as _build
 
 ZPP_OK, ZPP_ERR_INVALID_ARG, ZPP_ERR_MISALIGNED, ZPP_ERR_UNSUPPORTED, ZPP_ERR_CUDA = range(5)
 ZPP_F16, ZPP_BF16, ZPP_F32 = 0, 1, 2
-ZPP_STATE_BLOCK = 256
+ZPP_STATE_BLOCK, ZPP_MAX_TENSORS = 256, 1024
 
 HEADER = os.path.join(_build.ROOT, "include", "zpp.h")
 

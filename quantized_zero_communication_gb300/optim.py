@@ -13,7 +13,7 @@ from . import binding as _b
 
 
 class AdamW:
-    """AdamW (decoupled weight decay) over a list of contiguous fp32 CUDA tensors.
+    """AdamW (decoupled weight decay) over a list of at most 1024 contiguous fp32 CUDA tensors.
 
     state_bits 32 holds both states in fp32; 8 holds m and sqrt(v) as float8_e4m3fn codes
     with one fp32 scale per 256 elements, rounded stochastically from `seed` and the step
@@ -31,6 +31,9 @@ class AdamW:
         self.params = list(params)
         if not self.params:
             raise ValueError("AdamW needs at least one tensor")
+        if len(self.params) > _b.ZPP_MAX_TENSORS:
+            raise ValueError(f"AdamW: {len(self.params)} tensors, at most {_b.ZPP_MAX_TENSORS} to a call: "
+                             "flatten them, or take an optimiser for each part")
         if state_bits not in (8, 32):
             raise ValueError("state_bits: 8 or 32")
         if (exp_avg is None) != (exp_avg_sq is None):
