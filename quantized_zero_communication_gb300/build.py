@@ -39,11 +39,20 @@ def _inputs():
     return files + [os.path.join(INCLUDE, "zpp.h"), __file__]
 
 
-def _stale():
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
+def _stale(out):
+    if not os.path.exists(out):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    t = os.path.getmtime(out)
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _has_torch():
+    """Whether there is a torch to make the extension for (the C library needs none)."""
+    try:
+        import torch
+    except (ImportError, OSError):
+        return False
+    return torch.version.cuda is not None
 
 
 def _build_ext():
@@ -64,8 +73,20 @@ def _build_ext():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+    """Brings libzpp.so up to date, and the extension where torch is there; an extension that does not
+    compile is an error, raised once the library is in place."""
+    lib = force or _stale(LIB)
+    ext = _has_torch() and (force or _stale(EXT))
+    with concurrent.futures.ThreadPoolExecutor(1) as ex:
+        made = ex.submit(_build_ext) if ext else None
+        if lib:
+            _build_lib(verbose)
+        if made:
+            made.result()
+    return LIB
+
+
+def _build_lib(verbose):
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
 
@@ -80,10 +101,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        ext = ex.submit(_build_ext)
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        ext.result()
     objs = [o for o, _ in results]
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
@@ -94,7 +113,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         for _, log in results:
             print(log)
-    return LIB
 
 
 if __name__ == "__main__":
