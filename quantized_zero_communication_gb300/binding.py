@@ -600,6 +600,10 @@ def _tensors():
         if not os.path.exists(_build.EXT):
             raise RuntimeError(f"{_build.EXT} is missing: build it with __graft_entry__.build() "
                                "(there is no fallback path)")
+        built, here = _build.built_ext_abi(), _build.ext_abi()
+        if built not in (None, here):
+            raise RuntimeError(f"{_build.EXT} was built for {built}, this is {here}: "
+                               "build it again with __graft_entry__.build()")
         from . import _tensors as module
         _tensors_module = module
     return _tensors_module

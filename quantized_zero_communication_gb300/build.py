@@ -18,6 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libzpp.so")
 EXT = os.path.join(PKG, "_tensors.so")
+EXT_ABI = os.path.join(BUILD, "_tensors.abi")  # what EXT was compiled against
 SOURCES = ["zpp_abi.cu", "quant.cu", "reorder_quant.cu", "reorder_tensors_f16.cu",
            "reorder_tensors_bf16.cu", "dequant.cu", "qgz.cu", "adamw.cu", "grad_norm.cu",
            "matvec.cu"]
@@ -46,13 +47,25 @@ def _stale(out):
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
-def _has_torch():
-    """Whether there is a torch to make the extension for (the C library needs none)."""
+def ext_abi():
+    """The torch and the Python that the extension is for; None without a torch with CUDA (the C
+    library needs none)."""
     try:
         import torch
     except (ImportError, OSError):
-        return False
-    return torch.version.cuda is not None
+        return None
+    if torch.version.cuda is None:
+        return None
+    return f"torch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def built_ext_abi():
+    """Those that the extension in place was compiled against; None if that is not known."""
+    try:
+        with open(EXT_ABI) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _build_ext():
@@ -69,14 +82,20 @@ def _build_ext():
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiling tensor_access.cpp failed:\n{r.stderr}")
+    if os.path.exists(EXT_ABI):
+        os.remove(EXT_ABI)
     os.replace(tmp, EXT)
+    with open(EXT_ABI, "w") as f:
+        f.write(ext_abi())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Brings libzpp.so up to date, and the extension where torch is there; an extension that does not
     compile is an error, raised once the library is in place."""
     lib = force or _stale(LIB)
-    ext = _has_torch() and (force or _stale(EXT))
+    abi = ext_abi()
+    ext = abi is not None and (force or _stale(EXT) or built_ext_abi() != abi)
+    os.makedirs(BUILD, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(1) as ex:
         made = ex.submit(_build_ext) if ext else None
         if lib:
@@ -88,7 +107,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def _build_lib(verbose):
     nvcc = _nvcc()
-    os.makedirs(BUILD, exist_ok=True)
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
