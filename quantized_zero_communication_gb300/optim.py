@@ -13,7 +13,8 @@ from . import binding as _b
 
 
 class AdamW:
-    """AdamW (decoupled weight decay) over a list of at most 1024 contiguous fp32 CUDA tensors.
+    """AdamW (decoupled weight decay) over a list of at most 1024 contiguous fp32 CUDA tensors (or a
+    single one, here and wherever a list is named).
 
     state_bits 32 holds both states in fp32; 8 holds m and sqrt(v) as float8_e4m3fn codes
     with one fp32 scale per 256 elements, rounded stochastically from `seed` and the step
@@ -28,7 +29,8 @@ class AdamW:
                  step=0):
         torch = _b._torch()
         f32 = (_b.ZPP_F32,)
-        self.params = list(params)
+        as_list = lambda ts: [ts] if isinstance(ts, torch.Tensor) else list(ts)  # noqa: E731
+        self.params = as_list(params)
         if not self.params:
             raise ValueError("AdamW needs at least one tensor")
         if len(self.params) > _b.ZPP_MAX_TENSORS:
@@ -50,7 +52,7 @@ class AdamW:
 
         def states(given, sizes, dtype):
             if given is not None:
-                return list(given)
+                return as_list(given)
             # one buffer, every tensor's part 256 elements aligned
             at, end = [], 0
             for n in sizes:
@@ -67,7 +69,7 @@ class AdamW:
         if state_bits == 8:
             self.scales = tuple(states(s, self._blocks, torch.float32)
                                 for s in (scales or (None, None)))
-        self.weights = None if weights is None else list(weights)
+        self.weights = None if weights is None else as_list(weights)
         state = f32 if state_bits == 32 else (_b._E4M3,)
         self._lists = [("params", 0, self.params, self._sizes, f32),
                        ("exp_avg", 2, self.exp_avg, self._sizes, state),
