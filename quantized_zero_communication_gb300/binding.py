@@ -628,7 +628,7 @@ _GRAD_KINDS = (ZPP_F16, ZPP_BF16, ZPP_F32)
 
 
 def grad_norm(grads, max_norm=None, pre_scale=1.0, out=None):
-    """The global norm of a list of gradient tensors (one fp16 / bf16 / fp32 dtype) times
+    """The norm of a list of gradient tensors together (one fp16 / bf16 / fp32 dtype) times
     |pre_scale|, and the factor that clips it to `max_norm` (None: no clipping) with
     pre_scale folded in -> fp32 [2] (norm, factor) on the device. The factor is NaN when the
     norm is not finite: adamw_step then skips the step."""

@@ -129,11 +129,20 @@ class AdamW:
     def step(self, grads, *, max_norm=None, pre_scale=None, grad_scale=None, lr=None):
         """One step with `grads` (contiguous, one of fp16 / bf16 / fp32, in the parameters'
         order). max_norm and / or pre_scale: the gradients are multiplied by pre_scale (say 1 /
-        loss scale) and clipped to the global norm max_norm, and fp32 [2] (norm, factor) is
-        returned; a norm that is not finite leaves parameters, states and the count of steps as
-        they were. grad_scale: instead, an fp32 device tensor whose first element multiplies the
-        gradients (the factor of a norm taken over several ranks). lr replaces the
-        optimiser's for this step and the following ones."""
+        loss scale) and clipped to max_norm, the norm of these gradients together, and fp32 [2]
+        (norm, factor) is returned; a norm that is not finite leaves parameters, states and the count
+        of steps as they were. grad_scale: instead, an fp32 device tensor whose first element
+        multiplies the gradients. A rank that owns a slice of a model needs that form: the factor
+        has to be the same on all ranks, so their norms' squares are added up first (an
+        all-reduce), and a total that is not finite has to give NaN:
+
+            square = zpp.grad_norm(grads)[0].square()
+            torch.distributed.all_reduce(square)
+            total = square.sqrt()
+            factor = torch.where(total.isfinite(), (max_norm / total).clamp(max=1.0), math.nan)
+            opt.step(grads, grad_scale=factor.reshape(1))
+
+        lr replaces the optimiser's for this step and the following ones."""
         torch = _b._torch()
         grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
         self._gather()
