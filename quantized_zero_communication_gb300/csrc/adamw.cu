@@ -14,7 +14,7 @@
 // TB/s over 28 bytes each. 8-bit states (16.06 bytes) are bound by instruction issue, some 80 per
 // element: 268,435,456 elements 680 us, 6.34 TB/s, issue slots 79 % busy; a warp takes two blocks
 // there so that the loads of one cover the arithmetic of the other. A short list is bound by the
-// call: 1024 elements 6.3 us, 1.8 of them on the device.
+// call: 1024 elements 5.6 us, 1.8 of them on the device.
 #include <cuda_fp8.h>
 
 #include "zpp_device.cuh"
@@ -146,13 +146,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// sqrt(v) for v = 0 and for normal v by one Newton step from the approximate reciprocal root y:
-// s = v y, then s + (v - s^2) y / 2, whose residual is exact in a fused multiply-add. The error
-// before the last rounding is the square of y's, 2^-44, so the result is the correctly rounded
-// root but for about two values in a million. It costs 7 instructions where the correctly
-// rounded one, with its range checks, costs about 13: 10 % of the whole step with 8-bit states.
-// v below 2^-126 gives a root below 2^-63, too small by up to a factor of 2000; an infinite v
-// gives NaN.
+// sqrt(v) for v = 0 and for normal v by one Newton step with a fused residual (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, IBM J. Res. Dev. 34,
+// 1990) from the approximate reciprocal root y: s = v y, then s + (v - s^2) y / 2. From v = 2^-102 on
+// the residual is exact and the error before the last rounding below 2^-44, so the result is the
+// correctly rounded root but for 2^-19 of the values at most; down to 2^-126 it is within one ulp. 268,435,456
+// elements with 8-bit states: 680 us, 747 with __fsqrt_rn. v below 2^-126 gives a root below 2^-63,
+// too small by up to a factor of 2000; an infinite v gives NaN.
 __device__ __forceinline__ float sqrt_newton(float v) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 1.17549435e-38f)));
@@ -170,8 +170,9 @@ struct Factors {
 };
 
 // One element: p, m, v updated in place, root = sqrt(v). For the states every operation is
-// rounded by itself (no fused multiply-add), so that codes can be reproduced bit for bit by
-// elementary fp32 arithmetic. The quotient needs no such care: a reciprocal within one ulp.
+// rounded by itself (no fused multiply-add), so that m and v, and the codes and scales of m, can be
+// reproduced bit for bit by elementary fp32 arithmetic; those of the root but where it is not the
+// rounded one. The quotient needs no such care: a reciprocal within one ulp.
 template <bool FP8, bool COUNTED>
 __device__ __forceinline__ void update(const AdamwArgs& a, const Factors<COUNTED>& f, float g, float& p,
                                        float& m, float& v, float& root) {
