@@ -393,8 +393,8 @@ typedef struct zpp_adamw_clip {
  * zpp_adamw_step, counted: a step that a non-finite factor skips has no number, so bias
  * corrections and rounding bits go on from the last step that was taken. Nobody on the host
  * needs to know which ones were, and a captured step is the next one each time it is replayed.
- *   hp->step    : 0: this step is number record->step + 1 (nothing has to be in flight to it but
- *                 work on `stream`); >= 1: its number, where the caller knows it
+ *   hp->step    : 0: this step is number record->step + 1, read in the stream's order; >= 1: its
+ *                 number, where the caller knows it
  *   grad_scale  : as above; clip: NULL, or the factor comes from the norm of the gradients, left
  *                 in clip->out (HOST struct, read during the call; then grad_scale is NULL)
  *   record      : device; afterwards record->step is this step's number, or one less if it was
@@ -411,7 +411,9 @@ ZPP_API zpp_status zpp_adamw_step_counted(const zpp_adamw_tensor* tensors, int32
  * y = x W^T (+ bias) for a few vectors x, straight from the codes of a [rows][cols] matrix
  * quantised row-major by zpp_quant_blockwise (blocks may run across rows):
  *   y[j][r] = sum_c q[r][c] * scales[(r * cols + c) / block] * x[j][c]  (+ bias[r])
- * Products and sums are fp32 (code times x is exact), y is rounded once.
+ * Products and sums are fp32 (code times x is exact), y is rounded once. A scale multiplies the sum
+ * of its block's products, or of a part of them: an infinite one gives infinity of that sum's sign,
+ * or NaN where the sum is 0.
  *   codes, scales : as zpp_quant_blockwise writes them for n = rows * cols <= ZPP_MAX_ELEMS
  *   rows, cols    : 0 <= rows < 2^31, 1 <= cols < 2^31; block, bits as in zpp_quant_blockwise
  *   x             : [vecs] rows of cols elements of x_dt (ZPP_F16 or ZPP_BF16; ZPP_F32 ->

@@ -8,11 +8,14 @@
 // 8 vectors, and products (exact) and sums are fp32. (The warp-level matrix instruction, since one
 // vector fills an eighth of even its tile: what counts is that codes go from registers to the unit.)
 //
-// Measured (us; bytes at 6.78 TB/s in brackets): 24576 x 8192 INT4, one vector 24 (15.8); 8192 x
-// 32768 INT4, 8 vectors 39 (20.4); 8192 x 8192 INT8 12.6 (9.9); 50001 x 1003 INT4, 3 vectors, rows
-// that start inside words 15.7 (4.3); 1024 x 1024 4, which is the launch. Loads alone, in this
-// pattern, take 17 us for the first: the rest is the chain of each warp from shared memory through
-// the conversion to the matrix unit, of which registers let only four run per scheduler.
+// Measured (us; bytes at 6.78 TB/s in brackets): 24576 x 8192 INT4, one vector 24.9 (15.8); 8192 x
+// 32768 INT4, 8 vectors 38.2 (20.4); 8192 x 8192 INT8 13.1 (9.9); 50001 x 1003 INT4, 3 vectors, rows
+// that start inside words 15.7 (4.3); 1024 x 1024 3.9, which is the launch. Loads alone, in this
+// pattern, take 17 us for the first. In the rest no unit is saturated (issue slots 52 % busy, the
+// matrix unit 26 %): a warp waits for its own chain from shared memory through the conversion to
+// the matrix unit, and two CTAs of 124 registers fit an SM, four warps per scheduler. (Whether more
+// warps of fewer registers would be faster has not been measured.) The times beside the rules
+// below are of captured graphs, weights beyond L2.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -50,8 +53,8 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b, BF16) {
       __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// The constants come as kernel arguments: as immediates the compiler rebuilds one of them in a
-// register before every use.
+// The constants come as kernel arguments. (As immediates 24576 x 8192 INT4 takes 24.2 us with one
+// vector, 38.5 with eight, so 24.6 and 37.8; 8192 x 32768, 8 vectors 36.7, so 37.8.)
 __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t flip) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(mask), "r"(flip));
@@ -394,11 +397,12 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 3 : 2)
 // fragment is 16 of them CH apart. Where rows start at words (WORDS: the width and x's stride are
 // multiples of 8 INT4, 4 INT8 columns) a lane reads its words of x where they are; else x is laid
 // out in shared memory, shifted, as fragments, by each CTA, which costs more than the products from
-// four vectors on. (24576 x 8224 INT4, 1 / 8 vectors: in place 43 / 45 us, laid out 40 / 98; 2861 x
-// 20896: 22 / 23 and 22 / 62; 5120 x 1288 INT8: 6.5 / 6.7 and 6.6 / 11.) Blocks begin at other
+// four vectors on. (24576 x 8224 INT4, 1 / 8 vectors: in place 43 / 46 us, laid out 39 / 55; 2861 x
+// 20896: 22 / 23 and 22 / 39; 5120 x 1288 INT8: 6.5 / 6.7 and 6.7 / 12.) Blocks begin at other
 // columns in every row, so a product covers one chunk and is scaled per row and chunk; lane (g, t)
 // takes word t of the chunks of rows g and g + 8. Two sets of 8 vectors share the codes where there
-// are more than 8 (NT = 2: 24576 x 8224, 16 vectors 61 us from 79).
+// are more than 8 (NT = 2: 24576 x 8224, 16 vectors 61 us from 80; its INT4 form with x in place
+// spills 16 to 20 bytes per lane, the BF16 INT4 form of NT = 1 with x laid out 8).
 //
 // A stage is four chunks of a warp's 16 rows; a lane copies chunk t of its two rows, and its
 // scales, but reads word t of all four (the copies are swapped so that this is free of bank
@@ -411,7 +415,7 @@ struct AnyShape {
   static constexpr int PW = 16 / BITS;       // pairs per word
   static constexpr int XB = WC * 2;          // bytes of a word's columns of x
   static constexpr int STAGE = 2 * 512 + 2 * 128;  // codes, scales
-  static constexpr int DEPTH = 3;            // stages on their way (with 4: 50001 x 1003 16.5 us, not 16.0)
+  static constexpr int DEPTH = 3;            // stages on their way (with 4: 50001 x 1003 16.7 us, not 15.9)
   static constexpr int RING = DEPTH * STAGE;
 };
 // Stages of a row and a CTA's share of them (at most, over its warps and ranks).
@@ -709,9 +713,12 @@ static cudaError_t run_mma(const MatvecArgs& a, int log2b, const MvPlan& p, cuda
 }
 
 // `base` warps a row where it has as many units, then more warps and CTAs until some 13 warps per
-// SM have work, never more than units. (8192 x 8192 INT4, one vector, base 4: 2 / 4 / 8 warps
-// 15.4 / 12.3 / 14.7 us; 1024 x 16384, 8 warps: 1 / 2 / 4 CTAs 9.4 / 8.2 / 10.2 us; 32768 x 1024,
-// one unit a row: 1 / 2 warps 8.2 / 10.3 us.)
+// SM have work, never more than units. (INT4, 1 / 2 / 4 / 8 warps a row, us. One vector: 24576 x 8192
+// 34.3 / 29.3 / 24.6 / 25.2, rule 4; 8192 x 8192 31.0 / 17.9 / 11.2 / 10.1, rule 8; 1024 x 16384, 8
+// warps in 1 / 2 / 4 CTAs 6.8 / 5.5 / 8.7, rule 2; 32768 x 1024, 1 / 2 / 4 warps 6.8 / 6.7 / 11.6, rule
+// 1. Four vectors, 8192 x 32768: 167 / 89 / 48 / 34, eight 214 / 120 / 64 / 38, sixteen 278 / 142 / 76 / 55,
+// rule 8; one warp in each of 4 CTAs 48, 63 and 82. The rule is not the best of 24576 x 8192 with eight
+// vectors: 57 / 38 / 38 / 34, rule 4.)
 static MvPlan mv_plan(int64_t tiles, int64_t units, int base, bool ctas_first = false) {
   MvPlan p{1, 1};
   constexpr int64_t kBusy = 2000;
@@ -730,11 +737,12 @@ static cudaError_t run_any(const MatvecArgs& a, int log2b, cudaStream_t s) {
   const int64_t groups = ((a.rows + S::CH - 1) / S::CH + 15) / 16;  // tiles of one shift
   const bool words = a.cols % S::WC == 0 && a.x_stride % S::WC == 0;
   // A CTA that lays x out does so for all its tiles: with four vectors or more fewer warps share a
-  // row, so that a CTA has more tiles, and CTAs come before warps. (30000 x 6001, 8 vectors: 1 / 2 /
-  // 4 warps 54 / 65 / 90 us; 2861 x 20897, 8 vectors: CTAs first 39, warps first 66; but 4 vectors of
-  // the first 54 / 47 / 56, and one vector, with an earlier kernel, 2 / 4 / 8 warps 41.8 / 38.9 / 41.0;
-  // and 5121 x 1283 INT8, 13 vectors, CTAs first 14.7, warps first 12.8.) Short rows: 50001 x 1003, 9
-  // stages a row, 4 vectors 1 / 2 warps 17.8 / 17.0 us, 13 vectors 20.8 / 26.7.
+  // row, so that a CTA has more tiles, and CTAs come before warps. (30000 x 6001, 1 / 2 / 4 warps:
+  // 8 vectors 54 / 64 / 90 us, rule 1; 4 vectors 43 / 47 / 56, rule 2; one vector 2 / 4 / 8 warps 36.8 / 35.7
+  // / 38.7, rule 4. 2861 x 20897, 8 vectors: 8 warps of one CTA 66, one of 8 CTAs 37, two of 4, the
+  // rule, 39; 13 vectors 83 / 34 / 45. 5121 x 1283 INT8, 13 vectors: one warp of 8 CTAs, the rule, 13.8,
+  // 8 warps of one CTA 13.0, two of 2 12.1.) Short rows: 50001 x 1003, 9 stages a row, 1 / 2 warps: 4
+  // vectors 17.7 / 16.8 us, rule 2; 13 vectors 21.2 / 27.0, rule 1.
   const int stages = any_stages(a.cols, S::CH);
   const bool lay_out = !words && a.vecs > 3;
   const int base = stages < 16 ? (!words && a.vecs > 8 ? 1 : 2) : !lay_out ? 4 : a.vecs > 4 ? 1 : 2;
@@ -787,10 +795,12 @@ static cudaError_t run_planned(const MatvecArgs& a, int log2b, cudaStream_t s) {
 
 // Two fragments of rows per warp share every load and permutation of x. One vector has little of
 // those, so there the second fragment pays only once some seven warps per SM have a unit to do.
-// (One vector, one / two fragments: 24576 x 8192 25.0 / 23.9 us, 8192 x 8192 12.4 / 9.7; but 4096
-// x 4096 5.0 / 5.9, 2048 x 2048 INT8 4.0 / 5.9 us. Four vectors: 2048 x 2048 INT8 6.3 / 4.0, 4096 x
-// 4096 6.2 / 5.2.) More than eight vectors of blocks of 64 take one: four sets of results of 32
-// rows do not fit the registers.
+// (One vector, one / two fragments: 24576 x 8192 24.7 / 24.6 us, 8192 x 8192 13.4 / 10.1; but 4096
+// x 4096 4.8 / 6.6, 2048 x 2048 INT8 3.8 / 5.4 us. Four vectors: 2048 x 2048 INT8 4.7 / 3.9, 4096 x
+// 4096 6.1 / 5.3, 8192 x 8192 15.8 / 11.1.) More than eight vectors of blocks of 64 take one: four
+// sets of results of 32 rows do not fit the registers. Some INT4 forms in use spill all the same:
+// with 9 to 16 vectors 20 to 56 bytes per lane, fp16 with 5 to 8 vectors of blocks of 64 16, fp16 with
+// one vector and one fragment 8; INT8 forms none.
 template <typename TT, int BITS, int SP>
 static cudaError_t by_vecs(const MatvecArgs& a, int log2b, cudaStream_t s) {
   if (a.vecs == 1) {

@@ -175,9 +175,9 @@ struct AdamwTableOf {
   AdamwTensor t[CAP];
 };
 using AdamwTable = AdamwTableOf<kAdamwTensors>;
-// The parameter space is said to hold 32,764 bytes, but a build of k_adamw whose hints lay at its
-// byte 32,264 (behind 448 tensors, with fp32 states) found zeros there, and so the first tensor only.
-// So the table, with the 1 KB that precede the parameters, ends before 32 KB, the tensors last.
+// The parameter space is said to hold 32,764 bytes, but a build of k_adamw whose hints lay at its byte
+// 32,264 (behind 448 tensors, with fp32 states) stepped the first tensor of every list only; the
+// same code with the hints in front steps all. So the table ends before 31 KB, the tensors last.
 static_assert(sizeof(AdamwTable) <= 31 * 1024, "kernel parameter space");
 constexpr int adamw_warp_blocks(int state_bits) { return state_bits == 8 ? 2 : 1; }
 constexpr int adamw_chunk(int state_bits) {  // elements per CTA of 8 warps
