@@ -20,8 +20,8 @@ class AdamW:
     with one fp32 scale per 256 elements, rounded stochastically from `seed` and the step
     (see include/zpp.h). weights: fp16 or bf16 tensors of the parameters' sizes that each
     step fills, or None. exp_avg, exp_avg_sq, scales and step resume from a saved state()
-    (the tensors are taken over, not copied); by default the states start at zero. One
-    optimiser's steps belong on one stream at a time.
+    (the tensors are taken over, not copied); by default the states start at zero. An optimiser is
+    made and stepped on one stream, or on streams that wait for each other.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *,
@@ -90,7 +90,8 @@ class AdamW:
         # The number of the last step on the device (zpp_adamw_record), and here as long as no step
         # may have been skipped: _known is None afterwards.
         self._record = torch.zeros(8, dtype=torch.int64, device=self.params[0].device)
-        self._record[:1].fill_(step)
+        if step:
+            self._record[:1].fill_(step)
         self._known = step
 
     @property
