@@ -33,7 +33,7 @@
  * Conventions for every entry point:
  *   - All buffer pointers are DEVICE pointers owned by the caller. The library
  *     allocates nothing, never synchronises, and only enqueues kernels on `stream`
- *     (0 = the legacy default stream).
+ *     (0 = the legacy default stream). The stream's device has to be the current one.
  *   - Inputs and outputs must not overlap.
  *   - Arguments are checked on the host before any launch; on an error nothing is
  *     launched and nothing is written.
@@ -398,7 +398,7 @@ typedef struct zpp_adamw_clip {
  *   grad_scale  : as above; clip: NULL, or the factor comes from the norm of the gradients, left
  *                 in clip->out (HOST struct, read during the call; then grad_scale is NULL)
  *   record      : device; afterwards record->step is this step's number, or one less if it was
- *                 skipped
+ *                 skipped (a list without elements counts too)
  * Every argument is checked before the first launch. The rest as zpp_adamw_step.
  */
 ZPP_API zpp_status zpp_adamw_step_counted(const zpp_adamw_tensor* tensors, int32_t num_tensors,
