@@ -430,6 +430,53 @@ ZPP_API zpp_status zpp_matvec_blockwise(const void* codes, const float* scales, 
                                         const void* bias, void* y, zpp_dtype y_dt,
                                         int64_t y_stride, cudaStream_t stream);
 
+/*
+ * Matrices of e4m3 codes with a scale per block, and their products: the arithmetic of a linear layer
+ * that trains or answers in 8 bits (no counterpart in the pages). value = code * scale.
+ */
+#define ZPP_FP8_BLOCK 128 /* columns that share a scale */
+
+/* A matrix of codes, row-major; all pointers are device pointers. */
+typedef struct zpp_fp8_matrix {
+  void* codes;         /* 16-byte aligned; row r at codes + r * stride */
+  float* scales;       /* of element (r, c): scales[(r / tile) * scale_row + (c / 128) * scale_block] */
+  int64_t rows, cols;  /* 0 <= rows < 2^31, 1 <= cols < 2^31, rows * cols <= ZPP_MAX_ELEMS */
+  int64_t stride;      /* bytes between rows: a multiple of 16, cols <= stride <= ZPP_MAX_ELEMS */
+  int64_t scale_row, scale_block; /* >= 0, at most ZPP_MAX_ELEMS */
+  int32_t tile;        /* rows that share a scale: 1 or 128 */
+} zpp_fp8_matrix;
+
+/*
+ * A matrix to codes, and its transpose with it: a backward pass multiplies along the other index.
+ * Per block (128 columns of `tile` rows; those at the edges are smaller), amax over finite values:
+ *   scale = the smallest 2^e, e >= -126, with amax <= 448 * 2^e  (amax 0: scale 0, codes 0)
+ *   code  = x / scale rounded to nearest even (exact but for that: the scale is a power of two)
+ * An infinite or NaN value has the code NaN (0x7f or 0xff).
+ *   x            : [rows][cols] of x_dt (any zpp_dtype), row r at x + r * x_stride elements,
+ *                  cols <= x_stride <= ZPP_MAX_ELEMS, aligned to its elements
+ *   out          : HOST struct, read during the call; bytes between cols and stride are left as they were
+ *   transposed   : HOST struct or NULL; rows and cols are out's cols and rows, tile is out's. With tile 1
+ *                  its blocks are 128 rows of a column of x. With tile 128 a tile's scale is also that
+ *                  of its transpose: scales is not written (read out's with the strides exchanged).
+ */
+ZPP_API zpp_status zpp_quant_fp8(const void* x, zpp_dtype x_dt, int64_t x_stride,
+                                 const zpp_fp8_matrix* out, const zpp_fp8_matrix* transposed,
+                                 cudaStream_t stream);
+
+/*
+ * y = a b^T (+ bias): y[m][n] = sum_k a[m][k] b[n][k] (+ bias[n]) of the values that the codes stand
+ * for. Sums are fp32: of the codes within a block of 128, then of the blocks times both scales, in
+ * ascending order; y is rounded once. NaN codes and non-finite scales give what such values give.
+ *   a, b : HOST structs, read during the call; cols is the same in both. One may be the other
+ *   bias : NULL or [b.rows] of y_dt
+ *   y    : out, [a.rows][b.rows] of y_dt (any zpp_dtype), row m at y + m * y_stride elements,
+ *          b.rows <= y_stride <= ZPP_MAX_ELEMS; y and bias are aligned to their elements
+ * The products run on the tensor cores (waits inside: see zpp_device_fault). The call takes its
+ * kernel by the sizes: for few rows of a it is bound by reading b.
+ */
+ZPP_API zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix* b, const void* bias,
+                                  void* y, zpp_dtype y_dt, int64_t y_stride, cudaStream_t stream);
+
 /* Bytes of packed codes for n elements: n for INT8, ceil(n/2) for INT4; -1 on bad bits. */
 ZPP_API int64_t zpp_code_bytes(int64_t n, int32_t bits);
 
@@ -444,7 +491,8 @@ ZPP_API const char* zpp_status_string(zpp_status status);
  * data in flight (the INT8 fused-hop kernel waits on shared-memory barriers completed by
  * bulk copies) bound every wait to about a second; a wait that runs out sets a bit here,
  * the kernel still ends, and its outputs are unspecified. Bits: 1 and 2 -- a wait of the
- * INT8 fused hop ran out; 4 -- zpp_wait_selftest ran out (as it always does).
+ * INT8 fused hop ran out; 4 -- zpp_wait_selftest ran out (as it always does); 8 -- a wait of
+ * zpp_matmul_fp8.
  *   flags : out, the word (0 when nothing ran out since the last clear)
  *   clear : nonzero -> zero the word after reading it
  * Unlike the other calls this one synchronises with the device (it copies the word back);

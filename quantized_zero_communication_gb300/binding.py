@@ -48,6 +48,13 @@ class AdamwClip(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
+class Fp8Matrix(ctypes.Structure):
+    """A matrix of e4m3 codes (zpp_fp8_matrix): device addresses, sizes and strides."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("rows", "cols", "stride", "scale_row", "scale_block")] + [
+        ("tile", ctypes.c_int32)]
+
+
 class ZppError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -97,6 +104,8 @@ def lib():
         "zpp_adamw_step_counted": [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp],
         "zpp_matvec_blockwise": [vp, vp, i64, i64, i32, i32, vp, i32, i64, i64, vp, vp, i32, i64,
                                  vp],
+        "zpp_quant_fp8": [vp, i32, i64, vp, vp, vp],
+        "zpp_matmul_fp8": [vp, vp, vp, vp, i32, i64, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -250,6 +259,18 @@ def zpp_matvec_blockwise(codes, scales, rows, cols, block, bits, x, x_dt, vecs, 
                          y_dt, y_stride, stream=0):
     return lib().zpp_matvec_blockwise(codes, scales, rows, cols, block, bits, x, x_dt, vecs,
                                       x_stride, bias, y, y_dt, y_stride, stream)
+
+
+def zpp_quant_fp8(x, x_dt, x_stride, out, transposed=None, stream=0):
+    """out, transposed: Fp8Matrix (transposed: or None)."""
+    return lib().zpp_quant_fp8(x, x_dt, x_stride, ctypes.addressof(out),
+                               ctypes.addressof(transposed) if transposed else 0, stream)
+
+
+def zpp_matmul_fp8(a, b, bias, y, y_dt, y_stride, stream=0):
+    """a, b: Fp8Matrix."""
+    return lib().zpp_matmul_fp8(ctypes.addressof(a), ctypes.addressof(b), bias, y, y_dt, y_stride,
+                                stream)
 
 
 def zpp_code_bytes(n, bits):
@@ -814,6 +835,162 @@ def _rows(t, name):
     if t.dim() != 2 or (t.stride(1) != 1 and cols > 1) or t.stride(0) < cols:
         raise ValueError(f"{name}: rows must be contiguous and at least a row apart")
     return t.shape[0], t.stride(0)
+
+
+FP8_BLOCK = 128  # columns that share a scale
+
+
+def _matrix(t, name):
+    """A tensor [..., cols] as rows of contiguous elements, evenly spaced: (rows, cols, row stride)."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name}: [..., cols] with cols >= 1")
+    if not t.numel():
+        return 0, t.shape[-1], t.shape[-1]
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{name}: rows must be evenly spaced") from None
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be at least a row apart")
+    return rows, cols, t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _fp8(codes, scales, name, tile=None):
+    """The Fp8Matrix of a tensor of codes and its scales ([rows or row tiles, blocks], any strides). The
+    scales' shape says which tiles they are for."""
+    torch = _torch()
+    _need(codes, name, dtypes=(torch.float8_e4m3fn,))
+    _need(scales, f"{name}_scales", dtypes=(torch.float32,))
+    rows, cols, stride = _matrix(codes, name)
+    if rows <= 1:
+        stride = -(-stride // 16) * 16  # (one row may end anywhere)
+    blocks, tiles = -(-cols // FP8_BLOCK), -(-rows // FP8_BLOCK)
+    shape = tuple(scales.shape)
+    if shape == (rows, blocks) and tile != 128:
+        tile = 1
+    elif shape == (tiles, blocks) and tile != 1:
+        tile = 128
+    else:
+        raise ValueError(f"{name}_scales: {shape}, expected one of "
+                         f"{tuple(((rows, blocks), (tiles, blocks)))}")
+    if stride % 16 or (rows and codes.data_ptr() % 16):
+        raise ValueError(f"{name}: rows of codes start at multiples of 16 bytes, as quant_fp8 lays them")
+    return Fp8Matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, stride, scales.stride(0),
+                     scales.stride(1), tile)
+
+
+def _on_gpu(*ts):
+    """The index of the CUDA device that all tensors are on."""
+    if not all(t.is_cuda for t in ts):
+        raise ValueError("zpp operates on CUDA tensors only (no CPU path)")
+    if any(t.device != ts[0].device for t in ts):
+        raise ValueError("all tensors of a call must be on one device")
+    return ts[0].get_device()
+
+
+def _written(*ts):
+    """Marks a caller's buffers as written, so that a backward pass that kept their old contents
+    raises."""
+    mark = _torch().autograd.graph.increment_version
+    for t in ts:
+        if not t.is_inference():
+            mark(t)
+
+
+def _codes_like(shape, device):
+    """New e4m3 codes whose rows start at multiples of 16 bytes."""
+    torch = _torch()
+    wide = -(-shape[-1] // 16) * 16
+    return torch.empty((*shape[:-1], wide), dtype=torch.float8_e4m3fn, device=device)[..., :shape[-1]]
+
+
+def quant_fp8(x, tile=1, transposed=False, out=None):
+    """x [..., cols] (fp16 / bf16 / fp32; rows of contiguous elements, evenly spaced) -> (codes, scales):
+    codes float8_e4m3fn of x's shape, rows at multiples of 16 bytes, and power-of-two scales fp32,
+    [rows, ceil(cols / 128)] with tile 1 (a scale for each row and 128 columns: activations, gradients),
+    [ceil(rows / 128), ceil(cols / 128)] with tile 128 (weights). value = code * scale.
+
+    transposed: also (codes_t [cols, rows], scales_t) of the transposed matrix, made in the same pass.
+    With tile 1 its blocks are 128 rows of a column; with tile 128 scales_t is a view of scales. out: the
+    buffers to write, a tuple as an earlier call returned it."""
+    torch = _torch()
+    _need(x, "x", dtypes=(torch.float16, torch.bfloat16, torch.float32))
+    if tile not in (1, 128):
+        raise ValueError("tile: 1 or 128")
+    rows, cols, stride = _matrix(x, "x")
+    device = _on_gpu(x)
+    blocks, tiles = -(-cols // FP8_BLOCK), -(-rows // FP8_BLOCK)
+    given = out is not None
+    if not given:
+        codes = _codes_like(x.shape, x.device)
+        scales = (x.new_empty((blocks, rows), dtype=torch.float32).t() if tile == 1 else
+                  x.new_empty((tiles, blocks), dtype=torch.float32))
+        out = (codes, scales)
+        if transposed and rows:
+            out += (_codes_like((cols, rows), x.device),
+                    x.new_empty((tiles, cols), dtype=torch.float32).t() if tile == 1 else scales.t())
+        elif transposed:  # a matrix without rows: nothing to hold
+            out += (codes.new_empty((cols, 0)), scales.new_empty((cols if tile == 1 else blocks, 0)))
+    elif len(out) != (4 if transposed else 2):
+        raise ValueError(f"out: {4 if transposed else 2} tensors, as an earlier call returned them")
+    _on_gpu(x, *out)
+    if out[0].shape != x.shape:
+        raise ValueError(f"out: codes of {tuple(out[0].shape)} do not fit x")
+    to = _fp8(out[0], out[1], "codes", tile)
+    to_t = None
+    if transposed and rows:
+        if tuple(out[2].shape) != (cols, rows):
+            raise ValueError(f"out: transposed codes of {tuple(out[2].shape)} do not fit x")
+        to_t = _fp8(out[2], out[3], "codes_t", tile)
+        if tile == 128 and (to_t.scales, to_t.scale_row, to_t.scale_block) != (
+                to.scales, to.scale_block, to.scale_row):
+            raise ValueError("out: with tile 128 the transposed scales are those of the codes, transposed")
+    _launch(device, "zpp_quant_fp8", x.data_ptr(), _dt(x.dtype), stride, ctypes.addressof(to),
+            ctypes.addressof(to_t) if to_t else 0)
+    if given:
+        _written(*out)
+    return tuple(out)
+
+
+def matmul_fp8(a, a_scales, b, b_scales, bias=None, dtype=None, y=None):
+    """a [..., K] times the transpose of b [N, K], both e4m3 codes with scales as quant_fp8 gives them
+    (any fp32 scales of those shapes, any strides) -> y [..., N] of `dtype` (default bf16; fp16 and
+    fp32 too). bias: [N] of y's dtype. y: an output buffer, rows of contiguous elements evenly spaced."""
+    torch = _torch()
+    pa, pb = _fp8(a, a_scales, "a"), _fp8(b, b_scales, "b")
+    if b.dim() != 2 or pa.cols != pb.cols:
+        raise ValueError(f"b: {tuple(b.shape)}, expected [N, {pa.cols}]")
+    shape = (*a.shape[:-1], pb.rows)
+    tensors = [a, a_scales, b, b_scales]
+    given = y is not None
+    if given:
+        if tuple(y.shape) != shape or (dtype is not None and y.dtype != dtype):
+            raise ValueError(f"y: {tuple(y.shape)} of {y.dtype} does not fit the call")
+        _need(y, "y", dtypes=(torch.float16, torch.bfloat16, torch.float32))
+        tensors.append(y)
+    else:
+        if dtype is None:
+            dtype = torch.bfloat16
+        if dtype not in (torch.float16, torch.bfloat16, torch.float32):
+            raise ValueError(f"dtype: {dtype}, expected float16, bfloat16 or float32")
+    if bias is not None:
+        _need(bias, "bias", pb.rows, (dtype if y is None else y.dtype,))
+        if not bias.is_contiguous():
+            raise ValueError("zpp needs contiguous tensors")
+        tensors.append(bias)
+    device = _on_gpu(*tensors)
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=a.device)
+    y_stride = _matrix(y, "y")[2] if pb.rows else 0
+    _launch(device, "zpp_matmul_fp8", ctypes.addressof(pa), ctypes.addressof(pb),
+            0 if bias is None else bias.data_ptr(), y.data_ptr(), _dt(y.dtype), y_stride)
+    if given:
+        _written(y)
+    return y
 
 
 class QgzBuffers:

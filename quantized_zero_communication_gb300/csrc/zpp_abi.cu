@@ -551,10 +551,105 @@ zpp_status zpp_matvec_blockwise(const void* codes, const float* scales, int64_t 
   return from_cuda(zpp::launch_matvec(a, stream));
 }
 
+namespace {
+
+constexpr int64_t kDimEnd = int64_t{1} << 31;
+
+zpp_status check_fp8(const zpp_fp8_matrix* m) {
+  if (!m || (m->tile != 1 && m->tile != 128)) return ZPP_ERR_INVALID_ARG;
+  if (m->rows < 0 || m->rows >= kDimEnd || m->cols < 1 || m->cols >= kDimEnd ||
+      m->rows > ZPP_MAX_ELEMS / m->cols)
+    return ZPP_ERR_INVALID_ARG;
+  if (m->stride < m->cols || m->stride > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+  if (m->scale_row < 0 || m->scale_row > ZPP_MAX_ELEMS || m->scale_block < 0 ||
+      m->scale_block > ZPP_MAX_ELEMS)
+    return ZPP_ERR_INVALID_ARG;
+  return ZPP_OK;
+}
+zpp_status check_fp8_pointers(const zpp_fp8_matrix* m, bool scales) {
+  if (!m->codes || (scales && !m->scales)) return ZPP_ERR_INVALID_ARG;
+  if (!aligned(m->codes, 16) || m->stride % 16 != 0 || !aligned(m->scales, 4)) return ZPP_ERR_MISALIGNED;
+  return ZPP_OK;
+}
+uintptr_t size_of(zpp_dtype t) { return t == ZPP_F32 ? 4 : 2; }
+
+}  // namespace
+
+zpp_status zpp_quant_fp8(const void* x, zpp_dtype x_dt, int64_t x_stride, const zpp_fp8_matrix* out,
+                         const zpp_fp8_matrix* transposed, cudaStream_t stream) {
+  if (!valid_dtype(x_dt)) return ZPP_ERR_INVALID_ARG;
+  zpp_status st = check_fp8(out);
+  if (st != ZPP_OK) return st;
+  if (x_stride < out->cols || x_stride > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+  if (out->rows == 0) return ZPP_OK;
+  if (transposed) {
+    st = check_fp8(transposed);
+    if (st != ZPP_OK) return st;
+    if (transposed->rows != out->cols || transposed->cols != out->rows || transposed->tile != out->tile)
+      return ZPP_ERR_INVALID_ARG;
+  }
+  if (!x) return ZPP_ERR_INVALID_ARG;
+  st = check_fp8_pointers(out, true);
+  if (st == ZPP_OK && transposed) st = check_fp8_pointers(transposed, out->tile == 1);
+  if (st != ZPP_OK) return st;
+  if (!aligned(x, size_of(x_dt))) return ZPP_ERR_MISALIGNED;
+  zpp::QuantFp8Args a{};
+  a.x = x;
+  a.x_kind = static_cast<int32_t>(x_dt);
+  a.rows = out->rows;
+  a.cols = out->cols;
+  a.x_stride = x_stride;
+  a.tile = out->tile;
+  a.codes = static_cast<uint8_t*>(out->codes);
+  a.codes_stride = out->stride;
+  a.scales = out->scales;
+  a.scale_row = out->scale_row;
+  a.scale_block = out->scale_block;
+  if (transposed) {
+    a.codes_t = static_cast<uint8_t*>(transposed->codes);
+    a.codes_t_stride = transposed->stride;
+    a.scales_t = transposed->scales;
+    a.scale_t_row = transposed->scale_row;
+    a.scale_t_block = transposed->scale_block;
+  }
+  return from_cuda(zpp::launch_quant_fp8(a, stream));
+}
+
+zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix* b, const void* bias, void* y,
+                          zpp_dtype y_dt, int64_t y_stride, cudaStream_t stream) {
+  if (!valid_dtype(y_dt)) return ZPP_ERR_INVALID_ARG;
+  zpp_status st = check_fp8(a);
+  if (st == ZPP_OK) st = check_fp8(b);
+  if (st != ZPP_OK) return st;
+  if (a->cols != b->cols || y_stride < b->rows || y_stride > ZPP_MAX_ELEMS) return ZPP_ERR_INVALID_ARG;
+  if (a->rows == 0 || b->rows == 0) return ZPP_OK;
+  if (a->rows > ZPP_MAX_ELEMS / b->rows || !y) return ZPP_ERR_INVALID_ARG;
+  st = check_fp8_pointers(a, true);
+  if (st == ZPP_OK) st = check_fp8_pointers(b, true);
+  if (st != ZPP_OK) return st;
+  if (!aligned(y, size_of(y_dt)) || !aligned(bias, size_of(y_dt))) return ZPP_ERR_MISALIGNED;
+  const auto operand = [](const zpp_fp8_matrix* m) {
+    return zpp::MatmulOperand{static_cast<const uint8_t*>(m->codes), m->rows, m->stride, m->scales,
+                              m->scale_row, m->scale_block, m->tile};
+  };
+  zpp::MatmulArgs g{};
+  g.a = operand(a);
+  g.b = operand(b);
+  g.depth = a->cols;
+  g.bias = bias;
+  g.y = y;
+  g.y_kind = static_cast<int32_t>(y_dt);
+  g.y_stride = y_stride;
+  return from_cuda(zpp::launch_matmul_fp8(g, stream));
+}
+
 zpp_status zpp_device_fault(uint32_t* flags, int32_t clear) {
   if (!flags) return ZPP_ERR_INVALID_ARG;
   unsigned v = 0;
-  const zpp_status st = from_cuda(zpp::read_device_fault(&v, clear != 0));
+  zpp_status st = from_cuda(zpp::read_device_fault(&v, clear != 0));
+  unsigned w = 0;
+  if (st == ZPP_OK) st = from_cuda(zpp::read_matmul_fault(&w, clear != 0));
+  v |= w;
   *flags = st == ZPP_OK ? v : 0u;
   return st;
 }

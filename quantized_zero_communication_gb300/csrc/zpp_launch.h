@@ -207,6 +207,42 @@ struct MatvecArgs {
 };
 cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t s);
 
+// K10: y = a b^T (+ bias) of e4m3 matrices with a scale per block of 128 along the sum.
+struct MatmulOperand {
+  const uint8_t* codes;
+  int64_t rows, stride;  // stride in bytes
+  const float* scales;
+  int64_t scale_row, scale_block;
+  int32_t tile;          // rows that share a scale: 1 or 128
+};
+struct MatmulArgs {
+  MatmulOperand a, b;
+  int64_t depth;  // of the sum
+  const void* bias;
+  void* y;
+  int32_t y_kind;  // zpp_dtype of y and bias
+  int64_t y_stride;
+};
+cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s);
+cudaError_t read_matmul_fault(unsigned* flags, bool clear);
+
+// K11: e4m3 codes and power-of-two scales of a matrix, and of its transpose (codes_t null: not).
+struct QuantFp8Args {
+  const void* x;
+  int32_t x_kind;
+  int64_t rows, cols, x_stride;
+  int32_t tile;
+  uint8_t* codes;
+  int64_t codes_stride;
+  float* scales;
+  int64_t scale_row, scale_block;
+  uint8_t* codes_t;
+  int64_t codes_t_stride;
+  float* scales_t;  // tile 1 only
+  int64_t scale_t_row, scale_t_block;
+};
+cudaError_t launch_quant_fp8(const QuantFp8Args& a, cudaStream_t s);
+
 // Grid size when every CTA owns `per_cta` consecutive tiles and exits (no grid-stride
 // loop): on GB300 a streaming kernel launched this way sustains more HBM bandwidth than
 // a persistent grid sized to the SM count.

@@ -79,12 +79,14 @@ __device__ __forceinline__ U8x32 ld_after_vec32(const void* p) {
   return r;
 }
 
+// smem: dynamic shared memory.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_overlapped(void (*kern)(Params...), int grid, int threads, cudaStream_t s,
-                                     const Args&... args) {
+inline cudaError_t launch_overlapped_smem(void (*kern)(Params...), dim3 grid, int threads, int smem,
+                                          cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -92,6 +94,11 @@ inline cudaError_t launch_overlapped(void (*kern)(Params...), int grid, int thre
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped(void (*kern)(Params...), int grid, int threads, cudaStream_t s,
+                                     const Args&... args) {
+  return launch_overlapped_smem(kern, dim3(static_cast<unsigned>(grid)), threads, 0, s, args...);
 }
 
 }  // namespace zpp
