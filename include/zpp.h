@@ -477,6 +477,86 @@ ZPP_API zpp_status zpp_quant_fp8(const void* x, zpp_dtype x_dt, int64_t x_stride
 ZPP_API zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix* b, const void* bias,
                                   void* y, zpp_dtype y_dt, int64_t y_stride, cudaStream_t stream);
 
+/*
+ * Updates of matrices whose singular values are made nearly equal (no counterpart in the pages): beside
+ * the AdamW step for what is not a matrix.
+ *
+ * Newton-Schulz steps on a matrix x: X = x / max(|x|, eps), |x| the root of the sum of squares, then
+ * for each step k with (a, b, c) = coefficients[k]:
+ *   A = X X^T,  B = b A + c A A,  X = a X + B X
+ * (for a matrix with more rows than columns the same of its transpose). The products are those of
+ * fp16 operands with fp32 sums, the diagonals of A and B apart in fp32, and X with what fp16 loses of it
+ * in 16 further bits; a matrix with a side of at most 128 takes products of both parts. After the usual
+ * five steps some 1e-3 of the result's norm is error, 1e-5 for those small ones, hence the 16-bit
+ * types of a result. The largest singular value has to stay below 32 through the steps. |x| beyond
+ * fp32's range (of its squares) gives NaN.
+ */
+typedef struct zpp_newton_schulz {
+  const double* coefficients; /* HOST [steps][3], finite */
+  int32_t steps;              /* 1 .. 100 */
+  double eps;                 /* > 0, finite; one below 2^-126 counts as 2^-126 */
+} zpp_newton_schulz;
+
+#define ZPP_MAX_SIDE (((int64_t)1) << 30) /* rows and columns of a matrix below */
+
+typedef struct zpp_matrix {
+  const void* x;      /* [rows][cols] of x_dt, device, aligned to its elements */
+  void* out;          /* out, [rows][cols] of out_dt; may be x where the types are one */
+  int64_t rows, cols; /* 0 .. ZPP_MAX_SIDE, rows * cols <= ZPP_MAX_ELEMS; 0: no pointer is read */
+} zpp_matrix;
+
+/*
+ * The steps on a list of matrices; those of one shape share each launch's tiles.
+ *   list      : HOST array [num], read during the call only; num 0 .. ZPP_MAX_TENSORS
+ *   x_dt      : any zpp_dtype; out_dt: ZPP_F16 or ZPP_BF16 (ZPP_F32 -> ZPP_ERR_UNSUPPORTED)
+ *   workspace : device, 128-byte aligned, zpp_orthogonalize_workspace(list, num) bytes; not shared with
+ *               another stream's call in flight, nor by two captured graphs that may run at once
+ */
+ZPP_API zpp_status zpp_orthogonalize(const zpp_matrix* list, int32_t num, zpp_dtype x_dt,
+                                     zpp_dtype out_dt, const zpp_newton_schulz* ns, void* workspace,
+                                     cudaStream_t stream);
+
+/* Bytes of workspace; -1 on sizes that the call refuses. Only sizes are read, no pointers. */
+ZPP_API int64_t zpp_orthogonalize_workspace(const zpp_matrix* list, int32_t num);
+
+/* One matrix of a Muon step; all pointers are device pointers, aligned to their elements. */
+typedef struct zpp_muon_tensor {
+  float* param;       /* [rows][cols] fp32 master weights, updated */
+  const void* grad;   /* [rows][cols] of g_dt */
+  float* momentum;    /* [rows][cols], updated */
+  void* weight;       /* out, NULL or [rows][cols] of w_dt: the updated weights rounded */
+  int64_t rows, cols; /* as zpp_matrix */
+} zpp_muon_tensor;
+
+typedef struct zpp_muon_params {
+  double lr, momentum, weight_decay;
+  int32_t nesterov; /* 0 or 1 */
+  int32_t adjust;   /* ZPP_MUON_ORIGINAL, ZPP_MUON_MATCH_RMS_ADAMW or ZPP_MUON_NONE */
+  zpp_newton_schulz ns;
+} zpp_muon_params;
+
+#define ZPP_MUON_ORIGINAL 0        /* adj = sqrt(max(1, rows / cols)) */
+#define ZPP_MUON_MATCH_RMS_ADAMW 1 /* adj = 0.2 sqrt(max(rows, cols)) */
+#define ZPP_MUON_NONE 2            /* adj = 1 */
+
+/*
+ * One Muon step over a list of matrices. With c = *grad_scale (1 when NULL) and mu = momentum:
+ *   g = c * grad;  m = mu m + (1 - mu) g;  u = nesterov ? (1 - mu) g + mu m : m
+ *   param = param (1 - lr weight_decay) - lr adj X,  X = the Newton-Schulz steps on u
+ *   weight = param rounded to nearest even into w_dt
+ * If c is not finite the whole step is skipped: nothing is written. (zpp_grad_norm's factor is one.)
+ *   tensors   : HOST array [num], read during the call only; num 0 .. ZPP_MAX_TENSORS
+ *   g_dt      : any zpp_dtype; w_dt: ZPP_F16 or ZPP_BF16 (ZPP_F32 with a non-NULL weight:
+ *               ZPP_ERR_UNSUPPORTED)
+ *   hp        : HOST, read during the call: lr and weight_decay finite, 0 <= momentum < 1
+ *   grad_scale: device, 4-byte aligned, or NULL
+ *   workspace : as zpp_orthogonalize's, zpp_muon_workspace(tensors, num) bytes
+ */
+ZPP_API zpp_status zpp_muon_step(const zpp_muon_tensor* tensors, int32_t num, zpp_dtype g_dt,
+                                 zpp_dtype w_dt, const zpp_muon_params* hp, const float* grad_scale,
+                                 void* workspace, cudaStream_t stream);
+ZPP_API int64_t zpp_muon_workspace(const zpp_muon_tensor* tensors, int32_t num);
+
 /* Bytes of packed codes for n elements: n for INT8, ceil(n/2) for INT4; -1 on bad bits. */
 ZPP_API int64_t zpp_code_bytes(int64_t n, int32_t bits);
 
@@ -492,7 +572,7 @@ ZPP_API const char* zpp_status_string(zpp_status status);
  * bulk copies) bound every wait to about a second; a wait that runs out sets a bit here,
  * the kernel still ends, and its outputs are unspecified. Bits: 1 and 2 -- a wait of the
  * INT8 fused hop ran out; 4 -- zpp_wait_selftest ran out (as it always does); 8 -- a wait of
- * zpp_matmul_fp8.
+ * zpp_matmul_fp8; 16 -- a wait of zpp_orthogonalize or zpp_muon_step.
  *   flags : out, the word (0 when nothing ran out since the last clear)
  *   clear : nonzero -> zero the word after reading it
  * Unlike the other calls this one synchronises with the device (it copies the word back);

@@ -10,10 +10,10 @@ declared in ``include/zpp.h``.
 from .binding import (  # noqa: F401
     Fp8Matrix, LocalRange, QgzBuffers, Topology, ZppError, adamw_step, dequant_blockwise,
     dequant_reduce, dequant_reduce_local, dequant_reduce_requant, dequant_reduce_requant_local,
-    dequant_reduce_scaled, device_copy, grad_norm, matmul_fp8, matvec_blockwise, qgz_pipelined,
-    qgz_reorder_quant, qgz_reorder_quant_local, qgz_reorder_quant_tensors, quant_blockwise, quant_fp8,
-    zpp_code_bytes, zpp_device_fault, zpp_num_scales, zpp_status_string)
-from .optim import AdamW  # noqa: F401
+    dequant_reduce_scaled, device_copy, grad_norm, matmul_fp8, matvec_blockwise, orthogonalize,
+    qgz_pipelined, qgz_reorder_quant, qgz_reorder_quant_local, qgz_reorder_quant_tensors,
+    quant_blockwise, quant_fp8, zpp_code_bytes, zpp_device_fault, zpp_num_scales, zpp_status_string)
+from .optim import AdamW, Muon  # noqa: F401
 
 
 def __getattr__(name):  # (what needs torch when it is imported)

@@ -55,6 +55,28 @@ class Fp8Matrix(ctypes.Structure):
         ("tile", ctypes.c_int32)]
 
 
+class NewtonSchulz(ctypes.Structure):
+    """Steps, their coefficients (the address of [steps][3] doubles) and eps (zpp_newton_schulz)."""
+    _fields_ = [("coefficients", ctypes.c_void_p), ("steps", ctypes.c_int32), ("eps", ctypes.c_double)]
+
+
+class Matrix(ctypes.Structure):
+    """One matrix of zpp_orthogonalize."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
+class MuonTensor(ctypes.Structure):
+    """One matrix of zpp_muon_step (device addresses, sizes)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "momentum", "weight")] + [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class MuonParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "momentum", "weight_decay")] + [
+        ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32), ("ns", NewtonSchulz)]
+
+
 class ZppError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -106,6 +128,8 @@ def lib():
                                  vp],
         "zpp_quant_fp8": [vp, i32, i64, vp, vp, vp],
         "zpp_matmul_fp8": [vp, vp, vp, vp, i32, i64, vp],
+        "zpp_orthogonalize": [vp, i32, i32, i32, vp, vp, vp],
+        "zpp_muon_step": [vp, i32, i32, i32, vp, vp, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -117,6 +141,9 @@ def lib():
     L.zpp_num_scales.restype = i64
     L.zpp_grad_norm_workspace.argtypes = [i64, i32]
     L.zpp_grad_norm_workspace.restype = i64
+    for name in ("zpp_orthogonalize_workspace", "zpp_muon_workspace"):
+        getattr(L, name).argtypes = [vp, i32]
+        getattr(L, name).restype = i64
     L.zpp_status_string.argtypes = [ctypes.c_int]
     L.zpp_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -271,6 +298,35 @@ def zpp_matmul_fp8(a, b, bias, y, y_dt, y_stride, stream=0):
     """a, b: Fp8Matrix."""
     return lib().zpp_matmul_fp8(ctypes.addressof(a), ctypes.addressof(b), bias, y, y_dt, y_stride,
                                 stream)
+
+
+def _rows_of(kind, rows):
+    """(address of the C array of a sequence of structures, what keeps it alive)."""
+    fields = (kind * max(len(rows), 1))(*rows)
+    return ctypes.addressof(fields), fields
+
+
+def zpp_orthogonalize(matrices, x_dt, out_dt, ns, workspace, stream=0):
+    """matrices: a sequence of Matrix; ns: a NewtonSchulz."""
+    at, keep = _rows_of(Matrix, matrices)
+    return lib().zpp_orthogonalize(at, len(matrices), x_dt, out_dt, ctypes.addressof(ns), workspace, stream)
+
+
+def zpp_orthogonalize_workspace(matrices):
+    at, keep = _rows_of(Matrix, matrices)
+    return int(lib().zpp_orthogonalize_workspace(at, len(matrices)))
+
+
+def zpp_muon_step(tensors, g_dt, w_dt, hp, grad_scale, workspace, stream=0):
+    """tensors: a sequence of MuonTensor; hp: a MuonParams."""
+    at, keep = _rows_of(MuonTensor, tensors)
+    return lib().zpp_muon_step(at, len(tensors), g_dt, w_dt, ctypes.addressof(hp), grad_scale, workspace,
+                               stream)
+
+
+def zpp_muon_workspace(tensors):
+    at, keep = _rows_of(MuonTensor, tensors)
+    return int(lib().zpp_muon_workspace(at, len(tensors)))
 
 
 def zpp_code_bytes(n, bits):
@@ -991,6 +1047,67 @@ def matmul_fp8(a, a_scales, b, b_scales, bias=None, dtype=None, y=None):
     if given:
         _written(y)
     return y
+
+
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _steps(steps, coefficients, eps):
+    """(NewtonSchulz, what keeps its coefficients alive): one triple for every step, or one for each."""
+    rows = list(coefficients)
+    if rows and not hasattr(rows[0], "__len__"):
+        rows = [rows] * steps
+    if len(rows) != steps or steps < 1 or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients: (a, b, c), or one such triple for each of the steps (at least 1)")
+    held = array.array("d", [float(v) for r in rows for v in r])
+    return NewtonSchulz(held.buffer_info()[0], steps, eps), held
+
+
+def _sides(ts, name):
+    for i, t in enumerate(ts):
+        if t.dim() != 2:
+            raise ValueError(f"{name}[{i}]: {tuple(t.shape)}, expected a matrix")
+
+
+def orthogonalize(x, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, dtype=None, out=None):
+    """Newton-Schulz steps on a matrix, or on every matrix of a list (contiguous, one of fp16 / bf16 /
+    fp32): X = x / max(|x|, eps), then steps of A = X X^T, X = a X + (b A + c A A) X, which brings every
+    singular value near 1 (of the transpose where there are more rows than columns). coefficients:
+    (a, b, c) for all steps, or a triple for each. Returns new matrices of `dtype`, fp16 or bf16 (default:
+    x's, bf16 for fp32), or fills `out` (which may be x)."""
+    torch = _torch()
+    single = isinstance(x, torch.Tensor)
+    xs = [x] if single else list(x)
+    if not xs:
+        raise ValueError("orthogonalize needs at least one matrix")
+    ns, held = _steps(steps, coefficients, eps)
+    ptrs, _, kind, device = _dev_list(xs, "x", _GRAD_KINDS)
+    _sides(xs, "x")
+    given = out is not None
+    if given:
+        outs = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(outs) != len(xs) or any(o.shape != t.shape for o, t in zip(outs, xs)):
+            raise ValueError("out: matrices of x's shapes")
+        if dtype is not None and any(o.dtype != dtype for o in outs):
+            raise ValueError("out: matrices of the given dtype")
+    else:
+        if dtype is None:
+            dtype = torch.bfloat16 if kind == ZPP_F32 else xs[0].dtype
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"dtype: {dtype}, expected float16 or bfloat16")
+        outs = [torch.empty(t.shape, dtype=dtype, device=t.device) for t in xs]
+    out_ptrs, _, out_kind, out_device = _dev_list(outs, "out", (ZPP_F16, ZPP_BF16))
+    if out_device != device:
+        raise ValueError("all tensors of a call must be on one device")
+    table = [Matrix(p, o, *t.shape) for p, o, t in zip(ptrs, out_ptrs, xs)]
+    at, keep = _rows_of(Matrix, table)
+    need = int(lib().zpp_orthogonalize_workspace(at, len(table)))
+    work = torch.empty(max(need, 0), dtype=torch.uint8, device=xs[0].device)
+    _launch(device, "zpp_orthogonalize", at, len(table), kind, out_kind, ctypes.addressof(ns),
+            work.data_ptr())
+    if given:
+        _written(*outs)
+    return outs[0] if single else outs
 
 
 class QgzBuffers:

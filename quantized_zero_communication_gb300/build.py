@@ -21,7 +21,8 @@ EXT = os.path.join(PKG, "_tensors.so")
 EXT_ABI = os.path.join(BUILD, "_tensors.abi")  # what EXT was compiled against
 SOURCES = ["zpp_abi.cu", "quant.cu", "reorder_quant.cu", "reorder_tensors_f16.cu",
            "reorder_tensors_bf16.cu", "dequant.cu", "qgz.cu", "adamw.cu", "grad_norm.cu",
-           "matvec.cu", "tensor_map.cu", "quant_fp8.cu", "matmul_fp8.cu"]
+           "matvec.cu", "tensor_map.cu", "quant_fp8.cu", "matmul_fp8.cu",
+           "newton_schulz.cu", "muon.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++20", "-O3", "-lineinfo", "-fmad=false", "-prec-div=true", "-prec-sqrt=true",
          "-ftz=false", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -1,0 +1,412 @@
+// muon.cu -- K12, K13 and the order of a Muon step:
+//
+//   m = mu m + (1 - mu) c g,  u = (1 - mu) c g + mu m (nesterov) or m,  X = u / max(|u|_F, eps)   (K12, K13)
+//   five steps of K14's products, the last one  p = p (1 - lr decay) - lr adjust X
+//
+// K12 reads the gradient and the momentum, writes the momentum and one partial sum of squares per
+// CTA; K13 adds a matrix's partials in a fixed order, makes u again and writes X as two fp16.
+#include <algorithm>
+#include <cmath>
+#include <limits>
+#include <vector>
+
+#include "newton_schulz.cuh"
+#include "zpp_overlap.cuh"
+#include "zpp_tensor_map.h"
+
+namespace zpp {
+
+constexpr int kMuonPer = kThreads * 8;    // elements of a CTA's round
+constexpr int kMuonPartials = 1024;       // of a matrix, at most
+
+struct MuonTable {
+  int32_t count;
+  bool nesterov;
+  float mu, one_minus_mu, eps;
+  int32_t x_kind;
+  const float* factor;
+  float* partial;
+  ChunkHints hints;
+  int32_t first[kMuonMatrices + 1];  // CTAs of the matrices before this one
+  struct Item {
+    const void* x;
+    float* momentum;
+    uint16_t *high, *low;
+    int64_t n, per;       // elements, and those of a CTA (whole rounds)
+    int32_t cols, ld;
+  } item[kMuonMatrices];
+};
+static_assert(sizeof(MuonTable) <= 31 * 1024, "kernel parameter space");
+
+// Elements i .. i + 7 of n, zeros behind the last. vec: x is 16-byte aligned.
+template <int KIND>
+__device__ __forceinline__ void load8(const void* x, int64_t i, int64_t n, bool vec, float (&v)[8]) {
+  if (vec && i + 8 <= n) {
+    const char* p = static_cast<const char*>(x) + i * (KIND == 2 ? 4 : 2);
+#pragma unroll
+    for (int h = 0; h < (KIND == 2 ? 2 : 1); ++h) {
+      const uint4 w = ld_after_v4(p + 16 * h);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (KIND == 2) {
+          v[4 * h + k] = __uint_as_float(u[k]);
+        } else {
+          const float2 f = KIND == 0 ? unpack2(u[k], F16()) : unpack2(u[k], BF16());
+          v[2 * k] = f.x, v[2 * k + 1] = f.y;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = 0.0f;
+      if (i + k < n) {
+        if constexpr (KIND == 2) v[k] = static_cast<const float*>(x)[i + k];
+        else v[k] = KIND == 0 ? bits16_to_float(static_cast<const uint16_t*>(x)[i + k], F16())
+                              : bits16_to_float(static_cast<const uint16_t*>(x)[i + k], BF16());
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ double cta_sum(double v, double* part) {  // valid in every thread
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int w = 0; w < kWarps; ++w) v += part[w];
+  return v;
+}
+
+// K12 (SCALE false) and K13.
+template <int KIND, bool SCALE>
+__global__ void __launch_bounds__(kThreads) k_muon(const __grid_constant__ MuonTable t) {
+  __shared__ double part[kWarps];
+  grid_wait();
+  grid_release();
+  const float factor = t.factor ? ld_after_f32(t.factor) : 1.0f;
+  if (!isfinite(factor)) return;
+  const int m = tensor_of(t.hints, t.first, static_cast<int>(blockIdx.x));
+  const MuonTable::Item& it = t.item[m];
+  const int cta = static_cast<int>(blockIdx.x) - t.first[m];
+  const int64_t begin = cta * it.per, end = begin + it.per < it.n ? begin + it.per : it.n;
+  float inv = 0.0f;
+  if constexpr (SCALE) {
+    double total = 0.0;
+    for (int i = t.first[m] + static_cast<int>(threadIdx.x); i < t.first[m + 1]; i += kThreads)
+      total += static_cast<double>(ld_after_f32(t.partial + i));
+    total = cta_sum(total, part);
+    const float norm = static_cast<float>(sqrt(total));
+    // (a norm that is not a number passes through, and so does one that is infinite, as NaN)
+    inv = norm <= 3.402823466e38f ? __fdiv_rn(1.0f, fmaxf(norm, t.eps)) : __int_as_float(0x7fc00000);
+  }
+  const bool x_vec = (reinterpret_cast<uintptr_t>(it.x) & 15) == 0;
+  const bool m_vec = (reinterpret_cast<uintptr_t>(it.momentum) & 15) == 0;
+  float sum = 0.0f;
+  for (int64_t i = begin + threadIdx.x * 8; i < end; i += kMuonPer) {
+    float x[8], u[8];
+    load8<KIND>(it.x, i, it.n, x_vec, x);
+    if (it.momentum) {
+      float mo[8];
+      load8<2>(it.momentum, i, it.n, m_vec, mo);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float g = __fmul_rn(t.one_minus_mu, __fmul_rn(x[k], factor));
+        if constexpr (!SCALE) mo[k] = __fmaf_rn(t.mu, mo[k], g);
+        u[k] = t.nesterov ? __fmaf_rn(t.mu, mo[k], g) : mo[k];
+      }
+      if constexpr (!SCALE) {
+        if (m_vec && i + 8 <= it.n) {
+          st_v4(it.momentum + i, make_uint4(__float_as_uint(mo[0]), __float_as_uint(mo[1]), __float_as_uint(mo[2]),
+                                            __float_as_uint(mo[3])));
+          st_v4(it.momentum + i + 4, make_uint4(__float_as_uint(mo[4]), __float_as_uint(mo[5]),
+                                                __float_as_uint(mo[6]), __float_as_uint(mo[7])));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (i + k < it.n) it.momentum[i + k] = mo[k];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = x[k];
+    }
+    if constexpr (!SCALE) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = __fmaf_rn(u[k], u[k], sum);
+    } else {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __fmul_rn(__fmul_rn(u[2 * k], inv), kXScale),
+                    b = __fmul_rn(__fmul_rn(u[2 * k + 1], inv), kXScale);
+        hi[k] = pack2(a, b, F16());
+        const float2 f = unpack2(hi[k], F16());
+        lo[k] = pack2(__fsub_rn(a, f.x), __fsub_rn(b, f.y), F16());
+      }
+      if (it.cols == it.ld) {  // the rows lie as the matrix's: n is a multiple of 8
+        st_v4(it.high + i, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_v4(it.low + i, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      } else {
+        int64_t row = i / it.cols;
+        int col = static_cast<int>(i - row * it.cols);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (i + k < it.n) {
+            it.high[row * it.ld + col] = static_cast<uint16_t>(hi[k >> 1] >> (16 * (k & 1)));
+            it.low[row * it.ld + col] = static_cast<uint16_t>(lo[k >> 1] >> (16 * (k & 1)));
+          }
+          if (++col == it.cols) col = 0, ++row;
+        }
+      }
+    }
+  }
+  if constexpr (!SCALE) {
+    const double all = cta_sum(static_cast<double>(sum), part);
+    if (threadIdx.x == 0) t.partial[blockIdx.x] = static_cast<float>(all);
+  }
+}
+
+// ------------------------------------------------------------------------------------- the host's part
+namespace {
+
+struct Shape {
+  int64_t rows, cols;
+  int count = 0, first = 0;
+  int64_t small() const { return std::min(rows, cols); }
+  int64_t ld() const { return (cols + 7) / 8 * 8; }
+  int64_t small_ld() const { return (small() + 7) / 8 * 8; }
+  int64_t x_elems() const { return (rows * ld() + 63) / 64 * 64; }  // one matrix, 128-byte aligned
+  int64_t a_elems() const { return (small() * small_ld() + 63) / 64 * 64; }
+  int64_t diag_elems() const { return (small() + 31) / 32 * 32; }  // fp32
+  bool wide() const { return rows <= cols; }
+  bool exact() const { return small() <= kNsExactSide; }
+  // X twice and what it lost, A and B with their diagonals; what each lost too, and X's twice
+  int64_t bytes() const {
+    return count * ((exact() ? 4 : 3) * x_elems() * 2 + (exact() ? 4 : 2) * a_elems() * 2 + 2 * diag_elems() * 4);
+  }
+};
+
+// Matrices that are worked on together, in the order of their shapes.
+struct Batch {
+  std::vector<Shape> shapes;
+  std::vector<int> order;  // places in the list
+  int64_t elems = 0;
+  int64_t bytes() const {
+    int64_t b = 0;
+    for (const Shape& s : shapes) b += s.bytes();
+    return b + (static_cast<int64_t>(order.size()) * kMuonPartials * 4 + 127) / 128 * 128;
+  }
+};
+constexpr int64_t kBatchElems = int64_t{1} << 28;  // more than this starts another batch
+
+// Calls each(batch) for the list's batches.
+template <typename F>
+auto batches(const MuonMatrix* list, int count, const F& each) {
+  std::vector<std::vector<int>> of;
+  Batch b;
+  const auto flush = [&] {
+    for (size_t k = 0; k < b.shapes.size(); ++k) {
+      b.shapes[k].first = static_cast<int>(b.order.size());
+      b.order.insert(b.order.end(), of[k].begin(), of[k].end());
+    }
+    const auto r = each(b);
+    b = Batch{};
+    of.clear();
+    return r;
+  };
+  int held = 0;
+  for (int i = 0; i < count; ++i) {
+    const MuonMatrix& m = list[i];
+    const int64_t n = m.rows * m.cols;
+    if (n == 0) continue;
+    size_t k = 0;
+    while (k < b.shapes.size() && (b.shapes[k].rows != m.rows || b.shapes[k].cols != m.cols)) ++k;
+    if (held == kMuonMatrices || (held > 0 && b.elems + n > kBatchElems) ||
+        (k == b.shapes.size() && k == kMuonGroups)) {
+      if (const auto r = flush(); r) return r;
+      held = 0;
+      k = 0;
+    }
+    if (k == b.shapes.size()) {
+      Shape s;
+      s.rows = m.rows, s.cols = m.cols;
+      b.shapes.push_back(s);
+      of.emplace_back();
+    }
+    ++b.shapes[k].count;
+    of[k].push_back(i);
+    b.elems += n;
+    ++held;
+  }
+  return held ? flush() : decltype(each(b))(0);
+}
+
+float adjusted(const MuonArgs& a, int64_t rows, int64_t cols) {
+  const double r = static_cast<double>(rows), c = static_cast<double>(cols);
+  const double f = a.adjust == 0 ? std::sqrt(std::max(1.0, r / c)) : a.adjust == 1 ? 0.2 * std::sqrt(std::max(r, c)) : 1.0;
+  return static_cast<float>(a.lr * f);
+}
+
+cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a, uint8_t* workspace,
+                      cudaStream_t s) {
+  // ---- where things lie
+  struct Place {
+    uint16_t *x[2], *x_low[2], *a, *a_low, *b, *b_low;
+    float *a_diag, *b_diag;
+  };
+  std::vector<Place> place(b.shapes.size());
+  uint8_t* at = workspace;
+  for (size_t k = 0; k < b.shapes.size(); ++k) {
+    const Shape& sh = b.shapes[k];
+    const auto take = [&](int64_t elems, int size) {
+      uint8_t* p = at;
+      at += sh.count * elems * size;
+      return p;
+    };
+    const auto half = [&](int64_t elems) { return reinterpret_cast<uint16_t*>(take(elems, 2)); };
+    Place& p = place[k];
+    for (int i = 0; i < 2; ++i) {
+      p.x[i] = half(sh.x_elems());
+      p.x_low[i] = i == 0 || sh.exact() ? half(sh.x_elems()) : p.x_low[0];
+    }
+    p.a = half(sh.a_elems());
+    p.b = half(sh.a_elems());
+    p.a_low = sh.exact() ? half(sh.a_elems()) : nullptr;
+    p.b_low = sh.exact() ? half(sh.a_elems()) : nullptr;
+    p.a_diag = reinterpret_cast<float*>(take(sh.diag_elems(), 4));
+    p.b_diag = reinterpret_cast<float*>(take(sh.diag_elems(), 4));
+  }
+  // ---- K12, K13
+  MuonTable t{};
+  t.count = static_cast<int32_t>(b.order.size());
+  t.nesterov = a.nesterov;
+  t.mu = a.mu;
+  t.one_minus_mu = a.one_minus_mu;
+  t.eps = std::max(a.eps, std::numeric_limits<float>::min());
+  t.x_kind = a.x_kind;
+  t.factor = a.factor;
+  t.partial = reinterpret_cast<float*>(at);
+  t.first[0] = 0;
+  for (size_t k = 0, i = 0; k < b.shapes.size(); ++k) {
+    const Shape& sh = b.shapes[k];
+    for (int j = 0; j < sh.count; ++j, ++i) {
+      const MuonMatrix& m = list[b.order[i]];
+      MuonTable::Item& it = t.item[i];
+      it.x = m.x;
+      it.momentum = m.momentum;
+      it.high = place[k].x[0] + j * sh.x_elems();
+      it.low = place[k].x_low[0] + j * sh.x_elems();
+      it.n = sh.rows * sh.cols;
+      it.cols = static_cast<int32_t>(sh.cols);
+      it.ld = static_cast<int32_t>(sh.ld());
+      const int64_t rounds = (it.n + kMuonPer - 1) / kMuonPer;
+      const int64_t each = (rounds + kMuonPartials - 1) / kMuonPartials;
+      it.per = each * kMuonPer;
+      t.first[i + 1] = t.first[i] + static_cast<int32_t>((rounds + each - 1) / each);
+    }
+  }
+  t.hints.fill(t.first, t.count);
+  const int grid = t.first[t.count];
+  const auto prepare = [&](auto first, auto second) {
+    const cudaError_t e = launch_overlapped(first, grid, kThreads, s, t);
+    return e != cudaSuccess ? e : launch_overlapped(second, grid, kThreads, s, t);
+  };
+  cudaError_t e = a.x_kind == 2   ? prepare(k_muon<2, false>, k_muon<2, true>)
+                  : a.x_kind == 1 ? prepare(k_muon<1, false>, k_muon<1, true>)
+                                  : prepare(k_muon<0, false>, k_muon<0, true>);
+  if (e != cudaSuccess) return e;
+
+  // ---- K14
+  NsLaunch n{};
+  n.groups = static_cast<int32_t>(b.shapes.size());
+  n.decay = a.decay;
+  n.out_kind = a.out_kind;
+  n.factor = a.factor;
+  for (size_t i = 0; i < b.order.size(); ++i) n.result[i] = NsResult{list[b.order[i]].param, list[b.order[i]].out};
+  const auto map = [&](const uint16_t* p, int64_t rows, int64_t cols, int64_t ld, int64_t count, int64_t apart,
+                       bool mn, CUtensorMap* out) {
+    if (e == cudaSuccess)
+      e = make_tensor_map(out, p, 2, cols, rows, ld * 2, count, apart * 2, mn ? 64 : 128);
+  };
+  for (int step = 0; step < a.steps && e == cudaSuccess; ++step) {
+    const int from = step & 1;
+    n.a = static_cast<float>(a.coefficients[3 * step]);
+    n.b = static_cast<float>(a.coefficients[3 * step + 1]);
+    n.c = static_cast<float>(a.coefficients[3 * step + 2]);
+    n.early = step < a.steps - 3;
+    for (int op = kNsGram; op <= kNsApply; ++op) {
+      n.op = op == kNsApply && step == a.steps - 1 ? kNsLast : op;
+      n.tiles = 0;
+      for (size_t k = 0; k < b.shapes.size(); ++k) {
+        const Shape& sh = b.shapes[k];
+        NsGroup& g = n.group[k];
+        const int64_t m = sh.small(), ma = sh.small_ld();
+        const Place& pl = place[k];
+        const auto x_to = [&](bool mn, CUtensorMap* to, CUtensorMap* low) {
+          map(pl.x[from], sh.rows, sh.cols, sh.ld(), sh.count, sh.x_elems(), mn, to);
+          if (sh.exact()) map(pl.x_low[from], sh.rows, sh.cols, sh.ld(), sh.count, sh.x_elems(), mn, low);
+        };
+        const auto a_to = [&](const uint16_t* p, const uint16_t* p_low, CUtensorMap* to, CUtensorMap* low) {
+          map(p, m, m, ma, sh.count, sh.a_elems(), false, to);
+          if (sh.exact()) map(p_low, m, m, ma, sh.count, sh.a_elems(), false, low);
+        };
+        g.parts = sh.exact() ? 3 : 1;
+        g.rows = static_cast<int32_t>(op == kNsApply ? sh.rows : m);
+        g.cols = static_cast<int32_t>(op == kNsApply ? sh.cols : m);
+        g.depth = static_cast<int32_t>(op == kNsGram ? std::max(sh.rows, sh.cols) : m);
+        g.p_mn = op == kNsGram && !sh.wide();
+        g.q_mn = op == kNsGram ? !sh.wide() : op == kNsApply && sh.wide();
+        g.diag_apart = static_cast<int32_t>(sh.diag_elems());
+        g.diag_in = op == kNsPoly ? pl.a_diag : pl.b_diag;
+        g.diag_out = op == kNsGram ? pl.a_diag : pl.b_diag;
+        if (op == kNsGram) {
+          x_to(g.p_mn, &g.p, &g.p_low);
+          g.q = g.p, g.q_low = g.p_low;
+          g.out = pl.a, g.out_low = pl.a_low;
+        } else if (op == kNsPoly) {
+          a_to(pl.a, pl.a_low, &g.p, &g.p_low);
+          g.q = g.p, g.q_low = g.p_low;
+          g.in = pl.a, g.in_low = pl.a_low;
+          g.out = pl.b, g.out_low = pl.b_low;
+        } else {
+          if (sh.wide()) a_to(pl.b, pl.b_low, &g.p, &g.p_low), x_to(true, &g.q, &g.q_low);
+          else x_to(false, &g.p, &g.p_low), a_to(pl.b, pl.b_low, &g.q, &g.q_low);
+          g.in = pl.x[from], g.in_low = pl.x_low[from];
+          g.out = pl.x[from ^ 1], g.out_low = pl.x_low[from ^ 1];
+        }
+        g.ld = static_cast<int32_t>(op == kNsApply ? sh.ld() : ma);
+        g.apart = op == kNsApply ? sh.x_elems() : sh.a_elems();
+        g.step = adjusted(a, sh.rows, sh.cols);
+        g.p_tiles = (g.rows + 127) / 128;
+        g.q_tiles = (g.cols + 127) / 128;
+        g.per_matrix = op == kNsApply ? g.p_tiles * g.q_tiles : g.p_tiles * (g.p_tiles + 1) / 2;
+        g.first_tile = n.tiles;
+        g.first_matrix = sh.first;
+        n.tiles += g.per_matrix * sh.count;
+      }
+      if (e == cudaSuccess) e = launch_ns(n, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return e;
+}
+
+}  // namespace
+
+int64_t muon_workspace(const MuonMatrix* list, int count) {
+  int64_t most = 0;
+  batches(list, count, [&](const Batch& b) {
+    most = std::max(most, b.bytes());
+    return 0;
+  });
+  return most;
+}
+
+cudaError_t launch_muon(const MuonMatrix* list, int count, const MuonArgs& a, uint8_t* workspace,
+                        cudaStream_t s) {
+  return batches(list, count, [&](const Batch& b) { return run_batch(list, b, a, workspace, s); });
+}
+
+}  // namespace zpp

@@ -5,7 +5,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <exception>
 #include <limits>
+#include <vector>
 
 #include "zpp_device.cuh"
 #include "zpp_launch.h"
@@ -643,12 +645,146 @@ zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix* b, cons
   return from_cuda(zpp::launch_matmul_fp8(g, stream));
 }
 
+namespace {
+
+bool valid_sides(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > ZPP_MAX_SIDE || cols < 0 || cols > ZPP_MAX_SIDE) return false;
+  return cols == 0 || rows <= ZPP_MAX_ELEMS / cols;
+}
+zpp_status check_steps(const zpp_newton_schulz& ns) {
+  if (ns.steps < 1 || ns.steps > 100 || !ns.coefficients || !(ns.eps > 0.0) || !is_finite(ns.eps))
+    return ZPP_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < 3 * ns.steps; ++i)
+    if (!is_finite(ns.coefficients[i])) return ZPP_ERR_INVALID_ARG;
+  return ZPP_OK;
+}
+void set_steps(zpp::MuonArgs& a, const zpp_newton_schulz& ns) {
+  a.eps = static_cast<float>(ns.eps);
+  a.steps = ns.steps;
+  a.coefficients = ns.coefficients;
+}
+extern "C++" {  // (templates have no C names)
+// The sizes of a list, in the form that the step takes; false on ones that it refuses.
+template <typename T>
+bool sizes(const T* list, int32_t num, std::vector<zpp::MuonMatrix>& to) {
+  if (num < 0 || num > ZPP_MAX_TENSORS || (num > 0 && !list)) return false;
+  to.resize(static_cast<size_t>(num));
+  for (int32_t i = 0; i < num; ++i) {
+    if (!valid_sides(list[i].rows, list[i].cols)) return false;
+    to[i] = zpp::MuonMatrix{};
+    to[i].rows = list[i].rows;
+    to[i].cols = list[i].cols;
+  }
+  return true;
+}
+template <typename T>
+int64_t workspace_of(const T* list, int32_t num) {
+  try {
+    std::vector<zpp::MuonMatrix> m;
+    return sizes(list, num, m) ? zpp::muon_workspace(m.data(), num) : -1;
+  } catch (const std::exception&) {
+    return -1;
+  }
+}
+}
+zpp_status run_list(const std::vector<zpp::MuonMatrix>& list, const zpp::MuonArgs& a, void* workspace,
+                    cudaStream_t stream) {
+  bool elements = false;
+  for (const zpp::MuonMatrix& m : list) elements |= m.rows > 0 && m.cols > 0;
+  if (!elements) return ZPP_OK;
+  if (!workspace) return ZPP_ERR_INVALID_ARG;
+  if (!aligned(workspace, 128)) return ZPP_ERR_MISALIGNED;
+  return from_cuda(zpp::launch_muon(list.data(), static_cast<int>(list.size()), a,
+                                    static_cast<uint8_t*>(workspace), stream));
+}
+
+}  // namespace
+
+int64_t zpp_orthogonalize_workspace(const zpp_matrix* list, int32_t num) { return workspace_of(list, num); }
+int64_t zpp_muon_workspace(const zpp_muon_tensor* tensors, int32_t num) { return workspace_of(tensors, num); }
+
+zpp_status zpp_orthogonalize(const zpp_matrix* list, int32_t num, zpp_dtype x_dt, zpp_dtype out_dt,
+                             const zpp_newton_schulz* ns, void* workspace, cudaStream_t stream) {
+  static_assert(ZPP_MAX_SIDE + 128 < (int64_t{1} << 31), "tile coordinates are 32 bits");
+  if (!valid_dtype(x_dt) || !valid_dtype(out_dt) || !ns) return ZPP_ERR_INVALID_ARG;
+  const zpp_status st = check_steps(*ns);
+  if (st != ZPP_OK) return st;
+  try {
+    std::vector<zpp::MuonMatrix> m;
+    if (!sizes(list, num, m)) return ZPP_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num; ++i) {
+      if (m[i].rows == 0 || m[i].cols == 0) continue;
+      if (!list[i].x || !list[i].out) return ZPP_ERR_INVALID_ARG;
+      m[i].x = list[i].x;
+      m[i].out = list[i].out;
+    }
+    if (out_dt == ZPP_F32) return ZPP_ERR_UNSUPPORTED;
+    for (const zpp::MuonMatrix& t : m)
+      if (!aligned(t.x, size_of(x_dt)) || !aligned(t.out, 2)) return ZPP_ERR_MISALIGNED;
+    zpp::MuonArgs a{};
+    set_steps(a, *ns);
+    a.x_kind = static_cast<int32_t>(x_dt);
+    a.out_kind = static_cast<int32_t>(out_dt);
+    return run_list(m, a, workspace, stream);
+  } catch (const std::exception&) {  // the host's lists did not fit its memory
+    return ZPP_ERR_CUDA;
+  }
+}
+
+zpp_status zpp_muon_step(const zpp_muon_tensor* tensors, int32_t num, zpp_dtype g_dt, zpp_dtype w_dt,
+                         const zpp_muon_params* hp, const float* grad_scale, void* workspace,
+                         cudaStream_t stream) {
+  if (!valid_dtype(g_dt) || !valid_dtype(w_dt) || !hp) return ZPP_ERR_INVALID_ARG;
+  if (!is_finite(hp->lr) || !is_finite(hp->weight_decay) || !(hp->momentum >= 0.0 && hp->momentum < 1.0) ||
+      (hp->nesterov != 0 && hp->nesterov != 1) || hp->adjust < ZPP_MUON_ORIGINAL || hp->adjust > ZPP_MUON_NONE)
+    return ZPP_ERR_INVALID_ARG;
+  const zpp_status st = check_steps(hp->ns);
+  if (st != ZPP_OK) return st;
+  try {
+    std::vector<zpp::MuonMatrix> m;
+    if (!sizes(tensors, num, m)) return ZPP_ERR_INVALID_ARG;
+    bool any_weight = false;
+    for (int32_t i = 0; i < num; ++i) {
+      if (m[i].rows == 0 || m[i].cols == 0) continue;
+      const zpp_muon_tensor& t = tensors[i];
+      if (!t.param || !t.grad || !t.momentum) return ZPP_ERR_INVALID_ARG;
+      m[i].x = t.grad;
+      m[i].momentum = t.momentum;
+      m[i].param = t.param;
+      m[i].out = t.weight;
+      any_weight |= t.weight != nullptr;
+    }
+    if (any_weight && w_dt == ZPP_F32) return ZPP_ERR_UNSUPPORTED;
+    for (const zpp::MuonMatrix& t : m)
+      if (!aligned(t.x, size_of(g_dt)) || !aligned(t.momentum, 4) || !aligned(t.param, 4) || !aligned(t.out, 2))
+        return ZPP_ERR_MISALIGNED;
+    if (!aligned(grad_scale, 4)) return ZPP_ERR_MISALIGNED;
+    zpp::MuonArgs a{};
+    set_steps(a, hp->ns);
+    a.mu = static_cast<float>(hp->momentum);
+    a.one_minus_mu = static_cast<float>(1.0 - hp->momentum);
+    a.nesterov = hp->nesterov != 0;
+    a.decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
+    a.lr = hp->lr;
+    a.adjust = hp->adjust;
+    a.x_kind = static_cast<int32_t>(g_dt);
+    a.out_kind = static_cast<int32_t>(w_dt);
+    a.factor = grad_scale;
+    return run_list(m, a, workspace, stream);
+  } catch (const std::exception&) {
+    return ZPP_ERR_CUDA;
+  }
+}
+
 zpp_status zpp_device_fault(uint32_t* flags, int32_t clear) {
   if (!flags) return ZPP_ERR_INVALID_ARG;
   unsigned v = 0;
   zpp_status st = from_cuda(zpp::read_device_fault(&v, clear != 0));
   unsigned w = 0;
   if (st == ZPP_OK) st = from_cuda(zpp::read_matmul_fault(&w, clear != 0));
+  v |= w;
+  w = 0;
+  if (st == ZPP_OK) st = from_cuda(zpp::read_muon_fault(&w, clear != 0));
   v |= w;
   *flags = st == ZPP_OK ? v : 0u;
   return st;

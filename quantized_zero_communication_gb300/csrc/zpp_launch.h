@@ -243,6 +243,34 @@ struct QuantFp8Args {
 };
 cudaError_t launch_quant_fp8(const QuantFp8Args& a, cudaStream_t s);
 
+// K12 .. K14: Newton-Schulz products over a list of matrices, with the Muon step around them.
+constexpr int kMuonMatrices = 256;  // of a batch
+constexpr int kMuonGroups = 16;     // shapes of a batch
+struct MuonMatrix {
+  const void* x;     // the gradient, or the matrix itself
+  float* momentum;   // null: x itself is what becomes orthogonal
+  float* param;      // Muon: updated; else null
+  void* out;         // the result in 16 bits, or the updated parameter in 16 bits (may be null)
+  int64_t rows, cols;
+};
+struct MuonArgs {
+  float mu, one_minus_mu;
+  bool nesterov;
+  float decay;           // 1 - lr * weight_decay
+  double lr;
+  int32_t adjust;        // 0: sqrt(max(1, rows / cols)), 1: 0.2 sqrt(max(rows, cols)), 2: 1
+  float eps;
+  int32_t steps;
+  const double* coefficients;  // [steps][3], HOST
+  int32_t x_kind, out_kind;
+  const float* factor;   // device, or null
+};
+// Bytes of workspace; the list is taken in batches, one after the other.
+int64_t muon_workspace(const MuonMatrix* list, int count);
+cudaError_t launch_muon(const MuonMatrix* list, int count, const MuonArgs& a, uint8_t* workspace,
+                        cudaStream_t s);
+cudaError_t read_muon_fault(unsigned* flags, bool clear);
+
 // Grid size when every CTA owns `per_cta` consecutive tiles and exits (no grid-stride
 // loop): on GB300 a streaming kernel launched this way sustains more HBM bandwidth than
 // a persistent grid sized to the SM count.

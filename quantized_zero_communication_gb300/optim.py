@@ -1,6 +1,7 @@
 """AdamW over the tensors of a parameter shard: fp32 master weights, states in fp32 or in
 8 bits, one library call per step (``zpp_adamw_step_counted``), which also takes the gradient norm
-when it clips. Everything stays on the device; a step never synchronises.
+when it clips; and Muon (``zpp_muon_step``) for whole matrices. Everything stays on the device; a
+step never synchronises.
 
 The 16-bit tensors in ``weights`` receive the updated parameters, ready for the next
 all-gather's ``quant_blockwise``.
@@ -179,3 +180,109 @@ class AdamW:
         and the step count (which waits for the device once a step was clipped or scaled)."""
         return dict(exp_avg=self.exp_avg, exp_avg_sq=self.exp_avg_sq, scales=self.scales,
                     step=self.steps, seed=self.seed, state_bits=self.state_bits)
+
+
+_ADJUST = ("original", "match_rms_adamw", "none")
+
+
+class Muon:
+    """Muon over a list of at most 1024 contiguous fp32 CUDA matrices (or a single one): momentum, an
+    update made nearly orthogonal by Newton-Schulz steps, decoupled weight decay. It wants whole
+    matrices, not slices of a flat shard; vectors and embeddings go to AdamW.
+
+        m = momentum m + (1 - momentum) g,  u = (1 - momentum) g + momentum m  (nesterov; else m)
+        p = p (1 - lr weight_decay) - lr adj orthogonalize(u, steps, coefficients, eps)
+
+    adjust: "original": adj = sqrt(max(1, rows / cols)); "match_rms_adamw": 0.2 sqrt(max(rows, cols)),
+    with which AdamW's lr and weight_decay do; "none": 1. weights: fp16 or bf16 matrices of the
+    parameters' shapes that each step fills, or None. buffers: the momenta of a saved state() (taken over,
+    not copied); by default they start at zero. An optimiser is made and stepped on one stream, or on
+    streams that wait for each other.
+    """
+
+    def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.1, *, nesterov=True, steps=5,
+                 coefficients=_b.NS_COEFFICIENTS, eps=1e-7, adjust="original", weights=None,
+                 buffers=None):
+        torch = _b._torch()
+        as_list = lambda ts: [ts] if isinstance(ts, torch.Tensor) else list(ts)  # noqa: E731
+        self.params = as_list(params)
+        if not self.params:
+            raise ValueError("Muon needs at least one matrix")
+        if len(self.params) > _b.ZPP_MAX_TENSORS:
+            raise ValueError(f"Muon: {len(self.params)} matrices, at most {_b.ZPP_MAX_TENSORS} to a call: "
+                             "take an optimiser for each part")
+        if adjust not in _ADJUST:
+            raise ValueError(f"adjust: one of {_ADJUST}")
+        _b._sides(self.params, "params")
+        self._ns, self._coefficients = _b._steps(steps, coefficients, eps)
+        self.lr, self.momentum, self.weight_decay = lr, momentum, weight_decay
+        self.nesterov, self.adjust = nesterov, adjust
+        self._shapes = [tuple(p.shape) for p in self.params]
+        f32 = (_b.ZPP_F32,)
+        _b._dev_list(self.params, "params", f32)
+        self.buffers = ([torch.zeros_like(p) for p in self.params] if buffers is None
+                        else as_list(buffers))
+        self.weights = None if weights is None else as_list(weights)
+        self._table = (_b.MuonTensor * len(self.params))()
+        for row, (rows, cols) in zip(self._table, self._shapes):
+            row.rows, row.cols = rows, cols
+        self._lists = [("params", "param", self.params, f32), ("buffers", "momentum", self.buffers, f32)]
+        if self.weights is not None:
+            self._lists.append(("weights", "weight", self.weights, (_b.ZPP_F16, _b.ZPP_BF16)))
+        self._device, self._w_kind = None, _b.ZPP_BF16
+        self._gather()
+        self._work = int(_b.lib().zpp_muon_workspace(ctypes.addressof(self._table), len(self._table)))
+
+    def _enter(self, name, field, tensors, kinds):
+        """Checks a list and writes its addresses into the call's table; their dtype's kind."""
+        if len(tensors) != len(self._shapes):
+            raise ValueError(f"{name}: {len(tensors)} matrices, expected {len(self._shapes)}")
+        for i, (t, shape) in enumerate(zip(tensors, self._shapes)):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}[{i}]: {tuple(t.shape)}, expected {shape}")
+        ptrs, _, kind, device = _b._dev_list(tensors, name, kinds)
+        if self._device is None:
+            self._device = device
+        if device != self._device:
+            raise ValueError("all tensors of a call must be on one device")
+        for row, p in zip(self._table, ptrs):
+            setattr(row, field, p)
+        return kind
+
+    def _gather(self):
+        """Every tensor that the optimiser holds, as it is now (storage may have moved)."""
+        for name, field, tensors, kinds in self._lists:
+            kind = self._enter(name, field, tensors, kinds)
+            if name == "weights":
+                self._w_kind = kind
+
+    def step(self, grads, *, max_norm=None, pre_scale=None, grad_scale=None, lr=None):
+        """One step with `grads` (contiguous, one of fp16 / bf16 / fp32, in the parameters' order and
+        shapes). max_norm, pre_scale, grad_scale and what is returned: as AdamW.step; a factor that is
+        not finite leaves parameters, weights and momenta as they were. (The direction of an update
+        does not depend on the gradients' scale, but what they weigh in the momentum does.) lr replaces
+        the optimiser's for this step and the following ones."""
+        torch = _b._torch()
+        grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+        self._gather()
+        kind = self._enter("grads", "grad", grads, _b._GRAD_KINDS)
+        if lr is not None:
+            self.lr = lr
+        norm, scale = None, 0
+        if max_norm is not None or pre_scale is not None:
+            if grad_scale is not None:
+                raise ValueError("grad_scale replaces max_norm and pre_scale")
+            norm = _b.grad_norm(grads, max_norm, 1.0 if pre_scale is None else pre_scale)
+            scale = norm.data_ptr() + 4
+        elif grad_scale is not None:
+            scale = _b._scale_address(grads[0], grad_scale)
+        hp = _b.MuonParams(self.lr, self.momentum, self.weight_decay, bool(self.nesterov),
+                           _ADJUST.index(self.adjust), self._ns)
+        work = torch.empty(max(self._work, 0), dtype=torch.uint8, device=self.params[0].device)
+        _b._launch(self._device, "zpp_muon_step", ctypes.addressof(self._table), len(self._table), kind,
+                   self._w_kind, ctypes.addressof(hp), scale, work.data_ptr())
+        return norm
+
+    def state(self):
+        """What a checkpoint keeps, as the constructor takes it: the momenta themselves."""
+        return dict(buffers=self.buffers)
