@@ -5,7 +5,9 @@
 // The inner sums are tcgen05 products (fp32 in tensor memory), one block of 128 a slot of a ring there;
 // eight warps read each slot, multiply it by its scales and add it to the tile's sums, which stay in
 // registers, while the matrix unit fills the next slot. So a sum never mixes scales, and its length
-// in the matrix unit is 128.
+// in the matrix unit is 128. A warp each fetches the scales of P and Q, eight blocks ahead: fetched one
+// block ahead by the warps that use them, their latency (about 1 us beside the operands' traffic) was
+// the time of a block (8192 x 8192 x 8192: 1280 us).
 //
 // P is the operand whose rows are the 128 lanes of tensor memory, Q the one whose rows are a tile's
 // columns: a and b, or b and a where there are few rows of a.
@@ -21,19 +23,20 @@ constexpr unsigned kMatmulFault = 8;  // its bit of the fault word
 
 constexpr int kLanes = 128;        // rows of P in a tile
 constexpr int kStep = 128;         // codes of the sum in a block, and bytes of a row of a stage
-constexpr int kSumWarps = 8;       // warps that scale and add
-constexpr int kMatmulThreads = (kSumWarps + 2) * 32;
 
-template <int BN>
+// CTAS 2: a pair of CTAs on a tile of 256 x BN; each holds its half of both operands.
+template <int CTAS, int BN>
 struct MatmulGeo {
-  static constexpr int STAGE = (kLanes + BN) * kStep;
-  static constexpr int STAGES = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr int Q_ROWS = BN / CTAS;  // of a CTA's stage
+  static constexpr int STAGE = (kLanes + Q_ROWS) * kStep;
+  static constexpr int STAGES = Q_ROWS >= 128 ? 6 : 8;
   static constexpr int SLOT = BN < 32 ? 32 : BN;  // tensor-memory columns of a slot
   static constexpr int SLOTS = 512 / SLOT < 4 ? 512 / SLOT : 4;
   static constexpr int HALF = BN / 2;  // columns of a warp
-  static constexpr int BARS = STAGES * STAGE;
-  static constexpr int SCALES = BARS + (2 * STAGES + 2 * SLOTS + 1) * 8 + 16;
-  static constexpr int SMEM = 1024 + SCALES + 2 * BN * 4;
+  static constexpr int AHEAD = 8;      // blocks whose scales are on their way
+  static constexpr int SCALES = STAGES * STAGE;
+  static constexpr int BARS = SCALES + AHEAD * (kLanes + BN) * 4;
+  static constexpr int SMEM = 1024 + BARS + (2 * STAGES + 2 * SLOTS + 2 * AHEAD + 1) * 8 + 16;
 };
 
 struct MatmulSide {
@@ -46,11 +49,13 @@ struct MatmulRun {
   MatmulSide p, q;
   int32_t blocks;       // of the sum
   int32_t p_tiles, q_tiles;
+  int32_t band;         // P tiles that are walked through together, column by column
   void* y;
   int64_t y_p, y_q;     // strides of y along P's and Q's rows; one of them is 1
   int32_t y_kind;
   const void* bias;     // of y's type, along Q's rows (or P's: bias_p)
   int32_t bias_p;
+  bool vec;             // y's rows lie along Q's, and 8 results start at multiples of 16 bytes
 };
 
 __device__ __forceinline__ float load_kind(const void* p, int64_t i, int kind) {
@@ -63,76 +68,129 @@ __device__ __forceinline__ void store_kind(void* p, int64_t i, float v, int kind
   else static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(kind == 0 ? pack2(v, v, F16()) : pack2(v, v, BF16()));
 }
 
+// 8 columns of row p of P, from column q on.
+__device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int64_t q, float (&v)[8]) {
+  if (run.bias) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (q + i < run.q.rows) v[i] = __fadd_rn(v[i], load_kind(run.bias, run.bias_p ? p : q + i, run.y_kind));
+  }
+  const int64_t at = p * run.y_p + q * run.y_q;
+  if (run.vec && q + 8 <= run.q.rows) {  // consecutive and whole
+    if (run.y_kind == 2) {
+      float* y = static_cast<float*>(run.y) + at;
+      st_v4(y, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+      st_v4(y + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                              __float_as_uint(v[7])));
+    } else {
+      uint16_t* y = static_cast<uint16_t*>(run.y) + at;
+      st_v4(y, run.y_kind == 0 ? make_uint4(pack2(v[0], v[1], F16()), pack2(v[2], v[3], F16()),
+                                            pack2(v[4], v[5], F16()), pack2(v[6], v[7], F16()))
+                               : make_uint4(pack2(v[0], v[1], BF16()), pack2(v[2], v[3], BF16()),
+                                            pack2(v[4], v[5], BF16()), pack2(v[6], v[7], BF16())));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (q + i < run.q.rows) store_kind(run.y, at + i * run.y_q, v[i], run.y_kind);
+}
+
+// The tiles in the order they are taken: bands of P tiles, column by column, so that the CTAs at work at
+// one time share rows of both operands in L2.
+__device__ __forceinline__ void matmul_tile(const MatmulRun& run, int t, int& p, int& q) {
+  const int per = run.band * run.q_tiles, b = t / per;
+  const int height = min(run.band, run.p_tiles - b * run.band);
+  t -= b * per;
+  p = b * run.band + t % height;
+  q = t / height;
+}
+
 // QROWS: Q has a scale for each row (else per tile of 128 rows, in which a warp's columns lie).
-template <int BN, bool QROWS>
-__global__ void __launch_bounds__(kMatmulThreads, 1)
+template <int CTAS, int BN, bool QROWS>
+__global__ void __launch_bounds__(kTensorThreads, 1)
     k_matmul_fp8(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                  const MatmulRun run) {
-  using G = MatmulGeo<BN>;
+  using G = MatmulGeo<CTAS, BN>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::BARS);
   uint64_t* empty = full + G::STAGES;
   uint64_t* summed = empty + G::STAGES;  // a slot holds a block's sums
   uint64_t* taken = summed + G::SLOTS;   // and has been read
-  uint64_t* drained = taken + G::SLOTS;
+  uint64_t* scaled = taken + G::SLOTS;   // a block's scales are there
+  uint64_t* used = scaled + G::AHEAD;    // and have been used
+  uint64_t* drained = used + G::AHEAD;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
-  float* q_scales = reinterpret_cast<float*>(smem + G::SCALES);  // [2][BN]
+  float* p_scales = reinterpret_cast<float*>(smem + G::SCALES);  // [AHEAD][kLanes]
+  float* q_scales = p_scales + G::AHEAD * kLanes;                // [AHEAD][BN]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < G::SLOTS; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], kSumWarps);
+    for (int i = 0; i < G::SLOTS; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], CTAS * kResultWarps);
+    for (int i = 0; i < G::AHEAD; ++i) mbar_init(&scaled[i], 64), mbar_init(&used[i], kResultWarps);
     mbar_init(drained, 1);
     mbar_init_fence();
     tma_prefetch(&p_map);
     tma_prefetch(&q_map);
   }
-  if (warp == kSumWarps) {
-    tmem_alloc<1>(tmem_at, G::SLOT * G::SLOTS);
-    tmem_alloc_done<1>();
+  if (warp == kCopyWarp) {
+    tmem_alloc<CTAS>(tmem_at, G::SLOT * G::SLOTS);
+    tmem_alloc_done<CTAS>();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
   grid_wait();
   grid_release();
 
   const int tiles = run.p_tiles * run.q_tiles, blocks = run.blocks;
+  const int first = blockIdx.x / CTAS, apart = gridDim.x / CTAS;
   bool alive = true;
 
-  if (warp == kSumWarps) {  // ---------------------------------------------- copies into the stages
-    if (lane == 0) {
+  if (warp < kFirstResultWarp) {
+    fewer_registers();
+    if (warp == kCopyWarp && lane == 0) {  // -------------------------------- copies into the stages
       Ring<G::STAGES> r;
       int64_t issued = 0;
-      for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x) {
-        const int p0 = t % run.p_tiles * kLanes, q0 = t / run.p_tiles * BN;
+      for (int t = first; t < tiles && alive; t += apart) {
+        int p, q;
+        matmul_tile(run, t, p, q);
+        const int p0 = (p * CTAS + rank) * kLanes, q0 = q * BN + rank * G::Q_ROWS;
         for (int kb = 0; kb < blocks; ++kb) {
           tc_wait(&empty[r.at], r.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
           if (!alive) break;
           uint8_t* stage = smem + r.at * G::STAGE;
-          mbar_arrive_expect_tx(&full[r.at], G::STAGE);
-          tma_load(stage, &p_map, kb * kStep, p0, &full[r.at]);
-          tma_load(stage + kLanes * kStep, &q_map, kb * kStep, q0, &full[r.at]);
+          // (a pair's copies are counted by the first CTA, which uses them)
+          if (rank == 0) mbar_arrive_expect_tx(&full[r.at], CTAS * G::STAGE);
+          if constexpr (CTAS == 2) {
+            const uint32_t bar = cluster_addr(&full[r.at], 0);
+            tma_load_pair(stage, &p_map, kb * kStep, p0, bar);
+            tma_load_pair(stage + kLanes * kStep, &q_map, kb * kStep, q0, bar);
+          } else {
+            tma_load(stage, &p_map, kb * kStep, p0, &full[r.at]);
+            tma_load(stage + kLanes * kStep, &q_map, kb * kStep, q0, &full[r.at]);
+          }
           ++issued;
           r.next();
         }
       }
-      if (!alive) {  // copies that nobody may have waited for
+      if (!alive && rank == 0) {  // copies that nobody may have waited for
         bool wait = true;
         for (int64_t d = 0; d < G::STAGES && d < issued; ++d) {
           if (--r.at < 0) r.at = G::STAGES - 1, r.phase ^= 1u;
           tc_wait(&full[r.at], r.phase, wait, &g_matmul_fault, kMatmulFault);
         }
       }
-    }
-  } else if (warp == kSumWarps + 1) {  // ---------------------------------------------- the products
-    if (lane == 0) {
-      constexpr uint32_t instr = tc_instruction(kLanes, BN, 0, 0, false, false);
+    } else if (warp == kProductWarp && lane == 0 && rank == 0) {  // ------------------ the products
+      constexpr uint32_t instr = tc_instruction(CTAS * kLanes, BN, 0, 0, false, false);
       Ring<G::STAGES> r;
       Ring<G::SLOTS> s;
-      for (int t = blockIdx.x; t < tiles && alive; t += gridDim.x)
+      for (int t = first; t < tiles && alive; t += apart)
         for (int kb = 0; kb < blocks; ++kb) {
           tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
           tc_wait(&full[r.at], r.phase, alive, &g_matmul_fault, kMatmulFault);
@@ -141,50 +199,70 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
           const uint32_t p = smem_addr(smem + r.at * G::STAGE), q = p + kLanes * kStep;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_f8<1>(tmem + s.at * G::SLOT, tc_operand(p + 32 * k, 16, 1024),
-                         tc_operand(q + 32 * k, 16, 1024), instr, k > 0);
-          tc_commit(&empty[r.at]);
-          tc_commit(&summed[s.at]);
+            tc_mma_f8<CTAS>(tmem + s.at * G::SLOT, tc_operand(p + 32 * k, 16, 1024),
+                            tc_operand(q + 32 * k, 16, 1024), instr, k > 0);
+          tc_commit_to<CTAS>(&empty[r.at]);
+          tc_commit_to<CTAS>(&summed[s.at]);
           r.next();
           s.next();
         }
       if (!alive) {
         bool wait = true;
-        tc_commit(drained);
+        tc_commit_to<CTAS>(drained);
         tc_wait(drained, 0, wait, &g_matmul_fault, kMatmulFault);
       }
     }
+    if (warp >= kFirstScaleWarp) {  // ------------------------------------------------- the scales
+      const bool of_p = warp == kFirstScaleWarp;
+      const MatmulSide& side = of_p ? run.p : run.q;
+      // rows of scales: all lanes of P; Q's columns, or the tiles of 128 that they are in
+      constexpr int Q_SCALES = QROWS ? BN : (BN + 127) / 128;
+      const int count = of_p ? kLanes : Q_SCALES, step = of_p || QROWS ? 1 : 128;
+      float* to = of_p ? p_scales : q_scales;
+      const int to_step = of_p ? kLanes : BN;
+      Ring<G::AHEAD> x;
+      for (int t = first; t < tiles; t += apart) {
+        int p, q;
+        matmul_tile(run, t, p, q);
+        const int64_t row0 = of_p ? (static_cast<int64_t>(p) * CTAS + rank) * kLanes : static_cast<int64_t>(q) * BN;
+        const float* from[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // (rows beyond the last take the first row's; nothing uses them)
+          const int64_t row = row0 + static_cast<int64_t>(lane + 32 * i) * step;
+          from[i] = side.scales + (row < side.rows ? row >> side.shift : 0) * side.row;
+        }
+        for (int kb = 0; kb < blocks; ++kb) {
+          tc_wait(&used[x.at], x.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (lane + 32 * i < count) cp_async4(to + x.at * to_step + lane + 32 * i, from[i] + kb * side.block);
+          cp_async_arrive_noinc(&scaled[x.at]);  // counts even with no copies of its own
+          x.next();
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+    }
   } else {  // -------------------------------------------------------------- scales, sums, results
+    more_registers();
     constexpr int HALF = G::HALF, CHUNK = HALF < 32 ? HALF : 32;
-    const int half = warp >> 2, in_half = threadIdx.x & 127;
+    const int half = (warp - kFirstResultWarp) >> 2, in_cta = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * HALF;
     Ring<G::SLOTS> s;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const int64_t p0 = static_cast<int64_t>(t % run.p_tiles) * kLanes + (warp & 3) * 32 + lane;
-      const int64_t q0 = static_cast<int64_t>(t / run.p_tiles) * BN + half * HALF;
-      const bool p_in = p0 < run.p.rows;
-      const float* sp = run.p.scales + (p_in ? p0 >> run.p.shift : 0) * run.p.row;
-      const int64_t q_row = QROWS ? q0 + in_half : q0;
-      const bool q_in = (!QROWS || in_half < HALF) && q_row < run.q.rows;
-      const float* sq = run.q.scales + (q_in ? q_row >> run.q.shift : 0) * run.q.row;
-      float sums[HALF];
+    Ring<G::AHEAD> x;
+    for (int t = first; t < tiles; t += apart) {
+      int p, q;
+      matmul_tile(run, t, p, q);
+      const int64_t p0 = (static_cast<int64_t>(p) * CTAS + rank) * kLanes + in_cta;
+      const int64_t q0 = static_cast<int64_t>(q) * BN + half * HALF;
+      f32x2 sums[HALF / 2];
 #pragma unroll
-      for (int i = 0; i < HALF; ++i) sums[i] = 0.0f;
-      float sp_next = blocks ? *sp : 0.0f, sq_next = blocks ? *sq : 0.0f;
+      for (int i = 0; i < HALF / 2; ++i) sums[i] = f2(0.0f, 0.0f);
       for (int kb = 0; kb < blocks; ++kb) {
-        float scale = sp_next;
-        const float sq_now = sq_next;
-        if (kb + 1 < blocks) {
-          sp_next = sp[(kb + 1) * run.p.block];
-          sq_next = sq[(kb + 1) * run.q.block];
-        }
-        float* qs = q_scales + (kb & 1) * BN + half * HALF;
-        if constexpr (QROWS) {
-          if (in_half < HALF) qs[in_half] = sq_now;
-          named_barrier(1 + half, 128);
-        } else {
-          scale = __fmul_rn(scale, sq_now);
-        }
+        tc_wait(&scaled[x.at], x.phase, alive, &g_matmul_fault, kMatmulFault);
+        float scale = p_scales[x.at * kLanes + in_cta];
+        const float* qs = q_scales + x.at * BN + (QROWS ? half * HALF : half * HALF / 128);
+        if constexpr (!QROWS) scale = __fmul_rn(scale, *qs);
         tc_wait(&summed[s.at], s.phase, alive, &g_matmul_fault, kMatmulFault);
         tc_fence_after();
 #pragma unroll
@@ -193,55 +271,46 @@ __global__ void __launch_bounds__(kMatmulThreads, 1)
           tmem_ld(lanes + s.at * G::SLOT + c, v);
           tmem_ld_wait(v);
 #pragma unroll
-          for (int i = 0; i < CHUNK; ++i) {
-            float x = __uint_as_float(v[i]);
-            if constexpr (QROWS) x = __fmul_rn(x, qs[c + i]);
-            sums[c + i] = __fmaf_rn(x, scale, sums[c + i]);
+          for (int i = 0; i < CHUNK; i += 2) {
+            f32x2 x = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            if constexpr (QROWS) x = f2_mul(x, *reinterpret_cast<const f32x2*>(qs + c + i));
+            sums[(c + i) / 2] = f2_fma(x, f2(scale, scale), sums[(c + i) / 2]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[s.at]);
+        if (lane == 0) {
+          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(&taken[s.at], 0));
+          else mbar_arrive(&taken[s.at]);
+          mbar_arrive(&used[x.at]);
+        }
         s.next();
+        x.next();
       }
-      if (p_in) {
+      if (p0 < run.p.rows) {
 #pragma unroll
-        for (int i = 0; i < HALF; ++i) {
-          const int64_t q = q0 + i;
-          if (q < run.q.rows) {
-            float v = sums[i];
-            if (run.bias) v = __fadd_rn(v, load_kind(run.bias, run.bias_p ? p0 : q, run.y_kind));
-            store_kind(run.y, p0 * run.y_p + q * run.y_q, v, run.y_kind);
-          }
+        for (int i = 0; i < HALF; i += 8) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f2_split(sums[i / 2 + k], v[2 * k], v[2 * k + 1]);
+          store_sums(run, p0, q0 + i, v);
         }
       }
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == kSumWarps) {
+  if constexpr (CTAS == 2) cluster_sync();
+  else __syncthreads();
+  if (warp == kCopyWarp) {
     tc_fence_after();
-    tmem_free<1>(tmem, G::SLOT * G::SLOTS);
+    tmem_free<CTAS>(tmem, G::SLOT * G::SLOTS);
   }
 }
 
-template <int BN, bool QROWS>
-static cudaError_t run_matmul(const CUtensorMap& p, const CUtensorMap& q, const MatmulRun& run,
-                              cudaStream_t s) {
-  auto kern = k_matmul_fp8<BN, QROWS>;
-  constexpr int smem = MatmulGeo<BN>::SMEM;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  int64_t tiles = static_cast<int64_t>(run.p_tiles) * run.q_tiles;
-  const int grid = static_cast<int>(tiles < 152 ? tiles : 152);
-  return launch_overlapped_smem(kern, dim3(grid), kMatmulThreads, smem, s, p, q, run);
-}
-
-cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
-  // Few rows of a: they are the columns of the tiles, which are narrow then.
-  const bool swap = a.a.rows <= 64;
+template <int CTAS, int BN>
+static cudaError_t run_matmul(const MatmulArgs& a, bool swap, cudaStream_t s) {
+  using G = MatmulGeo<CTAS, BN>;
   const MatmulOperand &p = swap ? a.b : a.a, &q = swap ? a.a : a.b;
-  const int bn = !swap ? 128 : q.rows <= 16 ? 16 : q.rows <= 32 ? 32 : 64;
   MatmulRun run{};
   const auto side = [](const MatmulOperand& o) {
     return MatmulSide{o.scales, o.scale_row, o.scale_block, o.rows, o.tile == 128 ? 7 : 0};
@@ -249,27 +318,36 @@ cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
   run.p = side(p);
   run.q = side(q);
   run.blocks = static_cast<int32_t>((a.depth + kStep - 1) / kStep);
-  run.p_tiles = static_cast<int32_t>((p.rows + kLanes - 1) / kLanes);
-  run.q_tiles = static_cast<int32_t>((q.rows + bn - 1) / bn);
+  run.p_tiles = static_cast<int32_t>((p.rows + CTAS * kLanes - 1) / (CTAS * kLanes));
+  run.q_tiles = static_cast<int32_t>((q.rows + BN - 1) / BN);
+  run.band = 8;
   run.y = a.y;
   run.y_p = swap ? 1 : a.y_stride;
   run.y_q = swap ? a.y_stride : 1;
   run.y_kind = a.y_kind;
   run.bias = a.bias;
   run.bias_p = swap;
-  CUtensorMap p_map{}, q_map{};
-  if (run.blocks > 0) {
-    cudaError_t e = make_tensor_map(&p_map, p.codes, 1, a.depth, p.rows, p.stride, 0, 0, kLanes);
-    if (e == cudaSuccess) e = make_tensor_map(&q_map, q.codes, 1, a.depth, q.rows, q.stride, 0, 0, bn);
-    if (e != cudaSuccess) return e;
-  }
-  const bool rows = run.q.shift == 0;
-  switch (bn) {
-    case 16: return rows ? run_matmul<16, true>(p_map, q_map, run, s) : run_matmul<16, false>(p_map, q_map, run, s);
-    case 32: return rows ? run_matmul<32, true>(p_map, q_map, run, s) : run_matmul<32, false>(p_map, q_map, run, s);
-    case 64: return rows ? run_matmul<64, true>(p_map, q_map, run, s) : run_matmul<64, false>(p_map, q_map, run, s);
-    default: return rows ? run_matmul<128, true>(p_map, q_map, run, s) : run_matmul<128, false>(p_map, q_map, run, s);
-  }
+  const int64_t size = a.y_kind == 2 ? 4 : 2;
+  run.vec = !swap && ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.y_stride * size)) & 15) == 0;
+  CUtensorMap p_map, q_map;
+  cudaError_t e = make_tensor_map(&p_map, p.codes, 1, a.depth, p.rows, p.stride, 0, 0, kLanes);
+  if (e == cudaSuccess) e = make_tensor_map(&q_map, q.codes, 1, a.depth, q.rows, q.stride, 0, 0, G::Q_ROWS);
+  auto kern = run.q.shift == 0 ? k_matmul_fp8<CTAS, BN, true> : k_matmul_fp8<CTAS, BN, false>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>(run.p_tiles) * run.q_tiles, most = 152 / CTAS;
+  const unsigned grid = static_cast<unsigned>((tiles < most ? tiles : most) * CTAS);
+  return launch_overlapped_cluster(kern, dim3(grid), CTAS, kTensorThreads, G::SMEM, s, p_map, q_map, run);
+}
+
+cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
+  // Few rows of a: they are the columns of the tiles, which are narrow then.
+  if (a.a.rows <= 16) return run_matmul<1, 16>(a, true, s);
+  if (a.a.rows <= 32) return run_matmul<1, 32>(a, true, s);
+  if (a.a.rows <= 64) return run_matmul<1, 64>(a, true, s);
+  const int64_t pairs = ((a.a.rows + 255) / 256) * ((a.b.rows + 255) / 256);
+  if (pairs >= 48) return run_matmul<2, 256>(a, false, s);
+  return run_matmul<1, 128>(a, false, s);
 }
 
 cudaError_t read_matmul_fault(unsigned* flags, bool clear) {

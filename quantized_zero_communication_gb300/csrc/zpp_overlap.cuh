@@ -79,21 +79,29 @@ __device__ __forceinline__ U8x32 ld_after_vec32(const void* p) {
   return r;
 }
 
-// smem: dynamic shared memory.
+// smem: dynamic shared memory; cluster: CTAs of a cluster (along x).
 template <typename... Params, typename... Args>
-inline cudaError_t launch_overlapped_smem(void (*kern)(Params...), dim3 grid, int threads, int smem,
-                                          cudaStream_t s, const Args&... args) {
+inline cudaError_t launch_overlapped_cluster(void (*kern)(Params...), dim3 grid, int cluster, int threads,
+                                             int smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped_smem(void (*kern)(Params...), dim3 grid, int threads, int smem,
+                                          cudaStream_t s, const Args&... args) {
+  return launch_overlapped_cluster(kern, grid, 1, threads, smem, s, args...);
 }
 template <typename... Params, typename... Args>
 inline cudaError_t launch_overlapped(void (*kern)(Params...), int grid, int threads, cudaStream_t s,

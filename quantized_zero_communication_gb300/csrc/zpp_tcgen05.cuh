@@ -15,7 +15,7 @@
 
 namespace zpp {
 
-constexpr unsigned long long kTensorWaitNs = 1000000000ull;  // 1 s, then a wait gives up
+constexpr long long kTensorWaitClocks = 2000000000ll;  // about 1 s, then a wait gives up
 
 // ------------------------------------------------------------------ tensor memory and the matrix unit
 template <int CTAS>
@@ -66,6 +66,12 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
           "r"(smem_addr(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tc_commit_to(uint64_t* bar) {
+  if constexpr (CTAS == 2) tc_commit_pair(bar);
+  else tc_commit(bar);
 }
 
 // Descriptor of an operand tile at `addr` (a shared-memory address, 1024-byte aligned plus an
@@ -164,16 +170,69 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
       : "memory");
 }
 
+// ------------------------------------------------------------------------------------ pairs of CTAs
+// Two CTAs of a cluster work on one tile of 256 rows: each holds 128 rows of P and half of Q's, the
+// first one issues the products for both, and each has its rows' sums in its own tensor memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every CTA of the cluster; what was written before is visible after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a shared variable of this CTA in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+// (What it tells of is tensor memory that was read, ordered by tc_fence_before: no release of this
+// thread's other writes to the cluster is asked for, which takes 1000 clocks and more.)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// As tma_load, the bytes counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+      "{%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------------- warps' parts
+// A kernel of 3 warpgroups: the first one copies and issues products, the others work on results. The
+// registers of 384 threads with 168 each go 56 to the first and 224 to the others: 128 * 56 + 256 * 224
+// = 384 * 168.
+constexpr int kTensorThreads = 384;
+constexpr int kCopyWarp = 0, kProductWarp = 1, kFirstScaleWarp = 2, kFirstResultWarp = 4, kResultWarps = 8;
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+
 // -------------------------------------------------------------------------------- bounded waits
-// Waits for a barrier's phase; after kTensorWaitNs it sets `bit` of the fault word, and this
+// Waits for a barrier's phase; after kTensorWaitClocks it sets `bit` of the fault word, and this
 // thread's later waits return at once (`alive` is false: what it computes is unspecified, and the
-// kernel ends).
+// kernel ends). Inline: a call would hold registers that these kernels do not have.
 __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, bool& alive, unsigned* fault,
                                         unsigned bit) {
   if (mbar_try_wait(bar, parity) || !alive) return;
-  if (!mbar_wait_bounded(bar, parity, kTensorWaitNs)) {
-    alive = false;
-    atomicOr(fault, bit);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kTensorWaitClocks) {
+      alive = false;
+      atomicOr(fault, bit);
+      return;
+    }
   }
 }
 
