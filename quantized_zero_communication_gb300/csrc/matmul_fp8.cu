@@ -186,29 +186,38 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
           tc_wait(&full[r.at], r.phase, wait, &g_matmul_fault, kMatmulFault);
         }
       }
-    } else if (warp == kProductWarp && lane == 0 && rank == 0) {  // ------------------ the products
+    } else if (warp == kProductWarp && rank == 0) {  // ------------------------------- the products
       constexpr uint32_t instr = tc_instruction(CTAS * kLanes, BN, 0, 0, false, false);
+      const uint64_t p_desc = tc_operand(smem_addr(smem), 16, 1024),
+                     q_desc = tc_operand(smem_addr(smem) + kLanes * kStep, 16, 1024);
       Ring<G::STAGES> r;
       Ring<G::SLOTS> s;
       for (int t = first; t < tiles && alive; t += apart)
         for (int kb = 0; kb < blocks; ++kb) {
           tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
           tc_wait(&full[r.at], r.phase, alive, &g_matmul_fault, kMatmulFault);
-          if (!alive) break;
+          if (!__all_sync(~0u, alive)) {
+            alive = false;
+            break;
+          }
           tc_fence_after();
-          const uint32_t p = smem_addr(smem + r.at * G::STAGE), q = p + kLanes * kStep;
+          const uint64_t at = static_cast<uint64_t>(r.at * (G::STAGE >> 4));
+          const uint32_t to = tmem + s.at * G::SLOT;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_f8<CTAS>(tmem + s.at * G::SLOT, tc_operand(p + 32 * k, 16, 1024),
-                            tc_operand(q + 32 * k, 16, 1024), instr, k > 0);
-          tc_commit_to<CTAS>(&empty[r.at]);
-          tc_commit_to<CTAS>(&summed[s.at]);
+            for (int k = 0; k < 4; ++k)
+              tc_mma_f8<CTAS>(to, p_desc + at + 2 * k, q_desc + at + 2 * k, instr, k > 0);
+            tc_commit_to<CTAS>(&summed[s.at]);
+            tc_commit_to<CTAS>(&empty[r.at]);
+          }
+          __syncwarp();
           r.next();
           s.next();
         }
       if (!alive) {
         bool wait = true;
-        tc_commit_to<CTAS>(drained);
+        if (elect_one()) tc_commit_to<CTAS>(drained);
+        __syncwarp();
         tc_wait(drained, 0, wait, &g_matmul_fault, kMatmulFault);
       }
     }
@@ -248,6 +257,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     constexpr int HALF = G::HALF, CHUNK = HALF < 32 ? HALF : 32;
     const int half = (warp - kFirstResultWarp) >> 2, in_cta = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * HALF;
+    const uint32_t taken_at = CTAS == 2 ? cluster_addr(taken, 0) : smem_addr(taken);
+    const float* qs0 = q_scales + (QROWS ? half * HALF : half * HALF / 128);
     Ring<G::SLOTS> s;
     Ring<G::AHEAD> x;
     for (int t = first; t < tiles; t += apart) {
@@ -260,30 +271,37 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
       for (int i = 0; i < HALF / 2; ++i) sums[i] = f2(0.0f, 0.0f);
       for (int kb = 0; kb < blocks; ++kb) {
         tc_wait(&scaled[x.at], x.phase, alive, &g_matmul_fault, kMatmulFault);
+        const float* qs = qs0 + x.at * BN;
         float scale = p_scales[x.at * kLanes + in_cta];
-        const float* qs = q_scales + x.at * BN + (QROWS ? half * HALF : half * HALF / 128);
         if constexpr (!QROWS) scale = __fmul_rn(scale, *qs);
         tc_wait(&summed[s.at], s.phase, alive, &g_matmul_fault, kMatmulFault);
         tc_fence_after();
+        const uint32_t from = lanes + s.at * G::SLOT;
+        uint32_t v[2][CHUNK];
+        tmem_ld(from, v[0]);
 #pragma unroll
         for (int c = 0; c < HALF; c += CHUNK) {
-          uint32_t v[CHUNK];
-          tmem_ld(lanes + s.at * G::SLOT + c, v);
-          tmem_ld_wait(v);
+          uint32_t(&now)[CHUNK] = v[(c / CHUNK) & 1];
+          tmem_ld_wait(now);
+          if (c + CHUNK < HALF) {
+            tmem_ld(from + c + CHUNK, v[(c / CHUNK + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
+              else mbar_arrive(&taken[s.at]);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < CHUNK; i += 2) {
-            f32x2 x = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-            if constexpr (QROWS) x = f2_mul(x, *reinterpret_cast<const f32x2*>(qs + c + i));
-            sums[(c + i) / 2] = f2_fma(x, f2(scale, scale), sums[(c + i) / 2]);
+            f32x2 y = f2(__uint_as_float(now[i]), __uint_as_float(now[i + 1]));
+            if constexpr (QROWS) y = f2_mul(y, *reinterpret_cast<const f32x2*>(qs + c + i));
+            sums[(c + i) / 2] = f2_fma(y, f2(scale, scale), sums[(c + i) / 2]);
           }
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (CTAS == 2) mbar_arrive_cluster(cluster_addr(&taken[s.at], 0));
-          else mbar_arrive(&taken[s.at]);
-          mbar_arrive(&used[x.at]);
-        }
+        if (lane == 0) mbar_arrive(&used[x.at]);
         s.next();
         x.next();
       }

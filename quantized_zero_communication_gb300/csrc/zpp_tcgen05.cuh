@@ -236,6 +236,13 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, bool& al
   }
 }
 
+// One thread of a whole warp (the compiler knows it is one: what it issues takes uniform registers).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // A place in a ring of N and the parity of its current round.
 template <int N>
 struct Ring {
