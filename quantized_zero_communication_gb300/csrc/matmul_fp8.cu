@@ -5,7 +5,7 @@
 // The inner sums are tcgen05 products (fp32 in tensor memory), one block of 128 a slot of a ring there;
 // eight warps read each slot, multiply it by its scales and add it to the tile's sums, which stay in
 // registers, while the matrix unit fills the next slot. So a sum never mixes scales, and its length
-// in the matrix unit is 128. A warp each fetches the scales of P and Q, eight blocks ahead: fetched one
+// in the matrix unit is 128. A warp each fetches the scales of P and Q, up to 16 blocks ahead: fetched one
 // block ahead by the warps that use them, their latency (about 1 us beside the operands' traffic) was
 // the time of a block (8192 x 8192 x 8192: 1280 us).
 //
@@ -25,7 +25,7 @@ constexpr int kLanes = 128;        // rows of P in a tile
 constexpr int kStep = 128;         // codes of the sum in a block, and bytes of a row of a stage
 
 // CTAS 2: a pair of CTAs on a tile of 256 x BN; each holds its half of both operands.
-template <int CTAS, int BN>
+template <int CTAS, int BN, bool QROWS>
 struct MatmulGeo {
   static constexpr int Q_ROWS = BN / CTAS;  // of a CTA's stage
   static constexpr int STAGE = (kLanes + Q_ROWS) * kStep;
@@ -33,10 +33,12 @@ struct MatmulGeo {
   static constexpr int SLOT = BN < 32 ? 32 : BN;  // tensor-memory columns of a slot
   static constexpr int SLOTS = 512 / SLOT < 4 ? 512 / SLOT : 4;
   static constexpr int HALF = BN / 2;  // columns of a warp
-  static constexpr int AHEAD = 8;      // blocks whose scales are on their way
+  // Blocks whose scales are waited for together. (A wait costs some 100 clocks; where Q has a scale a
+  // column, one for every block measured better: 8192^3 613 us against 664.)
+  static constexpr int GROUP = QROWS ? 1 : 4, GROUPS = QROWS ? 8 : 4;
   static constexpr int SCALES = STAGES * STAGE;
-  static constexpr int BARS = SCALES + AHEAD * (kLanes + BN) * 4;
-  static constexpr int SMEM = 1024 + BARS + (2 * STAGES + 2 * SLOTS + 2 * AHEAD + 1) * 8 + 16;
+  static constexpr int BARS = SCALES + GROUPS * GROUP * (kLanes + BN) * 4;
+  static constexpr int SMEM = 1024 + BARS + (2 * STAGES + 2 * SLOTS + 2 * GROUPS + 1) * 8 + 16;
 };
 
 struct MatmulSide {
@@ -111,26 +113,26 @@ template <int CTAS, int BN, bool QROWS>
 __global__ void __launch_bounds__(kTensorThreads, 1)
     k_matmul_fp8(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                  const MatmulRun run) {
-  using G = MatmulGeo<CTAS, BN>;
+  using G = MatmulGeo<CTAS, BN, QROWS>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::BARS);
   uint64_t* empty = full + G::STAGES;
   uint64_t* summed = empty + G::STAGES;  // a slot holds a block's sums
   uint64_t* taken = summed + G::SLOTS;   // and has been read
-  uint64_t* scaled = taken + G::SLOTS;   // a block's scales are there
-  uint64_t* used = scaled + G::AHEAD;    // and have been used
-  uint64_t* drained = used + G::AHEAD;
+  uint64_t* scaled = taken + G::SLOTS;   // a group of blocks' scales are there
+  uint64_t* used = scaled + G::GROUPS;   // and have been used
+  uint64_t* drained = used + G::GROUPS;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
-  float* p_scales = reinterpret_cast<float*>(smem + G::SCALES);  // [AHEAD][kLanes]
-  float* q_scales = p_scales + G::AHEAD * kLanes;                // [AHEAD][BN]
+  float* p_scales = reinterpret_cast<float*>(smem + G::SCALES);  // [GROUPS * GROUP][kLanes]
+  float* q_scales = p_scales + G::GROUPS * G::GROUP * kLanes;    // [GROUPS * GROUP][BN]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < G::SLOTS; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], CTAS * kResultWarps);
-    for (int i = 0; i < G::AHEAD; ++i) mbar_init(&scaled[i], 64), mbar_init(&used[i], kResultWarps);
+    for (int i = 0; i < G::GROUPS; ++i) mbar_init(&scaled[i], 64), mbar_init(&used[i], kResultWarps);
     mbar_init(drained, 1);
     mbar_init_fence();
     tma_prefetch(&p_map);
@@ -192,10 +194,11 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
                      q_desc = tc_operand(smem_addr(smem) + kLanes * kStep, 16, 1024);
       Ring<G::STAGES> r;
       Ring<G::SLOTS> s;
+      bool free = false, there = false;  // what the block's waits are for has been seen already
       for (int t = first; t < tiles && alive; t += apart)
         for (int kb = 0; kb < blocks; ++kb) {
-          tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
-          tc_wait(&full[r.at], r.phase, alive, &g_matmul_fault, kMatmulFault);
+          if (!free) tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
+          if (!there) tc_wait(&full[r.at], r.phase, alive, &g_matmul_fault, kMatmulFault);
           if (!__all_sync(~0u, alive)) {
             alive = false;
             break;
@@ -203,16 +206,19 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
           tc_fence_after();
           const uint64_t at = static_cast<uint64_t>(r.at * (G::STAGE >> 4));
           const uint32_t to = tmem + s.at * G::SLOT;
+          uint64_t *use = &empty[r.at], *done = &summed[s.at];
+          r.next();
+          s.next();
+          there = mbar_test(&full[r.at], r.phase);
+          free = mbar_test(&taken[s.at], s.phase ^ 1u);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc_mma_f8<CTAS>(to, p_desc + at + 2 * k, q_desc + at + 2 * k, instr, k > 0);
-            tc_commit_to<CTAS>(&summed[s.at]);
-            tc_commit_to<CTAS>(&empty[r.at]);
+            tc_commit_to<CTAS>(done);
+            tc_commit_to<CTAS>(use);
           }
           __syncwarp();
-          r.next();
-          s.next();
         }
       if (!alive) {
         bool wait = true;
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
       const int count = of_p ? kLanes : Q_SCALES, step = of_p || QROWS ? 1 : 128;
       float* to = of_p ? p_scales : q_scales;
       const int to_step = of_p ? kLanes : BN;
-      Ring<G::AHEAD> x;
+      Ring<G::GROUPS> x;
       for (int t = first; t < tiles; t += apart) {
         int p, q;
         matmul_tile(run, t, p, q);
@@ -240,11 +246,13 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
           const int64_t row = row0 + static_cast<int64_t>(lane + 32 * i) * step;
           from[i] = side.scales + (row < side.rows ? row >> side.shift : 0) * side.row;
         }
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int kb = 0; kb < blocks; kb += G::GROUP) {
           tc_wait(&used[x.at], x.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
+          for (int b = 0; b < G::GROUP && kb + b < blocks; ++b)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (lane + 32 * i < count) cp_async4(to + x.at * to_step + lane + 32 * i, from[i] + kb * side.block);
+            for (int i = 0; i < 8; ++i)
+              if (lane + 32 * i < count)
+                cp_async4(to + (x.at * G::GROUP + b) * to_step + lane + 32 * i, from[i] + (kb + b) * side.block);
           cp_async_arrive_noinc(&scaled[x.at]);  // counts even with no copies of its own
           x.next();
         }
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     const uint32_t taken_at = CTAS == 2 ? cluster_addr(taken, 0) : smem_addr(taken);
     const float* qs0 = q_scales + (QROWS ? half * HALF : half * HALF / 128);
     Ring<G::SLOTS> s;
-    Ring<G::AHEAD> x;
+    Ring<G::GROUPS> x;
     for (int t = first; t < tiles; t += apart) {
       int p, q;
       matmul_tile(run, t, p, q);
@@ -270,9 +278,10 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
 #pragma unroll
       for (int i = 0; i < HALF / 2; ++i) sums[i] = f2(0.0f, 0.0f);
       for (int kb = 0; kb < blocks; ++kb) {
-        tc_wait(&scaled[x.at], x.phase, alive, &g_matmul_fault, kMatmulFault);
-        const float* qs = qs0 + x.at * BN;
-        float scale = p_scales[x.at * kLanes + in_cta];
+        const int in_group = kb % G::GROUP;
+        if (in_group == 0) tc_wait(&scaled[x.at], x.phase, alive, &g_matmul_fault, kMatmulFault);
+        const float* qs = qs0 + (x.at * G::GROUP + in_group) * BN;
+        float scale = p_scales[(x.at * G::GROUP + in_group) * kLanes + in_cta];
         if constexpr (!QROWS) scale = __fmul_rn(scale, *qs);
         tc_wait(&summed[s.at], s.phase, alive, &g_matmul_fault, kMatmulFault);
         tc_fence_after();
@@ -292,18 +301,26 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
               if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
               else mbar_arrive(&taken[s.at]);
             }
+            s.next();
           }
 #pragma unroll
-          for (int i = 0; i < CHUNK; i += 2) {
-            f32x2 y = f2(__uint_as_float(now[i]), __uint_as_float(now[i + 1]));
-            if constexpr (QROWS) y = f2_mul(y, *reinterpret_cast<const f32x2*>(qs + c + i));
-            sums[(c + i) / 2] = f2_fma(y, f2(scale, scale), sums[(c + i) / 2]);
+          for (int i = 0; i < CHUNK; i += 4) {
+            f32x2 y0 = f2(__uint_as_float(now[i]), __uint_as_float(now[i + 1])),
+                  y1 = f2(__uint_as_float(now[i + 2]), __uint_as_float(now[i + 3]));
+            if constexpr (QROWS) {
+              const float4 w = *reinterpret_cast<const float4*>(qs + c + i);
+              y0 = f2_mul(y0, f2(w.x, w.y));
+              y1 = f2_mul(y1, f2(w.z, w.w));
+            }
+            sums[(c + i) / 2] = f2_fma(y0, f2(scale, scale), sums[(c + i) / 2]);
+            sums[(c + i) / 2 + 1] = f2_fma(y1, f2(scale, scale), sums[(c + i) / 2 + 1]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&used[x.at]);
-        s.next();
-        x.next();
+        if (in_group == G::GROUP - 1 || kb + 1 == blocks) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&used[x.at]);
+          x.next();
+        }
       }
       if (p0 < run.p.rows) {
 #pragma unroll
@@ -325,9 +342,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
   }
 }
 
-template <int CTAS, int BN>
-static cudaError_t run_matmul(const MatmulArgs& a, bool swap, cudaStream_t s) {
-  using G = MatmulGeo<CTAS, BN>;
+template <int CTAS, int BN, bool QROWS>
+static cudaError_t run_matmul_as(const MatmulArgs& a, bool swap, cudaStream_t s) {
+  using G = MatmulGeo<CTAS, BN, QROWS>;
   const MatmulOperand &p = swap ? a.b : a.a, &q = swap ? a.a : a.b;
   MatmulRun run{};
   const auto side = [](const MatmulOperand& o) {
@@ -350,12 +367,18 @@ static cudaError_t run_matmul(const MatmulArgs& a, bool swap, cudaStream_t s) {
   CUtensorMap p_map, q_map;
   cudaError_t e = make_tensor_map(&p_map, p.codes, 1, a.depth, p.rows, p.stride, 0, 0, kLanes);
   if (e == cudaSuccess) e = make_tensor_map(&q_map, q.codes, 1, a.depth, q.rows, q.stride, 0, 0, G::Q_ROWS);
-  auto kern = run.q.shift == 0 ? k_matmul_fp8<CTAS, BN, true> : k_matmul_fp8<CTAS, BN, false>;
+  auto kern = k_matmul_fp8<CTAS, BN, QROWS>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(run.p_tiles) * run.q_tiles, most = 152 / CTAS;
   const unsigned grid = static_cast<unsigned>((tiles < most ? tiles : most) * CTAS);
   return launch_overlapped_cluster(kern, dim3(grid), CTAS, kTensorThreads, G::SMEM, s, p_map, q_map, run);
+}
+
+template <int CTAS, int BN>
+static cudaError_t run_matmul(const MatmulArgs& a, bool swap, cudaStream_t s) {
+  return (swap ? a.a : a.b).tile == 1 ? run_matmul_as<CTAS, BN, true>(a, swap, s)
+                                      : run_matmul_as<CTAS, BN, false>(a, swap, s);
 }
 
 cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {

@@ -249,6 +249,17 @@ float adjusted(const MuonArgs& a, int64_t rows, int64_t cols) {
   return static_cast<float>(a.lr * f);
 }
 
+int64_t tiles_of(const Batch& b, int op, int64_t side) {
+  int64_t tiles = 0;
+  for (const Shape& s : b.shapes) {
+    const int64_t m = (s.small() + side - 1) / side, n = (std::max(s.rows, s.cols) + side - 1) / side;
+    tiles += s.count * (op == kNsApply ? m * n : m * (m + 1) / 2);
+  }
+  return tiles;
+}
+// Tiles of 256 by pairs of CTAs where they fill the GPU.
+int tile_side(const Batch& b, int op) { return tiles_of(b, op, 256) >= 60 ? 256 : 128; }
+
 cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a, uint8_t* workspace,
                       cudaStream_t s) {
   // ---- where things lie
@@ -338,6 +349,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     n.early = step < a.steps - 3;
     for (int op = kNsGram; op <= kNsApply; ++op) {
       n.op = op == kNsApply && step == a.steps - 1 ? kNsLast : op;
+      n.side = tile_side(b, op);
       n.tiles = 0;
       for (size_t k = 0; k < b.shapes.size(); ++k) {
         const Shape& sh = b.shapes[k];
@@ -379,8 +391,8 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
         g.ld = static_cast<int32_t>(op == kNsApply ? sh.ld() : ma);
         g.apart = op == kNsApply ? sh.x_elems() : sh.a_elems();
         g.step = adjusted(a, sh.rows, sh.cols);
-        g.p_tiles = (g.rows + 127) / 128;
-        g.q_tiles = (g.cols + 127) / 128;
+        g.p_tiles = (g.rows + n.side - 1) / n.side;
+        g.q_tiles = (g.cols + n.side - 1) / n.side;
         g.per_matrix = op == kNsApply ? g.p_tiles * g.q_tiles : g.p_tiles * (g.p_tiles + 1) / 2;
         g.first_tile = n.tiles;
         g.first_matrix = sh.first;

@@ -28,14 +28,14 @@ namespace zpp {
 static __device__ unsigned g_muon_fault;
 constexpr unsigned kMuonFault = 16;  // its bit of the fault word
 
-constexpr int kNsTile = 128, kNsStep = 64;  // tile side, steps of the sum in a stage
-constexpr int kNsOperand = kNsTile * kNsStep * 2;
+constexpr int kNsSide = 128, kNsStep = 64;  // rows of an operand in a CTA, steps of the sum in a stage
+constexpr int kNsOperand = kNsSide * kNsStep * 2;
 constexpr int kNsStage = 2 * kNsOperand;
-constexpr int kNsStages = 6, kNsSlots = 4;
+constexpr int kNsStages = 6;
 constexpr int kNsBars = kNsStages * kNsStage;
-constexpr int kNsSmem = 1024 + kNsBars + (2 * kNsStages + 2 * kNsSlots + 1) * 8 + 16;
-constexpr int kNsWarps = 8;  // of the epilogue
-constexpr int kNsThreads = (kNsWarps + 2) * 32;
+constexpr int kNsSmem = 1024 + kNsBars + (2 * kNsStages + 2 * 2 + 1) * 8 + 16;
+// Tiles are squares of CTAS * 128: of one CTA, or of a pair that holds half of each operand.
+constexpr int kNsSlots = 2;
 
 struct NsTile {
   int group, matrix, p, q;
@@ -60,17 +60,21 @@ __device__ __forceinline__ NsTile ns_tile(const NsLaunch& n, int t) {
   return r;
 }
 
+// 128 rows of an operand, from row `at` on, over 64 steps of the sum from k on.
+template <int CTAS>
 __device__ __forceinline__ void ns_load(uint8_t* dst, const CUtensorMap* map, bool mn, int at, int k, int z,
                                         uint64_t* bar) {
-  if (mn) {
-    tma_load(dst, map, at, k, z, bar);
-    tma_load(dst + kNsOperand / 2, map, at + 64, k, z, bar);
+  if constexpr (CTAS == 2) {
+    const uint32_t there = cluster_addr(bar, 0);
+    tma_load_pair(dst, map, mn ? at : k, mn ? k : at, z, there);
+    if (mn) tma_load_pair(dst + kNsOperand / 2, map, at + 64, k, z, there);
   } else {
-    tma_load(dst, map, k, at, z, bar);
+    tma_load(dst, map, mn ? at : k, mn ? k : at, z, bar);
+    if (mn) tma_load(dst + kNsOperand / 2, map, at + 64, k, z, bar);
   }
 }
-__device__ __forceinline__ uint64_t ns_operand(uint32_t at, bool mn, int k) {
-  return mn ? tc_operand(at + 2048 * k, kNsOperand / 2, 1024) : tc_operand(at + 32 * k, 16, 1024);
+__device__ __forceinline__ uint64_t ns_operand(uint32_t at, bool mn) {
+  return mn ? tc_operand(at, kNsOperand / 2, 1024) : tc_operand(at, 16, 1024);
 }
 
 // v as two fp16 each: the nearest ones, and those nearest to what they lost.
@@ -189,7 +193,9 @@ __device__ __forceinline__ void ns_store(const NsLaunch& n, const NsGroup& g, in
   }
 }
 
-__global__ void __launch_bounds__(kNsThreads, 1) k_newton_schulz(const __grid_constant__ NsLaunch n) {
+template <int CTAS>
+__global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __grid_constant__ NsLaunch n) {
+  constexpr int TILE = CTAS * kNsSide, HALF = TILE / 2;  // columns of a warp
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kNsBars);
@@ -200,109 +206,125 @@ __global__ void __launch_bounds__(kNsThreads, 1) k_newton_schulz(const __grid_co
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNsStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < kNsSlots; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], kNsWarps);
+    for (int i = 0; i < kNsSlots; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], CTAS * kResultWarps);
     mbar_init(drained, 1);
     mbar_init_fence();
   }
-  if (warp == kNsWarps) {
-    tmem_alloc<1>(tmem_at, kNsTile * kNsSlots);
-    tmem_alloc_done<1>();
+  if (warp == kCopyWarp) {
+    tmem_alloc<CTAS>(tmem_at, TILE * kNsSlots);
+    tmem_alloc_done<CTAS>();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
   grid_wait();
   grid_release();
+  const int first = blockIdx.x / CTAS, apart = gridDim.x / CTAS;
   bool alive = true;
 
-  if (warp == kNsWarps) {  // ------------------------------------------------- copies into the stages
-    if (lane == 0) {
-      Ring<kNsStages> r;
-      int64_t issued = 0;
-      for (int t = blockIdx.x; t < n.tiles && alive; t += gridDim.x) {
-        const NsTile at = ns_tile(n, t);
-        const NsGroup& g = n.group[at.group];
-        for (int part = 0; part < g.parts && alive; ++part) {
-          const CUtensorMap *p = part == 2 ? &g.p_low : &g.p, *q = part == 1 ? &g.q_low : &g.q;
-          for (int k = 0; k < g.depth; k += kNsStep) {
-            tc_wait(&empty[r.at], r.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
-            if (!alive) break;
-            uint8_t* stage = smem + r.at * kNsStage;
-            mbar_arrive_expect_tx(&full[r.at], kNsStage);
-            ns_load(stage, p, g.p_mn, at.p * kNsTile, k, at.matrix, &full[r.at]);
-            ns_load(stage + kNsOperand, q, g.q_mn, at.q * kNsTile, k, at.matrix, &full[r.at]);
-            ++issued;
-            r.next();
-          }
-        }
-      }
-      if (!alive) {  // copies that nobody may have waited for
-        bool wait = true;
-        for (int64_t d = 0; d < kNsStages && d < issued; ++d) {
-          if (--r.at < 0) r.at = kNsStages - 1, r.phase ^= 1u;
-          tc_wait(&full[r.at], r.phase, wait, &g_muon_fault, kMuonFault);
-        }
-      }
-    }
-  } else if (warp == kNsWarps + 1) {  // ------------------------------------------------ the products
-    if (lane == 0) {
-      Ring<kNsStages> r;
-      Ring<kNsSlots> s;
-      for (int t = blockIdx.x; t < n.tiles && alive; t += gridDim.x) {
-        const NsGroup& g = n.group[ns_tile(n, t).group];
-        const uint32_t instr = tc_instruction(kNsTile, kNsTile, 0, 0, g.p_mn, g.q_mn);
-        tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
-        const int stages = g.parts * ((g.depth + kNsStep - 1) / kNsStep);
-        for (int k = 0; k < stages; ++k) {
-          tc_wait(&full[r.at], r.phase, alive, &g_muon_fault, kMuonFault);
-          if (!alive) break;
-          tc_fence_after();
-          const uint32_t p = smem_addr(smem + r.at * kNsStage), q = p + kNsOperand;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc_mma_f16<1>(tmem + s.at * kNsTile, ns_operand(p, g.p_mn, j), ns_operand(q, g.q_mn, j), instr,
-                          k > 0 || j > 0);
-          tc_commit(&empty[r.at]);
-          r.next();
-        }
-        if (!alive) break;
-        tc_commit(&summed[s.at]);
-        s.next();
-      }
-      if (!alive) {
-        bool wait = true;
-        tc_commit(drained);
-        tc_wait(drained, 0, wait, &g_muon_fault, kMuonFault);
-      }
-    }
-  } else {  // -------------------------------------------------------------------------- the results
-    const int half = warp >> 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * (kNsTile / 2);
-    const bool skip = n.op == kNsLast && n.factor && !isfinite(ld_after_f32(n.factor));
-    Ring<kNsSlots> s;
-    for (int t = blockIdx.x; t < n.tiles; t += gridDim.x) {
+  if (warp == kCopyWarp && lane == 0) {  // ----------------------------------- copies into the stages
+    Ring<kNsStages> r;
+    int64_t issued = 0;
+    for (int t = first; t < n.tiles && alive; t += apart) {
       const NsTile at = ns_tile(n, t);
       const NsGroup& g = n.group[at.group];
-      const int p = at.p * kNsTile + (warp & 3) * 32 + lane;
+      const int p0 = at.p * TILE + rank * kNsSide, q0 = at.q * TILE + rank * kNsSide;
+      for (int part = 0; part < g.parts && alive; ++part) {
+        const CUtensorMap *p = part == 2 ? &g.p_low : &g.p, *q = part == 1 ? &g.q_low : &g.q;
+        for (int k = 0; k < g.depth; k += kNsStep) {
+          tc_wait(&empty[r.at], r.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
+          if (!alive) break;
+          uint8_t* stage = smem + r.at * kNsStage;
+          // (a pair's copies are counted by the first CTA, which uses them)
+          if (rank == 0) mbar_arrive_expect_tx(&full[r.at], CTAS * kNsStage);
+          ns_load<CTAS>(stage, p, g.p_mn, p0, k, at.matrix, &full[r.at]);
+          ns_load<CTAS>(stage + kNsOperand, q, g.q_mn, q0, k, at.matrix, &full[r.at]);
+          ++issued;
+          r.next();
+        }
+      }
+    }
+    if (!alive && rank == 0) {  // copies that nobody may have waited for
+      bool wait = true;
+      for (int64_t d = 0; d < kNsStages && d < issued; ++d) {
+        if (--r.at < 0) r.at = kNsStages - 1, r.phase ^= 1u;
+        tc_wait(&full[r.at], r.phase, wait, &g_muon_fault, kMuonFault);
+      }
+    }
+  } else if (warp == kProductWarp && rank == 0) {  // ------------------------------------ the products
+    Ring<kNsStages> r;
+    Ring<kNsSlots> s;
+    for (int t = first; t < n.tiles && alive; t += apart) {
+      const NsGroup& g = n.group[ns_tile(n, t).group];
+      const uint32_t instr = tc_instruction(TILE, TILE, 0, 0, g.p_mn, g.q_mn);
+      const uint32_t base = smem_addr(smem), to = tmem + s.at * TILE;
+      const uint64_t p_desc = ns_operand(base, g.p_mn), q_desc = ns_operand(base + kNsOperand, g.q_mn);
+      const uint64_t p_step = g.p_mn ? 2048 >> 4 : 32 >> 4, q_step = g.q_mn ? 2048 >> 4 : 32 >> 4;
+      const int stages = g.parts * ((g.depth + kNsStep - 1) / kNsStep);
+      tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
+      bool there = false;  // the stage has been seen already
+      for (int k = 0; k < stages; ++k) {
+        if (!there) tc_wait(&full[r.at], r.phase, alive, &g_muon_fault, kMuonFault);
+        if (!__all_sync(~0u, alive)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t at = static_cast<uint64_t>(r.at * (kNsStage >> 4));
+        uint64_t* use = &empty[r.at];
+        r.next();
+        there = mbar_test(&full[r.at], r.phase);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc_mma_f16<CTAS>(to, p_desc + at + j * p_step, q_desc + at + j * q_step, instr, k > 0 || j > 0);
+          tc_commit_to<CTAS>(use);
+          if (k + 1 == stages) tc_commit_to<CTAS>(&summed[s.at]);
+        }
+        __syncwarp();
+      }
+      s.next();
+    }
+    if (!alive) {
+      bool wait = true;
+      if (elect_one()) tc_commit_to<CTAS>(drained);
+      __syncwarp();
+      tc_wait(drained, 0, wait, &g_muon_fault, kMuonFault);
+    }
+  } else if (warp >= kFirstResultWarp) {  // ---------------------------------------------- the results
+    const int half = (warp - kFirstResultWarp) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * HALF;
+    const uint32_t taken_at = CTAS == 2 ? cluster_addr(taken, 0) : 0;
+    const bool skip = n.op == kNsLast && n.factor && !isfinite(ld_after_f32(n.factor));
+    Ring<kNsSlots> s;
+    for (int t = first; t < n.tiles; t += apart) {
+      const NsTile at = ns_tile(n, t);
+      const NsGroup& g = n.group[at.group];
+      const int p = at.p * TILE + rank * kNsSide + (warp & 3) * 32 + lane;
       tc_wait(&summed[s.at], s.phase, alive, &g_muon_fault, kMuonFault);
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < kNsTile / 2; c += 32) {
+#pragma unroll 1
+      for (int c = 0; c < HALF; c += 32) {
         uint32_t v[32];
-        tmem_ld(lanes + s.at * kNsTile + c, v);
+        tmem_ld(lanes + s.at * TILE + c, v);
         tmem_ld_wait(v);
-        if (c + 32 == kNsTile / 2) {
+        if (c + 32 == HALF) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&taken[s.at]);
+          if (lane == 0) {
+            if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
+            else mbar_arrive(&taken[s.at]);
+          }
         }
         if (p < g.rows && !skip) {
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
-            const int q = at.q * kNsTile + half * (kNsTile / 2) + c + j;
+            const int q = at.q * TILE + half * HALF + c + j;
             float d[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) d[i] = __uint_as_float(v[j + i]);
@@ -314,20 +336,25 @@ __global__ void __launch_bounds__(kNsThreads, 1) k_newton_schulz(const __grid_co
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (warp == kNsWarps) {
+  if constexpr (CTAS == 2) cluster_sync();
+  else __syncthreads();
+  if (warp == kCopyWarp) {
     tc_fence_after();
-    tmem_free<1>(tmem, kNsTile * kNsSlots);
+    tmem_free<CTAS>(tmem, TILE * kNsSlots);
   }
 }
 
-cudaError_t launch_ns(const NsLaunch& n, cudaStream_t s) {
+template <int CTAS>
+static cudaError_t run_ns(const NsLaunch& n, cudaStream_t s) {
   const cudaError_t e =
-      cudaFuncSetAttribute(k_newton_schulz, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
+      cudaFuncSetAttribute(k_newton_schulz<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped_smem(k_newton_schulz, dim3(static_cast<unsigned>(n.tiles < 152 ? n.tiles : 152)),
-                                kNsThreads, kNsSmem, s, n);
+  const int most = 152 / CTAS;
+  return launch_overlapped_cluster(k_newton_schulz<CTAS>,
+                                   dim3(static_cast<unsigned>((n.tiles < most ? n.tiles : most) * CTAS)), CTAS,
+                                   kTensorThreads, kNsSmem, s, n);
 }
+cudaError_t launch_ns(const NsLaunch& n, cudaStream_t s) { return n.side == 256 ? run_ns<2>(n, s) : run_ns<1>(n, s); }
 
 cudaError_t read_muon_fault(unsigned* flags, bool clear) {
   const cudaError_t err = cudaMemcpyFromSymbol(flags, g_muon_fault, sizeof(unsigned));

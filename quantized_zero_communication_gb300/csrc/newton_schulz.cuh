@@ -47,6 +47,7 @@ struct NsResult {  // last: where a matrix's result goes
 };
 struct NsLaunch {
   int32_t op, groups, tiles;
+  int32_t side;  // of a tile: 128, or 256 by a pair of CTAs
   float a, b, c;
   int32_t early;  // apply: three steps or more follow
   float decay;

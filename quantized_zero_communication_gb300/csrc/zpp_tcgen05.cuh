@@ -236,6 +236,17 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, bool& al
   }
 }
 
+// Whether a barrier's phase has completed, without waiting: asked while something else is going on.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One thread of a whole warp (the compiler knows it is one: what it issues takes uniform registers).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
