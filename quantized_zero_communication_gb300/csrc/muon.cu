@@ -1,7 +1,7 @@
 // muon.cu -- K12, K13 and the order of a Muon step:
 //
 //   m = mu m + (1 - mu) c g,  u = (1 - mu) c g + mu m (nesterov) or m,  X = u / max(|u|_F, eps)   (K12, K13)
-//   five steps of K14's products, the last one  p = p (1 - lr decay) - lr adjust X
+//   the steps of K14, after the last one  p = p (1 - lr decay) - lr adjust X
 //
 // K12 reads the gradient and the momentum, writes the momentum and one partial sum of squares per
 // CTA; K13 adds a matrix's partials in a fixed order, makes u again and writes X as two fp16.
@@ -26,6 +26,7 @@ struct MuonTable {
   int32_t x_kind;
   const float* factor;
   float* partial;
+  uint32_t* arrived;  // K14's count, zeroed by K13
   ChunkHints hints;
   int32_t first[kMuonMatrices + 1];  // CTAs of the matrices before this one
   struct Item {
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kThreads) k_muon(const __grid_constant__ MuonT
   __shared__ double part[kWarps];
   grid_wait();
   grid_release();
+  if (SCALE && blockIdx.x == 0 && threadIdx.x == 0) *t.arrived = 0u;
   const float factor = t.factor ? ld_after_f32(t.factor) : 1.0f;
   if (!isfinite(factor)) return;
   const int m = tensor_of(t.hints, t.first, static_cast<int>(blockIdx.x));
@@ -175,8 +177,8 @@ struct Shape {
   int64_t rows, cols;
   int count = 0, first = 0;
   int64_t small() const { return std::min(rows, cols); }
-  int64_t ld() const { return (cols + 7) / 8 * 8; }
-  int64_t small_ld() const { return (small() + 7) / 8 * 8; }
+  int64_t ld() const { return (cols + 15) / 16 * 16; }
+  int64_t small_ld() const { return (small() + 15) / 16 * 16; }
   int64_t x_elems() const { return (rows * ld() + 63) / 64 * 64; }  // one matrix, 128-byte aligned
   int64_t a_elems() const { return (small() * small_ld() + 63) / 64 * 64; }
   int64_t diag_elems() const { return (small() + 31) / 32 * 32; }  // fp32
@@ -196,7 +198,7 @@ struct Batch {
   int64_t bytes() const {
     int64_t b = 0;
     for (const Shape& s : shapes) b += s.bytes();
-    return b + (static_cast<int64_t>(order.size()) * kMuonPartials * 4 + 127) / 128 * 128;
+    return 128 + b + (static_cast<int64_t>(order.size()) * kMuonPartials * 4 + 127) / 128 * 128;
   }
 };
 constexpr int64_t kBatchElems = int64_t{1} << 28;  // more than this starts another batch
@@ -249,16 +251,32 @@ float adjusted(const MuonArgs& a, int64_t rows, int64_t cols) {
   return static_cast<float>(a.lr * f);
 }
 
-int64_t tiles_of(const Batch& b, int op, int64_t side) {
-  int64_t tiles = 0;
-  for (const Shape& s : b.shapes) {
-    const int64_t m = (s.small() + side - 1) / side, n = (std::max(s.rows, s.cols) + side - 1) / side;
-    tiles += s.count * (op == kNsApply ? m * n : m * (m + 1) / 2);
+// The side of K14's tiles: 256 by a pair of CTAs, or 128, which share themselves out more evenly. A stage
+// takes either about as long (0.3 us): counted are those of the slowest CTA.
+int tile_side(const Batch& b) {
+  double cost[2];
+  for (int pair = 0; pair < 2; ++pair) {
+    const int64_t side = pair ? 256 : 128, at_once = pair ? 76 : 152;
+    double tiles[3] = {}, work[3] = {}, longest[3] = {};
+    for (const Shape& s : b.shapes) {
+      const int64_t small = s.small(), large = std::max(s.rows, s.cols);
+      const int64_t m = (small + side - 1) / side, n = (large + side - 1) / side;
+      for (int op = 0; op < 3; ++op) {
+        const double t = static_cast<double>(s.count * (op == kNsApply ? m * n : m * (m + 1) / 2));
+        const double depth = static_cast<double>(op == kNsGram ? large : small) * (s.exact() ? 3 : 1);
+        tiles[op] += t;
+        work[op] += t * depth;
+        longest[op] = std::max(longest[op], depth);
+      }
+    }
+    cost[pair] = 0.0;
+    for (int op = 0; op < 3; ++op) {
+      const double rounds = std::ceil(tiles[op] / static_cast<double>(at_once));
+      cost[pair] += std::max(longest[op], work[op] / tiles[op] * rounds);
+    }
   }
-  return tiles;
+  return cost[1] < cost[0] ? 256 : 128;
 }
-// Tiles of 256 by pairs of CTAs where they fill the GPU.
-int tile_side(const Batch& b, int op) { return tiles_of(b, op, 256) >= 60 ? 256 : 128; }
 
 cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a, uint8_t* workspace,
                       cudaStream_t s) {
@@ -268,7 +286,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     float *a_diag, *b_diag;
   };
   std::vector<Place> place(b.shapes.size());
-  uint8_t* at = workspace;
+  uint8_t* at = workspace + 128;  // (the first bytes count CTAs)
   for (size_t k = 0; k < b.shapes.size(); ++k) {
     const Shape& sh = b.shapes[k];
     const auto take = [&](int64_t elems, int size) {
@@ -299,6 +317,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
   t.x_kind = a.x_kind;
   t.factor = a.factor;
   t.partial = reinterpret_cast<float*>(at);
+  t.arrived = reinterpret_cast<uint32_t*>(workspace);
   t.first[0] = 0;
   for (size_t k = 0, i = 0; k < b.shapes.size(); ++k) {
     const Shape& sh = b.shapes[k];
@@ -331,78 +350,56 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
 
   // ---- K14
   NsLaunch n{};
-  n.groups = static_cast<int32_t>(b.shapes.size());
-  n.decay = a.decay;
+  const int side = tile_side(b);
+  n.steps = a.steps;
+  n.shapes = static_cast<int32_t>(b.shapes.size());
   n.out_kind = a.out_kind;
+  n.decay = a.decay;
   n.factor = a.factor;
+  n.arrived = t.arrived;
+  for (int i = 0; i < 3 * a.steps; ++i) n.coefficients[i] = static_cast<float>(a.coefficients[i]);
   for (size_t i = 0; i < b.order.size(); ++i) n.result[i] = NsResult{list[b.order[i]].param, list[b.order[i]].out};
-  const auto map = [&](const uint16_t* p, int64_t rows, int64_t cols, int64_t ld, int64_t count, int64_t apart,
-                       bool mn, CUtensorMap* out) {
-    if (e == cudaSuccess)
-      e = make_tensor_map(out, p, 2, cols, rows, ld * 2, count, apart * 2, mn ? 64 : 128);
-  };
-  for (int step = 0; step < a.steps && e == cudaSuccess; ++step) {
-    const int from = step & 1;
-    n.a = static_cast<float>(a.coefficients[3 * step]);
-    n.b = static_cast<float>(a.coefficients[3 * step + 1]);
-    n.c = static_cast<float>(a.coefficients[3 * step + 2]);
-    n.early = step < a.steps - 3;
-    for (int op = kNsGram; op <= kNsApply; ++op) {
-      n.op = op == kNsApply && step == a.steps - 1 ? kNsLast : op;
-      n.side = tile_side(b, op);
-      n.tiles = 0;
-      for (size_t k = 0; k < b.shapes.size(); ++k) {
-        const Shape& sh = b.shapes[k];
-        NsGroup& g = n.group[k];
-        const int64_t m = sh.small(), ma = sh.small_ld();
-        const Place& pl = place[k];
-        const auto x_to = [&](bool mn, CUtensorMap* to, CUtensorMap* low) {
-          map(pl.x[from], sh.rows, sh.cols, sh.ld(), sh.count, sh.x_elems(), mn, to);
-          if (sh.exact()) map(pl.x_low[from], sh.rows, sh.cols, sh.ld(), sh.count, sh.x_elems(), mn, low);
-        };
-        const auto a_to = [&](const uint16_t* p, const uint16_t* p_low, CUtensorMap* to, CUtensorMap* low) {
-          map(p, m, m, ma, sh.count, sh.a_elems(), false, to);
-          if (sh.exact()) map(p_low, m, m, ma, sh.count, sh.a_elems(), false, low);
-        };
-        g.parts = sh.exact() ? 3 : 1;
-        g.rows = static_cast<int32_t>(op == kNsApply ? sh.rows : m);
-        g.cols = static_cast<int32_t>(op == kNsApply ? sh.cols : m);
-        g.depth = static_cast<int32_t>(op == kNsGram ? std::max(sh.rows, sh.cols) : m);
-        g.p_mn = op == kNsGram && !sh.wide();
-        g.q_mn = op == kNsGram ? !sh.wide() : op == kNsApply && sh.wide();
-        g.diag_apart = static_cast<int32_t>(sh.diag_elems());
-        g.diag_in = op == kNsPoly ? pl.a_diag : pl.b_diag;
-        g.diag_out = op == kNsGram ? pl.a_diag : pl.b_diag;
-        if (op == kNsGram) {
-          x_to(g.p_mn, &g.p, &g.p_low);
-          g.q = g.p, g.q_low = g.p_low;
-          g.out = pl.a, g.out_low = pl.a_low;
-        } else if (op == kNsPoly) {
-          a_to(pl.a, pl.a_low, &g.p, &g.p_low);
-          g.q = g.p, g.q_low = g.p_low;
-          g.in = pl.a, g.in_low = pl.a_low;
-          g.out = pl.b, g.out_low = pl.b_low;
-        } else {
-          if (sh.wide()) a_to(pl.b, pl.b_low, &g.p, &g.p_low), x_to(true, &g.q, &g.q_low);
-          else x_to(false, &g.p, &g.p_low), a_to(pl.b, pl.b_low, &g.q, &g.q_low);
-          g.in = pl.x[from], g.in_low = pl.x_low[from];
-          g.out = pl.x[from ^ 1], g.out_low = pl.x_low[from ^ 1];
-        }
-        g.ld = static_cast<int32_t>(op == kNsApply ? sh.ld() : ma);
-        g.apart = op == kNsApply ? sh.x_elems() : sh.a_elems();
-        g.step = adjusted(a, sh.rows, sh.cols);
-        g.p_tiles = (g.rows + n.side - 1) / n.side;
-        g.q_tiles = (g.cols + n.side - 1) / n.side;
-        g.per_matrix = op == kNsApply ? g.p_tiles * g.q_tiles : g.p_tiles * (g.p_tiles + 1) / 2;
-        g.first_tile = n.tiles;
-        g.first_matrix = sh.first;
-        n.tiles += g.per_matrix * sh.count;
+  for (size_t k = 0; k < b.shapes.size(); ++k) {
+    const Shape& sh = b.shapes[k];
+    const Place& pl = place[k];
+    NsShape& g = n.shape[k];
+    g.rows = static_cast<int32_t>(sh.rows), g.cols = static_cast<int32_t>(sh.cols);
+    g.x_ld = static_cast<int32_t>(sh.ld()), g.a_ld = static_cast<int32_t>(sh.small_ld());
+    g.x_apart = sh.x_elems(), g.a_apart = sh.a_elems(), g.diag_apart = static_cast<int32_t>(sh.diag_elems());
+    g.wide = sh.wide(), g.exact = sh.exact();
+    g.count = sh.count, g.first_matrix = sh.first;
+    g.side_tiles = static_cast<int32_t>((sh.small() + side - 1) / side);
+    g.row_tiles = static_cast<int32_t>((sh.rows + side - 1) / side);
+    g.col_tiles = static_cast<int32_t>((sh.cols + side - 1) / side);
+    g.first_tile[0] = n.tiles[0], g.first_tile[1] = n.tiles[1];
+    n.tiles[0] += sh.count * g.side_tiles * (g.side_tiles + 1) / 2;
+    n.tiles[1] += sh.count * g.row_tiles * g.col_tiles;
+    g.step = adjusted(a, sh.rows, sh.cols);
+    g.a_at = pl.a, g.a_low_at = pl.a_low, g.b_at = pl.b, g.b_low_at = pl.b_low;
+    g.a_diag = pl.a_diag, g.b_diag = pl.b_diag;
+    const auto map = [&](const uint16_t* p, bool of_x, bool mn, CUtensorMap* to) {
+      if (e == cudaSuccess)
+        e = make_tensor_map(to, p, 2, of_x ? sh.cols : sh.small(), of_x ? sh.rows : sh.small(),
+                            (of_x ? sh.ld() : sh.small_ld()) * 2, sh.count,
+                            (of_x ? sh.x_elems() : sh.a_elems()) * 2, mn ? 64 : 128);
+    };
+    for (int i = 0; i < 2; ++i) {
+      g.x_at[i] = pl.x[i], g.x_low_at[i] = pl.x_low[i];
+      map(pl.x[i], true, !sh.wide(), &g.x[i]);
+      map(pl.x[i], true, sh.wide(), &g.xt[i]);
+      if (sh.exact()) {
+        map(pl.x_low[i], true, !sh.wide(), &g.x_low[i]);
+        map(pl.x_low[i], true, sh.wide(), &g.xt_low[i]);
       }
-      if (e == cudaSuccess) e = launch_ns(n, s);
-      if (e != cudaSuccess) return e;
+    }
+    map(pl.a, false, false, &g.a);
+    map(pl.b, false, false, &g.b);
+    if (sh.exact()) {
+      map(pl.a_low, false, false, &g.a_low);
+      map(pl.b_low, false, false, &g.b_low);
     }
   }
-  return e;
+  return e != cudaSuccess ? e : launch_ns(n, side, s);
 }
 
 }  // namespace

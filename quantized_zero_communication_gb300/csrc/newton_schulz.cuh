@@ -1,4 +1,4 @@
-// newton_schulz.cuh -- the products of K14: what a launch is told (internal to the Muon step).
+// newton_schulz.cuh -- K14: what its launch is told (internal to the Muon step).
 #pragma once
 
 #include <cuda.h>
@@ -14,50 +14,52 @@ constexpr float kXScale = 1024.0f;
 // Matrices whose smaller side is at most this are worked on with products of both fp16.
 constexpr int kNsExactSide = 128;
 
+// The three products of a step, in their order.
 enum NsOp : int32_t {
   kNsGram = 0,   // A = X X^T (or X^T X): the smaller of the two, symmetric
   kNsPoly = 1,   // B = b A + c A A, symmetric
-  kNsApply = 2,  // X = a X + B X (or X B)
-  kNsLast = 3,   // the same, written as the result
+  kNsApply = 2,  // X = a X + B X (or X B); of the last step the result
 };
+constexpr int kNsMaxSteps = 100;
 
-// The matrices of one shape in a launch: D[rows][cols] = P Q^T, the sum over `depth`. parts 3: P and Q
-// are sums of two fp16, and D = P Q^T + P Qlow^T + Plow Q^T.
-struct NsGroup {
-  CUtensorMap p, q, p_low, q_low;
-  int32_t parts;
-  int32_t p_mn, q_mn;        // the operand's rows are steps of the sum
-  int32_t rows, cols, depth;
-  int32_t p_tiles, q_tiles;  // symmetric: q_tiles == p_tiles, tiles on and above the diagonal
-  int32_t per_matrix;        // tiles of one matrix
-  int32_t first_tile;        // of the group in the launch
-  int32_t first_matrix;      // of the group in the batch
-  int32_t ld;                // of in, low and out (elements)
-  int64_t apart;             // elements between matrices of in, low and out
-  const uint16_t *in, *in_low;  // A (poly) or X (apply), fp16 and what that lost (or null)
-  uint16_t *out, *out_low;
-  const float* diag_in;      // of A (poly), B (apply); the fp16 matrices hold zeros there
-  float* diag_out;
-  int32_t diag_apart;        // between matrices
-  float step;                // last, Muon: the learning rate of the shape
+// The matrices of one shape. Matrices of fp16 come in pairs: the nearest values and (`low`) what those
+// lost; A's and B's `low` only for exact ones.
+struct NsShape {
+  CUtensorMap x[2], x_low[2];    // X as the gram reads it: rows along the sum if wide, else across it
+  CUtensorMap xt[2], xt_low[2];  // X as the apply reads it: the other way round
+  CUtensorMap a, a_low, b, b_low;
+  uint16_t *x_at[2], *x_low_at[2], *a_at, *a_low_at, *b_at, *b_low_at;
+  float *a_diag, *b_diag;        // fp32; the fp16 matrices hold zeros there
+  int64_t x_apart, a_apart;      // elements between matrices
+  int32_t rows, cols, x_ld, a_ld, diag_apart;
+  int32_t wide, exact;           // rows <= cols; products of both parts
+  int32_t count, first_matrix;   // in the batch
+  int32_t side_tiles;            // of A's side
+  int32_t row_tiles, col_tiles;  // of X
+  int32_t first_tile[2];         // of the shape, in a symmetric op and in the apply
+  float step;                    // Muon: the learning rate of the shape
 };
-struct NsResult {  // last: where a matrix's result goes
+struct NsResult {  // where a matrix's result goes
   float* param;
   void* out;
 };
-struct NsLaunch {
-  int32_t op, groups, tiles;
-  int32_t side;  // of a tile: 128, or 256 by a pair of CTAs
-  float a, b, c;
-  int32_t early;  // apply: three steps or more follow
-  float decay;
+// A launch: all steps of a batch, the GPU's CTAs waiting for each other between two products.
+template <int SHAPES, int MATRICES>
+struct NsLaunchOf {
+  int32_t steps, shapes, tiles[2];  // of a symmetric op and of the apply
   int32_t out_kind;
+  float decay;
   const float* factor;
-  NsResult result[kMuonMatrices];
-  NsGroup group[kMuonGroups];
+  uint32_t* arrived;                // zero before: CTAs that have ended a product
+  float coefficients[3 * kNsMaxSteps];
+  NsResult result[MATRICES];
+  NsShape shape[SHAPES];
 };
+using NsLaunch = NsLaunchOf<kMuonGroups, kMuonMatrices>;
+using NsLaunchFew = NsLaunchOf<2, 32>;
 static_assert(sizeof(NsLaunch) <= 31 * 1024, "kernel parameter space");
 
-cudaError_t launch_ns(const NsLaunch& n, cudaStream_t s);
+// side: of a tile, 128 or 256 (by a pair of CTAs).
+cudaError_t launch_ns(const NsLaunch& n, int side, cudaStream_t s);
 
 }  // namespace zpp

@@ -220,20 +220,24 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
 
 // -------------------------------------------------------------------------------- bounded waits
-// Waits for a barrier's phase; after kTensorWaitClocks it sets `bit` of the fault word, and this
+// Waits for a barrier's phase; after so many clocks it sets `bit` of the fault word, and this
 // thread's later waits return at once (`alive` is false: what it computes is unspecified, and the
 // kernel ends). Inline: a call would hold registers that these kernels do not have.
-__device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, bool& alive, unsigned* fault,
-                                        unsigned bit) {
+__device__ __forceinline__ void tc_wait_long(uint64_t* bar, unsigned parity, bool& alive, unsigned* fault,
+                                             unsigned bit, long long clocks) {
   if (mbar_try_wait(bar, parity) || !alive) return;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kTensorWaitClocks) {
+    if (clock64() - t0 > clocks) {
       alive = false;
       atomicOr(fault, bit);
       return;
     }
   }
+}
+__device__ __forceinline__ void tc_wait(uint64_t* bar, unsigned parity, bool& alive, unsigned* fault,
+                                        unsigned bit) {
+  tc_wait_long(bar, parity, alive, fault, bit, kTensorWaitClocks);
 }
 
 // Whether a barrier's phase has completed, without waiting: asked while something else is going on.
