@@ -973,6 +973,12 @@ def quant_fp8(x, tile=1, transposed=False, out=None):
     transposed: also (codes_t [cols, rows], scales_t) of the transposed matrix, made in the same pass.
     With tile 1 its blocks are 128 rows of a column; with tile 128 scales_t is a view of scales. out: the
     buffers to write, a tuple as an earlier call returned it."""
+    if out is None:
+        made = _tensors().quant_fp8(_address("zpp_quant_fp8"), x, tile, transposed)
+        if made is not None:
+            if type(made) is int:
+                raise ZppError(made, "zpp_quant_fp8")
+            return made
     torch = _torch()
     _need(x, "x", dtypes=(torch.float16, torch.bfloat16, torch.float32))
     if tile not in (1, 128):
@@ -1017,6 +1023,13 @@ def matmul_fp8(a, a_scales, b, b_scales, bias=None, dtype=None, y=None):
     (any fp32 scales of those shapes, any strides) -> y [..., N] of `dtype` (default bf16; fp16 and
     fp32 too). bias: [N] of y's dtype. y: an output buffer, rows of contiguous elements evenly spaced."""
     torch = _torch()
+    if y is None and (dtype is None or dtype in (torch.float16, torch.bfloat16, torch.float32)):
+        made = _tensors().matmul_fp8(_address("zpp_matmul_fp8"), a, a_scales, b, b_scales, bias,
+                                     ZPP_BF16 if dtype is None else _dt(dtype))
+        if made is not None:
+            if type(made) is int:
+                raise ZppError(made, "zpp_matmul_fp8")
+            return made
     pa, pb = _fp8(a, a_scales, "a"), _fp8(b, b_scales, "b")
     if b.dim() != 2 or pa.cols != pb.cols:
         raise ValueError(f"b: {tuple(b.shape)}, expected [N, {pa.cols}]")

@@ -4,15 +4,22 @@
 // (60 us for 150 tensors, more than the step itself takes on the GPU), here some 10 ns. And a
 // product for one token takes the GPU 4 us: its wrapper's common case (plain contiguous
 // tensors, a new output) is one call here too, 14 us of host time otherwise. The norm of 40
-// small gradients takes 8 us as one call, 22 through Python.
+// small gradients takes 8 us as one call, 22 through Python. A training pass of a small linear layer
+// in fp8 is six kernels of 43 us together, which took the host 600 us through Python's autograd
+// functions and wrappers: here it is a C++ autograd function.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_strided.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <zpp.h>
 
@@ -344,6 +351,270 @@ PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return result;
 }
 
+// ------------------------------------------------------------------------------ e4m3 matrices
+at::ScalarType type_of(long kind) {
+  return kind == ZPP_F16 ? at::kHalf : kind == ZPP_BF16 ? at::kBFloat16 : at::kFloat;
+}
+using QuantFp8 = decltype(&zpp_quant_fp8);
+using MatmulFp8 = decltype(&zpp_matmul_fp8);
+cudaStream_t stream_of(long device) {
+  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+}
+int64_t blocks_of(int64_t n) { return (n + ZPP_FP8_BLOCK - 1) / ZPP_FP8_BLOCK; }
+
+// New codes of a matrix of `shape`, rows at multiples of 16 bytes, and its scales.
+struct Coded {
+  at::Tensor codes, scales;
+};
+at::Tensor new_codes(at::IntArrayRef shape, const at::TensorOptions& like) {
+  std::vector<int64_t> strides(shape.size(), 1);
+  int64_t apart = (shape.back() + 15) / 16 * 16;
+  for (size_t k = shape.size() - 1; k-- > 0;) strides[k] = apart, apart *= shape[k];
+  return at::empty_strided(shape, strides, like.dtype(at::kFloat8_e4m3fn));
+}
+Coded new_coded(at::IntArrayRef shape, int64_t rows, int64_t tile, const at::TensorOptions& like) {
+  const int64_t across = blocks_of(shape.back()), down = tile == 1 ? rows : blocks_of(rows);
+  const auto floats = like.dtype(at::kFloat);
+  return {new_codes(shape, like), tile == 1 ? at::empty_strided({down, across}, {1, down}, floats)
+                                            : at::empty({down, across}, floats)};
+}
+zpp_fp8_matrix matrix_of(const Coded& c, int64_t rows, int64_t cols, int64_t tile) {
+  zpp_fp8_matrix m{};
+  m.codes = c.codes.data_ptr();
+  m.scales = static_cast<float*>(c.scales.data_ptr());
+  m.rows = rows;
+  m.cols = cols;
+  m.stride = rows > 1 ? c.codes.stride(-2) : (cols + 15) / 16 * 16;
+  m.scale_row = c.scales.stride(0);
+  m.scale_block = c.scales.stride(1);
+  m.tile = static_cast<int32_t>(tile);
+  return m;
+}
+// x, contiguous with at least one row, to codes; with `turned` its transpose's too.
+zpp_status quantise(QuantFp8 fn, const at::Tensor& x, int64_t tile, Coded& to, Coded* turned) {
+  const int64_t cols = x.size(-1), rows = x.numel() / cols;
+  to = new_coded(x.sizes(), rows, tile, x.options());
+  const zpp_fp8_matrix m = matrix_of(to, rows, cols, tile);
+  zpp_fp8_matrix t{};
+  if (turned) {
+    if (tile == 1) *turned = new_coded({cols, rows}, cols, 1, x.options());
+    else *turned = {new_codes({cols, rows}, x.options()), to.scales.t()};
+    t = matrix_of(*turned, cols, rows, tile);
+  }
+  return fn(x.data_ptr(), static_cast<zpp_dtype>(kind_of(x)), cols, &m, turned ? &t : nullptr, stream_of(gpu_of(x)));
+}
+
+// quant_fp8(address of zpp_quant_fp8, x, tile, transposed): the codes and scales as a tuple, a status
+// other than ZPP_OK as an int, or None where something is not the plain case.
+PyObject* quant_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "quant_fp8: 4 arguments");
+    return nullptr;
+  }
+  if (!plain(args[1])) Py_RETURN_NONE;
+  const auto fn = reinterpret_cast<QuantFp8>(PyLong_AsVoidPtr(args[0]));
+  const long tile = PyLong_AsLong(args[2]);
+  const int transposed = PyObject_IsTrue(args[3]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  try {
+    const at::Tensor& x = THPVariable_Unpack(args[1]);
+    const long kind = kind_of(x);
+    if ((tile != 1 && tile != 128) || kind < 0 || kind > ZPP_F32 || !current(gpu_of(x)) || x.dim() < 1 ||
+        !x.is_contiguous() || x.numel() == 0)
+      Py_RETURN_NONE;
+    Coded c, t;
+    const zpp_status st = quantise(fn, x.detach(), tile, c, transposed ? &t : nullptr);
+    if (st != ZPP_OK) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(transposed ? 4 : 2);
+    if (!out) return nullptr;
+    PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(std::move(c.codes)));
+    PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(std::move(c.scales)));
+    if (transposed) {
+      PyTuple_SET_ITEM(out, 2, THPVariable_Wrap(std::move(t.codes)));
+      PyTuple_SET_ITEM(out, 3, THPVariable_Wrap(std::move(t.scales)));
+    }
+    return out;
+  } catch (const std::exception& e) {
+    set_error(e);
+    return nullptr;
+  }
+}
+
+// A 2-D matrix of codes as the library takes it; false where something is not the plain case.
+bool coded_matrix(const at::Tensor& codes, const at::Tensor& scales, long device, zpp_fp8_matrix& m) {
+  if (kind_of(codes) != 4 || kind_of(scales) != ZPP_F32 || gpu_of(codes) != device || gpu_of(scales) != device ||
+      codes.dim() != 2 || scales.dim() != 2)
+    return false;
+  const int64_t rows = codes.size(0), cols = codes.size(1);
+  if (rows < 1 || cols < 1 || (cols > 1 && codes.stride(1) != 1) || scales.size(1) != blocks_of(cols)) return false;
+  const bool by_rows = scales.size(0) == rows;
+  if (!by_rows && scales.size(0) != blocks_of(rows)) return false;
+  m = matrix_of({codes, scales}, rows, cols, by_rows ? 1 : 128);
+  return m.stride >= cols && m.stride % 16 == 0 && reinterpret_cast<uintptr_t>(m.codes) % 16 == 0;
+}
+
+// matmul_fp8(address of zpp_matmul_fp8, a, a_scales, b, b_scales, bias or None, out kind): the product in a
+// new tensor, a status other than ZPP_OK as an int, or None where something is not the plain case.
+PyObject* matmul_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "matmul_fp8: 7 arguments");
+    return nullptr;
+  }
+  for (int i = 1; i <= 4; ++i)
+    if (!plain(args[i])) Py_RETURN_NONE;
+  const bool has_bias = args[5] != Py_None;
+  if (has_bias && !plain(args[5])) Py_RETURN_NONE;
+  const auto fn = reinterpret_cast<MatmulFp8>(PyLong_AsVoidPtr(args[0]));
+  const long kind = PyLong_AsLong(args[6]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  try {
+    const at::Tensor& a = THPVariable_Unpack(args[1]);
+    const long device = gpu_of(a);
+    zpp_fp8_matrix ma, mb;
+    if (!current(device) || kind < 0 || kind > ZPP_F32 ||
+        !coded_matrix(a, THPVariable_Unpack(args[2]), device, ma) ||
+        !coded_matrix(THPVariable_Unpack(args[3]), THPVariable_Unpack(args[4]), device, mb) || ma.cols != mb.cols)
+      Py_RETURN_NONE;
+    const void* bias = nullptr;
+    if (has_bias) {
+      const at::Tensor& t = THPVariable_Unpack(args[5]);
+      if (kind_of(t) != kind || t.numel() != mb.rows || gpu_of(t) != device || !t.is_contiguous()) Py_RETURN_NONE;
+      bias = t.data_ptr();
+    }
+    at::Tensor y = at::empty({ma.rows, mb.rows}, a.options().dtype(type_of(kind)));
+    const zpp_status st =
+        fn(&ma, &mb, bias, y.data_ptr(), static_cast<zpp_dtype>(kind), mb.rows, stream_of(device));
+    if (st != ZPP_OK) return PyLong_FromLong(st);
+    return THPVariable_Wrap(std::move(y));
+  } catch (const std::exception& e) {
+    set_error(e);
+    return nullptr;
+  }
+}
+
+// The fp8 linear layer as an autograd function: see linear.py.
+void demand(zpp_status st, const char* where) {
+  TORCH_CHECK(st == ZPP_OK, where, ": status ", static_cast<int>(st));
+}
+at::Tensor product(MatmulFp8 fn, const at::Tensor& a, const at::Tensor& a_scales, int64_t a_tile,
+                   const at::Tensor& b, const at::Tensor& b_scales, int64_t b_tile, at::ScalarType type) {
+  at::Tensor y = at::empty({a.size(0), b.size(0)}, a.options().dtype(type));
+  if (y.numel() == 0) return y;
+  const zpp_fp8_matrix ma = matrix_of({a, a_scales}, a.size(0), a.size(1), a_tile),
+                       mb = matrix_of({b, b_scales}, b.size(0), b.size(1), b_tile);
+  demand(fn(&ma, &mb, nullptr, y.data_ptr(), static_cast<zpp_dtype>(kind_of(y)), y.size(1), stream_of(gpu_of(y))),
+         "zpp_matmul_fp8");
+  return y;
+}
+struct Linear : torch::autograd::Function<Linear> {
+  // held: the weight's codes, scales and those of its transpose, or none. (By pointer: a list of tensors
+  // would count as inputs with gradients of their own.)
+  static at::Tensor forward(torch::autograd::AutogradContext* ctx, const at::Tensor& x, const at::Tensor& weight,
+                            const std::vector<at::Tensor>* held, int64_t quant, int64_t matmul, bool for_x,
+                            bool for_w) {
+    const c10::cuda::CUDAGuard guard(x.device());
+    const auto quant_fn = reinterpret_cast<QuantFp8>(quant);
+    const auto matmul_fn = reinterpret_cast<MatmulFp8>(matmul);
+    const at::Tensor rows = x.reshape({-1, x.size(-1)}).contiguous();
+    Coded w, wt, q, qt;
+    if (!held->empty()) {
+      w = {held->at(0), held->at(1)};
+      if (held->size() == 4) wt = {held->at(2), held->at(3)};
+    } else if (weight.numel()) {
+      demand(quantise(quant_fn, weight.contiguous(), 128, w, for_x ? &wt : nullptr), "zpp_quant_fp8");
+    }
+    std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = weight.size(0);
+    at::Tensor y;
+    if (rows.size(0) && weight.size(0)) {
+      demand(quantise(quant_fn, rows, 1, q, for_w ? &qt : nullptr), "zpp_quant_fp8");
+      y = product(matmul_fn, q.codes, q.scales, 1, w.codes, w.scales, 128, x.scalar_type()).view(shape);
+    } else {
+      y = at::empty(shape, x.options());
+    }
+    // (to what is saved a later write is noticed)
+    ctx->save_for_backward({for_x ? wt.codes : at::Tensor(), for_x ? wt.scales : at::Tensor(),
+                            for_w ? qt.codes : at::Tensor(), for_w ? qt.scales : at::Tensor()});
+    ctx->saved_data["fns"] = std::vector<int64_t>{quant, matmul};
+    ctx->saved_data["x"] = x.sizes().vec();
+    ctx->saved_data["types"] = std::vector<int64_t>{static_cast<int64_t>(x.scalar_type()),
+                                                    static_cast<int64_t>(weight.scalar_type()), for_x, for_w};
+    return y;
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list grads) {
+    const auto saved = ctx->get_saved_variables();
+    const auto fns = ctx->saved_data["fns"].toIntVector(), shape = ctx->saved_data["x"].toIntVector(),
+               types = ctx->saved_data["types"].toIntVector();
+    const auto quant_fn = reinterpret_cast<QuantFp8>(fns[0]);
+    const auto matmul_fn = reinterpret_cast<MatmulFp8>(fns[1]);
+    const auto x_type = static_cast<at::ScalarType>(types[0]), w_type = static_cast<at::ScalarType>(types[1]);
+    torch::autograd::variable_list out(7);
+    if (!grads[0].defined()) return out;
+    const bool twice = at::GradMode::is_enabled();
+    {
+      const at::NoGradGuard no_grad;
+      const at::Tensor& dy = grads[0];
+      const c10::cuda::CUDAGuard guard(dy.device());
+      const int64_t n = dy.size(-1), k = shape.back();
+      int64_t count = 1;
+      for (size_t i = 0; i + 1 < shape.size(); ++i) count *= shape[i];
+      const bool empty = count == 0 || n == 0;
+      Coded q, qt;
+      if (!empty)
+        demand(quantise(quant_fn, dy.reshape({count, n}).contiguous(), 1, q, types[3] ? &qt : nullptr), "zpp_quant_fp8");
+      if (types[2])
+        out[0] = empty ? at::zeros(shape, dy.options().dtype(x_type))
+                       : product(matmul_fn, q.codes, q.scales, 1, saved[0], saved[1], 128, x_type).view(shape);
+      if (types[3])
+        out[1] = empty ? at::zeros({n, k}, dy.options().dtype(w_type))
+                       : product(matmul_fn, qt.codes, qt.scales, 1, saved[2], saved[3], 1, w_type);
+    }
+    if (twice) {  // differentiable once: a derivative of these raises
+      auto error = std::make_shared<torch::autograd::DelayedError>(
+          "linear_fp8 is differentiable once, and this is its second derivative", 7);
+      torch::autograd::variable_list in;
+      for (int i = 0; i < 2; ++i)
+        if (out[i].defined()) in.push_back(out[i].detach().requires_grad_());
+      auto marked = (*error)(std::move(in));
+      for (int i = 0, j = 0; i < 2; ++i)
+        if (out[i].defined()) out[i] = marked[j++];
+    }
+    return out;
+  }
+};
+
+// linear_fp8(address of zpp_quant_fp8, address of zpp_matmul_fp8, x, weight, None or a tuple of the
+// weight's codes and scales): y. The arguments have been checked.
+PyObject* linear_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 5 || !plain(args[2]) || !plain(args[3])) {
+    PyErr_SetString(PyExc_TypeError, "linear_fp8: two addresses, x, weight, codes");
+    return nullptr;
+  }
+  const int64_t quant = reinterpret_cast<int64_t>(PyLong_AsVoidPtr(args[0])),
+                matmul = reinterpret_cast<int64_t>(PyLong_AsVoidPtr(args[1]));
+  if (PyErr_Occurred()) return nullptr;
+  try {
+    std::vector<at::Tensor> held;
+    if (PyTuple_Check(args[4]))
+      for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args[4]); ++i)
+        held.push_back(THPVariable_Unpack(PyTuple_GET_ITEM(args[4], i)));
+    const at::Tensor &x = THPVariable_Unpack(args[2]), &w = THPVariable_Unpack(args[3]);
+    const bool grads = at::GradMode::is_enabled();
+    return THPVariable_Wrap(
+        Linear::apply(x, w, static_cast<const std::vector<at::Tensor>*>(&held), quant, matmul, grads && x.requires_grad(), grads && w.requires_grad()));
+  } catch (const std::exception& e) {
+    set_error(e);
+    return nullptr;
+  }
+}
+
 PyMethodDef methods[] = {
     {"step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(step)), METH_FASTCALL,
      "one counted AdamW step from a table of addresses"},
@@ -355,6 +626,12 @@ PyMethodDef methods[] = {
      "addresses of a list of tensors into a column of a table; (kind, device, same sizes)"},
     {"matvec", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matvec)), METH_FASTCALL,
      "the product with a quantised matrix, plain case"},
+    {"quant_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_fp8)), METH_FASTCALL,
+     "a matrix to e4m3 codes, plain case"},
+    {"matmul_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matmul_fp8)), METH_FASTCALL,
+     "the product of e4m3 matrices, plain case"},
+    {"linear_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_fp8)), METH_FASTCALL,
+     "the fp8 linear layer, differentiable"},
     {"probe", probe, METH_O, "(address, elements, kind, device, contiguous) of a tensor"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,

@@ -1,8 +1,8 @@
 """A linear layer whose three products, one forward and two backward, run on e4m3 codes with a scale
-per block of 128 (``zpp_quant_fp8``, ``zpp_matmul_fp8``), as a differentiable torch function.
+per block of 128 (``zpp_quant_fp8``, ``zpp_matmul_fp8``), as a differentiable torch function (whose
+passes are in the extension ``_tensors``).
 """
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as _b
 
@@ -30,35 +30,9 @@ def linear_fp8(x, weight, quantized=None):
             raise ValueError(f"quantized: codes of {tuple(quantized[0].shape)} do not fit weight")
         if len(quantized) == 4 and tuple(quantized[2].shape) != tuple(weight.shape[::-1]):
             raise ValueError("quantized: quant_fp8(weight, 128, transposed=True)")
-    return _Linear.apply(x, weight, quantized)
-
-
-class _Linear(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, quantized):
-        for_x, for_w = ctx.needs_input_grad[:2]
-        q = quantized
-        if q is None:
-            q = _b.quant_fp8(weight, 128, transposed=for_x)
-        rows = x.reshape(-1, x.shape[-1])
-        qx = _b.quant_fp8(rows, 1, transposed=for_w)
-        y = _b.matmul_fp8(qx[0], qx[1], q[0], q[1], dtype=x.dtype)
-        ctx.for_x, ctx.for_w = for_x, for_w
-        ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, weight.dtype
-        ctx.save_for_backward(*(q[2:] if for_x else (None, None)), *(qx[2:] if for_w else (None, None)))
-        return y.view(*x.shape[:-1], weight.shape[0])
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        w_t, w_t_scales, x_t, x_t_scales = ctx.saved_tensors
-        rows = dy.reshape(-1, dy.shape[-1]).contiguous()
-        qy = _b.quant_fp8(rows, 1, transposed=ctx.for_w)
-        dx = dw = None
-        if ctx.for_x:
-            dx = _b.matmul_fp8(qy[0], qy[1], w_t, w_t_scales, dtype=ctx.x_dtype).view(ctx.x_shape)
-        if ctx.for_w and rows.shape[0]:
-            dw = _b.matmul_fp8(qy[2], qy[3], x_t, x_t_scales, dtype=ctx.w_dtype)
-        elif ctx.for_w:  # no rows: a sum without terms
-            dw = dy.new_zeros((dy.shape[-1], ctx.x_shape[-1]), dtype=ctx.w_dtype)
-        return dx, dw, None
+        for name, codes, scales, tile in zip(("codes", "codes_t"), quantized[::2], quantized[1::2], (128, 128)):
+            _b._fp8(codes, scales, name, tile)
+        quantized = tuple(quantized)
+    _b._on_gpu(x, weight, *(quantized or ()))
+    return _b._tensors().linear_fp8(_b._address("zpp_quant_fp8"), _b._address("zpp_matmul_fp8"), x, weight,
+                                    quantized)

@@ -116,3 +116,14 @@ def test_training_pass_in_a_graph():
         dy.mul_(4.0)
     graph.replay()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], 4 * want[1]) and torch.equal(got[2], 4 * want[2])
+
+
+def test_second_derivative_raises():
+    x = torch.randn(20, 64, device=DEV).bfloat16().requires_grad_()
+    w = torch.randn(48, 64, device=DEV).requires_grad_()
+    y = zpp.linear_fp8(x, w)
+    dx, = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        dx.float().sum().backward()
+    with torch.no_grad():
+        assert not zpp.linear_fp8(x, w).requires_grad
