@@ -45,48 +45,51 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// x times the inverse scale; an infinite value (`odd`: the block may hold one) becomes NaN.
-__device__ __forceinline__ float scaled(float x, float inv, bool odd) {
-  float v = __fmul_rn(x, inv);
-  if (odd && !(fabsf(x) <= 3.402823466e38f)) v = __int_as_float(0x7fc00000);
-  return v;
-}
-__device__ __forceinline__ uint32_t codes4(const float* x, const float* inv, int inv_step, bool odd) {
-  const uint32_t a = e4m3x2(scaled(x[0], inv[0], odd), scaled(x[1], inv[inv_step], odd));
-  const uint32_t b = e4m3x2(scaled(x[2], inv[2 * inv_step], odd), scaled(x[3], inv[3 * inv_step], odd));
-  return a | (b << 16);
+__device__ __forceinline__ uint32_t codes4(f32x2 a, f32x2 b) {
+  float x, y, z, w;
+  f2_split(a, x, y);
+  f2_split(b, z, w);
+  return __byte_perm(e4m3x2(x, y), e4m3x2(z, w), 0x5410u);
 }
 
+// 16 values of a row as they lie in memory: 8 words of two 16-bit values, or 16 words.
 template <int KIND>
-__device__ __forceinline__ float element(const void* p, int64_t i) {
-  if constexpr (KIND == 2) return static_cast<const float*>(p)[i];
-  const uint16_t b = static_cast<const uint16_t*>(p)[i];
-  return KIND == 0 ? bits16_to_float(b, F16()) : bits16_to_float(b, BF16());
+struct Row {
+  static constexpr int WORDS = KIND == 2 ? 16 : 8;
+  uint32_t w[WORDS];
+  // values 2k and 2k + 1
+  __device__ __forceinline__ f32x2 pair(int k) const {
+    if constexpr (KIND == 2) return f2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    const float2 f = KIND == 0 ? unpack2(w[k], F16()) : unpack2(w[k], BF16());
+    return f2(f.x, f.y);
+  }
+};
+
+template <int KIND>
+__device__ __forceinline__ uint32_t element_bits(const void* p, int64_t i) {
+  return KIND == 2 ? static_cast<const uint32_t*>(p)[i] : static_cast<const uint16_t*>(p)[i];
 }
 
 // 16 values of a row, zeros outside the matrix.
 template <int KIND>
-__device__ __forceinline__ void load_row(const QuantFp8Run& a, int64_t row, int64_t col, float (&v)[16]) {
+__device__ __forceinline__ void load_row(const QuantFp8Run& a, int64_t row, int64_t col, Row<KIND>& v) {
   if (row < a.rows && a.whole && col + 16 <= a.cols) {
     const char* p = static_cast<const char*>(a.x) + (row * a.x_stride + col) * (KIND == 2 ? 4 : 2);
 #pragma unroll
-    for (int h = 0; h < (KIND == 2 ? 4 : 2); ++h) {
+    for (int h = 0; h < Row<KIND>::WORDS / 4; ++h) {
       const uint4 w = ld_after_v4(p + 16 * h);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (KIND == 2) {
-          v[4 * h + k] = __uint_as_float(u[k]);
-        } else {
-          const float2 f = KIND == 0 ? unpack2(u[k], F16()) : unpack2(u[k], BF16());
-          v[8 * h + 2 * k] = f.x, v[8 * h + 2 * k + 1] = f.y;
-        }
-      }
+      v.w[4 * h] = w.x, v.w[4 * h + 1] = w.y, v.w[4 * h + 2] = w.z, v.w[4 * h + 3] = w.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      v[j] = row < a.rows && col + j < a.cols ? element<KIND>(a.x, row * a.x_stride + col + j) : 0.0f;
+    for (int j = 0; j < Row<KIND>::WORDS; ++j) {
+      v.w[j] = 0u;
+#pragma unroll
+      for (int h = 0; h < 16 / Row<KIND>::WORDS; ++h) {
+        const int64_t c = col + j * (16 / Row<KIND>::WORDS) + h;
+        if (row < a.rows && c < a.cols) v.w[j] |= element_bits<KIND>(a.x, row * a.x_stride + c) << (16 * h);
+      }
+    }
   }
 }
 
@@ -101,54 +104,93 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int64_t at, int64_t n,
   }
 }
 
-// The largest finite magnitude, and whether there is an infinite one (a NaN is passed over).
-__device__ __forceinline__ float finite_max(float m, float v) {
-  const float a = fabsf(v);
-  return a <= 3.402823466e38f ? fmaxf(m, a) : m;
+// Magnitudes are compared as bits, which order as the values do: 32-bit ones, or 16-bit ones two to a
+// word. finite_only: an infinite or NaN one counts as 0.
+template <int KIND>
+struct Top {
+  static constexpr uint32_t SIGN = KIND == 2 ? 0x7fffffffu : 0x7fff7fffu;
+  static constexpr uint32_t INF = KIND == 2 ? 0x7f800000u : KIND == 1 ? 0x7f80u : 0x7c00u;
+  __device__ __forceinline__ static uint32_t more(uint32_t a, uint32_t b) {
+    return KIND == 2 ? max(a, b) : __vmaxu2(a, b);
+  }
+  __device__ __forceinline__ static uint32_t size(uint32_t w, bool finite_only) {
+    w &= SIGN;
+    if (finite_only) {
+      if constexpr (KIND == 2) {
+        if (w >= INF) w = 0u;
+      } else {
+        if ((w & 0xffffu) >= INF) w &= 0xffff0000u;
+        if ((w >> 16) >= INF) w &= 0xffffu;
+      }
+    }
+    return w;
+  }
+  __device__ __forceinline__ static float value(uint32_t bits) {  // of one magnitude
+    return KIND == 2 ? __uint_as_float(bits) : KIND == 1 ? bits16_to_float(bits, BF16()) : bits16_to_float(bits, F16());
+  }
+};
+// x times the inverse scale. odd: an infinite value becomes NaN.
+__device__ __forceinline__ f32x2 scaled(f32x2 x, f32x2 inv, bool odd) {
+  f32x2 r = f2_mul(x, inv);
+  if (odd) {
+    float a, b, u, v;
+    f2_split(x, a, b);
+    f2_split(r, u, v);
+    if (!(fabsf(a) <= 3.402823466e38f)) u = __int_as_float(0x7fc00000);
+    if (!(fabsf(b) <= 3.402823466e38f)) v = __int_as_float(0x7fc00000);
+    r = f2(u, v);
+  }
+  return r;
 }
 
 template <int KIND, bool TILE, bool TRANS>
-__global__ void __launch_bounds__(256) k_quant_fp8(const QuantFp8Run a) {
-  __shared__ float red[8][kQuantTile];
-  __shared__ float col_inv[kQuantTile];
-  __shared__ __align__(16) uint32_t turned[TRANS ? kQuantTile * 32 : 1];
-  grid_wait();
-  grid_release();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kQuantTile, c0 = static_cast<int64_t>(blockIdx.x) * kQuantTile;
-  const int rq = warp * 4 + (lane >> 3);  // which 4 rows of the tile
-  const int cg = lane & 7;                // which 16 columns
-  const int64_t row = r0 + rq * 4, col = c0 + cg * 16;
-  float v[4][16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load_row<KIND>(a, row + i, col, v[i]);
+struct QuantShared {
+  uint32_t red[8][KIND == 2 ? kQuantTile : kQuantTile / 2];
+  float col_inv[kQuantTile];
+  alignas(16) uint32_t turned[TRANS ? kQuantTile * 32 : 1];
+};
 
-  float row_inv[4], tile_inv = 0.0f;
+// A tile whose values have been loaded. ODD: some of them may be infinite or NaN.
+template <int KIND, bool TILE, bool TRANS, bool ODD>
+__device__ __forceinline__ void quant_tile_fp8(const QuantFp8Run& a, QuantShared<KIND, TILE, TRANS>& sh,
+                                               const Row<KIND> (&v)[4], int64_t r0, int64_t c0) {
+  using T = Top<KIND>;
+  constexpr int WORDS = Row<KIND>::WORDS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rq = warp * 4 + (lane >> 3), cg = lane & 7;
+  const int64_t row = r0 + rq * 4, col = c0 + cg * 16;
+  // (what `more` gives of a row's or column's words; for 16-bit values both halves of a word)
+  uint32_t top[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top[i] = T::size(v[i].w[0], ODD);
+#pragma unroll
+    for (int k = 1; k < WORDS; ++k) top[i] = T::more(top[i], T::size(v[i].w[k], ODD));
+    if constexpr (KIND != 2) top[i] = max(top[i] & 0xffffu, top[i] >> 16);
+  }
+  float row_inv[4];
   if constexpr (TILE) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) m = finite_max(m, v[i][j]);
-    m = warp_max(m, 32);
-    if (lane == 0) red[0][warp] = m;
+    uint32_t m = max(max(top[0], top[1]), max(top[2], top[3]));
+    m = __reduce_max_sync(~0u, m);
+    if (lane == 0) sh.red[0][warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[0][w]);
+    for (int w = 0; w < 8; ++w) m = max(m, sh.red[0][w]);
     float scale;
-    power_scale(m, scale, tile_inv);
+    power_scale(T::value(m), scale, row_inv[0]);
     if (threadIdx.x == 0)
       a.scales[static_cast<int64_t>(blockIdx.y) * a.scale_row + static_cast<int64_t>(blockIdx.x) * a.scale_block] = scale;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row_inv[i] = tile_inv;
+    for (int i = 1; i < 4; ++i) row_inv[i] = row_inv[0];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float m = 0.0f, scale;
+    for (int off = 4; off > 0; off >>= 1)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) m = finite_max(m, v[i][j]);
-      m = warp_max(m, 8);
-      power_scale(m, scale, row_inv[i]);
+      for (int i = 0; i < 4; ++i) top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], off));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float scale;
+      power_scale(T::value(top[i]), scale, row_inv[i]);
       if (cg == 0 && row + i < a.rows)
         a.scales[(row + i) * a.scale_row + static_cast<int64_t>(blockIdx.x) * a.scale_block] = scale;
     }
@@ -157,49 +199,77 @@ __global__ void __launch_bounds__(256) k_quant_fp8(const QuantFp8Run a) {
   for (int i = 0; i < 4; ++i) {
     if (row + i >= a.rows) break;
     uint32_t w[4];
+    const f32x2 inv = f2(row_inv[i], row_inv[i]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = codes4(&v[i][4 * k], &row_inv[i], 0, true);
+    for (int k = 0; k < 4; ++k) w[k] = codes4(scaled(v[i].pair(2 * k), inv, ODD), scaled(v[i].pair(2 * k + 1), inv, ODD));
     store_codes(a.codes + (row + i) * a.codes_stride, col, a.cols, w);
   }
   if constexpr (TRANS) {
     if constexpr (!TILE) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = finite_max(m, v[i][j]);
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-        if (lane < 8) red[warp][cg * 16 + j] = m;
+      for (int k = 0; k < WORDS; ++k) {
+        uint32_t m = T::more(T::more(T::size(v[0].w[k], ODD), T::size(v[1].w[k], ODD)),
+                             T::more(T::size(v[2].w[k], ODD), T::size(v[3].w[k], ODD)));
+        m = T::more(m, __shfl_xor_sync(~0u, m, 8));
+        m = T::more(m, __shfl_xor_sync(~0u, m, 16));
+        if (lane < 8) sh.red[warp][cg * WORDS + k] = m;
       }
       __syncthreads();
       if (threadIdx.x < kQuantTile) {
-        float m = 0.0f, scale, inv;
+        const int word = KIND == 2 ? threadIdx.x : threadIdx.x >> 1;
+        uint32_t m = 0u;
+        float scale, inv;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w][threadIdx.x]);
-        power_scale(m, scale, inv);
-        col_inv[threadIdx.x] = inv;
+        for (int w = 0; w < 8; ++w) m = T::more(m, sh.red[w][word]);
+        if constexpr (KIND != 2) m = (threadIdx.x & 1) ? m >> 16 : m & 0xffffu;
+        power_scale(T::value(m), scale, inv);
+        sh.col_inv[threadIdx.x] = inv;
         if (c0 + threadIdx.x < a.cols)
           a.scales_t[(c0 + threadIdx.x) * a.scale_t_row + static_cast<int64_t>(blockIdx.y) * a.scale_t_block] = scale;
       }
       __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int c = cg * 16 + j;
-      const float inv = TILE ? tile_inv : col_inv[c];
-      const float x[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
-      turned[c * 32 + (rq ^ (cg << 2))] = codes4(x, &inv, 0, true);
+    for (int k = 0; k < 8; ++k) {  // columns 2k and 2k + 1: words of 4 rows
+      const int c = cg * 16 + 2 * k;
+      const f32x2 inv = TILE ? f2(row_inv[0], row_inv[0]) : *reinterpret_cast<const f32x2*>(&sh.col_inv[c]);
+      float x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f2_split(scaled(v[i].pair(k), inv, ODD), x[i], y[i]);
+      sh.turned[c * 32 + (rq ^ (cg << 2))] = codes4(f2(x[0], x[1]), f2(x[2], x[3]));
+      sh.turned[(c + 1) * 32 + (rq ^ (cg << 2))] = codes4(f2(y[0], y[1]), f2(y[2], y[3]));
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // 16 rows of codes at a time: 8 threads a column of the tile
       const int c = k * 32 + (threadIdx.x >> 3), g = threadIdx.x & 7;
-      const uint4 t = *reinterpret_cast<const uint4*>(&turned[c * 32 + ((g ^ ((c >> 4) & 7)) << 2)]);
+      const uint4 t = *reinterpret_cast<const uint4*>(&sh.turned[c * 32 + ((g ^ ((c >> 4) & 7)) << 2)]);
       const uint32_t w[4] = {t.x, t.y, t.z, t.w};
       if (c0 + c < a.cols) store_codes(a.codes_t + (c0 + c) * a.codes_t_stride, r0 + g * 16, a.rows, w);
     }
   }
+}
+
+template <int KIND, bool TILE, bool TRANS>
+__global__ void __launch_bounds__(256, KIND == 2 ? 2 : 3) k_quant_fp8(const QuantFp8Run a) {
+  __shared__ QuantShared<KIND, TILE, TRANS> sh;
+  grid_wait();
+  grid_release();
+  const int rq = (threadIdx.x >> 5) * 4 + ((threadIdx.x & 31) >> 3), cg = threadIdx.x & 7;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kQuantTile, c0 = static_cast<int64_t>(blockIdx.x) * kQuantTile;
+  Row<KIND> v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_row<KIND>(a, r0 + rq * 4 + i, c0 + cg * 16, v[i]);
+  using T = Top<KIND>;
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < Row<KIND>::WORDS; ++k) m = T::more(m, T::size(v[i].w[k], false));
+  const bool odd = KIND == 2 ? m >= T::INF : (m & 0xffffu) >= T::INF || (m >> 16) >= T::INF;
+  // (values that are not finite take code of their own: the common one has no selections)
+  if (__syncthreads_or(odd)) quant_tile_fp8<KIND, TILE, TRANS, true>(a, sh, v, r0, c0);
+  else quant_tile_fp8<KIND, TILE, TRANS, false>(a, sh, v, r0, c0);
 }
 
 template <int KIND>
