@@ -16,6 +16,7 @@
 namespace zpp {
 
 constexpr int kQuantTile = 128;
+constexpr int kAheadTiles = 304;  // 2 tiles for each SM
 
 struct QuantFp8Run {
   const void* x;
@@ -250,6 +251,22 @@ __device__ __forceinline__ void quant_tile_fp8(const QuantFp8Run& a, QuantShared
   }
 }
 
+// Brings a tile that some CTA will take a little later into L2: a thread a row.
+template <int KIND>
+__device__ __forceinline__ void prefetch_tile(const QuantFp8Run& a) {
+  constexpr int64_t SIZE = KIND == 2 ? 4 : 2;
+  const int64_t t = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x + kAheadTiles;
+  const int64_t row = t / gridDim.x * kQuantTile + threadIdx.x, col = t % gridDim.x * kQuantTile;
+  if (!a.whole || threadIdx.x >= kQuantTile || row >= a.rows) return;
+  const int64_t left = a.cols - col;
+  const uint32_t bytes = static_cast<uint32_t>((left < kQuantTile ? left : kQuantTile) * SIZE) & ~15u;
+  if (bytes)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const char*>(a.x) +
+                                                                     (row * a.x_stride + col) * SIZE),
+                 "r"(bytes)
+                 : "memory");
+}
+
 template <int KIND, bool TILE, bool TRANS>
 __global__ void __launch_bounds__(256, KIND == 2 ? 2 : 3) k_quant_fp8(const QuantFp8Run a) {
   __shared__ QuantShared<KIND, TILE, TRANS> sh;
@@ -260,6 +277,7 @@ __global__ void __launch_bounds__(256, KIND == 2 ? 2 : 3) k_quant_fp8(const Quan
   Row<KIND> v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) load_row<KIND>(a, r0 + rq * 4 + i, c0 + cg * 16, v[i]);
+  prefetch_tile<KIND>(a);
   using T = Top<KIND>;
   uint32_t m = 0u;
 #pragma unroll
