@@ -10,7 +10,7 @@
 // the time of a block (8192 x 8192 x 8192: 1280 us).
 //
 // P is the operand whose rows are the 128 lanes of tensor memory, Q the one whose rows are a tile's
-// columns: a and b, or b and a where there are few rows of a.
+// columns: a and b, or b and a where there are few rows of a (a kernel of its own, below).
 #include "zpp_launch.h"
 #include "zpp_overlap.cuh"
 #include "zpp_tcgen05.cuh"
@@ -96,6 +96,13 @@ __device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int6
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (q + i < run.q.rows) store_kind(run.y, at + i * run.y_q, v[i], run.y_kind);
+}
+
+// One result (neighbouring lanes have neighbouring rows of P: of y's columns where P is b).
+__device__ __forceinline__ void store_one(const MatmulRun& run, int64_t p, int64_t q, float v) {
+  if (q >= run.q.rows) return;
+  if (run.bias) v = __fadd_rn(v, load_kind(run.bias, run.bias_p ? p : q, run.y_kind));
+  store_kind(run.y, p * run.y_p + q * run.y_q, v, run.y_kind);
 }
 
 // The tiles in the order they are taken: bands of P tiles, column by column, so that the CTAs at work at
@@ -342,19 +349,18 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
   }
 }
 
-template <int CTAS, int BN, bool QROWS>
-static cudaError_t run_matmul_as(const MatmulArgs& a, bool swap, cudaStream_t s) {
-  using G = MatmulGeo<CTAS, BN, QROWS>;
+// swap: P is b. Tiles of p_side x q_side, of whose Q a CTA holds q_rows.
+static cudaError_t describe(const MatmulArgs& a, bool swap, int p_side, int q_side, int q_rows, MatmulRun& run,
+                            CUtensorMap& p_map, CUtensorMap& q_map) {
   const MatmulOperand &p = swap ? a.b : a.a, &q = swap ? a.a : a.b;
-  MatmulRun run{};
   const auto side = [](const MatmulOperand& o) {
     return MatmulSide{o.scales, o.scale_row, o.scale_block, o.rows, o.tile == 128 ? 7 : 0};
   };
   run.p = side(p);
   run.q = side(q);
   run.blocks = static_cast<int32_t>((a.depth + kStep - 1) / kStep);
-  run.p_tiles = static_cast<int32_t>((p.rows + CTAS * kLanes - 1) / (CTAS * kLanes));
-  run.q_tiles = static_cast<int32_t>((q.rows + BN - 1) / BN);
+  run.p_tiles = static_cast<int32_t>((p.rows + p_side - 1) / p_side);
+  run.q_tiles = static_cast<int32_t>((q.rows + q_side - 1) / q_side);
   run.band = 8;
   run.y = a.y;
   run.y_p = swap ? 1 : a.y_stride;
@@ -364,9 +370,16 @@ static cudaError_t run_matmul_as(const MatmulArgs& a, bool swap, cudaStream_t s)
   run.bias_p = swap;
   const int64_t size = a.y_kind == 2 ? 4 : 2;
   run.vec = !swap && ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.y_stride * size)) & 15) == 0;
+  const cudaError_t e = make_tensor_map(&p_map, p.codes, 1, a.depth, p.rows, p.stride, 0, 0, kLanes);
+  return e != cudaSuccess ? e : make_tensor_map(&q_map, q.codes, 1, a.depth, q.rows, q.stride, 0, 0, q_rows);
+}
+
+template <int CTAS, int BN, bool QROWS>
+static cudaError_t run_tiles(const MatmulArgs& a, bool swap, cudaStream_t s) {
+  using G = MatmulGeo<CTAS, BN, QROWS>;
+  MatmulRun run{};
   CUtensorMap p_map, q_map;
-  cudaError_t e = make_tensor_map(&p_map, p.codes, 1, a.depth, p.rows, p.stride, 0, 0, kLanes);
-  if (e == cudaSuccess) e = make_tensor_map(&q_map, q.codes, 1, a.depth, q.rows, q.stride, 0, 0, G::Q_ROWS);
+  cudaError_t e = describe(a, swap, CTAS * kLanes, BN, G::Q_ROWS, run, p_map, q_map);
   auto kern = k_matmul_fp8<CTAS, BN, QROWS>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
@@ -375,20 +388,284 @@ static cudaError_t run_matmul_as(const MatmulArgs& a, bool swap, cudaStream_t s)
   return launch_overlapped_cluster(kern, dim3(grid), CTAS, kTensorThreads, G::SMEM, s, p_map, q_map, run);
 }
 
+
+// ------------------------------------------------------------------------------------------------
+// Few rows of a, or few tiles: P is b, 128 of its rows a CTA, and Q is a, up to BN rows. Bound by reading b, so what
+// counts is that every SM has copies in flight until the end: CTAs are small enough that two share an
+// SM, take one tile each, and the CTAs of a cluster share a tile's sum where there are few tiles
+// (each adds up its part of the blocks; the parts are exchanged through shared memory and added in the order
+// of the blocks, so the result does not depend on which CTA was first).
+template <int BN>
+struct FewGeo {
+  static constexpr int RESULT_WARPS = BN == 128 ? 8 : 4;
+  static constexpr int THREADS = (RESULT_WARPS + 4) * 32;
+  static constexpr int PER_SM = BN == 128 ? 1 : 2;
+  static constexpr int STAGE = (kLanes + BN) * kStep;
+  static constexpr int STAGES = BN == 128 ? 6 : BN == 64 ? 4 : 5;
+  static constexpr int SLOT = BN < 32 ? 32 : BN;
+  static constexpr int SLOTS = 4;
+  static constexpr int COLS = BN / (RESULT_WARPS / 4);  // of a warp
+  static constexpr int GROUPS = 8;                      // blocks whose scales are on their way
+  static constexpr int SCALES = STAGES * STAGE;
+  static constexpr int BARS = SCALES + GROUPS * (kLanes + BN) * 4;
+  static constexpr int SMEM = 1024 + BARS + (2 * STAGES + 2 * SLOTS + 2 * GROUPS + 1) * 8 + 16;
+  static_assert(kLanes * BN * 4 <= STAGES * STAGE, "the exchanged sums take the stages' place");
+};
+
+template <int BN, bool QROWS>
+__global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
+    k_matmul_fp8_few(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                     const MatmulRun run, const int split) {
+  using G = FewGeo<BN>;
+  constexpr int R = G::RESULT_WARPS;  // warps R .. R + 3 copy, multiply, and fetch scales
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::BARS);
+  uint64_t* empty = full + G::STAGES;
+  uint64_t* summed = empty + G::STAGES;
+  uint64_t* taken = summed + G::SLOTS;
+  uint64_t* scaled = taken + G::SLOTS;
+  uint64_t* used = scaled + G::GROUPS;
+  uint64_t* drained = used + G::GROUPS;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  float* p_scales = reinterpret_cast<float*>(smem + G::SCALES);  // [GROUPS][kLanes]
+  float* q_scales = p_scales + G::GROUPS * kLanes;               // [GROUPS][BN]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::STAGES; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < G::SLOTS; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], R);
+    for (int i = 0; i < G::GROUPS; ++i) mbar_init(&scaled[i], 64), mbar_init(&used[i], R);
+    mbar_init(drained, 1);
+    mbar_init_fence();
+    tma_prefetch(&p_map);
+    tma_prefetch(&q_map);
+  }
+  if (warp == R) {
+    tmem_alloc<1>(tmem_at, G::SLOT * G::SLOTS);
+    tmem_alloc_done<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  grid_wait();
+  grid_release();
+
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;  // (a cluster is `split` CTAs in a row)
+  const int p_tile = tile % run.p_tiles, q_tile = tile / run.p_tiles;
+  const int begin = static_cast<int>(static_cast<int64_t>(run.blocks) * rank / split);
+  const int end = static_cast<int>(static_cast<int64_t>(run.blocks) * (rank + 1) / split);
+  bool alive = true;
+  f32x2 sums[G::COLS / 2];
+#pragma unroll
+  for (int i = 0; i < G::COLS / 2; ++i) sums[i] = f2(0.0f, 0.0f);
+
+  if (warp == R) {
+    if (lane == 0) {
+      Ring<G::STAGES> r;
+      int issued = 0;
+      for (int kb = begin; kb < end; ++kb) {
+        tc_wait(&empty[r.at], r.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
+        if (!alive) break;
+        uint8_t* stage = smem + r.at * G::STAGE;
+        mbar_arrive_expect_tx(&full[r.at], G::STAGE);
+        tma_load(stage, &p_map, kb * kStep, p_tile * kLanes, &full[r.at]);
+        tma_load(stage + kLanes * kStep, &q_map, kb * kStep, q_tile * BN, &full[r.at]);
+        ++issued;
+        r.next();
+      }
+      if (!alive) {  // copies that nobody may have waited for
+        bool wait = true;
+        for (int d = 0; d < G::STAGES && d < issued; ++d) {
+          if (--r.at < 0) r.at = G::STAGES - 1, r.phase ^= 1u;
+          tc_wait(&full[r.at], r.phase, wait, &g_matmul_fault, kMatmulFault);
+        }
+      }
+    }
+  } else if (warp == R + 1) {
+    constexpr uint32_t instr = tc_instruction(kLanes, BN, 0, 0, false, false);
+    const uint64_t p_desc = tc_operand(smem_addr(smem), 16, 1024),
+                   q_desc = tc_operand(smem_addr(smem) + kLanes * kStep, 16, 1024);
+    Ring<G::STAGES> r;
+    Ring<G::SLOTS> s;
+    for (int kb = begin; kb < end; ++kb) {
+      tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
+      tc_wait(&full[r.at], r.phase, alive, &g_matmul_fault, kMatmulFault);
+      if (!__all_sync(~0u, alive)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t at = static_cast<uint64_t>(r.at * (G::STAGE >> 4));
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_f8<1>(tmem + s.at * G::SLOT, p_desc + at + 2 * k, q_desc + at + 2 * k, instr, k > 0);
+        tc_commit(&summed[s.at]);
+        tc_commit(&empty[r.at]);
+      }
+      __syncwarp();
+      r.next();
+      s.next();
+    }
+    if (!alive) {
+      bool wait = true;
+      if (elect_one()) tc_commit(drained);
+      __syncwarp();
+      tc_wait(drained, 0, wait, &g_matmul_fault, kMatmulFault);
+    }
+  } else if (warp >= R + 2) {
+    const bool of_p = warp == R + 2;
+    const MatmulSide& side = of_p ? run.p : run.q;
+    const int64_t row0 = of_p ? static_cast<int64_t>(p_tile) * kLanes : static_cast<int64_t>(q_tile) * BN;
+    const int count = side.shift ? 1 : of_p ? kLanes : BN;  // a tile of 128 rows has one scale
+    float* to = of_p ? p_scales : q_scales;
+    const int to_step = of_p ? kLanes : BN;
+    const float* from[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (rows beyond the last take the first row's; nothing uses them)
+      const int64_t row = row0 + lane + 32 * i;
+      from[i] = side.scales + (row < side.rows ? row >> side.shift : 0) * side.row;
+    }
+    Ring<G::GROUPS> x;
+    for (int kb = begin; kb < end; ++kb) {
+      tc_wait(&used[x.at], x.phase ^ 1u, alive, &g_matmul_fault, kMatmulFault);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane + 32 * i < count) cp_async4(to + x.at * to_step + lane + 32 * i, from[i] + kb * side.block);
+      cp_async_arrive_noinc(&scaled[x.at]);  // counts even with no copies of its own
+      x.next();
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else {
+    constexpr int CHUNK = G::COLS < 32 ? G::COLS : 32;
+    const int part = warp >> 2, in_cta = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + part * G::COLS;
+    const int p_at = run.p.shift ? 0 : in_cta;
+    Ring<G::SLOTS> s;
+    Ring<G::GROUPS> x;
+    for (int kb = begin; kb < end; ++kb) {
+      tc_wait(&scaled[x.at], x.phase, alive, &g_matmul_fault, kMatmulFault);
+      const float* qs = q_scales + x.at * BN + (QROWS ? part * G::COLS : 0);
+      float scale = p_scales[x.at * kLanes + p_at];
+      if constexpr (!QROWS) scale = __fmul_rn(scale, *qs);
+      tc_wait(&summed[s.at], s.phase, alive, &g_matmul_fault, kMatmulFault);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < G::COLS; c += CHUNK) {
+        uint32_t v[CHUNK];
+        tmem_ld(lanes + s.at * G::SLOT + c, v);
+        tmem_ld_wait(v);
+        if (c + CHUNK == G::COLS) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&taken[s.at]);
+        }
+#pragma unroll
+        for (int i = 0; i < CHUNK; i += 2) {
+          f32x2 y = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          if constexpr (QROWS) y = f2_mul(y, *reinterpret_cast<const f32x2*>(qs + c + i));
+          sums[(c + i) / 2] = f2_fma(y, f2(scale, scale), sums[(c + i) / 2]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&used[x.at]);
+      s.next();
+      x.next();
+    }
+  }
+
+  // Every product of this CTA has been read, so the stages are free; the other CTAs' are after the barrier.
+  __syncwarp();
+  const bool results = warp < R;
+  const int part = warp >> 2, in_cta = (warp & 3) * 32 + lane;
+  const int64_t p = static_cast<int64_t>(p_tile) * kLanes + in_cta, q0 = static_cast<int64_t>(q_tile) * BN;
+  if (split == 1) {
+    if (results && p < run.p.rows) {
+#pragma unroll
+      for (int i = 0; i < G::COLS / 2; ++i) {
+        float a, b;
+        f2_split(sums[i], a, b);
+        store_one(run, p, q0 + part * G::COLS + 2 * i, a);
+        store_one(run, p, q0 + part * G::COLS + 2 * i + 1, b);
+      }
+    }
+  } else {
+    const int own = BN / split;  // columns that a CTA adds up: [source][column][lane] in its stages
+    cluster_sync();
+    if (results) {
+      const uint32_t at = smem_addr(smem);
+#pragma unroll
+      for (int i = 0; i < G::COLS; ++i) {
+        float a, b;
+        f2_split(sums[i / 2], a, b);
+        const int c = part * G::COLS + i, owner = c / own;
+        st_cluster(map_rank(at + ((rank * own + c % own) * kLanes + in_cta) * 4, owner), (i & 1) ? b : a);
+      }
+    }
+    cluster_sync();
+    if (results && p < run.p.rows) {
+      const float* parts = reinterpret_cast<const float*>(smem);
+      for (int c = part; c < own; c += R / 4) {
+        float sum = parts[c * kLanes + in_cta];
+        for (int k = 1; k < split; ++k) sum = __fadd_rn(sum, parts[(k * own + c) * kLanes + in_cta]);
+        store_one(run, p, q0 + rank * own + c, sum);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == R) {
+    tc_fence_after();
+    tmem_free<1>(tmem, G::SLOT * G::SLOTS);
+  }
+}
+
+template <int BN, bool QROWS>
+static cudaError_t run_few_as(const MatmulArgs& a, cudaStream_t s) {
+  using G = FewGeo<BN>;
+  MatmulRun run{};
+  CUtensorMap p_map, q_map;
+  cudaError_t e = describe(a, true, kLanes, BN, BN, run, p_map, q_map);
+  auto kern = k_matmul_fp8_few<BN, QROWS>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+  if (e != cudaSuccess) return e;
+  // As many CTAs as run at one time, if each has two blocks or more.
+  const int64_t tiles = static_cast<int64_t>(run.p_tiles) * run.q_tiles;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 152 * G::PER_SM && run.blocks >= 4 * split) split *= 2;
+  return launch_overlapped_cluster(kern, dim3(static_cast<unsigned>(tiles * split)), split, G::THREADS, G::SMEM, s, p_map,
+                                   q_map, run, split);
+}
+template <int BN>
+static cudaError_t run_few(const MatmulArgs& a, cudaStream_t s) {
+  return a.a.tile == 1 ? run_few_as<BN, true>(a, s) : run_few_as<BN, false>(a, s);
+}
+
 template <int CTAS, int BN>
-static cudaError_t run_matmul(const MatmulArgs& a, bool swap, cudaStream_t s) {
-  return (swap ? a.a : a.b).tile == 1 ? run_matmul_as<CTAS, BN, true>(a, swap, s)
-                                      : run_matmul_as<CTAS, BN, false>(a, swap, s);
+static cudaError_t run_tiles(const MatmulArgs& a, bool swap, cudaStream_t s) {
+  return (swap ? a.a : a.b).tile == 1 ? run_tiles<CTAS, BN, true>(a, swap, s) : run_tiles<CTAS, BN, false>(a, swap, s);
 }
 
 cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
-  // Few rows of a: they are the columns of the tiles, which are narrow then.
-  if (a.a.rows <= 16) return run_matmul<1, 16>(a, true, s);
-  if (a.a.rows <= 32) return run_matmul<1, 32>(a, true, s);
-  if (a.a.rows <= 64) return run_matmul<1, 64>(a, true, s);
+  if (a.a.rows <= 16) return run_few<16>(a, s);
+  if (a.a.rows <= 32) return run_few<32>(a, s);
+  if (a.a.rows <= 64) return run_few<64>(a, s);
+  // So few tiles that the CTAs of a cluster can share the sum of each (100 x 1024 x 8192: 13 us from 28,
+  // 1024 x 1024 x 1024 9 from 17).
+  const int64_t squares = ((a.a.rows + 127) / 128) * ((a.b.rows + 127) / 128);
+  if (squares <= 76 && a.depth > 4 * kStep) return run_few<128>(a, s);
+  // A warp's stores: 32 rows of P, 16 bytes of each, or, with P and Q exchanged, 32 neighbours. So
+  // they are exchanged where y's rows do not start at multiples of 16 bytes, and where a fits one tile's
+  // columns (77 x 50001 x 1003 in fp32: 20 us against 65).
+  const int64_t size = a.y_kind == 2 ? 4 : 2;
+  const bool whole = ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.y_stride * size)) & 15) == 0;
+  const bool swap = a.a.rows <= 128 || !whole;
   const int64_t pairs = ((a.a.rows + 255) / 256) * ((a.b.rows + 255) / 256);
-  if (pairs >= 48) return run_matmul<2, 256>(a, false, s);
-  return run_matmul<1, 128>(a, false, s);
+  if (a.a.rows > 128 && pairs >= 48) return run_tiles<2, 256>(a, swap, s);
+  return run_tiles<1, 128>(a, swap, s);
 }
 
 cudaError_t read_matmul_fault(unsigned* flags, bool clear) {
