@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
       }
     }
   } else {
-    const int own = BN / split;  // columns that a CTA adds up: [source][column][lane] in its stages
+    // columns that a CTA adds up, a power of two: [source][column][lane] in its stages
+    const int shift = __ffs(BN / split) - 1, own = 1 << shift;
     cluster_sync();
     if (results) {
       const uint32_t at = smem_addr(smem);
@@ -601,8 +602,8 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
       for (int i = 0; i < G::COLS; ++i) {
         float a, b;
         f2_split(sums[i / 2], a, b);
-        const int c = part * G::COLS + i, owner = c / own;
-        st_cluster(map_rank(at + ((rank * own + c % own) * kLanes + in_cta) * 4, owner), (i & 1) ? b : a);
+        const int c = part * G::COLS + i, owner = c >> shift;
+        st_cluster(map_rank(at + ((rank * own + (c & (own - 1))) * kLanes + in_cta) * 4, owner), (i & 1) ? b : a);
       }
     }
     cluster_sync();
@@ -653,10 +654,10 @@ cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
   if (a.a.rows <= 16) return run_few<16>(a, s);
   if (a.a.rows <= 32) return run_few<32>(a, s);
   if (a.a.rows <= 64) return run_few<64>(a, s);
-  // So few tiles that the CTAs of a cluster can share the sum of each (100 x 1024 x 8192: 13 us from 28,
-  // 1024 x 1024 x 1024 9 from 17).
+  // So few tiles and so long a sum that the CTAs of a cluster share each (100 x 1024 x 8192: 11 us from 28;
+  // at a depth of 4096 both take 13 us, at 1024 the exchange costs 3 us more than it saves).
   const int64_t squares = ((a.a.rows + 127) / 128) * ((a.b.rows + 127) / 128);
-  if (squares <= 76 && a.depth > 4 * kStep) return run_few<128>(a, s);
+  if (squares <= 38 && a.depth > 32 * kStep) return run_few<128>(a, s);
   // A warp's stores: 32 rows of P, 16 bytes of each, or, with P and Q exchanged, 32 neighbours. So
   // they are exchanged where y's rows do not start at multiples of 16 bytes, and where a fits one tile's
   // columns (77 x 50001 x 1003 in fp32: 20 us against 65).
