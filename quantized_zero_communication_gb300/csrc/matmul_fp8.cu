@@ -71,11 +71,12 @@ __device__ __forceinline__ void store_kind(void* p, int64_t i, float v, int kind
 }
 
 // 8 columns of row p of P, from column q on.
-__device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int64_t q, float (&v)[8]) {
+// bias: that of row p, where it goes by P's rows.
+__device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int64_t q, float bias, float (&v)[8]) {
   if (run.bias) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (q + i < run.q.rows) v[i] = __fadd_rn(v[i], load_kind(run.bias, run.bias_p ? p : q + i, run.y_kind));
+      if (q + i < run.q.rows) v[i] = __fadd_rn(v[i], run.bias_p ? bias : load_kind(run.bias, q + i, run.y_kind));
   }
   const int64_t at = p * run.y_p + q * run.y_q;
   if (run.vec && q + 8 <= run.q.rows) {  // consecutive and whole
@@ -99,9 +100,10 @@ __device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int6
 }
 
 // One result (neighbouring lanes have neighbouring rows of P: of y's columns where P is b).
-__device__ __forceinline__ void store_one(const MatmulRun& run, int64_t p, int64_t q, float v) {
+// bias: that of row p of P.
+__device__ __forceinline__ void store_one(const MatmulRun& run, int64_t p, int64_t q, float v, float bias) {
   if (q >= run.q.rows) return;
-  if (run.bias) v = __fadd_rn(v, load_kind(run.bias, run.bias_p ? p : q, run.y_kind));
+  if (run.bias) v = __fadd_rn(v, bias);
   store_kind(run.y, p * run.y_p + q * run.y_q, v, run.y_kind);
 }
 
@@ -330,12 +332,13 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         }
       }
       if (p0 < run.p.rows) {
+        const float bias = run.bias && run.bias_p ? load_kind(run.bias, p0, run.y_kind) : 0.0f;
 #pragma unroll
         for (int i = 0; i < HALF; i += 8) {
           float v[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) f2_split(sums[i / 2 + k], v[2 * k], v[2 * k + 1]);
-          store_sums(run, p0, q0 + i, v);
+          store_sums(run, p0, q0 + i, bias, v);
         }
       }
     }
@@ -582,14 +585,15 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
   const bool results = warp < R;
   const int part = warp >> 2, in_cta = (warp & 3) * 32 + lane;
   const int64_t p = static_cast<int64_t>(p_tile) * kLanes + in_cta, q0 = static_cast<int64_t>(q_tile) * BN;
+  const float bias = run.bias && results && p < run.p.rows ? load_kind(run.bias, p, run.y_kind) : 0.0f;
   if (split == 1) {
     if (results && p < run.p.rows) {
 #pragma unroll
       for (int i = 0; i < G::COLS / 2; ++i) {
         float a, b;
         f2_split(sums[i], a, b);
-        store_one(run, p, q0 + part * G::COLS + 2 * i, a);
-        store_one(run, p, q0 + part * G::COLS + 2 * i + 1, b);
+        store_one(run, p, q0 + part * G::COLS + 2 * i, a, bias);
+        store_one(run, p, q0 + part * G::COLS + 2 * i + 1, b, bias);
       }
     }
   } else {
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
       for (int c = part; c < own; c += R / 4) {
         float sum = parts[c * kLanes + in_cta];
         for (int k = 1; k < split; ++k) sum = __fadd_rn(sum, parts[(k * own + c) * kLanes + in_cta]);
-        store_one(run, p, q0 + rank * own + c, sum);
+        store_one(run, p, q0 + rank * own + c, sum, bias);
       }
     }
   }

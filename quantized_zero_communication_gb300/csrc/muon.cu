@@ -181,7 +181,7 @@ struct Shape {
   int64_t small_ld() const { return (small() + 15) / 16 * 16; }
   int64_t x_elems() const { return (rows * ld() + 63) / 64 * 64; }  // one matrix, 128-byte aligned
   int64_t a_elems() const { return (small() * small_ld() + 63) / 64 * 64; }
-  int64_t diag_elems() const { return (small() + 31) / 32 * 32; }  // fp32
+  int64_t diag_elems() const { return (small() + 63) / 64 * 64; }  // fp32
   bool wide() const { return rows <= cols; }
   bool exact() const { return small() <= kNsExactSide; }
   // X twice and what it lost, A and B with their diagonals; what each lost too, and X's twice
@@ -319,6 +319,8 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
   t.partial = reinterpret_cast<float*>(at);
   t.arrived = reinterpret_cast<uint32_t*>(workspace);
   t.first[0] = 0;
+  // Rounds of a CTA: as few as 8 CTAs an SM leave (each adds up its matrix's partials in K13).
+  const int64_t enough = std::max<int64_t>(1, b.elems / (int64_t{152} * 8 * kMuonPer));
   for (size_t k = 0, i = 0; k < b.shapes.size(); ++k) {
     const Shape& sh = b.shapes[k];
     for (int j = 0; j < sh.count; ++j, ++i) {
@@ -332,7 +334,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
       it.cols = static_cast<int32_t>(sh.cols);
       it.ld = static_cast<int32_t>(sh.ld());
       const int64_t rounds = (it.n + kMuonPer - 1) / kMuonPer;
-      const int64_t each = (rounds + kMuonPartials - 1) / kMuonPartials;
+      const int64_t each = std::max((rounds + kMuonPartials - 1) / kMuonPartials, enough);
       it.per = each * kMuonPer;
       t.first[i + 1] = t.first[i] + static_cast<int32_t>((rounds + each - 1) / each);
     }
@@ -364,8 +366,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     const Place& pl = place[k];
     NsShape& g = n.shape[k];
     g.rows = static_cast<int32_t>(sh.rows), g.cols = static_cast<int32_t>(sh.cols);
-    g.x_ld = static_cast<int32_t>(sh.ld()), g.a_ld = static_cast<int32_t>(sh.small_ld());
-    g.x_apart = sh.x_elems(), g.a_apart = sh.a_elems(), g.diag_apart = static_cast<int32_t>(sh.diag_elems());
+    g.diag_apart = static_cast<int32_t>(sh.diag_elems());
     g.wide = sh.wide(), g.exact = sh.exact();
     g.count = sh.count, g.first_matrix = sh.first;
     g.side_tiles = static_cast<int32_t>((sh.small() + side - 1) / side);
@@ -375,7 +376,6 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     n.tiles[0] += sh.count * g.side_tiles * (g.side_tiles + 1) / 2;
     n.tiles[1] += sh.count * g.row_tiles * g.col_tiles;
     g.step = adjusted(a, sh.rows, sh.cols);
-    g.a_at = pl.a, g.a_low_at = pl.a_low, g.b_at = pl.b, g.b_low_at = pl.b_low;
     g.a_diag = pl.a_diag, g.b_diag = pl.b_diag;
     const auto map = [&](const uint16_t* p, bool of_x, bool mn, CUtensorMap* to) {
       if (e == cudaSuccess)
@@ -384,16 +384,16 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
                             (of_x ? sh.x_elems() : sh.a_elems()) * 2, mn ? 64 : 128);
     };
     for (int i = 0; i < 2; ++i) {
-      g.x_at[i] = pl.x[i], g.x_low_at[i] = pl.x_low[i];
       map(pl.x[i], true, !sh.wide(), &g.x[i]);
       map(pl.x[i], true, sh.wide(), &g.xt[i]);
-      if (sh.exact()) {
-        map(pl.x_low[i], true, !sh.wide(), &g.x_low[i]);
-        map(pl.x_low[i], true, sh.wide(), &g.xt_low[i]);
-      }
+      // (what X lost is an operand of exact shapes only; the apply reads and writes it across)
+      if (sh.exact() || sh.wide()) map(pl.x_low[i], true, !sh.wide(), &g.x_low[i]);
+      if (sh.exact() || !sh.wide()) map(pl.x_low[i], true, sh.wide(), &g.xt_low[i]);
     }
     map(pl.a, false, false, &g.a);
     map(pl.b, false, false, &g.b);
+    map(pl.a, false, true, &g.a_turned);
+    map(pl.b, false, true, &g.b_turned);
     if (sh.exact()) {
       map(pl.a_low, false, false, &g.a_low);
       map(pl.b_low, false, false, &g.b_low);

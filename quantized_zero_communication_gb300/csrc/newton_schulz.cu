@@ -33,15 +33,22 @@ constexpr unsigned kMuonFault = 16;  // its bit of the fault word
 constexpr int kNsSide = 128, kNsStep = 64;  // rows of an operand in a CTA, steps of the sum in a stage
 constexpr int kNsOperand = kNsSide * kNsStep * 2;
 constexpr int kNsStage = 2 * kNsOperand;
-constexpr int kNsStages = 6;
-constexpr int kNsBars = kNsStages * kNsStage;
-constexpr int kNsSmem = 1024 + kNsBars + (2 * kNsStages + 2 * 2 + 1) * 8 + 16;
+constexpr int kNsStages = 5;
+// Results go through shared memory: 128 rows of 64 columns at a time, of each half of the tile's columns,
+// as 16-bit values and what those lost, laid out as a tensor copy lays them.
+constexpr int kNsChunk = 64, kNsHalfChunk = kNsSide * kNsChunk * 2;
+constexpr int kNsResults = kNsStages * kNsStage;
+constexpr int kNsDiag = kNsResults + 2 * 2 * kNsHalfChunk;  // and the diagonal at a chunk's columns
+constexpr int kNsBars = kNsDiag + 2 * kNsChunk * 4;
+constexpr int kNsSmem = 1024 + kNsBars + (2 * kNsStages + 2 * 2 + 2 + 2) * 8 + 16;
+static_assert(kNsSmem <= 227 * 1024, "shared memory of a CTA");
 // Tiles are squares of CTAS * 128: of one CTA, or of a pair that holds half of each operand.
 constexpr int kNsSlots = 2;
 
 // ------------------------------------------------------------------------- between two products
-// Every CTA of the launch ends a product before any begins the next one. `arrived` counts ends; each role
-// of a CTA waits for it by itself. (The launch is cooperative, so all CTAs run at once.)
+// Every CTA of the launch ends a product before any begins the next one. `arrived` counts ends; one thread
+// of a CTA reads it (the count's line is one place in L2: asked by every role it answers later), and the
+// others wait for that thread. (The launch is cooperative, so all CTAs run at once.)
 constexpr long long kGridWaitClocks = 40000000000ll;  // some 20 s: a product may take long
 __device__ __forceinline__ void ns_wait_grid(const uint32_t* arrived, uint32_t ends, bool& alive) {
   const long long t0 = clock64();
@@ -55,8 +62,8 @@ __device__ __forceinline__ void ns_wait_grid(const uint32_t* arrived, uint32_t e
     }
   }
 }
-// By every thread that wrote, before one of them tells: the next product's copies read through another
-// path (the asynchronous proxy).
+// Between other threads' ordinary writes, which this one knows of, and copies: those go through another path
+// (the asynchronous proxy).
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 struct NsTile {
@@ -116,142 +123,141 @@ __device__ __forceinline__ uint64_t ns_operand(uint32_t at, bool mn) {
 }
 
 // ---------------------------------------------------------------------------------------- the results
-// A thread has a row p and 16 consecutive columns at a time, from q on (a multiple of 16). Rows of the
-// matrices in the workspace start at multiples of 32 bytes, so whole vectors of 16 stay inside them.
-struct NsIn {         // what a result needs beside its sum
-  U8x32 x, low;       // poly: A; apply: X
-  float diag_p;       // of A (poly) or B (apply) at the row
-  float diag_q[16];   // at the columns
-};
-__device__ __forceinline__ void ns_diag_q(const float* diag, float (&d)[16]) {
+// A thread has a row of a chunk, 8 consecutive columns (16 bytes) at a time.
+__device__ __forceinline__ uint8_t* ns_place(uint8_t* chunk, int row, int piece) {
+  return chunk + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+// v as two fp16 each: the nearest ones, and those nearest to what they lost.
+__device__ __forceinline__ void two_halves(const float (&v)[8], uint4& high, uint4& low) {
+  uint32_t h[4], l[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 w = ld_after_shared_v4(diag + 4 * i);
-    d[4 * i] = __uint_as_float(w.x), d[4 * i + 1] = __uint_as_float(w.y);
-    d[4 * i + 2] = __uint_as_float(w.z), d[4 * i + 3] = __uint_as_float(w.w);
+  for (int k = 0; k < 4; ++k) {
+    h[k] = pack2(v[2 * k], v[2 * k + 1], F16());
+    const float2 f = unpack2(h[k], F16());
+    l[k] = pack2(__fsub_rn(v[2 * k], f.x), __fsub_rn(v[2 * k + 1], f.y), F16());
   }
+  high = make_uint4(h[0], h[1], h[2], h[3]);
+  low = make_uint4(l[0], l[1], l[2], l[3]);
 }
-__device__ __forceinline__ void ns_fetch(const NsShape& g, int op, int from, int matrix, int p, int q, NsIn& in) {
-  if (op == kNsGram) return;
-  const bool apply = op == kNsApply;
-  const int64_t at = matrix * (apply ? g.x_apart : g.a_apart) + static_cast<int64_t>(p) * (apply ? g.x_ld : g.a_ld) + q;
-  in.x = ld_after_vec32<true>((apply ? g.x_at[from] : g.a_at) + at);
-  if (apply || g.exact) in.low = ld_after_vec32<true>((apply ? g.x_low_at[from] : g.a_low_at) + at);
-  const float* diag = (apply ? g.b_diag : g.a_diag) + static_cast<int64_t>(matrix) * g.diag_apart;
-  if (!apply || g.wide) in.diag_p = ld_after_f32(diag + p);
-  if (!apply || !g.wide) ns_diag_q(diag + q, in.diag_q);
+__device__ __forceinline__ void eight(const float* at, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ void halves(const U8x32& w, float (&v)[16]) {
+// What a tile's results are made with. (From the kernel's parameters, which lie in constant memory beyond
+// what its cache holds: read again for every 8 columns they took 5000 clocks of a chunk.)
+template <typename T>
+__device__ __forceinline__ T held_in_register(T v) {
+  if constexpr (std::is_same_v<T, float>) asm volatile("" : "+f"(v));
+  else if constexpr (sizeof(T) == 8) asm volatile("" : "+l"(v));
+  else asm volatile("" : "+r"(v));
+  return v;
+}
+struct NsTask {
+  int op, exact, wide, early;
+  int diagonal;     // a symmetric tile on it; the others go to their transposed place too
+  float* diag_out;
+  float a, b, c;
+};
+__device__ __forceinline__ void halves(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 f = unpack2(w.w[k], F16());
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2(u[k], F16());
     v[2 * k] = f.x, v[2 * k + 1] = f.y;
   }
 }
-// v as two fp16 each: the nearest ones, and those nearest to what they lost.
-__device__ __forceinline__ void two_halves(const float (&v)[16], U8x32& high, U8x32& low) {
+// A (gram) or B (poly) from the sums d; high, low: A's values, dp, diag: its diagonal at the row and at
+// the columns (poly).
+__device__ __forceinline__ void ns_symmetric(const NsTask& g, int p, int q, float dp, const float* diag,
+                                             const uint4& high, const uint4& low, float (&d)[8]) {
+  if (g.op == kNsGram) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    high.w[k] = pack2(v[2 * k], v[2 * k + 1], F16());
-    const float2 f = unpack2(high.w[k], F16());
-    low.w[k] = pack2(__fsub_rn(v[2 * k], f.x), __fsub_rn(v[2 * k + 1], f.y), F16());
-  }
-}
-// The transposed place of 16 columns of a row: a warp's 32 rows lie side by side there.
-__device__ __forceinline__ void ns_mirror(uint16_t* to, int ld, int side, int p, int q, const U8x32& w) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (q + i < side) to[static_cast<int64_t>(q + i) * ld + p] = static_cast<uint16_t>(w.w[i >> 1] >> (16 * (i & 1)));
-}
-
-__device__ __forceinline__ void ns_symmetric(const NsShape& g, int op, float b, float c, int matrix, bool mirror,
-                                             int p, int q, int side, const NsIn& in, float (&d)[16]) {
-  if (op == kNsGram) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) d[i] = __fmul_rn(d[i], 1.0f / (kXScale * kXScale));
+    for (int i = 0; i < 8; ++i) d[i] = __fmul_rn(d[i], 1.0f / (kXScale * kXScale));
   } else {
-    float x[16];
-    halves(in.x, x);
+    float x[8], dq[8];
+    eight(diag, dq);
+    halves(high, x);
     if (g.exact) {
-      float l[16];
-      halves(in.low, l);
+      float l[8];
+      halves(low, l);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fadd_rn(x[i], l[i]);
+      for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], l[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool on = p == q + i;  // the diagonal: A' is 0 there
-      const float a = on ? in.diag_p : x[i], with = on ? in.diag_p : __fadd_rn(in.diag_p, in.diag_q[i]);
-      d[i] = __fmaf_rn(c, __fmaf_rn(with, a, d[i]), __fmul_rn(b, a));
+    for (int i = 0; i < 8; ++i) {
+      float with = __fadd_rn(dp, dq[i]), a = x[i];
+      if (g.diagonal && p == q + i) with = a = dp;  // (A' is 0 there)
+      d[i] = __fmaf_rn(g.c, __fmaf_rn(with, a, d[i]), __fmul_rn(g.b, a));
     }
   }
-  if (p >= q && p < q + 16) {
-    float* to = (op == kNsGram ? g.a_diag : g.b_diag) + static_cast<int64_t>(matrix) * g.diag_apart + p;
+  if (g.diagonal && p >= q && p < q + 8) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (p == q + i) *to = d[i], d[i] = 0.0f;
-  }
-  U8x32 high, low;
-  two_halves(d, high, low);
-  const int64_t base = matrix * g.a_apart, at = base + static_cast<int64_t>(p) * g.a_ld + q;
-  uint16_t* to = op == kNsGram ? g.a_at : g.b_at;
-  st_v8(to + at, high);
-  if (mirror) ns_mirror(to + base, g.a_ld, side, p, q, high);
-  if (g.exact) {
-    to = op == kNsGram ? g.a_low_at : g.b_low_at;
-    st_v8(to + at, low);
-    if (mirror) ns_mirror(to + base, g.a_ld, side, p, q, low);
+    for (int i = 0; i < 8; ++i)
+      if (p == q + i) g.diag_out[p] = d[i], d[i] = 0.0f;
   }
 }
-// a X + B X from B' X (d): X counts with its first part alone in E X where `early`.
-__device__ __forceinline__ void ns_applied(const NsShape& g, float a, bool early, const NsIn& in, float (&d)[16]) {
-  float x[16], l[16];
-  halves(in.x, x);
-  halves(in.low, l);
+// a X + B X from B' X (d); high, low: X. In E X, X counts with its first part alone where `early`.
+__device__ __forceinline__ void ns_applied(const NsTask& g, float diag_p, const float* diag, const uint4& high,
+                                           const uint4& low, float (&d)[8]) {
+  float x[8], l[8], e[8];
+  if (g.wide) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float w = __fadd_rn(x[i], l[i]), e = g.wide ? in.diag_p : in.diag_q[i];
-    d[i] = __fmaf_rn(a, w, __fmaf_rn(e, early && !g.exact ? x[i] : w, d[i]));
+    for (int i = 0; i < 8; ++i) e[i] = diag_p;
+  } else {
+    eight(diag, e);
+  }
+  halves(high, x);
+  halves(low, l);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float w = __fadd_rn(x[i], l[i]);
+    d[i] = __fmaf_rn(g.a, w, __fmaf_rn(e[i], g.early ? x[i] : w, d[i]));
   }
 }
+// 8 columns of a row to their place in the transposed chunk: 64 rows of columns, twice 64 of the 128 rows. A
+// warp's 32 rows lie side by side there.
+__device__ __forceinline__ void ns_turn(uint8_t* chunk, int row, int col, const uint4& w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint8_t* half = chunk + (row >> 6) * (kNsHalfChunk / 2) + (row & 7) * 2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint16_t*>(half + (col + i) * 128 + ((((row >> 3) & 7) ^ ((col + i) & 7)) << 4)) =
+        static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+}
+// A chunk of fp32 results, whose upper and lower 16 bits lie in its two parts, to where they go: a warp
+// takes 32 rows, a row at a time, two columns a lane.
 template <typename L>
-__device__ __forceinline__ void ns_result(const L& n, const NsShape& g, int matrix, int p, int q, float (&d)[16]) {
+__device__ __forceinline__ void ns_result(const L& n, const NsShape& g, int matrix, int p0, int q0, uint8_t* high,
+                                          uint8_t* low, int warp, int lane) {
   const NsResult& r = n.result[g.first_matrix + matrix];
-  const int64_t at = static_cast<int64_t>(p) * g.cols + q;
-  float* param = r.param + at;
-  uint16_t* out = static_cast<uint16_t*>(r.out) + at;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) d[i] = __fmul_rn(d[i], 1.0f / kXScale);
-  if (r.param) {
-    const bool vec = q + 16 <= g.cols && (reinterpret_cast<uintptr_t>(param) & 31) == 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (vec) {
-        U8x32 w = ld_after_vec32<true>(param + 8 * h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d[8 * h + i] = __fmaf_rn(-g.step, d[8 * h + i], __fmul_rn(__uint_as_float(w.w[i]), n.decay));
-          w.w[i] = __float_as_uint(d[8 * h + i]);
-        }
-        st_v8(param + 8 * h, w);
+  const int q = q0 + 2 * lane, left = g.cols - q;
+  if (left <= 0) return;
+  for (int row = warp * 32; row < warp * 32 + 32 && p0 + row < g.rows; ++row) {
+    const uint32_t at = row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+    const uint32_t h = *reinterpret_cast<const uint32_t*>(high + at), l = *reinterpret_cast<const uint32_t*>(low + at);
+    float x = __uint_as_float((h << 16) | (l & 0xffffu)), y = __uint_as_float((h & 0xffff0000u) | (l >> 16));
+    const int64_t to = static_cast<int64_t>(p0 + row) * g.cols + q;
+    if (r.param) {
+      float* param = r.param + to;
+      if (left >= 2 && (reinterpret_cast<uintptr_t>(param) & 7) == 0) {
+        float2 w = *reinterpret_cast<const float2*>(param);
+        w.x = x = __fmaf_rn(-g.step, x, __fmul_rn(w.x, n.decay));
+        w.y = y = __fmaf_rn(-g.step, y, __fmul_rn(w.y, n.decay));
+        *reinterpret_cast<float2*>(param) = w;
       } else {
-#pragma unroll
-        for (int i = 8 * h; i < 8 * h + 8; ++i)
-          if (q + i < g.cols) param[i] = d[i] = __fmaf_rn(-g.step, d[i], __fmul_rn(param[i], n.decay));
+        param[0] = x = __fmaf_rn(-g.step, x, __fmul_rn(param[0], n.decay));
+        if (left >= 2) param[1] = y = __fmaf_rn(-g.step, y, __fmul_rn(param[1], n.decay));
       }
     }
-  }
-  if (r.out) {
-    U8x32 w;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      w.w[k] = n.out_kind == 0 ? pack2(d[2 * k], d[2 * k + 1], F16()) : pack2(d[2 * k], d[2 * k + 1], BF16());
-    if (q + 16 <= g.cols && (reinterpret_cast<uintptr_t>(out) & 31) == 0) {
-      st_v8(out, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (q + i < g.cols) out[i] = static_cast<uint16_t>(w.w[i >> 1] >> (16 * (i & 1)));
+    if (r.out) {
+      uint16_t* out = static_cast<uint16_t*>(r.out) + to;
+      const uint32_t w = n.out_kind == 0 ? pack2(x, y, F16()) : pack2(x, y, BF16());
+      if (left >= 2 && (reinterpret_cast<uintptr_t>(out) & 3) == 0) {
+        *reinterpret_cast<uint32_t*>(out) = w;
+      } else {
+        out[0] = static_cast<uint16_t>(w);
+        if (left >= 2) out[1] = static_cast<uint16_t>(w >> 16);
+      }
     }
   }
 }
@@ -265,7 +271,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
   uint64_t* empty = full + kNsStages;
   uint64_t* summed = empty + kNsStages;
   uint64_t* taken = summed + kNsSlots;
-  uint64_t* drained = taken + kNsSlots;
+  uint64_t* held = taken + kNsSlots;  // a half's chunk holds what its results need
+  uint64_t* go = held + 2;  // the product before has ended everywhere
+  uint64_t* drained = go + 1;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -273,6 +281,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNsStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < kNsSlots; ++i) mbar_init(&summed[i], 1), mbar_init(&taken[i], CTAS * kResultWarps);
+    mbar_init(&held[0], 1);
+    mbar_init(&held[1], 1);
+    mbar_init(go, 1);
     mbar_init(drained, 1);
     mbar_init_fence();
   }
@@ -295,6 +306,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
     for (int at_op = 0; at_op < ops && alive; ++at_op) {
       const int op = at_op % 3, from = (at_op / 3) & 1, tiles = n.tiles[op == kNsApply];
       ns_wait_grid(n.arrived, at_op * gridDim.x, alive);
+      mbar_arrive(go);
       proxy_fence();
       for (int t = first; t < tiles && alive; t += apart) {
         const NsTile at = ns_tile(n, op, t);
@@ -339,7 +351,6 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
     Ring<kNsSlots> s;
     for (int at_op = 0; at_op < ops && alive; ++at_op) {
       const int op = at_op % 3, tiles = n.tiles[op == kNsApply];
-      ns_wait_grid(n.arrived, at_op * gridDim.x, alive);
       for (int t = first; t < tiles && alive; t += apart) {
         const NsShape& g = n.shape[ns_tile(n, op, t).shape];
         const bool p_mn = ns_p_mn(g, op), q_mn = ns_q_mn(g, op);
@@ -351,7 +362,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
         tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
         bool there = false;  // the stage has been seen already
         for (int k = 0; k < stages; ++k) {
-          if (!there) tc_wait(&full[r.at], r.phase, alive, &g_muon_fault, kMuonFault);
+          // (the first copies of a product come when it begins)
+          if (!there) tc_wait_long(&full[r.at], r.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
           if (!__all_sync(~0u, alive)) {
             alive = false;
             break;
@@ -380,68 +392,158 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
       tc_wait(drained, 0, wait, &g_muon_fault, kMuonFault);
     }
   } else if (warp >= kFirstResultWarp) {  // ---------------------------------------------- the results
-    const int half = (warp - kFirstResultWarp) >> 2;
+    const int half = (warp - kFirstResultWarp) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * HALF;
     const uint32_t taken_at = CTAS == 2 ? cluster_addr(taken, 0) : 0;
+    uint8_t* high = smem + kNsResults + half * 2 * kNsHalfChunk;
+    uint8_t* low = high + kNsHalfChunk;
+    float* diag_q = reinterpret_cast<float*>(smem + kNsDiag) + half * kNsChunk;
+    const bool leader = row == 0;  // of the 4 warps of a half
     const bool skip = n.factor && !isfinite(ld_after_f32(n.factor));
+    unsigned held_phase = 0;
     Ring<kNsSlots> s;
     for (int at_op = 0; at_op < ops; ++at_op) {
       const int op = at_op % 3, step = at_op / 3, from = step & 1, tiles = n.tiles[op == kNsApply];
-      const float a = n.coefficients[3 * step], b = n.coefficients[3 * step + 1], c = n.coefficients[3 * step + 2];
-      const bool early = step < n.steps - 3, last = step == n.steps - 1;
-      if (threadIdx.x == kFirstResultWarp * 32) ns_wait_grid(n.arrived, at_op * gridDim.x, alive);
-      named_barrier(1, kResultWarps * 32);
+      const bool last = op == kNsApply && step == n.steps - 1;
+      NsTask task;
+      task.op = op;
+      task.a = held_in_register(n.coefficients[3 * step]);
+      task.b = held_in_register(n.coefficients[3 * step + 1]);
+      task.c = held_in_register(n.coefficients[3 * step + 2]);
+      tc_wait_long(go, at_op & 1, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
+      if (leader) proxy_fence();
       for (int t = first; t < tiles; t += apart) {
         const NsTile at = ns_tile(n, op, t);
         const NsShape& g = n.shape[at.shape];
-        const int small = g.wide ? g.rows : g.cols;
-        const int rows = op == kNsApply ? g.rows : small, cols = op == kNsApply ? g.cols : small;
-        const int p = at.p * TILE + rank * kNsSide + (warp & 3) * 32 + lane, q0 = at.q * TILE + half * HALF;
-        const bool on = p < rows && !(skip && op == kNsApply && last);
-        NsIn in[2];
-        if (on && q0 < cols) ns_fetch(g, op, from, at.matrix, p, q0, in[0]);
+        task.exact = held_in_register(g.exact);
+        task.wide = held_in_register(g.wide);
+        const int side = held_in_register(task.wide ? g.rows : g.cols);
+        task.early = step < n.steps - 3 && !task.exact;
+        task.diagonal = at.p == at.q;
+        task.diag_out = held_in_register((op == kNsGram ? g.a_diag : g.b_diag) +
+                                         static_cast<int64_t>(at.matrix) * g.diag_apart);
+        const int rows = op == kNsApply ? held_in_register(g.rows) : side,
+                  cols = op == kNsApply ? held_in_register(g.cols) : side;
+        // (exact shapes have one tile, so a chunk's second part is free where a tile goes transposed)
+        const bool turn = op != kNsApply && !task.diagonal;
+        const CUtensorMap* turned = op == kNsGram ? &g.a_turned : &g.b_turned;
+        const int p0 = at.p * TILE + rank * kNsSide, p = p0 + row;
+        const bool lows = op == kNsApply || task.exact;  // the chunk's second part is in use
+        const CUtensorMap *in, *in_low, *out, *out_low;
+        if (op == kNsApply) {
+          in = g.wide ? &g.x[from] : &g.xt[from], in_low = g.wide ? &g.x_low[from] : &g.xt_low[from];
+          out = g.wide ? &g.x[from ^ 1] : &g.xt[from ^ 1], out_low = g.wide ? &g.x_low[from ^ 1] : &g.xt_low[from ^ 1];
+        } else {
+          in = &g.a, in_low = &g.a_low;
+          out = op == kNsGram ? &g.a : &g.b, out_low = op == kNsGram ? &g.a_low : &g.b_low;
+        }
+        // A's diagonal by rows and columns; B's by those of X that B is as wide as.
+        const bool by_p = op == kNsPoly || (op == kNsApply && task.wide), by_q = op == kNsPoly || (op == kNsApply && !task.wide);
+        const float* diag = (op == kNsApply ? g.b_diag : g.a_diag) + static_cast<int64_t>(at.matrix) * g.diag_apart;
+        // Chunk k of this half: the copies that are under way from it end, and its inputs are fetched.
+        const auto fetch = [&](int k) {
+          const int q0 = at.q * TILE + half * HALF + k * kNsChunk;
+          if (!leader || !alive || p0 >= rows || q0 >= cols) return;
+          tma_store_wait_read();
+          if (op == kNsGram) return;
+          mbar_arrive_expect_tx(&held[half], (lows ? 2 : 1) * kNsHalfChunk + (by_q ? kNsChunk * 4 : 0));
+          tma_load(high, in, q0, p0, at.matrix, &held[half]);
+          if (lows) tma_load(low, in_low, q0, p0, at.matrix, &held[half]);
+          if (by_q) bulk_load(diag_q, diag + q0, kNsChunk * 4, &held[half]);
+        };
+        float diag_p = 0.0f;
+        if (by_p && p < rows) diag_p = ld_after_f32(diag + p);
+        fetch(0);
         tc_wait_long(&summed[s.at], s.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
         tc_fence_after();
-#pragma unroll 2
-        for (int k = 0; k < HALF / 16; ++k) {
-          const int q = q0 + 16 * k;
-          uint32_t v[16];
-          tmem_ld(lanes + s.at * TILE + 16 * k, v);
-          if (k + 1 < HALF / 16 && on && q + 16 < cols) ns_fetch(g, op, from, at.matrix, p, q + 16, in[(k + 1) & 1]);
-          tmem_ld_wait(v);
-          if (k + 1 == HALF / 16) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
-              else mbar_arrive(&taken[s.at]);
+#pragma unroll 1
+        for (int k = 0; k < HALF / kNsChunk; ++k) {
+          const int q0 = at.q * TILE + half * HALF + k * kNsChunk;
+          const bool inside = p0 < rows && q0 < cols;  // the same for the half's 4 warps
+          if (k > 0) fetch(k);
+          if (inside && op != kNsGram) {
+            tc_wait(&held[half], held_phase, alive, &g_muon_fault, kMuonFault);
+            held_phase ^= 1u;
+          }
+          if (inside && op == kNsGram) named_barrier(2 + half, 128);  // (the chunk is free)
+#pragma unroll
+          for (int h = 0; h < kNsChunk; h += 32) {
+            uint32_t v[32];
+            tmem_ld(lanes + s.at * TILE + k * kNsChunk + h, v);
+            tmem_ld_wait(v);
+            if (k + 1 == HALF / kNsChunk && h + 32 == kNsChunk) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
+                else mbar_arrive(&taken[s.at]);
+              }
+            }
+            if (inside && p < rows) {
+              uint4 x[4], y[4];  // (all read before the first is written: they are places of one buffer)
+              if (op != kNsGram) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  x[j] = *reinterpret_cast<const uint4*>(ns_place(high, row, h / 8 + j));
+                  if (lows) y[j] = *reinterpret_cast<const uint4*>(ns_place(low, row, h / 8 + j));
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = __uint_as_float(v[8 * j + i]);
+                uint4 w, l;
+                if (op != kNsApply) {
+                  ns_symmetric(task, p, q0 + h + 8 * j, diag_p, diag_q + h + 8 * j, x[j], y[j], d);
+                  two_halves(d, w, l);
+                  if (turn) ns_turn(low, row, h + 8 * j, w);
+                } else {
+                  ns_applied(task, diag_p, diag_q + h + 8 * j, x[j], y[j], d);
+                  if (last) {
+                    uint32_t u[4], f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const uint32_t a = __float_as_uint(__fmul_rn(d[2 * i], 1.0f / kXScale)),
+                                     b = __float_as_uint(__fmul_rn(d[2 * i + 1], 1.0f / kXScale));
+                      u[i] = __byte_perm(a, b, 0x7632u), f[i] = __byte_perm(a, b, 0x5410u);
+                    }
+                    w = make_uint4(u[0], u[1], u[2], u[3]), l = make_uint4(f[0], f[1], f[2], f[3]);
+                  } else {
+                    two_halves(d, w, l);
+                  }
+                }
+                *reinterpret_cast<uint4*>(ns_place(high, row, h / 8 + j)) = w;
+                if (lows) *reinterpret_cast<uint4*>(ns_place(low, row, h / 8 + j)) = l;
+              }
             }
           }
-          if (on && q < cols) {
-            float d[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) d[i] = __uint_as_float(v[i]);
-            if (op != kNsApply) {
-              ns_symmetric(g, op, b, c, at.matrix, at.p != at.q, p, q, small, in[k & 1], d);
-            } else {
-              ns_applied(g, a, early, in[k & 1], d);
-              if (last) {
-                ns_result(n, g, at.matrix, p, q, d);
-              } else {
-                U8x32 high, low;
-                two_halves(d, high, low);
-                const int64_t to = at.matrix * g.x_apart + static_cast<int64_t>(p) * g.x_ld + q;
-                st_v8(g.x_at[from ^ 1] + to, high);
-                st_v8(g.x_low_at[from ^ 1] + to, low);
+          if (!inside) continue;
+          if (last) {
+            named_barrier(2 + half, 128);
+            if (!skip) ns_result(n, g, at.matrix, p0, q0, high, low, warp & 3, lane);
+            tma_store_fence();  // (read before the next copy into the chunk)
+            named_barrier(2 + half, 128);
+          } else {
+            tma_store_fence();
+            named_barrier(2 + half, 128);
+            if (leader) {
+              tma_store(out, q0, p0, at.matrix, high);
+              if (lows) tma_store(out_low, q0, p0, at.matrix, low);
+              if (turn) {
+                tma_store(turned, p0, q0, at.matrix, low);
+                if (p0 + 64 < rows) tma_store(turned, p0 + 64, q0, at.matrix, low + kNsHalfChunk / 2);
               }
+              tma_store_commit();
             }
           }
         }
         s.next();
       }
-      proxy_fence();
+      if (leader) tma_store_wait();
       named_barrier(1, kResultWarps * 32);
       if (threadIdx.x == kFirstResultWarp * 32) {
+        proxy_fence();
         __threadfence();
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(n.arrived) : "memory");
       }

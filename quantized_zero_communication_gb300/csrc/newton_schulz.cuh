@@ -28,10 +28,9 @@ struct NsShape {
   CUtensorMap x[2], x_low[2];    // X as the gram reads it: rows along the sum if wide, else across it
   CUtensorMap xt[2], xt_low[2];  // X as the apply reads it: the other way round
   CUtensorMap a, a_low, b, b_low;
-  uint16_t *x_at[2], *x_low_at[2], *a_at, *a_low_at, *b_at, *b_low_at;
+  CUtensorMap a_turned, b_turned;  // for a tile's transposed place: boxes of 64 rows
   float *a_diag, *b_diag;        // fp32; the fp16 matrices hold zeros there
-  int64_t x_apart, a_apart;      // elements between matrices
-  int32_t rows, cols, x_ld, a_ld, diag_apart;
+  int32_t rows, cols, diag_apart;
   int32_t wide, exact;           // rows <= cols; products of both parts
   int32_t count, first_matrix;   // in the batch
   int32_t side_tiles;            // of A's side

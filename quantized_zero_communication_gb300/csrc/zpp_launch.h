@@ -245,7 +245,7 @@ cudaError_t launch_quant_fp8(const QuantFp8Args& a, cudaStream_t s);
 
 // K12 .. K14: Newton-Schulz products over a list of matrices, with the Muon step around them.
 constexpr int kMuonMatrices = 256;  // of a batch
-constexpr int kMuonGroups = 13;     // shapes of a batch
+constexpr int kMuonGroups = 12;     // shapes of a batch
 struct MuonMatrix {
   const void* x;     // the gradient, or the matrix itself
   float* momentum;   // null: x itself is what becomes orthogonal
