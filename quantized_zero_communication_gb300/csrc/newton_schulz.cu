@@ -183,11 +183,17 @@ __device__ __forceinline__ void ns_symmetric(const NsTask& g, int p, int q, floa
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], l[i]);
     }
+    if (!g.diagonal) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float with = __fadd_rn(dp, dq[i]), a = x[i];
-      if (g.diagonal && p == q + i) with = a = dp;  // (A' is 0 there)
-      d[i] = __fmaf_rn(g.c, __fmaf_rn(with, a, d[i]), __fmul_rn(g.b, a));
+      for (int i = 0; i < 8; ++i)
+        d[i] = __fmaf_rn(g.c, __fmaf_rn(__fadd_rn(dp, dq[i]), x[i], d[i]), __fmul_rn(g.b, x[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool on = p == q + i;  // (A' is 0 there)
+        const float a = on ? dp : x[i], with = on ? dp : __fadd_rn(dp, dq[i]);
+        d[i] = __fmaf_rn(g.c, __fmaf_rn(with, a, d[i]), __fmul_rn(g.b, a));
+      }
     }
   }
   if (g.diagonal && p >= q && p < q + 8) {
@@ -225,41 +231,75 @@ __device__ __forceinline__ void ns_turn(uint8_t* chunk, int row, int col, const 
         static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
 }
 // A chunk of fp32 results, whose upper and lower 16 bits lie in its two parts, to where they go: a warp
-// takes 32 rows, a row at a time, two columns a lane.
+// takes 32 rows, 8 of them at a time (so that as many loads are under way), two columns a lane.
 template <typename L>
-__device__ __forceinline__ void ns_result(const L& n, const NsShape& g, int matrix, int p0, int q0, uint8_t* high,
-                                          uint8_t* low, int warp, int lane) {
-  const NsResult& r = n.result[g.first_matrix + matrix];
-  const int q = q0 + 2 * lane, left = g.cols - q;
+__device__ __forceinline__ void ns_result(const L& n, const NsShape& g, int matrix, int p0, int q0,
+                                          const uint8_t* high, const uint8_t* low, int warp, int lane) {
+  const NsResult& res = n.result[g.first_matrix + matrix];
+  const int q = q0 + 2 * lane, left = g.cols - q, rows = g.rows - p0;
   if (left <= 0) return;
-  for (int row = warp * 32; row < warp * 32 + 32 && p0 + row < g.rows; ++row) {
-    const uint32_t at = row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
-    const uint32_t h = *reinterpret_cast<const uint32_t*>(high + at), l = *reinterpret_cast<const uint32_t*>(low + at);
-    float x = __uint_as_float((h << 16) | (l & 0xffffu)), y = __uint_as_float((h & 0xffff0000u) | (l >> 16));
-    const int64_t to = static_cast<int64_t>(p0 + row) * g.cols + q;
-    if (r.param) {
-      float* param = r.param + to;
-      if (left >= 2 && (reinterpret_cast<uintptr_t>(param) & 7) == 0) {
-        float2 w = *reinterpret_cast<const float2*>(param);
-        w.x = x = __fmaf_rn(-g.step, x, __fmul_rn(w.x, n.decay));
-        w.y = y = __fmaf_rn(-g.step, y, __fmul_rn(w.y, n.decay));
-        *reinterpret_cast<float2*>(param) = w;
-      } else {
-        param[0] = x = __fmaf_rn(-g.step, x, __fmul_rn(param[0], n.decay));
-        if (left >= 2) param[1] = y = __fmaf_rn(-g.step, y, __fmul_rn(param[1], n.decay));
+  const int64_t cols = g.cols;
+  float* const param = res.param ? res.param + p0 * cols + q : nullptr;
+  uint16_t* const out = res.out ? static_cast<uint16_t*>(res.out) + p0 * cols + q : nullptr;
+  const bool pair = left >= 2 && (cols & 1) == 0;  // both columns by one access
+  const bool param_pair = pair && (reinterpret_cast<uintptr_t>(param) & 7) == 0;
+  const bool out_pair = pair && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
+  const float step = g.step, decay = n.decay;
+  const bool f16 = n.out_kind == 0;
+#pragma unroll 1
+  for (int r0 = warp * 32; r0 < warp * 32 + 32 && r0 < rows; r0 += 8) {
+    float2 old[8];
+    if (param) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* at = param + (r0 + i) * cols;
+        if (r0 + i < rows) {
+          if (param_pair) old[i] = *reinterpret_cast<const float2*>(at);
+          else old[i] = make_float2(at[0], left >= 2 ? at[1] : 0.0f);
+        }
       }
     }
-    if (r.out) {
-      uint16_t* out = static_cast<uint16_t*>(r.out) + to;
-      const uint32_t w = n.out_kind == 0 ? pack2(x, y, F16()) : pack2(x, y, BF16());
-      if (left >= 2 && (reinterpret_cast<uintptr_t>(out) & 3) == 0) {
-        *reinterpret_cast<uint32_t*>(out) = w;
-      } else {
-        out[0] = static_cast<uint16_t>(w);
-        if (left >= 2) out[1] = static_cast<uint16_t>(w >> 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + i;
+      if (row >= rows) break;
+      const uint32_t at = row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4;
+      const uint32_t h = *reinterpret_cast<const uint32_t*>(high + at), l = *reinterpret_cast<const uint32_t*>(low + at);
+      float x = __uint_as_float(__byte_perm(h, l, 0x1054u)), y = __uint_as_float(__byte_perm(h, l, 0x3276u));
+      if (param) {
+        x = __fmaf_rn(-step, x, __fmul_rn(old[i].x, decay));
+        y = __fmaf_rn(-step, y, __fmul_rn(old[i].y, decay));
+        float* to = param + row * cols;
+        if (param_pair) {
+          *reinterpret_cast<float2*>(to) = make_float2(x, y);
+        } else {
+          to[0] = x;
+          if (left >= 2) to[1] = y;
+        }
+      }
+      if (out) {
+        uint16_t* to = out + row * cols;
+        const uint32_t w = f16 ? pack2(x, y, F16()) : pack2(x, y, BF16());
+        if (out_pair) {
+          *reinterpret_cast<uint32_t*>(to) = w;
+        } else {
+          to[0] = static_cast<uint16_t>(w);
+          if (left >= 2) to[1] = static_cast<uint16_t>(w >> 16);
+        }
       }
     }
   }
+}
+// The old parameters of a row of a chunk, brought into L2 while its sums are made.
+template <typename L>
+__device__ __forceinline__ void ns_result_ahead(const L& n, const NsShape& g, int matrix, int p, int q0, int cols) {
+  const float* param = n.result[g.first_matrix + matrix].param;
+  if (!param) return;
+  const float* at = param + static_cast<int64_t>(p) * g.cols + q0;
+  const int left = g.cols - q0 < cols ? g.cols - q0 : cols;
+  if (left > 0 && (reinterpret_cast<uintptr_t>(at) & 15) == 0 && left * 4 >= 16)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(static_cast<uint32_t>(left * 4) & ~15u)
+                 : "memory");
 }
 
 template <int CTAS, typename L>
@@ -454,6 +494,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
         float diag_p = 0.0f;
         if (by_p && p < rows) diag_p = ld_after_f32(diag + p);
         fetch(0);
+        if (last && !skip && p < rows) ns_result_ahead(n, g, at.matrix, p, at.q * TILE + half * HALF, HALF);
         tc_wait_long(&summed[s.at], s.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
         tc_fence_after();
 #pragma unroll 1
