@@ -1,10 +1,10 @@
 """GB300 (sm_103a) ZeRO++ block-quantisation hot path: qwZ quantise / dequantise and
 the qgZ reorder-quantise, fused intra-node dequant-reduce-requant and final
-dequant-reduce, and on either side of them the AdamW step with its gradient norm, the
-product with quantised weights and the products of a linear layer in fp8, behind the C ABI
+dequant-reduce, and on either side of them the AdamW step with its gradient norm, the Muon step,
+the product with quantised weights and the products of a linear layer in fp8, behind the C ABI
 declared in ``include/zpp.h``.
 
-``binding`` is the ctypes layer over ``libzpp.so``; ``optim`` the optimiser; ``linear`` the linear layer;
+``binding`` is the ctypes layer over ``libzpp.so``; ``optim`` the optimisers; ``linear`` the linear layer;
 ``inputs`` holds the seeded synthetic workloads. The library is loaded on first use.
 """
 from .binding import (  # noqa: F401

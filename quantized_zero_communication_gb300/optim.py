@@ -272,7 +272,9 @@ class Muon:
         if max_norm is not None or pre_scale is not None:
             if grad_scale is not None:
                 raise ValueError("grad_scale replaces max_norm and pre_scale")
-            norm = _b.grad_norm(grads, max_norm, 1.0 if pre_scale is None else pre_scale)
+            # (matrices may start anywhere, the norm's tensors at multiples of 16 bytes: others are copied)
+            norm = _b.grad_norm([g if g.data_ptr() % 16 == 0 else g.clone() for g in grads], max_norm,
+                                1.0 if pre_scale is None else pre_scale)
             scale = norm.data_ptr() + 4
         elif grad_scale is not None:
             scale = _b._scale_address(grads[0], grad_scale)

@@ -247,6 +247,22 @@ def test_muon_skips_what_is_not_finite_and_resumes():
     assert torch.equal(other.params[0], params[0]) and torch.equal(other.buffers[0], opt.buffers[0])
 
 
+def test_muon_of_views_that_start_anywhere():
+    """Stacks of odd-sized matrices: parameters, gradients, momenta and weights off every alignment."""
+    shapes = (3, 37, 53)
+    stack = torch.randn(shapes, generator=gen(1), device=DEV)
+    apart = [t.clone() for t in stack]
+    low = torch.zeros(shapes, dtype=torch.bfloat16, device=DEV)
+    g = torch.stack([matrix(37, 53, i) for i in range(3)]).bfloat16()
+    opt = zpp.Muon(list(stack), weights=list(low), buffers=list(torch.zeros(shapes, device=DEV)))
+    plain = zpp.Muon(apart)
+    for _ in range(2):
+        a = opt.step(list(g), max_norm=1e-3)
+        b = plain.step([t.clone() for t in g], max_norm=1e-3)
+        assert torch.equal(a, b)
+    assert torch.equal(stack, torch.stack(apart)) and torch.equal(low, stack.bfloat16())
+
+
 def test_muon_in_a_graph_and_beside_another_stream():
     params = [torch.randn(s, generator=gen(1), device=DEV) for s in ((96, 64), (64, 200))]
     twin = [p.clone() for p in params]
