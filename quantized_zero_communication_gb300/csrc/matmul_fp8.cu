@@ -29,9 +29,9 @@ template <int CTAS, int BN, bool QROWS>
 struct MatmulGeo {
   static constexpr int Q_ROWS = BN / CTAS;  // of a CTA's stage
   static constexpr int STAGE = (kLanes + Q_ROWS) * kStep;
-  static constexpr int STAGES = Q_ROWS >= 128 ? 6 : 8;
-  static constexpr int SLOT = BN < 32 ? 32 : BN;  // tensor-memory columns of a slot
-  static constexpr int SLOTS = 512 / SLOT < 4 ? 512 / SLOT : 4;
+  static constexpr int STAGES = 6;
+  static constexpr int SLOT = BN == 96 ? 128 : BN;  // tensor-memory columns of a slot
+  static constexpr int SLOTS = 512 / SLOT;
   static constexpr int HALF = BN / 2;  // columns of a warp
   // Blocks whose scales are waited for together. (A wait costs some 100 clocks; where Q has a scale a
   // column, one for every block measured better: 8192^3 613 us against 664.)
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     }
   } else {  // -------------------------------------------------------------- scales, sums, results
     more_registers();
-    constexpr int HALF = G::HALF, CHUNK = HALF < 32 ? HALF : 32;
+    constexpr int HALF = G::HALF, CHUNK = HALF % 32 ? 16 : 32;
     const int half = (warp - kFirstResultWarp) >> 2, in_cta = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * HALF;
     const uint32_t taken_at = CTAS == 2 ? cluster_addr(taken, 0) : smem_addr(taken);
@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
       f32x2 sums[HALF / 2];
 #pragma unroll
       for (int i = 0; i < HALF / 2; ++i) sums[i] = f2(0.0f, 0.0f);
+      const float bias = run.bias && run.bias_p && p0 < run.p.rows ? load_kind(run.bias, p0, run.y_kind) : 0.0f;
       for (int kb = 0; kb < blocks; ++kb) {
         const int in_group = kb % G::GROUP;
         if (in_group == 0) tc_wait(&scaled[x.at], x.phase, alive, &g_matmul_fault, kMatmulFault);
@@ -332,7 +333,6 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         }
       }
       if (p0 < run.p.rows) {
-        const float bias = run.bias && run.bias_p ? load_kind(run.bias, p0, run.y_kind) : 0.0f;
 #pragma unroll
         for (int i = 0; i < HALF; i += 8) {
           float v[8];
@@ -464,6 +464,10 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
 #pragma unroll
   for (int i = 0; i < G::COLS / 2; ++i) sums[i] = f2(0.0f, 0.0f);
 
+  const int in_cta = (warp & 3) * 32 + lane;
+  const int64_t p = static_cast<int64_t>(p_tile) * kLanes + in_cta, q0 = static_cast<int64_t>(q_tile) * BN;
+  const float bias = run.bias && warp < R && p < run.p.rows ? load_kind(run.bias, p, run.y_kind) : 0.0f;
+
   if (warp == R) {
     if (lane == 0) {
       Ring<G::STAGES> r;
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
     cp_async_wait<0>();
   } else {
     constexpr int CHUNK = G::COLS < 32 ? G::COLS : 32;
-    const int part = warp >> 2, in_cta = (warp & 3) * 32 + lane;
+    const int part = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + part * G::COLS;
     const int p_at = run.p.shift ? 0 : in_cta;
     Ring<G::SLOTS> s;
@@ -583,9 +587,7 @@ __global__ void __launch_bounds__(FewGeo<BN>::THREADS, FewGeo<BN>::PER_SM)
   // Every product of this CTA has been read, so the stages are free; the other CTAs' are after the barrier.
   __syncwarp();
   const bool results = warp < R;
-  const int part = warp >> 2, in_cta = (warp & 3) * 32 + lane;
-  const int64_t p = static_cast<int64_t>(p_tile) * kLanes + in_cta, q0 = static_cast<int64_t>(q_tile) * BN;
-  const float bias = run.bias && results && p < run.p.rows ? load_kind(run.bias, p, run.y_kind) : 0.0f;
+  const int part = warp >> 2;
   if (split == 1) {
     if (results && p < run.p.rows) {
 #pragma unroll
@@ -670,7 +672,7 @@ cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s) {
   const bool swap = a.a.rows <= 128 || !whole;
   const int64_t pairs = ((a.a.rows + 255) / 256) * ((a.b.rows + 255) / 256);
   if (a.a.rows > 128 && pairs >= 48) return run_tiles<2, 256>(a, swap, s);
-  return run_tiles<1, 128>(a, swap, s);
+  return a.a.rows <= 96 ? run_tiles<1, 96>(a, true, s) : run_tiles<1, 128>(a, swap, s);
 }
 
 cudaError_t read_matmul_fault(unsigned* flags, bool clear) {

@@ -151,24 +151,30 @@ struct QuantShared {
   alignas(16) uint32_t turned[TRANS ? kQuantTile * 32 : 1];
 };
 
-// A tile whose values have been loaded. ODD: some of them may be infinite or NaN.
+// The largest magnitude of each of a thread's rows.
+template <int KIND, bool FINITE_ONLY>
+__device__ __forceinline__ void row_tops(const Row<KIND> (&v)[4], uint32_t (&top)[4]) {
+  using T = Top<KIND>;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top[i] = T::size(v[i].w[0], FINITE_ONLY);
+#pragma unroll
+    for (int k = 1; k < Row<KIND>::WORDS; ++k) top[i] = T::more(top[i], T::size(v[i].w[k], FINITE_ONLY));
+    if constexpr (KIND != 2) top[i] = max(top[i] & 0xffffu, top[i] >> 16);
+  }
+}
+
+// A tile whose values have been loaded; top: of each row (ODD: made again). ODD: some of them may be infinite or NaN.
 template <int KIND, bool TILE, bool TRANS, bool ODD>
 __device__ __forceinline__ void quant_tile_fp8(const QuantFp8Run& a, QuantShared<KIND, TILE, TRANS>& sh,
-                                               const Row<KIND> (&v)[4], int64_t r0, int64_t c0) {
+                                               const Row<KIND> (&v)[4], uint32_t (&top)[4], int64_t r0,
+                                               int64_t c0) {
   using T = Top<KIND>;
   constexpr int WORDS = Row<KIND>::WORDS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rq = warp * 4 + (lane >> 3), cg = lane & 7;
   const int64_t row = r0 + rq * 4, col = c0 + cg * 16;
-  // (what `more` gives of a row's or column's words; for 16-bit values both halves of a word)
-  uint32_t top[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    top[i] = T::size(v[i].w[0], ODD);
-#pragma unroll
-    for (int k = 1; k < WORDS; ++k) top[i] = T::more(top[i], T::size(v[i].w[k], ODD));
-    if constexpr (KIND != 2) top[i] = max(top[i] & 0xffffu, top[i] >> 16);
-  }
+  if constexpr (ODD) row_tops<KIND, true>(v, top);
   float row_inv[4];
   if constexpr (TILE) {
     uint32_t m = max(max(top[0], top[1]), max(top[2], top[3]));
@@ -278,16 +284,12 @@ __global__ void __launch_bounds__(256, KIND == 2 ? 2 : 3) k_quant_fp8(const Quan
 #pragma unroll
   for (int i = 0; i < 4; ++i) load_row<KIND>(a, r0 + rq * 4 + i, c0 + cg * 16, v[i]);
   prefetch_tile<KIND>(a);
-  using T = Top<KIND>;
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < Row<KIND>::WORDS; ++k) m = T::more(m, T::size(v[i].w[k], false));
-  const bool odd = KIND == 2 ? m >= T::INF : (m & 0xffffu) >= T::INF || (m >> 16) >= T::INF;
+  uint32_t top[4];
+  row_tops<KIND, false>(v, top);
+  const bool odd = max(max(top[0], top[1]), max(top[2], top[3])) >= Top<KIND>::INF;
   // (values that are not finite take code of their own: the common one has no selections)
-  if (__syncthreads_or(odd)) quant_tile_fp8<KIND, TILE, TRANS, true>(a, sh, v, r0, c0);
-  else quant_tile_fp8<KIND, TILE, TRANS, false>(a, sh, v, r0, c0);
+  if (__syncthreads_or(odd)) quant_tile_fp8<KIND, TILE, TRANS, true>(a, sh, v, top, r0, c0);
+  else quant_tile_fp8<KIND, TILE, TRANS, false>(a, sh, v, top, r0, c0);
 }
 
 template <int KIND>
