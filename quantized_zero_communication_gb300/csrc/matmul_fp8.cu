@@ -70,13 +70,12 @@ __device__ __forceinline__ void store_kind(void* p, int64_t i, float v, int kind
   else static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(kind == 0 ? pack2(v, v, F16()) : pack2(v, v, BF16()));
 }
 
-// 8 columns of row p of P, from column q on.
-// bias: that of row p, where it goes by P's rows.
-__device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int64_t q, float bias, float (&v)[8]) {
-  if (run.bias) {
+// 8 columns of row p of P, from column q on (a bias by P's rows is in v already).
+__device__ __forceinline__ void store_sums(const MatmulRun& run, int64_t p, int64_t q, float (&v)[8]) {
+  if (run.bias && !run.bias_p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (q + i < run.q.rows) v[i] = __fadd_rn(v[i], run.bias_p ? bias : load_kind(run.bias, q + i, run.y_kind));
+      if (q + i < run.q.rows) v[i] = __fadd_rn(v[i], load_kind(run.bias, q + i, run.y_kind));
   }
   const int64_t at = p * run.y_p + q * run.y_q;
   if (run.vec && q + 8 <= run.q.rows) {  // consecutive and whole
@@ -333,12 +332,16 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
         }
       }
       if (p0 < run.p.rows) {
+        if (run.bias && run.bias_p) {
+#pragma unroll
+          for (int i = 0; i < HALF / 2; ++i) sums[i] = f2_add(sums[i], f2(bias, bias));
+        }
 #pragma unroll
         for (int i = 0; i < HALF; i += 8) {
           float v[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) f2_split(sums[i / 2 + k], v[2 * k], v[2 * k + 1]);
-          store_sums(run, p0, q0 + i, bias, v);
+          store_sums(run, p0, q0 + i, v);
         }
       }
     }
