@@ -207,12 +207,59 @@ struct Batch {
   std::vector<Shape> shapes;
   std::vector<int> order;  // places in the list
   int64_t elems = 0;
-  int64_t bytes() const {
-    int64_t b = 0;
-    for (const Shape& s : shapes) b += s.bytes();
-    return 128 + b + (static_cast<int64_t>(order.size()) * kMuonPartials * 4 + 127) / 128 * 128;
-  }
 };
+// How K14 takes a batch: the side of its tiles, 256 by a pair of CTAs, or 128, which share themselves out more
+// evenly; and into how many parts a gram's sum is split where its tiles leave most CTAs without work
+// (worth the pass that joins them, 5 us, from 48 stages on: 100 x 6000 in five steps 460 us without).
+// A stage takes either side about as long (0.3 us): counted are those of the slowest CTA.
+struct Plan {
+  int side = 128, split = 1;
+  int64_t parts = 0;  // of tiles, in the gram
+};
+Plan plan_of(const Batch& b) {
+  Plan best;
+  double least = 0.0;
+  for (int pair = 0; pair < 2; ++pair) {
+    Plan p;
+    p.side = pair ? 256 : 128;
+    const int64_t at_once = pair ? 76 : 152;
+    double tiles[3] = {}, work[3] = {}, longest[3] = {};
+    int64_t symmetric = 0, stages = 0;
+    for (const Shape& s : b.shapes) {
+      const int64_t small = s.small(), large = std::max(s.rows, s.cols);
+      const int64_t m = (small + p.side - 1) / p.side, n = (large + p.side - 1) / p.side;
+      for (int op = 0; op < 3; ++op) {
+        const double t = static_cast<double>(s.count * (op == kNsApply ? m * n : m * (m + 1) / 2));
+        const double depth = static_cast<double>(((op == kNsGram ? large : small) + 63) / 64 * (s.exact() ? 3 : 1));
+        tiles[op] += t;
+        work[op] += t * depth;
+        longest[op] = std::max(longest[op], depth);
+      }
+      symmetric += s.count * (m * (m + 1) / 2);
+      stages = std::max(stages, (large + 63) / 64 * (s.exact() ? 3 : 1));
+    }
+    if (2 * symmetric <= at_once && stages >= 48)
+      p.split = static_cast<int>(std::min<int64_t>({at_once / symmetric, stages / 8, 16}));
+    p.parts = symmetric * p.split;
+    double cost = 0.0;
+    for (int op = 0; op < 3; ++op) {
+      const double split = op == kNsGram ? p.split : 1;
+      const double rounds = std::ceil(split * tiles[op] / static_cast<double>(at_once));
+      cost += std::max(longest[op] / split, work[op] / split / tiles[op] * rounds);
+    }
+    if (p.split > 1) cost += 16.0;
+    if (pair == 0 || cost < least) best = p, least = cost;
+  }
+  return best;
+}
+
+int64_t bytes_of(const Batch& b) {
+  int64_t n = 128;  // (the first ones count CTAs)
+  for (const Shape& s : b.shapes) n += s.bytes();
+  const Plan p = plan_of(b);
+  if (p.split > 1) n += p.parts * p.side * p.side * 4;
+  return n + static_cast<int64_t>(b.order.size()) * kMuonPartials * 4;
+}
 constexpr int64_t kBatchElems = int64_t{1} << 28;  // more than this starts another batch
 
 // Calls each(batch) for the list's batches.
@@ -263,33 +310,6 @@ float adjusted(const MuonArgs& a, int64_t rows, int64_t cols) {
   return static_cast<float>(a.lr * f);
 }
 
-// The side of K14's tiles: 256 by a pair of CTAs, or 128, which share themselves out more evenly. A stage
-// takes either about as long (0.3 us): counted are those of the slowest CTA.
-int tile_side(const Batch& b) {
-  double cost[2];
-  for (int pair = 0; pair < 2; ++pair) {
-    const int64_t side = pair ? 256 : 128, at_once = pair ? 76 : 152;
-    double tiles[3] = {}, work[3] = {}, longest[3] = {};
-    for (const Shape& s : b.shapes) {
-      const int64_t small = s.small(), large = std::max(s.rows, s.cols);
-      const int64_t m = (small + side - 1) / side, n = (large + side - 1) / side;
-      for (int op = 0; op < 3; ++op) {
-        const double t = static_cast<double>(s.count * (op == kNsApply ? m * n : m * (m + 1) / 2));
-        const double depth = static_cast<double>(op == kNsGram ? large : small) * (s.exact() ? 3 : 1);
-        tiles[op] += t;
-        work[op] += t * depth;
-        longest[op] = std::max(longest[op], depth);
-      }
-    }
-    cost[pair] = 0.0;
-    for (int op = 0; op < 3; ++op) {
-      const double rounds = std::ceil(tiles[op] / static_cast<double>(at_once));
-      cost[pair] += std::max(longest[op], work[op] / tiles[op] * rounds);
-    }
-  }
-  return cost[1] < cost[0] ? 256 : 128;
-}
-
 cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a, uint8_t* workspace,
                       cudaStream_t s) {
   // ---- where things lie
@@ -329,6 +349,8 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
   t.x_kind = a.x_kind;
   t.factor = a.factor;
   t.partial = reinterpret_cast<float*>(at);
+  at += static_cast<int64_t>(b.order.size()) * kMuonPartials * 4;
+  float* parts = reinterpret_cast<float*>(at);  // of K14's split sums
   t.arrived = reinterpret_cast<uint32_t*>(workspace);
   t.first[0] = 0;
   // Rounds of a CTA: as few as 8 CTAs an SM leave (each adds up its matrix's partials in K13).
@@ -364,13 +386,16 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
 
   // ---- K14
   NsLaunch n{};
-  const int side = tile_side(b);
+  const Plan plan = plan_of(b);
+  const int side = plan.side;
+  n.join = plan.split > 1;
   n.steps = a.steps;
   n.shapes = static_cast<int32_t>(b.shapes.size());
   n.out_kind = a.out_kind;
   n.decay = a.decay;
   n.factor = a.factor;
   n.arrived = t.arrived;
+  n.partial = parts;
   for (int i = 0; i < 3 * a.steps; ++i) n.coefficients[i] = static_cast<float>(a.coefficients[i]);
   for (size_t i = 0; i < b.order.size(); ++i) n.result[i] = NsResult{list[b.order[i]].param, list[b.order[i]].out};
   for (size_t k = 0; k < b.shapes.size(); ++k) {
@@ -384,7 +409,11 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     g.side_tiles = static_cast<int32_t>((sh.small() + side - 1) / side);
     g.row_tiles = static_cast<int32_t>((sh.rows + side - 1) / side);
     g.col_tiles = static_cast<int32_t>((sh.cols + side - 1) / side);
-    g.first_tile[0] = n.tiles[0], g.first_tile[1] = n.tiles[1];
+    const int64_t stages = (std::max(sh.rows, sh.cols) + 63) / 64 * (sh.exact() ? 3 : 1);
+    g.split = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(plan.split, stages / 8)));
+    g.a_at = pl.a, g.a_low_at = pl.a_low, g.a_ld = static_cast<int32_t>(sh.small_ld()), g.a_apart = sh.a_elems();
+    for (int i = 0; i < 3; ++i) g.first_tile[i] = n.tiles[i];
+    n.tiles[2] += sh.count * g.side_tiles * (g.side_tiles + 1) / 2 * g.split;
     n.tiles[0] += sh.count * g.side_tiles * (g.side_tiles + 1) / 2;
     n.tiles[1] += sh.count * g.row_tiles * g.col_tiles;
     g.step = adjusted(a, sh.rows, sh.cols);
@@ -419,7 +448,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
 int64_t muon_workspace(const MuonMatrix* list, int count) {
   int64_t most = 0;
   batches(list, count, [&](const Batch& b) {
-    most = std::max(most, b.bytes());
+    most = std::max(most, bytes_of(b));
     return 0;
   });
   return most;

@@ -18,7 +18,8 @@
 //
 // That leaves 0.2e-3 .. 1.1e-3, and 1e-6 .. 3e-6 for the small ones (256 x 1024 noise 0.5e-3).
 //
-// A and B are symmetric: only tiles on and above the diagonal are computed, and stored twice.
+// A and B are symmetric: only tiles on and above the diagonal are computed, and stored twice. Where X is long
+// and A has few tiles, several CTAs share a tile's sum and another pass adds their parts.
 #include <atomic>
 
 #include "newton_schulz.cuh"
@@ -66,18 +67,27 @@ __device__ __forceinline__ void ns_wait_grid(const uint32_t* arrived, uint32_t e
 // (the asynchronous proxy).
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+// The kind of op `at_op` of a launch, the ops of a step being `per`: 3, or 4 with the join.
+__device__ __forceinline__ int ns_op(int at_op, int per) {
+  const int k = per == 3 ? at_op % 3 : at_op & 3;
+  return k == 0 ? kNsGram : k == per - 1 ? kNsApply : k == per - 2 ? kNsPoly : kNsJoin;
+}
+// Which of NsLaunch::tiles an op walks over.
+__device__ __forceinline__ int ns_kind(int op) { return op == kNsApply ? 1 : op == kNsGram ? 2 : 0; }
 struct NsTile {
   int shape, matrix, p, q;
+  int unit, part;  // (symmetric) the tile's number in its shape; the part of its sum (gram)
 };
 template <typename L>
-__device__ __forceinline__ NsTile ns_tile(const L& n, int op, int t) {
-  const int kind = op == kNsApply;
+__device__ __forceinline__ NsTile ns_tile(const L& n, bool join, int op, int t) {
+  const int kind = ns_kind(op);
   NsTile r;
   r.shape = 0;
   while (r.shape + 1 < n.shapes && n.shape[r.shape + 1].first_tile[kind] <= t) ++r.shape;
   const NsShape& g = n.shape[r.shape];
   int in = t - g.first_tile[kind];
-  if (kind) {
+  r.unit = r.part = 0;
+  if (kind == 1) {
     const int per = g.row_tiles * g.col_tiles;
     r.matrix = in / per;
     in -= r.matrix * per;
@@ -88,6 +98,12 @@ __device__ __forceinline__ NsTile ns_tile(const L& n, int op, int t) {
     r.q = in / height;
   } else {
     const int per = g.side_tiles * (g.side_tiles + 1) / 2;
+    if (join && kind == 2 && g.split > 1) {
+      const int whole = in / g.split;
+      r.part = in - whole * g.split;
+      in = whole;
+    }
+    r.unit = in;
     r.matrix = in / per;
     in -= r.matrix * per;
     r.p = 0;  // row by row of the upper triangle
@@ -98,6 +114,14 @@ __device__ __forceinline__ NsTile ns_tile(const L& n, int op, int t) {
 }
 __device__ __forceinline__ int ns_depth(const NsShape& g, int op) {
   return (op == kNsGram) == (g.wide != 0) ? g.cols : g.rows;  // gram: the longer side, else the shorter
+}
+// The stages of a tile's sum (of its part): first and behind the last, of ns_stages().
+__device__ __forceinline__ int ns_stages(const NsShape& g, int op) {
+  return (g.exact ? 3 : 1) * ((ns_depth(g, op) + kNsStep - 1) / kNsStep);
+}
+__device__ __forceinline__ int ns_stage(const NsShape& g, bool join, int op, int stages, int part) {
+  if (!join || op != kNsGram || g.split == 1) return part * stages;
+  return static_cast<int>(static_cast<int64_t>(stages) * part / g.split);
 }
 // Whether the operands' rows are steps of the sum.
 __device__ __forceinline__ bool ns_p_mn(const NsShape& g, int op) { return op == kNsGram && !g.wide; }
@@ -302,7 +326,51 @@ __device__ __forceinline__ void ns_result_ahead(const L& n, const NsShape& g, in
                  : "memory");
 }
 
+// The parts of the grams' sums, in their order, and what ns_symmetric makes of them: by every result warp, 32
+// rows and 4 columns at a time.
 template <int CTAS, typename L>
+__device__ __forceinline__ void ns_join(const L& n, int warp, int lane) {
+  constexpr int TILE = CTAS * kNsSide, ITEMS = (TILE / 4) * (TILE / 32);
+  const int total = n.tiles[0] * ITEMS;
+  for (int w = blockIdx.x * kResultWarps + warp; w < total; w += gridDim.x * kResultWarps) {
+    const int t = w / ITEMS, item = w - t * ITEMS;
+    const NsTile at = ns_tile(n, true, kNsPoly, t);
+    const NsShape& g = n.shape[at.shape];
+    if (g.split == 1) continue;
+    const int cg = item / (TILE / 32), row = item % (TILE / 32) * 32 + lane;
+    const int side = g.wide ? g.rows : g.cols, p = at.p * TILE + row, q = at.q * TILE + 4 * cg;
+    if (p >= side || q >= side) continue;
+    const int64_t unit = g.first_tile[2] + static_cast<int64_t>(at.unit) * g.split;
+    const float* from = n.partial + unit * TILE * TILE + (cg * TILE + row) * 4;
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < g.split; ++k) {
+      const uint4 v = ld_after_v4(from + static_cast<int64_t>(k) * TILE * TILE);
+      d[0] = __fadd_rn(d[0], __uint_as_float(v.x)), d[1] = __fadd_rn(d[1], __uint_as_float(v.y));
+      d[2] = __fadd_rn(d[2], __uint_as_float(v.z)), d[3] = __fadd_rn(d[3], __uint_as_float(v.w));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d[i] = __fmul_rn(d[i], 1.0f / (kXScale * kXScale));
+      if (p == q + i) g.a_diag[static_cast<int64_t>(at.matrix) * g.diag_apart + p] = d[i], d[i] = 0.0f;
+    }
+    const uint32_t h[2] = {pack2(d[0], d[1], F16()), pack2(d[2], d[3], F16())};
+    const float2 f0 = unpack2(h[0], F16()), f1 = unpack2(h[1], F16());
+    const uint32_t l[2] = {pack2(__fsub_rn(d[0], f0.x), __fsub_rn(d[1], f0.y), F16()),
+                           pack2(__fsub_rn(d[2], f1.x), __fsub_rn(d[3], f1.y), F16())};
+    const int64_t base = at.matrix * g.a_apart, to = base + static_cast<int64_t>(p) * g.a_ld + q;
+    st_v2(g.a_at + to, make_uint2(h[0], h[1]));
+    if (g.exact) st_v2(g.a_low_at + to, make_uint2(l[0], l[1]));
+    if (at.p != at.q) {  // (exact shapes have one tile)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (q + i < side)
+          g.a_at[base + static_cast<int64_t>(q + i) * g.a_ld + p] = static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
+// join: some shape's sums are split. (A kernel of its own: the others run 3 % slower with the code in it.)
+template <int CTAS, bool join, typename L>
 __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __grid_constant__ L n) {
   constexpr int TILE = CTAS * kNsSide, HALF = TILE / 2;  // columns of a warp
   extern __shared__ uint8_t raw[];
@@ -337,24 +405,31 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
   const int first = blockIdx.x / CTAS, apart = gridDim.x / CTAS;
-  const int ops = 3 * n.steps;
+  constexpr int per = join ? 4 : 3;
+  const int ops = per * n.steps;
   bool alive = true;
 
   if (warp == kCopyWarp && lane == 0) {  // ----------------------------------- copies into the stages
     Ring<kNsStages> r;
     int64_t issued = 0;
     for (int at_op = 0; at_op < ops && alive; ++at_op) {
-      const int op = at_op % 3, from = (at_op / 3) & 1, tiles = n.tiles[op == kNsApply];
+      const int op = ns_op(at_op, per), from = (at_op / per) & 1;
       ns_wait_grid(n.arrived, at_op * gridDim.x, alive);
       mbar_arrive(go);
+      if (op == kNsJoin) continue;
+      const int tiles = n.tiles[ns_kind(op)];
       proxy_fence();
       for (int t = first; t < tiles && alive; t += apart) {
-        const NsTile at = ns_tile(n, op, t);
+        const NsTile at = ns_tile(n, join, op, t);
         const NsShape& g = n.shape[at.shape];
         const int p0 = at.p * TILE + rank * kNsSide, q0 = at.q * TILE + rank * kNsSide;
         const bool p_mn = ns_p_mn(g, op), q_mn = ns_q_mn(g, op);
-        const int depth = ns_depth(g, op), parts = g.exact ? 3 : 1;
+        const int stages = ns_stages(g, op), of_part = g.exact ? stages / 3 : stages;
+        const int begin = ns_stage(g, join, op, stages, at.part), end = ns_stage(g, join, op, stages, at.part + 1);
+        const int parts = g.exact ? 3 : 1;
         for (int part = 0; part < parts && alive; ++part) {
+          // (the stages of this product that are this tile's)
+          const int from_k = max(begin - part * of_part, 0) * kNsStep, to_k = min(end - part * of_part, of_part) * kNsStep;
           const bool p_low = part == 2, q_low = part == 1;
           const CUtensorMap *p, *q;
           if (op == kNsGram) {
@@ -365,7 +440,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
             p = p_low ? &g.b_low : &g.b, q = q_low ? &g.xt_low[from] : &g.xt[from];
             if (!g.wide) p = p_low ? &g.xt_low[from] : &g.xt[from], q = q_low ? &g.b_low : &g.b;
           }
-          for (int k = 0; k < depth; k += kNsStep) {
+          for (int k = from_k; k < to_k; k += kNsStep) {
             tc_wait(&empty[r.at], r.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
             if (!alive) break;
             uint8_t* stage = smem + r.at * kNsStage;
@@ -390,15 +465,17 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
     Ring<kNsStages> r;
     Ring<kNsSlots> s;
     for (int at_op = 0; at_op < ops && alive; ++at_op) {
-      const int op = at_op % 3, tiles = n.tiles[op == kNsApply];
+      const int op = ns_op(at_op, per), tiles = op == kNsJoin ? 0 : n.tiles[ns_kind(op)];
       for (int t = first; t < tiles && alive; t += apart) {
-        const NsShape& g = n.shape[ns_tile(n, op, t).shape];
+        const NsTile tile = ns_tile(n, join, op, t);
+        const NsShape& g = n.shape[tile.shape];
         const bool p_mn = ns_p_mn(g, op), q_mn = ns_q_mn(g, op);
         const uint32_t instr = tc_instruction(TILE, TILE, 0, 0, p_mn, q_mn);
         const uint32_t base = smem_addr(smem), to = tmem + s.at * TILE;
         const uint64_t p_desc = ns_operand(base, p_mn), q_desc = ns_operand(base + kNsOperand, q_mn);
         const uint64_t p_step = p_mn ? 2048 >> 4 : 32 >> 4, q_step = q_mn ? 2048 >> 4 : 32 >> 4;
-        const int stages = (g.exact ? 3 : 1) * ((ns_depth(g, op) + kNsStep - 1) / kNsStep);
+        const int whole = ns_stages(g, op),
+                  stages = ns_stage(g, join, op, whole, tile.part + 1) - ns_stage(g, join, op, whole, tile.part);
         tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
         bool there = false;  // the stage has been seen already
         for (int k = 0; k < stages; ++k) {
@@ -443,7 +520,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
     unsigned held_phase = 0;
     Ring<kNsSlots> s;
     for (int at_op = 0; at_op < ops; ++at_op) {
-      const int op = at_op % 3, step = at_op / 3, from = step & 1, tiles = n.tiles[op == kNsApply];
+      const int op = ns_op(at_op, per), step = at_op / per, from = step & 1;
+      const int tiles = op == kNsJoin ? 0 : n.tiles[ns_kind(op)];
       const bool last = op == kNsApply && step == n.steps - 1;
       NsTask task;
       task.op = op;
@@ -452,9 +530,33 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
       task.c = held_in_register(n.coefficients[3 * step + 2]);
       tc_wait_long(go, at_op & 1, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
       if (leader) proxy_fence();
+      if (op == kNsJoin) ns_join<CTAS>(n, warp - kFirstResultWarp, lane);
       for (int t = first; t < tiles; t += apart) {
-        const NsTile at = ns_tile(n, op, t);
+        const NsTile at = ns_tile(n, join, op, t);
         const NsShape& g = n.shape[at.shape];
+        if (join && op == kNsGram && g.split > 1) {  // a part of a tile's sums, as they are
+          float* to = n.partial + static_cast<int64_t>(t) * TILE * TILE +
+                      (half * (HALF / 4) * TILE + rank * kNsSide + row) * 4;
+          tc_wait_long(&summed[s.at], s.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HALF; c += 32) {
+            uint32_t v[32];
+            tmem_ld(lanes + s.at * TILE + c, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st_v4(to + (c / 4 + i) * TILE * 4, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
+            else mbar_arrive(&taken[s.at]);
+          }
+          s.next();
+          continue;
+        }
         task.exact = held_in_register(g.exact);
         task.wide = held_in_register(g.wide);
         const int side = held_in_register(task.wide ? g.rows : g.cols);
@@ -599,9 +701,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
   }
 }
 
-template <int CTAS, typename L>
+template <int CTAS, bool join, typename L>
 static cudaError_t run_ns(const L& n, cudaStream_t s) {
-  auto kern = k_newton_schulz<CTAS, L>;
+  auto kern = k_newton_schulz<CTAS, join, L>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(152);
   cfg.blockDim = dim3(kTensorThreads);
@@ -628,20 +730,23 @@ static cudaError_t run_ns(const L& n, cudaStream_t s) {
     if (fit < 1) return cudaErrorCooperativeLaunchTooLarge;
     if (device < 64) known[device].store(fit, std::memory_order_release);
   }
-  const int tiles = n.tiles[0] > n.tiles[1] ? n.tiles[0] : n.tiles[1];
+  int tiles = n.tiles[1];
+  for (int i = 0; i < 3; ++i) tiles = n.tiles[i] > tiles ? n.tiles[i] : tiles;
   cfg.gridDim = dim3(static_cast<unsigned>((tiles < fit ? tiles : fit) * CTAS));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, n);
 }
 template <typename L>
 static cudaError_t run_ns(const L& n, int side, cudaStream_t s) {
-  return side == 256 ? run_ns<2>(n, s) : run_ns<1>(n, s);
+  if (n.join) return side == 256 ? run_ns<2, true>(n, s) : run_ns<1, true>(n, s);
+  return side == 256 ? run_ns<2, false>(n, s) : run_ns<1, false>(n, s);
 }
 cudaError_t launch_ns(const NsLaunch& n, int side, cudaStream_t s) {
   const NsShape& last = n.shape[n.shapes - 1];
   if (n.shapes > 2 || last.first_matrix + last.count > 32) return run_ns(n, side, s);
   NsLaunchFew few;  // (a launch's parameters are copied by the driver)
-  few.steps = n.steps, few.shapes = n.shapes, few.tiles[0] = n.tiles[0], few.tiles[1] = n.tiles[1];
+  few.steps = n.steps, few.shapes = n.shapes, few.join = n.join, few.partial = n.partial;
+  for (int i = 0; i < 3; ++i) few.tiles[i] = n.tiles[i];
   few.out_kind = n.out_kind, few.decay = n.decay, few.factor = n.factor, few.arrived = n.arrived;
   for (int i = 0; i < 3 * n.steps; ++i) few.coefficients[i] = n.coefficients[i];
   for (int i = 0; i < last.first_matrix + last.count; ++i) few.result[i] = n.result[i];

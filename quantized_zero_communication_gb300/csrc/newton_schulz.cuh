@@ -14,11 +14,12 @@ constexpr float kXScale = 1024.0f;
 // Matrices whose smaller side is at most this are worked on with products of both fp16.
 constexpr int kNsExactSide = 128;
 
-// The three products of a step, in their order.
+// The products of a step, in their order.
 enum NsOp : int32_t {
   kNsGram = 0,   // A = X X^T (or X^T X): the smaller of the two, symmetric
   kNsPoly = 1,   // B = b A + c A A, symmetric
   kNsApply = 2,  // X = a X + B X (or X B); of the last step the result
+  kNsJoin = 3,   // after a gram whose sums were split: the parts added up
 };
 constexpr int kNsMaxSteps = 100;
 
@@ -29,13 +30,17 @@ struct NsShape {
   CUtensorMap xt[2], xt_low[2];  // X as the apply reads it: the other way round
   CUtensorMap a, a_low, b, b_low;
   CUtensorMap a_turned, b_turned;  // for a tile's transposed place: boxes of 64 rows
+  uint16_t *a_at, *a_low_at;     // as a_ld and a_apart: for the join
   float *a_diag, *b_diag;        // fp32; the fp16 matrices hold zeros there
   int32_t rows, cols, diag_apart;
   int32_t wide, exact;           // rows <= cols; products of both parts
   int32_t count, first_matrix;   // in the batch
   int32_t side_tiles;            // of A's side
   int32_t row_tiles, col_tiles;  // of X
-  int32_t first_tile[2];         // of the shape, in a symmetric op and in the apply
+  int32_t split;                 // parts of a gram's sum
+  int32_t a_ld;
+  int64_t a_apart;
+  int32_t first_tile[3];         // of the shape: in the poly, in the apply, and parts of tiles in the gram
   float step;                    // Muon: the learning rate of the shape
 };
 struct NsResult {  // where a matrix's result goes
@@ -45,7 +50,9 @@ struct NsResult {  // where a matrix's result goes
 // A launch: all steps of a batch, the GPU's CTAs waiting for each other between two products.
 template <int SHAPES, int MATRICES>
 struct NsLaunchOf {
-  int32_t steps, shapes, tiles[2];  // of a symmetric op and of the apply
+  int32_t steps, shapes, tiles[3];  // of the poly, of the apply, and parts of tiles of the gram
+  int32_t join;                     // some shape's sums are split
+  float* partial;                   // [parts of tiles][columns / 4][rows][4], where they are
   int32_t out_kind;
   float decay;
   const float* factor;

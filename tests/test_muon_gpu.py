@@ -146,6 +146,20 @@ def test_large_matrices():
         assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("rows,cols", [(100, 6000), (9000, 40), (300, 20000), (7000, 200), (1, 40000), (700, 9000)])
+def test_long_matrices(rows, cols):
+    """Few tiles of long sums: shared between CTAs and joined."""
+    x = matrix(rows, cols, rows, "strong")
+    got = zpp.orthogonalize(x, dtype=torch.float16)
+    check(got, x)
+    assert torch.equal(got, zpp.orthogonalize(x, dtype=torch.float16))
+    check_one(zpp.orthogonalize(x, 1, dtype=torch.float16), x, USUAL)
+    short = [matrix(20, 30, i) for i in range(3)]  # beside short ones
+    for y, z in zip(zpp.orthogonalize([short[0], x, *short[1:]], dtype=torch.float16), (short[0], x, *short[1:])):
+        check(y, z)
+    assert zpp.zpp_device_fault() == 0
+
+
 def test_lists_of_many_shapes_and_places():
     """More shapes and matrices than one batch holds; views that start anywhere."""
     shapes = [(1 + i % 23, 3 + i % 19) for i in range(300)]
