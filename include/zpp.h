@@ -466,7 +466,8 @@ ZPP_API zpp_status zpp_quant_fp8(const void* x, zpp_dtype x_dt, int64_t x_stride
 /*
  * y = a b^T (+ bias): y[m][n] = sum_k a[m][k] b[n][k] (+ bias[n]) of the values that the codes stand
  * for. Sums are fp32: of the codes within a block of 128, then of the blocks times both scales, in
- * ascending order; y is rounded once. NaN codes and non-finite scales give what such values give.
+ * ascending order; y is rounded once. The product of two scales may be rounded to fp32 first. NaN codes
+ * and non-finite scales give what such values give.
  *   a, b : HOST structs, read during the call; cols is the same in both. One may be the other
  *   bias : NULL or [b.rows] of y_dt
  *   y    : out, [a.rows][b.rows] of y_dt (any zpp_dtype), row m at y + m * y_stride elements,
@@ -488,8 +489,8 @@ ZPP_API zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix*
  * fp16 operands with fp32 sums, the diagonals of A and B apart in fp32, and X with what fp16 loses of it
  * in 16 further bits; a matrix with a side of at most 128 takes products of both parts. After the usual
  * five steps some 1e-3 of the result's norm is error, 1e-5 for those small ones, hence the 16-bit
- * types of a result. The largest singular value has to stay below 32 through the steps. |x| beyond
- * fp32's range (of its squares) gives NaN.
+ * types of a result. Singular values have to stay below 8 through the steps and coefficients below 15
+ * (the usual ones keep to 1.3). |x| beyond fp32's range (of its squares) gives NaN.
  */
 typedef struct zpp_newton_schulz {
   const double* coefficients; /* HOST [steps][3], finite */

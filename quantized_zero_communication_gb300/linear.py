@@ -20,7 +20,7 @@ def linear_fp8(x, weight, quantized=None):
         raise ValueError("linear_fp8: x and weight are tensors")
     if x.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"x: dtype {x.dtype}, expected float16 or bfloat16")
-    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1] or not weight.shape[1]:
         raise ValueError(f"weight: {tuple(weight.shape)} does not fit x {tuple(x.shape)}")
     grads = torch.is_grad_enabled() and x.requires_grad
     if quantized is not None:

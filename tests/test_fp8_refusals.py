@@ -124,6 +124,7 @@ def test_linear_wrapper_checks():
     raises("x: dtype", lambda: zpp.linear_fp8(z((4, 256)), w))
     raises("does not fit x", lambda: zpp.linear_fp8(x, z((200, 255), BF16)))
     raises("does not fit x", lambda: zpp.linear_fp8(x, z(256, BF16)))
+    raises("does not fit x", lambda: zpp.linear_fp8(z((4, 0), BF16), z((200, 0), BF16)))
     raises("tensors", lambda: zpp.linear_fp8(x, None))
     raises("quantized", lambda: zpp.linear_fp8(x, w, quantized=(w,)))
     raises("do not fit weight", lambda: zpp.linear_fp8(x, w, quantized=(x, x)))
