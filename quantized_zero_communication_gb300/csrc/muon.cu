@@ -209,13 +209,21 @@ struct Batch {
   int64_t elems = 0;
 };
 // How K14 takes a batch: the side of its tiles, 256 by a pair of CTAs, or 128, which share themselves out more
-// evenly; and into how many parts a gram's sum is split where its tiles leave most CTAs without work
-// (worth the pass that joins them, 5 us, from 48 stages on: 100 x 6000 in five steps 460 us without).
+// evenly; and into how many parts a gram's sum is split. Once where its tiles leave most CTAs without work
+// (worth the pass that joins them, 5 us, from 48 stages on: 100 x 6000 in five steps 460 us without), and
+// always after 512 stages: the matrix unit cuts its running sum in each of a stage's four steps, so a sum of
+// squares falls short by some 2^-25 of itself a step (4 million rows: the result 0.25 % off).
 // A stage takes either side about as long (0.3 us): counted are those of the slowest CTA.
 struct Plan {
-  int side = 128, split = 1;
+  int side = 128, share = 1;
   int64_t parts = 0;  // of tiles, in the gram
+  bool join = false;
 };
+int64_t stages_of(const Shape& s) { return (std::max(s.rows, s.cols) + 63) / 64 * (s.exact() ? 3 : 1); }
+int64_t split_of(const Shape& s, const Plan& p) {
+  const int64_t n = stages_of(s);
+  return std::max((n + 511) / 512, std::min<int64_t>(p.share, n / 8));
+}
 Plan plan_of(const Batch& b) {
   Plan best;
   double least = 0.0;
@@ -236,18 +244,22 @@ Plan plan_of(const Batch& b) {
         longest[op] = std::max(longest[op], depth);
       }
       symmetric += s.count * (m * (m + 1) / 2);
-      stages = std::max(stages, (large + 63) / 64 * (s.exact() ? 3 : 1));
+      stages = std::max(stages, stages_of(s));
     }
     if (2 * symmetric <= at_once && stages >= 48)
-      p.split = static_cast<int>(std::min<int64_t>({at_once / symmetric, stages / 8, 16}));
-    p.parts = symmetric * p.split;
+      p.share = static_cast<int>(std::min<int64_t>({at_once / symmetric, stages / 8, 16}));
+    for (const Shape& s : b.shapes) {
+      const int64_t m = (s.small() + p.side - 1) / p.side, split = split_of(s, p);
+      p.parts += s.count * (m * (m + 1) / 2) * split;
+      p.join |= split > 1;
+    }
     double cost = 0.0;
     for (int op = 0; op < 3; ++op) {
-      const double split = op == kNsGram ? p.split : 1;
+      const double split = op == kNsGram ? p.share : 1;
       const double rounds = std::ceil(split * tiles[op] / static_cast<double>(at_once));
       cost += std::max(longest[op] / split, work[op] / split / tiles[op] * rounds);
     }
-    if (p.split > 1) cost += 16.0;
+    if (p.join) cost += 16.0;
     if (pair == 0 || cost < least) best = p, least = cost;
   }
   return best;
@@ -257,7 +269,7 @@ int64_t bytes_of(const Batch& b) {
   int64_t n = 128;  // (the first ones count CTAs)
   for (const Shape& s : b.shapes) n += s.bytes();
   const Plan p = plan_of(b);
-  if (p.split > 1) n += p.parts * p.side * p.side * 4;
+  if (p.join) n += p.parts * p.side * p.side * 4;
   return n + static_cast<int64_t>(b.order.size()) * kMuonPartials * 4;
 }
 constexpr int64_t kBatchElems = int64_t{1} << 28;  // more than this starts another batch
@@ -388,7 +400,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
   NsLaunch n{};
   const Plan plan = plan_of(b);
   const int side = plan.side;
-  n.join = plan.split > 1;
+  n.join = plan.join;
   n.steps = a.steps;
   n.shapes = static_cast<int32_t>(b.shapes.size());
   n.out_kind = a.out_kind;
@@ -409,8 +421,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     g.side_tiles = static_cast<int32_t>((sh.small() + side - 1) / side);
     g.row_tiles = static_cast<int32_t>((sh.rows + side - 1) / side);
     g.col_tiles = static_cast<int32_t>((sh.cols + side - 1) / side);
-    const int64_t stages = (std::max(sh.rows, sh.cols) + 63) / 64 * (sh.exact() ? 3 : 1);
-    g.split = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(plan.split, stages / 8)));
+    g.split = static_cast<int32_t>(split_of(sh, plan));
     g.a_at = pl.a, g.a_low_at = pl.a_low, g.a_ld = static_cast<int32_t>(sh.small_ld()), g.a_apart = sh.a_elems();
     for (int i = 0; i < 3; ++i) g.first_tile[i] = n.tiles[i];
     n.tiles[2] += sh.count * g.side_tiles * (g.side_tiles + 1) / 2 * g.split;
