@@ -18,6 +18,13 @@
 //
 // That leaves 0.2e-3 .. 1.1e-3, and 1e-6 .. 3e-6 for the small ones (256 x 1024 noise 0.5e-3).
 //
+// Tiles of 128 x 128, or of 256 x 256 by a pair of CTAs, a stage 64 steps of the sum (5 stages of 32 KB), the sums
+// of two tiles in tensor memory, so that one is taken while the next is made. Large matrices are bound
+// by the matrix unit at the clock that the power limit leaves (8192 x 8192: 6.9 ms, 1.59 PFLOP/s of the
+// products that count, 0.92 of the sustained rate); sides of 1024 by what a CTA can take in (64 bytes a clock:
+// 10,000 of a tile's 13,000 clocks); small ones by the way from one product to the next (256 x 1024: 15 of them
+// 118 us, 2.5 of each between two and 1 to the first copy).
+//
 // A and B are symmetric: only tiles on and above the diagonal are computed, and stored twice. Where X is long
 // and A has few tiles, several CTAs share a tile's sum and another pass adds their parts.
 #include <atomic>
@@ -412,15 +419,28 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
   if (warp == kCopyWarp && lane == 0) {  // ----------------------------------- copies into the stages
     Ring<kNsStages> r;
     int64_t issued = 0;
+    // The descriptors of a few shapes, at hand from the start (a first use waits for its own).
+    for (int k = 0; k < n.shapes && k < 2; ++k) {
+      const NsShape& g = n.shape[k];
+      for (int i = 0; i < 2; ++i) {
+        tma_prefetch(&g.x[i]);
+        tma_prefetch(&g.xt[i]);
+        if (g.exact || g.wide) tma_prefetch(&g.x_low[i]);
+        if (g.exact || !g.wide) tma_prefetch(&g.xt_low[i]);
+      }
+      tma_prefetch(&g.a);
+      tma_prefetch(&g.b);
+    }
     for (int at_op = 0; at_op < ops && alive; ++at_op) {
       const int op = ns_op(at_op, per), from = (at_op / per) & 1;
+      const int tiles = op == kNsJoin ? 0 : held_in_register(n.tiles[ns_kind(op)]);
+      NsTile next{};  // (looked up before the wait)
+      if (first < tiles) next = ns_tile(n, join, op, first);
       ns_wait_grid(n.arrived, at_op * gridDim.x, alive);
       mbar_arrive(go);
-      if (op == kNsJoin) continue;
-      const int tiles = n.tiles[ns_kind(op)];
       proxy_fence();
       for (int t = first; t < tiles && alive; t += apart) {
-        const NsTile at = ns_tile(n, join, op, t);
+        const NsTile at = t == first ? next : ns_tile(n, join, op, t);
         const NsShape& g = n.shape[at.shape];
         const int p0 = at.p * TILE + rank * kNsSide, q0 = at.q * TILE + rank * kNsSide;
         const bool p_mn = ns_p_mn(g, op), q_mn = ns_q_mn(g, op);
