@@ -7,6 +7,9 @@
 // quotient. A block is 128 columns of one row, or a tile of 128 x 128. amax is over finite values; an
 // infinite or NaN value has the code NaN.
 //
+// Bound by DRAM for tiles (24576 x 8192 fp32, both ways: 184 us, 6.55 TB/s), by issue where rows and columns
+// have scales of their own (16384 x 8192 bf16, both ways: 97 us, 5.6 TB/s; rows alone 61 us, 6.6 TB/s).
+//
 // One CTA per tile of 128 x 128; a thread holds 4 consecutive rows of 16 columns, which it reads
 // once. The transposed codes go through shared memory in words of 4 rows, their places permuted so
 // that neither side meets a bank twice.
@@ -16,7 +19,8 @@
 namespace zpp {
 
 constexpr int kQuantTile = 128;
-constexpr int kAheadTiles = 304;  // 2 tiles for each SM
+// Tiles that are brought into L2 ahead: 2 for each SM (24576 x 8192 fp32: 184 us; 4 for each 189, 6 223, none 245).
+constexpr int kAheadTiles = 304;
 
 struct QuantFp8Run {
   const void* x;
