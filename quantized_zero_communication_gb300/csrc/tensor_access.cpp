@@ -512,6 +512,17 @@ at::Tensor product(MatmulFp8 fn, const at::Tensor& a, const at::Tensor& a_scales
          "zpp_matmul_fp8");
   return y;
 }
+// A captured backward pass cannot hand a gradient to the default stream, which takes no part in captures. It
+// would have to where the tensor's place in the graph was made there and is still held, by an eager
+// pass of the same leaf for one; the engine's own failure at that point ends the process.
+void demand_stream(torch::autograd::Node& of, size_t edge, const char* name) {
+  const auto& to = of.next_edge(edge).function;
+  const auto stream = to ? to->stream() : std::nullopt;
+  TORCH_CHECK(!stream || c10::cuda::CUDAStream(*stream) != c10::cuda::getDefaultCUDAStream(stream->device_index()),
+              "linear_fp8: this backward pass is captured, and ", name,
+              "'s gradient would go to the default stream, where a graph that is still alive was made; "
+              "drop that graph's outputs first, or make it on another stream");
+}
 struct Linear : torch::autograd::Function<Linear> {
   // held: the weight's codes, scales and those of its transpose, or none. (By pointer: a list of tensors
   // would count as inputs with gradients of their own.)
@@ -558,21 +569,27 @@ struct Linear : torch::autograd::Function<Linear> {
     torch::autograd::variable_list out(7);
     if (!grads[0].defined()) return out;
     const bool twice = at::GradMode::is_enabled();
+    const bool for_x = types[2] && ctx->needs_input_grad(0), for_w = types[3] && ctx->needs_input_grad(1);
     {
       const at::NoGradGuard no_grad;
       const at::Tensor& dy = grads[0];
       const c10::cuda::CUDAGuard guard(dy.device());
+      if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+        const auto node = torch::autograd::get_current_node();
+        if (for_x) demand_stream(*node, 0, "x");
+        if (for_w) demand_stream(*node, 1, "weight");
+      }
       const int64_t n = dy.size(-1), k = shape.back();
       int64_t count = 1;
       for (size_t i = 0; i + 1 < shape.size(); ++i) count *= shape[i];
       const bool empty = count == 0 || n == 0;
       Coded q, qt;
       if (!empty)
-        demand(quantise(quant_fn, dy.reshape({count, n}).contiguous(), 1, q, types[3] ? &qt : nullptr), "zpp_quant_fp8");
-      if (types[2])
+        demand(quantise(quant_fn, dy.reshape({count, n}).contiguous(), 1, q, for_w ? &qt : nullptr), "zpp_quant_fp8");
+      if (for_x)
         out[0] = empty ? at::zeros(shape, dy.options().dtype(x_type))
                        : product(matmul_fn, q.codes, q.scales, 1, saved[0], saved[1], 128, x_type).view(shape);
-      if (types[3])
+      if (for_w)
         out[1] = empty ? at::zeros({n, k}, dy.options().dtype(w_type))
                        : product(matmul_fn, qt.codes, qt.scales, 1, saved[2], saved[3], 1, w_type);
     }

@@ -13,6 +13,7 @@ def linear_fp8(x, weight, quantized=None):
 
     Differentiable once: with dy rounded like x (along N for dx, along the rows for dweight),
     dx = dy weight in x's dtype and dweight = dy^T x in weight's. A bias is added by the caller.
+    A captured backward pass raises while a graph made on the default stream holds x or weight.
 
     quantized: quant_fp8(weight, 128, transposed=True), for a weight that several passes use (micro-
     batches, or answers: there without the transpose). It has to be that of the weight as it is."""

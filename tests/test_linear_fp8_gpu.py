@@ -2,6 +2,8 @@
 codes stand for, and its gradient against differences of the quantised layer's own function.
 
 A product's result is within (20 + K / 128) u S + half an ulp of its type (see test_fp8_gpu.py)."""
+import gc
+
 import pytest
 import torch
 
@@ -116,6 +118,45 @@ def test_training_pass_in_a_graph():
         dy.mul_(4.0)
     graph.replay()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], 4 * want[1]) and torch.equal(got[2], 4 * want[2])
+
+
+def test_captured_backward_beside_an_eager_graph_raises():
+    g = gen(4)
+    x = torch.randn(64, 256, generator=g, device=DEV).bfloat16()
+    w = torch.randn(96, 256, generator=g, device=DEV).requires_grad_()
+    dy = torch.randn(64, 96, generator=g, device=DEV).bfloat16()
+    eager = zpp.linear_fp8(x, w)
+    want, = torch.autograd.grad(eager, w, dy, retain_graph=True)
+
+    def capture():
+        graph, got = torch.cuda.CUDAGraph(), None
+        try:
+            with torch.cuda.graph(graph):
+                got, = torch.autograd.grad(zpp.linear_fp8(x, w), w, dy)
+        except RuntimeError as e:
+            return str(e), None
+        return graph, got
+
+    said, _ = capture()
+    assert isinstance(said, str) and "weight's gradient would go to the default stream" in said
+    del eager
+    gc.collect()
+    graph, got = capture()
+    graph.replay()
+    assert torch.equal(got, want)
+
+
+def test_only_gradients_that_are_asked_for():
+    g = gen(5)
+    x = torch.randn(40, 200, generator=g, device=DEV).bfloat16().requires_grad_()
+    w = torch.randn(72, 200, generator=g, device=DEV).requires_grad_()
+    y = zpp.linear_fp8(x, w)
+    dx, dw = torch.autograd.grad(y, (x, w), torch.ones_like(y), retain_graph=True)
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    one, = torch.autograd.grad(y, x, torch.ones_like(y), retain_graph=True)
+    assert torch.equal(one, dx) and torch.cuda.max_memory_allocated() - held < 72 * 200 * 4
+    assert torch.equal(torch.autograd.grad(y, w, torch.ones_like(y))[0], dw)
 
 
 def test_second_derivative_raises():
