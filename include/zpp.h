@@ -485,11 +485,10 @@ ZPP_API zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix*
  * Newton-Schulz steps on a matrix x: X = x / max(|x|, eps), |x| the root of the sum of squares, then
  * for each step k with (a, b, c) = coefficients[k]:
  *   A = X X^T,  B = b A + c A A,  X = a X + B X
- * (for a matrix with more rows than columns the same of its transpose). The products are those of
- * fp16 operands with fp32 sums, the diagonals of A and B apart in fp32, and X with what fp16 loses of it
- * in 16 further bits; a matrix with a side of at most 128 takes products of both parts. After the usual
- * five steps some 1e-3 of the result's norm is error, 1e-5 for those small ones, hence the 16-bit
- * types of a result. Singular values have to stay below 8 through the steps and coefficients below 15
+ * (for a matrix with more rows than columns the same of its transpose). Every value is held in two fp16
+ * (the second one what the first lost), sums and the diagonals of A and B in fp32. After the usual five
+ * steps some 3e-6 of the result's norm is error, a few 1e-5 where the longer side is beyond 10,000.
+ * Singular values have to stay below 8 through the steps and coefficients below 15
  * (the usual ones keep to 1.3). |x| beyond fp32's range (of its squares) gives NaN.
  */
 typedef struct zpp_newton_schulz {

@@ -197,11 +197,8 @@ struct Shape {
   int64_t a_elems() const { return (small() * small_ld() + 63) / 64 * 64; }
   int64_t diag_elems() const { return (small() + 63) / 64 * 64; }  // fp32
   bool wide() const { return rows <= cols; }
-  bool exact() const { return small() <= kNsExactSide; }
-  // X twice and what it lost, A and B with their diagonals; what each lost too, and X's twice
-  int64_t bytes() const {
-    return count * ((exact() ? 4 : 3) * x_elems() * 2 + (exact() ? 4 : 2) * a_elems() * 2 + 2 * diag_elems() * 4);
-  }
+  // X twice, A and B, each in two fp16, and the diagonals
+  int64_t bytes() const { return count * (4 * x_elems() * 2 + 4 * a_elems() * 2 + 2 * diag_elems() * 4); }
 };
 
 // Matrices that are worked on together, in the order of their shapes.
@@ -213,18 +210,19 @@ struct Batch {
 // How K14 takes a batch: the side of its tiles, 256 by a pair of CTAs, or 128, which share themselves out more
 // evenly; and into how many parts a gram's sum is split. Once where its tiles leave most CTAs without work
 // (worth the pass that joins them, 5 us, from 48 stages on: 100 x 6000 in five steps 460 us without), and
-// always after 512 stages: the matrix unit cuts its running sum in each of a stage's four steps, so a sum of
-// squares falls short by some 2^-25 of itself a step (4 million rows: the result 0.25 % off).
+// always after 512 stages of a product: the matrix unit cuts its running sum in each of a stage's four steps, so
+// a sum of squares falls short by some 2^-26 of itself a step (4 million rows: the result 0.25 % off).
 // A stage takes either side about as long (0.3 us): counted are those of the slowest CTA.
 struct Plan {
   int side = 128, share = 1;
   int64_t parts = 0;  // of tiles, in the gram
   bool join = false;
 };
-int64_t stages_of(const Shape& s) { return (std::max(s.rows, s.cols) + 63) / 64 * (s.exact() ? 3 : 1); }
+// Stages of the three products together.
+int64_t stages_of(int64_t depth) { return 3 * ((depth + 63) / 64); }
 int64_t split_of(const Shape& s, const Plan& p) {
-  const int64_t n = stages_of(s);
-  return std::max((n + 511) / 512, std::min<int64_t>(p.share, n / 8));
+  const int64_t n = stages_of(std::max(s.rows, s.cols));
+  return std::max((n + 1535) / 1536, std::min<int64_t>(p.share, n / 8));
 }
 Plan plan_of(const Batch& b) {
   Plan best;
@@ -240,13 +238,13 @@ Plan plan_of(const Batch& b) {
       const int64_t m = (small + p.side - 1) / p.side, n = (large + p.side - 1) / p.side;
       for (int op = 0; op < 3; ++op) {
         const double t = static_cast<double>(s.count * (op == kNsApply ? m * n : m * (m + 1) / 2));
-        const double depth = static_cast<double>(((op == kNsGram ? large : small) + 63) / 64 * (s.exact() ? 3 : 1));
+        const double depth = static_cast<double>(stages_of(op == kNsGram ? large : small));
         tiles[op] += t;
         work[op] += t * depth;
         longest[op] = std::max(longest[op], depth);
       }
       symmetric += s.count * (m * (m + 1) / 2);
-      stages = std::max(stages, stages_of(s));
+      stages = std::max(stages, stages_of(large));
     }
     if (2 * symmetric <= at_once && stages >= 48)
       p.share = static_cast<int>(std::min<int64_t>({at_once / symmetric, stages / 8, 16}));
@@ -344,12 +342,12 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     Place& p = place[k];
     for (int i = 0; i < 2; ++i) {
       p.x[i] = half(sh.x_elems());
-      p.x_low[i] = i == 0 || sh.exact() ? half(sh.x_elems()) : p.x_low[0];
+      p.x_low[i] = half(sh.x_elems());
     }
     p.a = half(sh.a_elems());
     p.b = half(sh.a_elems());
-    p.a_low = sh.exact() ? half(sh.a_elems()) : nullptr;
-    p.b_low = sh.exact() ? half(sh.a_elems()) : nullptr;
+    p.a_low = half(sh.a_elems());
+    p.b_low = half(sh.a_elems());
     p.a_diag = reinterpret_cast<float*>(take(sh.diag_elems(), 4));
     p.b_diag = reinterpret_cast<float*>(take(sh.diag_elems(), 4));
   }
@@ -418,7 +416,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     NsShape& g = n.shape[k];
     g.rows = static_cast<int32_t>(sh.rows), g.cols = static_cast<int32_t>(sh.cols);
     g.diag_apart = static_cast<int32_t>(sh.diag_elems());
-    g.wide = sh.wide(), g.exact = sh.exact();
+    g.wide = sh.wide();
     g.count = sh.count, g.first_matrix = sh.first;
     g.side_tiles = static_cast<int32_t>((sh.small() + side - 1) / side);
     g.row_tiles = static_cast<int32_t>((sh.rows + side - 1) / side);
@@ -440,18 +438,17 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
     for (int i = 0; i < 2; ++i) {
       map(pl.x[i], true, !sh.wide(), &g.x[i]);
       map(pl.x[i], true, sh.wide(), &g.xt[i]);
-      // (what X lost is an operand of exact shapes only; the apply reads and writes it across)
-      if (sh.exact() || sh.wide()) map(pl.x_low[i], true, !sh.wide(), &g.x_low[i]);
-      if (sh.exact() || !sh.wide()) map(pl.x_low[i], true, sh.wide(), &g.xt_low[i]);
+      map(pl.x_low[i], true, !sh.wide(), &g.x_low[i]);
+      map(pl.x_low[i], true, sh.wide(), &g.xt_low[i]);
     }
     map(pl.a, false, false, &g.a);
     map(pl.b, false, false, &g.b);
     map(pl.a, false, true, &g.a_turned);
     map(pl.b, false, true, &g.b_turned);
-    if (sh.exact()) {
-      map(pl.a_low, false, false, &g.a_low);
-      map(pl.b_low, false, false, &g.b_low);
-    }
+    map(pl.a_low, false, false, &g.a_low);
+    map(pl.b_low, false, false, &g.b_low);
+    map(pl.a_low, false, true, &g.a_turned_low);
+    map(pl.b_low, false, true, &g.b_turned_low);
   }
   return e != cudaSuccess ? e : launch_ns(n, side, s);
 }

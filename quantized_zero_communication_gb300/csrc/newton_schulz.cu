@@ -3,29 +3,28 @@
 //   A = X X^T,  B = b A + c A A,  X = a X + B X          (X with fewer rows than columns; else A = X^T X
 //                                                          and X = a X + X B)
 //
-// Operands are fp16, sums fp32 in tensor memory. What the steps lose early they multiply by up to 3.4^5,
-// so plain 16-bit operands are poor: bf16 leaves 1.1e-2 of the result's norm in error on normal values
-// of 512 x 1024, fp16 1.3e-3, and 4.6e-2 and 6.8e-3 where singular values lie over four decades. Hence:
+// Sums are fp32 in tensor memory, operands fp16, each value in two of them: the nearest one and the one nearest
+// to what that lost. A product takes three of the unit's: first by first part, first by second, second by first.
+// What the steps lose early they multiply by up to 3.4^5, so one 16-bit part is poor: bf16 leaves 1.1e-2 of the
+// result's norm in error on normal values of 512 x 1024, fp16 1.3e-3, and 4.6e-2 and 6.8e-3 where singular values lie
+// over four decades. One part with the diagonals apart, as below, leaves 0.2e-3 .. 1.1e-3 in 1/2.7 of the time,
+// several times the rounding of an fp16 result; two leave 1e-6 .. 3e-6, as fp32 operands do.
 //
-//  - What fp16 loses of X is kept in a second fp16 and enters a X. (B hardly reaches the directions that
-//    grow most, so B X does with the first.)
-//  - The diagonals of A and B are kept in fp32 and enter elementwise:
-//      A = A' + D,  A A = A' A' + D A' + A' D + D D,  B X = B' X + E X
-//    A' and B' are small beside them, and so is what their rounding and X's leaves. In E X, X counts
-//    with both parts; with the first alone while three steps or more follow, where B X of a direction
-//    that is still to grow has to cancel.
-//  - Matrices with a side of up to 128 take all products of both parts but the smallest.
+// The diagonals of A and B are kept in fp32 and enter elementwise:
+//   A = A' + D,  A A = A' A' + D A' + A' D + D D,  B X = B' X + E X
+// A' and B' are small beside them, and so is what their rounding and X's leaves.
 //
-// That leaves 0.2e-3 .. 1.1e-3, and 1e-6 .. 3e-6 for the small ones (256 x 1024 noise 0.5e-3).
+// The two products with a second part come first in a sum: the matrix unit cuts the running sum to fp32 in each of
+// its steps, and what is cut is in proportion to it.
 //
-// Tiles of 128 x 128, or of 256 x 256 by a pair of CTAs, a stage 64 steps of the sum (5 stages of 32 KB), the sums
+// Tiles of 128 x 128, or of 256 x 256 by a pair of CTAs, a stage 64 steps of a product (5 stages of 32 KB), the sums
 // of two tiles in tensor memory, so that one is taken while the next is made. Large matrices are bound
-// by the matrix unit at the clock that the power limit leaves (8192 x 8192: 6.9 ms, 1.59 PFLOP/s of the
-// products that count, 0.92 of the sustained rate); sides of 1024 by what a CTA can take in (64 bytes a clock:
-// 10,000 of a tile's 13,000 clocks); small ones by the way from one product to the next (256 x 1024: 15 of them
-// 118 us, 2.5 of each between two and 1 to the first copy).
+// by the matrix unit at the clock that the power limit leaves (4096 x 16384: 8.8 ms, 1.5 PFLOP/s of the three
+// products); sides of 1024 by what a CTA can take in (64 bytes a clock); small ones by the way from one product to
+// the next (256 x 1024: 15 of them 193 us).
 //
-// A and B are symmetric: only tiles on and above the diagonal are computed, and stored twice. Where X is long
+// A and B are symmetric: only tiles on and above the diagonal are computed, and stored twice (the second time
+// turned in shared memory, where the tile lies). Where X is long
 // and A has few tiles, several CTAs share a tile's sum and another pass adds their parts.
 #include <atomic>
 
@@ -42,6 +41,7 @@ constexpr int kNsSide = 128, kNsStep = 64;  // rows of an operand in a CTA, step
 constexpr int kNsOperand = kNsSide * kNsStep * 2;
 constexpr int kNsStage = 2 * kNsOperand;
 constexpr int kNsStages = 5;
+constexpr int kNsProducts = 3;  // of two factors in two fp16 each: all but that of what both lost
 // Results go through shared memory: 128 rows of 64 columns at a time, of each half of the tile's columns,
 // as 16-bit values and what those lost, laid out as a tensor copy lays them.
 constexpr int kNsChunk = 64, kNsHalfChunk = kNsSide * kNsChunk * 2;
@@ -122,9 +122,9 @@ __device__ __forceinline__ NsTile ns_tile(const L& n, bool join, int op, int t) 
 __device__ __forceinline__ int ns_depth(const NsShape& g, int op) {
   return (op == kNsGram) == (g.wide != 0) ? g.cols : g.rows;  // gram: the longer side, else the shorter
 }
-// The stages of a tile's sum (of its part): first and behind the last, of ns_stages().
+// The stages that a tile's sum has in each of the three products; the first of a part of it.
 __device__ __forceinline__ int ns_stages(const NsShape& g, int op) {
-  return (g.exact ? 3 : 1) * ((ns_depth(g, op) + kNsStep - 1) / kNsStep);
+  return (ns_depth(g, op) + kNsStep - 1) / kNsStep;
 }
 __device__ __forceinline__ int ns_stage(const NsShape& g, bool join, int op, int stages, int part) {
   if (!join || op != kNsGram || g.split == 1) return part * stages;
@@ -184,7 +184,7 @@ __device__ __forceinline__ T held_in_register(T v) {
   return v;
 }
 struct NsTask {
-  int op, exact, wide, early;
+  int op, wide;
   int diagonal;     // a symmetric tile on it; the others go to their transposed place too
   float* diag_out;
   float a, b, c;
@@ -205,15 +205,12 @@ __device__ __forceinline__ void ns_symmetric(const NsTask& g, int p, int q, floa
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] = __fmul_rn(d[i], 1.0f / (kXScale * kXScale));
   } else {
-    float x[8], dq[8];
+    float x[8], l[8], dq[8];
     eight(diag, dq);
     halves(high, x);
-    if (g.exact) {
-      float l[8];
-      halves(low, l);
+    halves(low, l);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], l[i]);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], l[i]);
     if (!g.diagonal) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -233,7 +230,7 @@ __device__ __forceinline__ void ns_symmetric(const NsTask& g, int p, int q, floa
       if (p == q + i) g.diag_out[p] = d[i], d[i] = 0.0f;
   }
 }
-// a X + B X from B' X (d); high, low: X. In E X, X counts with its first part alone where `early`.
+// a X + B X from B' X (d); high, low: X.
 __device__ __forceinline__ void ns_applied(const NsTask& g, float diag_p, const float* diag, const uint4& high,
                                            const uint4& low, float (&d)[8]) {
   float x[8], l[8], e[8];
@@ -248,7 +245,7 @@ __device__ __forceinline__ void ns_applied(const NsTask& g, float diag_p, const 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float w = __fadd_rn(x[i], l[i]);
-    d[i] = __fmaf_rn(g.a, w, __fmaf_rn(e[i], g.early ? x[i] : w, d[i]));
+    d[i] = __fmaf_rn(g.a, w, __fmaf_rn(e[i], w, d[i]));
   }
 }
 // 8 columns of a row to their place in the transposed chunk: 64 rows of columns, twice 64 of the 128 rows. A
@@ -366,12 +363,15 @@ __device__ __forceinline__ void ns_join(const L& n, int warp, int lane) {
                            pack2(__fsub_rn(d[2], f1.x), __fsub_rn(d[3], f1.y), F16())};
     const int64_t base = at.matrix * g.a_apart, to = base + static_cast<int64_t>(p) * g.a_ld + q;
     st_v2(g.a_at + to, make_uint2(h[0], h[1]));
-    if (g.exact) st_v2(g.a_low_at + to, make_uint2(l[0], l[1]));
-    if (at.p != at.q) {  // (exact shapes have one tile)
+    st_v2(g.a_low_at + to, make_uint2(l[0], l[1]));
+    if (at.p != at.q) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (q + i < side)
-          g.a_at[base + static_cast<int64_t>(q + i) * g.a_ld + p] = static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1)));
+        if (q + i < side) {
+          const int64_t turned = base + static_cast<int64_t>(q + i) * g.a_ld + p;
+          g.a_at[turned] = static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1)));
+          g.a_low_at[turned] = static_cast<uint16_t>(l[i >> 1] >> (16 * (i & 1)));
+        }
     }
   }
 }
@@ -425,11 +425,13 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
       for (int i = 0; i < 2; ++i) {
         tma_prefetch(&g.x[i]);
         tma_prefetch(&g.xt[i]);
-        if (g.exact || g.wide) tma_prefetch(&g.x_low[i]);
-        if (g.exact || !g.wide) tma_prefetch(&g.xt_low[i]);
+        tma_prefetch(&g.x_low[i]);
+        tma_prefetch(&g.xt_low[i]);
       }
       tma_prefetch(&g.a);
       tma_prefetch(&g.b);
+      tma_prefetch(&g.a_low);
+      tma_prefetch(&g.b_low);
     }
     for (int at_op = 0; at_op < ops && alive; ++at_op) {
       const int op = ns_op(at_op, per), from = (at_op / per) & 1;
@@ -444,13 +446,11 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
         const NsShape& g = n.shape[at.shape];
         const int p0 = at.p * TILE + rank * kNsSide, q0 = at.q * TILE + rank * kNsSide;
         const bool p_mn = ns_p_mn(g, op), q_mn = ns_q_mn(g, op);
-        const int stages = ns_stages(g, op), of_part = g.exact ? stages / 3 : stages;
+        const int stages = ns_stages(g, op);
         const int begin = ns_stage(g, join, op, stages, at.part), end = ns_stage(g, join, op, stages, at.part + 1);
-        const int parts = g.exact ? 3 : 1;
-        for (int part = 0; part < parts && alive; ++part) {
-          // (the stages of this product that are this tile's)
-          const int from_k = max(begin - part * of_part, 0) * kNsStep, to_k = min(end - part * of_part, of_part) * kNsStep;
-          const bool p_low = part == 2, q_low = part == 1;
+        // (the two small products first: each step cuts the running sum to fp32)
+        for (int part = 0; part < kNsProducts && alive; ++part) {
+          const bool p_low = part == 0, q_low = part == 1;
           const CUtensorMap *p, *q;
           if (op == kNsGram) {
             p = p_low ? &g.x_low[from] : &g.x[from], q = q_low ? &g.x_low[from] : &g.x[from];
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
             p = p_low ? &g.b_low : &g.b, q = q_low ? &g.xt_low[from] : &g.xt[from];
             if (!g.wide) p = p_low ? &g.xt_low[from] : &g.xt[from], q = q_low ? &g.b_low : &g.b;
           }
-          for (int k = from_k; k < to_k; k += kNsStep) {
+          for (int k = begin * kNsStep; k < end * kNsStep; k += kNsStep) {
             tc_wait(&empty[r.at], r.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
             if (!alive) break;
             uint8_t* stage = smem + r.at * kNsStage;
@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
         const uint32_t base = smem_addr(smem), to = tmem + s.at * TILE;
         const uint64_t p_desc = ns_operand(base, p_mn), q_desc = ns_operand(base + kNsOperand, q_mn);
         const uint64_t p_step = p_mn ? 2048 >> 4 : 32 >> 4, q_step = q_mn ? 2048 >> 4 : 32 >> 4;
-        const int whole = ns_stages(g, op),
-                  stages = ns_stage(g, join, op, whole, tile.part + 1) - ns_stage(g, join, op, whole, tile.part);
+        const int whole = ns_stages(g, op), stages = kNsProducts * (ns_stage(g, join, op, whole, tile.part + 1) -
+                                                                    ns_stage(g, join, op, whole, tile.part));
         tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
         bool there = false;  // the stage has been seen already
         for (int k = 0; k < stages; ++k) {
@@ -577,20 +577,17 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
           s.next();
           continue;
         }
-        task.exact = held_in_register(g.exact);
         task.wide = held_in_register(g.wide);
         const int side = held_in_register(task.wide ? g.rows : g.cols);
-        task.early = step < n.steps - 3 && !task.exact;
         task.diagonal = at.p == at.q;
         task.diag_out = held_in_register((op == kNsGram ? g.a_diag : g.b_diag) +
                                          static_cast<int64_t>(at.matrix) * g.diag_apart);
         const int rows = op == kNsApply ? held_in_register(g.rows) : side,
                   cols = op == kNsApply ? held_in_register(g.cols) : side;
-        // (exact shapes have one tile, so a chunk's second part is free where a tile goes transposed)
         const bool turn = op != kNsApply && !task.diagonal;
-        const CUtensorMap* turned = op == kNsGram ? &g.a_turned : &g.b_turned;
+        const CUtensorMap *turned = op == kNsGram ? &g.a_turned : &g.b_turned,
+                          *turned_low = op == kNsGram ? &g.a_turned_low : &g.b_turned_low;
         const int p0 = at.p * TILE + rank * kNsSide, p = p0 + row;
-        const bool lows = op == kNsApply || task.exact;  // the chunk's second part is in use
         const CUtensorMap *in, *in_low, *out, *out_low;
         if (op == kNsApply) {
           in = g.wide ? &g.x[from] : &g.xt[from], in_low = g.wide ? &g.x_low[from] : &g.xt_low[from];
@@ -608,9 +605,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
           if (!leader || !alive || p0 >= rows || q0 >= cols) return;
           tma_store_wait_read();
           if (op == kNsGram) return;
-          mbar_arrive_expect_tx(&held[half], (lows ? 2 : 1) * kNsHalfChunk + (by_q ? kNsChunk * 4 : 0));
+          mbar_arrive_expect_tx(&held[half], 2 * kNsHalfChunk + (by_q ? kNsChunk * 4 : 0));
           tma_load(high, in, q0, p0, at.matrix, &held[half]);
-          if (lows) tma_load(low, in_low, q0, p0, at.matrix, &held[half]);
+          tma_load(low, in_low, q0, p0, at.matrix, &held[half]);
           if (by_q) bulk_load(diag_q, diag + q0, kNsChunk * 4, &held[half]);
         };
         float diag_p = 0.0f;
@@ -648,7 +645,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   x[j] = *reinterpret_cast<const uint4*>(ns_place(high, row, h / 8 + j));
-                  if (lows) y[j] = *reinterpret_cast<const uint4*>(ns_place(low, row, h / 8 + j));
+                  y[j] = *reinterpret_cast<const uint4*>(ns_place(low, row, h / 8 + j));
                 }
               }
 #pragma unroll
@@ -660,7 +657,6 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
                 if (op != kNsApply) {
                   ns_symmetric(task, p, q0 + h + 8 * j, diag_p, diag_q + h + 8 * j, x[j], y[j], d);
                   two_halves(d, w, l);
-                  if (turn) ns_turn(low, row, h + 8 * j, w);
                 } else {
                   ns_applied(task, diag_p, diag_q + h + 8 * j, x[j], y[j], d);
                   if (last) {
@@ -677,7 +673,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
                   }
                 }
                 *reinterpret_cast<uint4*>(ns_place(high, row, h / 8 + j)) = w;
-                if (lows) *reinterpret_cast<uint4*>(ns_place(low, row, h / 8 + j)) = l;
+                *reinterpret_cast<uint4*>(ns_place(low, row, h / 8 + j)) = l;
               }
             }
           }
@@ -692,12 +688,31 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
             named_barrier(2 + half, 128);
             if (leader) {
               tma_store(out, q0, p0, at.matrix, high);
-              if (lows) tma_store(out_low, q0, p0, at.matrix, low);
-              if (turn) {
-                tma_store(turned, p0, q0, at.matrix, low);
-                if (p0 + 64 < rows) tma_store(turned, p0 + 64, q0, at.matrix, low + kNsHalfChunk / 2);
-              }
+              tma_store(out_low, q0, p0, at.matrix, low);
               tma_store_commit();
+            }
+            if (turn) {  // the chunk once more, transposed where it lies: every thread takes its row out first
+              if (leader) tma_store_wait_read();
+              named_barrier(2 + half, 128);
+#pragma unroll
+              for (int of = 0; of < 2; ++of) {
+                uint8_t* chunk = of == 0 ? high : low;
+                uint4 x[kNsChunk / 8];
+#pragma unroll
+                for (int j = 0; j < kNsChunk / 8; ++j) x[j] = *reinterpret_cast<const uint4*>(ns_place(chunk, row, j));
+                named_barrier(2 + half, 128);
+#pragma unroll
+                for (int j = 0; j < kNsChunk / 8; ++j) ns_turn(chunk, row, 8 * j, x[j]);
+              }
+              tma_store_fence();
+              named_barrier(2 + half, 128);
+              if (leader) {
+                for (int i = 0; i < 2 && p0 + 64 * i < rows; ++i) {
+                  tma_store(turned, p0 + 64 * i, q0, at.matrix, high + i * (kNsHalfChunk / 2));
+                  tma_store(turned_low, p0 + 64 * i, q0, at.matrix, low + i * (kNsHalfChunk / 2));
+                }
+                tma_store_commit();
+              }
             }
           }
         }

@@ -11,8 +11,6 @@ namespace zpp {
 // X is held times 2^10, so that fp16 keeps its 11 bits down to elements of 2^-24; what rounding it
 // to fp16 lost is held in a second fp16.
 constexpr float kXScale = 1024.0f;
-// Matrices whose smaller side is at most this are worked on with products of both fp16.
-constexpr int kNsExactSide = 128;
 
 // The products of a step, in their order.
 enum NsOp : int32_t {
@@ -23,17 +21,16 @@ enum NsOp : int32_t {
 };
 constexpr int kNsMaxSteps = 100;
 
-// The matrices of one shape. Matrices of fp16 come in pairs: the nearest values and (`low`) what those
-// lost; A's and B's `low` only for exact ones.
+// The matrices of one shape. Matrices of fp16 come in pairs: the nearest values and (`low`) what those lost.
 struct NsShape {
   CUtensorMap x[2], x_low[2];    // X as the gram reads it: rows along the sum if wide, else across it
   CUtensorMap xt[2], xt_low[2];  // X as the apply reads it: the other way round
   CUtensorMap a, a_low, b, b_low;
-  CUtensorMap a_turned, b_turned;  // for a tile's transposed place: boxes of 64 rows
+  CUtensorMap a_turned, a_turned_low, b_turned, b_turned_low;  // for a tile's transposed place: boxes of 64 rows
   uint16_t *a_at, *a_low_at;     // as a_ld and a_apart: for the join
   float *a_diag, *b_diag;        // fp32; the fp16 matrices hold zeros there
   int32_t rows, cols, diag_apart;
-  int32_t wide, exact;           // rows <= cols; products of both parts
+  int32_t wide;                  // rows <= cols
   int32_t count, first_matrix;   // in the batch
   int32_t side_tiles;            // of A's side
   int32_t row_tiles, col_tiles;  // of X
