@@ -208,21 +208,18 @@ struct Batch {
   int64_t elems = 0;
 };
 // How K14 takes a batch: the side of its tiles, 256 by a pair of CTAs, or 128, which share themselves out more
-// evenly; and into how many parts a gram's sum is split. Once where its tiles leave most CTAs without work
-// (worth the pass that joins them, 5 us, from 48 stages on: 100 x 6000 in five steps 460 us without), and
-// always after 512 stages of a product: the matrix unit cuts its running sum in each of a stage's four steps, so
-// a sum of squares falls short by some 2^-26 of itself a step (4 million rows: the result 0.25 % off).
+// evenly; and into how many parts a gram's sum is split where its tiles leave most CTAs without work (worth
+// the pass that joins them, 5 us, from 48 stages on: 100 x 6000 in five steps 460 us without).
 // A stage takes either side about as long (0.3 us): counted are those of the slowest CTA.
 struct Plan {
   int side = 128, share = 1;
   int64_t parts = 0;  // of tiles, in the gram
   bool join = false;
+  bool runs = false;  // some sum takes more than one
 };
-// Stages of the three products together.
-int64_t stages_of(int64_t depth) { return 3 * ((depth + 63) / 64); }
+int64_t stages_of(int64_t depth) { return kNsProducts * ((depth + 63) / 64); }
 int64_t split_of(const Shape& s, const Plan& p) {
-  const int64_t n = stages_of(std::max(s.rows, s.cols));
-  return std::max((n + 1535) / 1536, std::min<int64_t>(p.share, n / 8));
+  return std::max<int64_t>(1, std::min<int64_t>(p.share, stages_of(std::max(s.rows, s.cols)) / 8));
 }
 Plan plan_of(const Batch& b) {
   Plan best;
@@ -246,6 +243,7 @@ Plan plan_of(const Batch& b) {
       symmetric += s.count * (m * (m + 1) / 2);
       stages = std::max(stages, stages_of(large));
     }
+    p.runs = stages > kNsProducts * kNsRun;
     if (2 * symmetric <= at_once && stages >= 48)
       p.share = static_cast<int>(std::min<int64_t>({at_once / symmetric, stages / 8, 16}));
     for (const Shape& s : b.shapes) {
@@ -270,6 +268,7 @@ int64_t bytes_of(const Batch& b) {
   for (const Shape& s : b.shapes) n += s.bytes();
   const Plan p = plan_of(b);
   if (p.join) n += p.parts * p.side * p.side * 4;
+  if (p.runs) n += ns_run_floats(p.side) * 4;
   return n + static_cast<int64_t>(b.order.size()) * kMuonPartials * 4;
 }
 constexpr int64_t kBatchElems = int64_t{1} << 28;  // more than this starts another batch
@@ -408,6 +407,7 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
   n.factor = a.factor;
   n.arrived = t.arrived;
   n.partial = parts;
+  n.runs = parts + (plan.join ? plan.parts * side * side : 0);
   for (int i = 0; i < 3 * a.steps; ++i) n.coefficients[i] = static_cast<float>(a.coefficients[i]);
   for (size_t i = 0; i < b.order.size(); ++i) n.result[i] = NsResult{list[b.order[i]].param, list[b.order[i]].out};
   for (size_t k = 0; k < b.shapes.size(); ++k) {

@@ -7,21 +7,21 @@
 // to what that lost. A product takes three of the unit's: first by first part, first by second, second by first.
 // What the steps lose early they multiply by up to 3.4^5, so one 16-bit part is poor: bf16 leaves 1.1e-2 of the
 // result's norm in error on normal values of 512 x 1024, fp16 1.3e-3, and 4.6e-2 and 6.8e-3 where singular values lie
-// over four decades. One part with the diagonals apart, as below, leaves 0.2e-3 .. 1.1e-3 in 1/2.7 of the time,
-// several times the rounding of an fp16 result; two leave 1e-6 .. 3e-6, as fp32 operands do.
+// over four decades. One part with the diagonals apart, as below, leaves 0.2e-3 .. 1.1e-3 in 1/2.8 of the time,
+// several times the rounding of an fp16 result; two leave 2e-6 (256 x 1024) .. 1e-5 (4096 x 16384), as fp32 products do.
 //
 // The diagonals of A and B are kept in fp32 and enter elementwise:
 //   A = A' + D,  A A = A' A' + D A' + A' D + D D,  B X = B' X + E X
 // A' and B' are small beside them, and so is what their rounding and X's leaves.
 //
 // The two products with a second part come first in a sum: the matrix unit cuts the running sum to fp32 in each of
-// its steps, and what is cut is in proportion to it.
+// its steps, and what is cut is in proportion to it. It adds up a limited number of steps in a row (kNsRun).
 //
 // Tiles of 128 x 128, or of 256 x 256 by a pair of CTAs, a stage 64 steps of a product (5 stages of 32 KB), the sums
 // of two tiles in tensor memory, so that one is taken while the next is made. Large matrices are bound
-// by the matrix unit at the clock that the power limit leaves (4096 x 16384: 8.8 ms, 1.5 PFLOP/s of the three
+// by the matrix unit at the clock that the power limit leaves (4096 x 16384: 9.1 ms, 1.5 PFLOP/s of the three
 // products); sides of 1024 by what a CTA can take in (64 bytes a clock); small ones by the way from one product to
-// the next (256 x 1024: 15 of them 193 us).
+// the next (256 x 1024: 15 of them 195 us).
 //
 // A and B are symmetric: only tiles on and above the diagonal are computed, and stored twice (the second time
 // turned in shared memory, where the tile lies). Where X is long
@@ -41,7 +41,6 @@ constexpr int kNsSide = 128, kNsStep = 64;  // rows of an operand in a CTA, step
 constexpr int kNsOperand = kNsSide * kNsStep * 2;
 constexpr int kNsStage = 2 * kNsOperand;
 constexpr int kNsStages = 5;
-constexpr int kNsProducts = 3;  // of two factors in two fp16 each: all but that of what both lost
 // Results go through shared memory: 128 rows of 64 columns at a time, of each half of the tile's columns,
 // as 16-bit values and what those lost, laid out as a tensor copy lays them.
 constexpr int kNsChunk = 64, kNsHalfChunk = kNsSide * kNsChunk * 2;
@@ -246,6 +245,20 @@ __device__ __forceinline__ void ns_applied(const NsTask& g, float diag_p, const 
   for (int i = 0; i < 8; ++i) {
     const float w = __fadd_rn(x[i], l[i]);
     d[i] = __fmaf_rn(g.a, w, __fmaf_rn(e[i], w, d[i]));
+  }
+}
+// 32 columns of a row from where the runs before left them, added to this run's.
+__device__ __forceinline__ void add_run(const float* from, uint32_t (&v)[32]) {
+  uint4 f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const uint4*>(from + i * kNsSide * 4);
+  const auto add = [](uint32_t a, uint32_t b) { return __float_as_uint(__fadd_rn(__uint_as_float(a), __uint_as_float(b))); };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[4 * i] = add(f[i].x, v[4 * i]);
+    v[4 * i + 1] = add(f[i].y, v[4 * i + 1]);
+    v[4 * i + 2] = add(f[i].z, v[4 * i + 2]);
+    v[4 * i + 3] = add(f[i].w, v[4 * i + 3]);
   }
 }
 // 8 columns of a row to their place in the transposed chunk: 64 rows of columns, twice 64 of the 128 rows. A
@@ -491,35 +504,40 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
         const NsShape& g = n.shape[tile.shape];
         const bool p_mn = ns_p_mn(g, op), q_mn = ns_q_mn(g, op);
         const uint32_t instr = tc_instruction(TILE, TILE, 0, 0, p_mn, q_mn);
-        const uint32_t base = smem_addr(smem), to = tmem + s.at * TILE;
+        const uint32_t base = smem_addr(smem);
         const uint64_t p_desc = ns_operand(base, p_mn), q_desc = ns_operand(base + kNsOperand, q_mn);
         const uint64_t p_step = p_mn ? 2048 >> 4 : 32 >> 4, q_step = q_mn ? 2048 >> 4 : 32 >> 4;
-        const int whole = ns_stages(g, op), stages = kNsProducts * (ns_stage(g, join, op, whole, tile.part + 1) -
-                                                                    ns_stage(g, join, op, whole, tile.part));
-        tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
+        const int whole = ns_stages(g, op),
+                  each = ns_stage(g, join, op, whole, tile.part + 1) - ns_stage(g, join, op, whole, tile.part),
+                  stages = kNsProducts * each;
         bool there = false;  // the stage has been seen already
-        for (int k = 0; k < stages; ++k) {
-          // (the first copies of a product come when it begins)
-          if (!there) tc_wait_long(&full[r.at], r.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
-          if (!__all_sync(~0u, alive)) {
-            alive = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t at = static_cast<uint64_t>(r.at * (kNsStage >> 4));
-          uint64_t* use = &empty[r.at];
-          r.next();
-          there = mbar_test(&full[r.at], r.phase);
-          if (elect_one()) {
+        for (int run = 0, end; run < stages && alive; run = end) {
+          end = min((run == 0 ? stages - each : run) + kNsRun, stages);
+          const uint32_t to = tmem + s.at * TILE;
+          tc_wait(&taken[s.at], s.phase ^ 1u, alive, &g_muon_fault, kMuonFault);
+          for (int k = run; k < end; ++k) {
+            // (the first copies of a product come when it begins)
+            if (!there) tc_wait_long(&full[r.at], r.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
+            if (!__all_sync(~0u, alive)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t at = static_cast<uint64_t>(r.at * (kNsStage >> 4));
+            uint64_t* use = &empty[r.at];
+            r.next();
+            there = mbar_test(&full[r.at], r.phase);
+            if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tc_mma_f16<CTAS>(to, p_desc + at + j * p_step, q_desc + at + j * q_step, instr, k > 0 || j > 0);
-            tc_commit_to<CTAS>(use);
-            if (k + 1 == stages) tc_commit_to<CTAS>(&summed[s.at]);
+              for (int j = 0; j < 4; ++j)
+                tc_mma_f16<CTAS>(to, p_desc + at + j * p_step, q_desc + at + j * q_step, instr, k > run || j > 0);
+              tc_commit_to<CTAS>(use);
+              if (k + 1 == end) tc_commit_to<CTAS>(&summed[s.at]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          s.next();
         }
-        s.next();
       }
     }
     if (!alive) {
@@ -537,6 +555,8 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
     float* diag_q = reinterpret_cast<float*>(smem + kNsDiag) + half * kNsChunk;
     const bool leader = row == 0;  // of the 4 warps of a half
     const bool skip = n.factor && !isfinite(ld_after_f32(n.factor));
+    // this thread's place among the sums that runs leave: [columns / 4][rows][4] for a CTA
+    float* const runs = n.runs + static_cast<int64_t>(blockIdx.x) * kNsSide * TILE + (half * (HALF / 4) * kNsSide + row) * 4;
     unsigned held_phase = 0;
     Ring<kNsSlots> s;
     for (int at_op = 0; at_op < ops; ++at_op) {
@@ -554,6 +574,32 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
       for (int t = first; t < tiles; t += apart) {
         const NsTile at = ns_tile(n, join, op, t);
         const NsShape& g = n.shape[at.shape];
+        const int whole = ns_stages(g, op),
+                  each = ns_stage(g, join, op, whole, at.part + 1) - ns_stage(g, join, op, whole, at.part);
+        // All runs of a long sum but the last, added up.
+        for (int run = kNsRun; run < each; run += kNsRun) {
+          tc_wait_long(&summed[s.at], s.phase, alive, &g_muon_fault, kMuonFault, kGridWaitClocks);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HALF; c += 32) {
+            uint32_t v[32];
+            tmem_ld(lanes + s.at * TILE + c, v);
+            tmem_ld_wait(v);
+            float* to = runs + (c / 4) * kNsSide * 4;
+            if (run > kNsRun) add_run(to, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(to + i * kNsSide * 4) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CTAS == 2) mbar_arrive_cluster(taken_at + 8 * s.at);
+            else mbar_arrive(&taken[s.at]);
+          }
+          s.next();
+        }
+        const bool more = each > kNsRun;
         if (join && op == kNsGram && g.split > 1) {  // a part of a tile's sums, as they are
           float* to = n.partial + static_cast<int64_t>(t) * TILE * TILE +
                       (half * (HALF / 4) * TILE + rank * kNsSide + row) * 4;
@@ -564,6 +610,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
             uint32_t v[32];
             tmem_ld(lanes + s.at * TILE + c, v);
             tmem_ld_wait(v);
+            if (more) add_run(runs + (c / 4) * kNsSide * 4, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               st_v4(to + (c / 4 + i) * TILE * 4, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
@@ -639,6 +686,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
                 else mbar_arrive(&taken[s.at]);
               }
             }
+            if (more) add_run(runs + ((k * kNsChunk + h) / 4) * kNsSide * 4, v);
             if (inside && p < rows) {
               uint4 x[4], y[4];  // (all read before the first is written: they are places of one buffer)
               if (op != kNsGram) {
@@ -740,7 +788,7 @@ template <int CTAS, bool join, typename L>
 static cudaError_t run_ns(const L& n, cudaStream_t s) {
   auto kern = k_newton_schulz<CTAS, join, L>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(152);
+  cfg.gridDim = dim3(kNsCtas);
   cfg.blockDim = dim3(kTensorThreads);
   cfg.dynamicSmemBytes = kNsSmem;
   cfg.stream = s;
@@ -767,6 +815,7 @@ static cudaError_t run_ns(const L& n, cudaStream_t s) {
   }
   int tiles = n.tiles[1];
   for (int i = 0; i < 3; ++i) tiles = n.tiles[i] > tiles ? n.tiles[i] : tiles;
+  fit = fit < kNsCtas / CTAS ? fit : kNsCtas / CTAS;
   cfg.gridDim = dim3(static_cast<unsigned>((tiles < fit ? tiles : fit) * CTAS));
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, n);
@@ -780,7 +829,7 @@ cudaError_t launch_ns(const NsLaunch& n, int side, cudaStream_t s) {
   const NsShape& last = n.shape[n.shapes - 1];
   if (n.shapes > 2 || last.first_matrix + last.count > 32) return run_ns(n, side, s);
   NsLaunchFew few;  // (a launch's parameters are copied by the driver)
-  few.steps = n.steps, few.shapes = n.shapes, few.join = n.join, few.partial = n.partial;
+  few.steps = n.steps, few.shapes = n.shapes, few.join = n.join, few.partial = n.partial, few.runs = n.runs;
   for (int i = 0; i < 3; ++i) few.tiles[i] = n.tiles[i];
   few.out_kind = n.out_kind, few.decay = n.decay, few.factor = n.factor, few.arrived = n.arrived;
   for (int i = 0; i < 3 * n.steps; ++i) few.coefficients[i] = n.coefficients[i];

@@ -12,6 +12,17 @@ namespace zpp {
 // to fp16 lost is held in a second fp16.
 constexpr float kXScale = 1024.0f;
 
+constexpr int kNsProducts = 3;  // of two factors in two fp16 each: all but that of what both lost
+// Stages of the product of first parts that the matrix unit adds up in a row, at most. It cuts the running sum to
+// fp32 in each of a stage's four steps, by up to 2^-23 of it, and a gram's diagonal, a sum of squares, falls short by
+// as much; the steps multiply that by ten. So the sums of several runs are added by the warps that take them, in the
+// workspace, rounded to nearest. (4096 x 16384, normal values, against 64 bits: 1.0e-5 of the result, as much as by
+// fp32 products; 1e-4 in one run; 7e-6 in runs of half the length, 8 % slower.) The products with second parts are
+// small and go with the first run.
+constexpr int kNsRun = 32;
+constexpr int kNsCtas = 152;  // at most
+constexpr int64_t ns_run_floats(int side) { return int64_t{kNsCtas} * 128 * side; }  // of all CTAs' tiles
+
 // The products of a step, in their order.
 enum NsOp : int32_t {
   kNsGram = 0,   // A = X X^T (or X^T X): the smaller of the two, symmetric
@@ -50,6 +61,7 @@ struct NsLaunchOf {
   int32_t steps, shapes, tiles[3];  // of the poly, of the apply, and parts of tiles of the gram
   int32_t join;                     // some shape's sums are split
   float* partial;                   // [parts of tiles][columns / 4][rows][4], where they are
+  float* runs;                      // ns_run_floats(), where a sum takes more than one run
   int32_t out_kind;
   float decay;
   const float* factor;

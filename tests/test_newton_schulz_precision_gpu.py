@@ -14,7 +14,7 @@ the root mean square of F's difference quotients: between two singular values, b
 negative, and between one and 0 for the n - s directions that X lacks.
 Cuts, of one direction: a sum's running value is cut to fp32 in each of its K / 16 steps, by 2^-24 of itself in the
 mean, half of its end in the mean, so a sum of squares falls short by d(K) = (K / 16) 2^-25 of itself (K up
-to a multiple of 64). With t a singular value: A by d(n) t^2, which is d(n) (b t^3 + 2 c t^5) of the next X, A A by d(s) t^4
+to a multiple of 64, and 2048 at most: longer sums are added up from such ones by fp32 additions). With t a singular value: A by d(n) t^2, which is d(n) (b t^3 + 2 c t^5) of the next X, A A by d(s) t^4
 and B X by d(s) (b t^3 + c t^5); the steps after it multiply that by F'.
 All are added up, and 3 times their sum is allowed: roundings are not all independent."""
 import math
@@ -53,7 +53,7 @@ def lost(x, coefficients, eps=1e-7):
     y = y / max(norm(y), eps)
     s, n = y.shape
     h, rs = 2.0 ** -22 / 3, s ** 0.5
-    cut = lambda k: math.ceil(k / 64) * 4 * 2.0 ** -25  # noqa: E731
+    cut = lambda k: min(math.ceil(k / 64), 32) * 4 * 2.0 ** -25  # noqa: E731
     low = (s * n) ** 0.5 * 2.0 ** -35
     total = (h * norm(y) + low) * growth(torch.linalg.svdvals(y), n, coefficients)
     for k, (a, b, c) in enumerate(coefficients):
@@ -110,3 +110,37 @@ def test_result_has_its_types_error():
         x = matrix(rows, cols, rows, kind).half()
         want = exact(x, (USUAL,) * 5)
         assert norm(zpp.orthogonalize(x).double() - want) <= 3 ** -0.5 * 2.0 ** -11 * norm(want)
+
+
+@pytest.mark.parametrize("rows,cols", [(4096, 65536), (65536, 4096), (4096, 4096)])
+def test_sums_of_any_length(rows, cols):
+    """Rows of a Hadamard matrix, all of one singular value, so that the result is the matrix times F(s) / s: what the
+    sums' cuts leave shows as a factor. The terms of a sum are one number, so every step of 16 may cut it by nearly a
+    whole unit, 2^-23 of the running sum, which is half of its end in the mean: A is short by up to d = 128 * 2^-24 after
+    the 128 steps that are made in a row, the next s is a s + b s^3 (1 - d) + c s^5 (1 - d)^2, and B X is short by d as
+    well. The fp16 pairs and the fp32 results leave 4 * 2^-22 of each step."""
+    n, m = max(rows, cols), min(rows, cols)
+    i, j = torch.arange(m, device=DEV)[:, None], torch.arange(n, device=DEV)
+    bits = i & j
+    for shift in (8, 4, 2, 1):
+        bits = bits ^ (bits >> shift)
+    x = (1 - 2 * (bits & 1)).half()
+    del bits
+    x = x if rows <= cols else x.t().contiguous()
+
+    def size(short, each):
+        a, b, c = USUAL
+        s = m ** -0.5
+        for _ in range(5):
+            g = s * s * (1 - short)
+            s = (a + (b * g + c * g * g) * (1 - short)) * s * (1 + each)
+        return s
+
+    want = size(0.0, 0.0)
+    d = 128 * 2.0 ** -24
+    off = max(abs(size(e * d, f * 4 * 2.0 ** -22) - want) for e in (0, 1) for f in (-1, 1))
+    p = torch.zeros(rows, cols, device=DEV)
+    zpp.Muon([p], lr=1.0, momentum=0.0, weight_decay=0.0, nesterov=False, adjust="none").step([x])
+    got = -p.double() * x.double() * n ** 0.5  # (entries of X are s / sqrt(n))
+    assert abs(float(got.mean()) - want) <= off
+    assert norm(got - want) <= 2 * off * got.numel() ** 0.5
