@@ -18,6 +18,7 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/Exception.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -51,8 +52,13 @@ bool plain(PyObject* o) {
   return THPVariable_Check(o) && THPVariable_Unpack(o).layout() == at::kStrided;
 }
 
-// Python's exception for `e`: torch's own where memory ran out, as its allocations in Python raise it.
+// Python's exception for `e`: torch's own where memory ran out, as its allocations in Python raise it, and one that
+// Python code raised on the way (a hook on saved tensors; checkpoints stop a recomputation with one) as it is.
 void set_error(const std::exception& e) {
+  if (const auto* raised = dynamic_cast<const python_error*>(&e)) {
+    python_error(*raised).restore();
+    return;
+  }
   const auto* memory = dynamic_cast<const c10::OutOfMemoryError*>(&e);
   PyObject* torch = memory ? PyImport_ImportModule("torch") : nullptr;
   PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
