@@ -518,6 +518,22 @@ at::Tensor product(MatmulFp8 fn, const at::Tensor& a, const at::Tensor& a_scales
          "zpp_matmul_fp8");
   return y;
 }
+// What the graph kept of a matrix [rows, cols], as a product takes it. Hooks may have put copies in its place: those of
+// codes come back from the host without the padding of their rows, and are laid out again.
+Coded kept(const at::Tensor& codes, const at::Tensor& scales, int64_t rows, int64_t cols, int64_t tile, long device) {
+  const std::vector<int64_t> shape{rows, cols}, of_scales{tile == 1 ? rows : blocks_of(rows), blocks_of(cols)};
+  TORCH_CHECK(codes.defined() && scales.defined() && kind_of(codes) == 4 && kind_of(scales) == ZPP_F32 &&
+                  gpu_of(codes) == device && gpu_of(scales) == device && codes.sizes() == shape &&
+                  scales.sizes() == of_scales,
+              "linear_fp8: a saved tensor came back with another shape, type or device");
+  const bool fits = (cols == 1 || codes.stride(1) == 1) &&
+                    (rows == 1 || (codes.stride(0) >= cols && codes.stride(0) % 16 == 0)) &&
+                    reinterpret_cast<uintptr_t>(codes.data_ptr()) % 16 == 0;
+  if (fits) return {codes, scales};
+  at::Tensor again = new_codes(shape, codes.options());
+  again.copy_(codes);
+  return {again, scales};
+}
 // A captured backward pass cannot hand a gradient to the default stream, which takes no part in captures. It
 // would have to where the tensor's place in the graph was made there and is still held, by an eager
 // pass of the same leaf for one; the engine's own failure at that point ends the process.
@@ -592,12 +608,16 @@ struct Linear : torch::autograd::Function<Linear> {
       Coded q, qt;
       if (!empty)
         demand(quantise(quant_fn, dy.reshape({count, n}).contiguous(), 1, q, for_w ? &qt : nullptr), "zpp_quant_fp8");
-      if (for_x)
-        out[0] = empty ? at::zeros(shape, dy.options().dtype(x_type))
-                       : product(matmul_fn, q.codes, q.scales, 1, saved[0], saved[1], 128, x_type).view(shape);
-      if (for_w)
-        out[1] = empty ? at::zeros({n, k}, dy.options().dtype(w_type))
-                       : product(matmul_fn, qt.codes, qt.scales, 1, saved[2], saved[3], 1, w_type);
+      if (for_x && empty) out[0] = at::zeros(shape, dy.options().dtype(x_type));
+      if (for_w && empty) out[1] = at::zeros({n, k}, dy.options().dtype(w_type));
+      if (for_x && !empty) {
+        const Coded wt = kept(saved[0], saved[1], k, n, 128, gpu_of(dy));
+        out[0] = product(matmul_fn, q.codes, q.scales, 1, wt.codes, wt.scales, 128, x_type).view(shape);
+      }
+      if (for_w && !empty) {
+        const Coded xt = kept(saved[2], saved[3], k, count, 1, gpu_of(dy));
+        out[1] = product(matmul_fn, qt.codes, qt.scales, 1, xt.codes, xt.scales, 1, w_type);
+      }
     }
     if (twice) {  // differentiable once: a derivative of these raises
       auto error = std::make_shared<torch::autograd::DelayedError>(
