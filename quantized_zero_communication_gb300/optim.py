@@ -261,7 +261,8 @@ class Muon:
         shapes). max_norm, pre_scale, grad_scale and what is returned: as AdamW.step; a factor that is
         not finite leaves parameters, weights and momenta as they were. (The direction of an update
         does not depend on the gradients' scale, but what they weigh in the momentum does.) lr replaces
-        the optimiser's for this step and the following ones."""
+        the optimiser's for this step and the following ones. A graph that kept a parameter's, weight's or
+        momentum's values of before the step raises in its backward pass."""
         torch = _b._torch()
         grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
         self._gather()
@@ -283,6 +284,7 @@ class Muon:
         work = torch.empty(max(self._work, 0), dtype=torch.uint8, device=self.params[0].device)
         _b._launch(self._device, "zpp_muon_step", ctypes.addressof(self._table), len(self._table), kind,
                    self._w_kind, ctypes.addressof(hp), scale, work.data_ptr())
+        _b._written(*self.params, *self.buffers, *(self.weights or ()))
         return norm
 
     def state(self):
