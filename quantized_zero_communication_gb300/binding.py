@@ -972,7 +972,7 @@ def quant_fp8(x, tile=1, transposed=False, out=None):
 
     transposed: also (codes_t [cols, rows], scales_t) of the transposed matrix, made in the same pass.
     With tile 1 its blocks are 128 rows of a column; with tile 128 scales_t is a view of scales. out: the
-    buffers to write, a tuple as an earlier call returned it."""
+    buffers to write, a tuple as an earlier call returned it. Codes and scales carry no gradient to x."""
     if out is None:
         made = _tensors().quant_fp8(_address("zpp_quant_fp8"), x, tile, transposed)
         if made is not None:
@@ -1021,8 +1021,15 @@ def quant_fp8(x, tile=1, transposed=False, out=None):
 def matmul_fp8(a, a_scales, b, b_scales, bias=None, dtype=None, y=None):
     """a [..., K] times the transpose of b [N, K], both e4m3 codes with scales as quant_fp8 gives them
     (any fp32 scales of those shapes, any strides) -> y [..., N] of `dtype` (default bf16; fp16 and
-    fp32 too). bias: [N] of y's dtype. y: an output buffer, rows of contiguous elements evenly spaced."""
+    fp32 too). bias: [N] of y's dtype. y: an output buffer, rows of contiguous elements evenly spaced.
+    Not differentiable: an operand that requires a gradient is refused where gradients are recorded
+    (linear_fp8 is the layer; a bias that is trained is added to its result)."""
     torch = _torch()
+    if torch.is_grad_enabled():
+        for name, t in (("bias", bias), ("a", a), ("a_scales", a_scales), ("b", b), ("b_scales", b_scales)):
+            if getattr(t, "requires_grad", False):
+                raise ValueError(f"{name}: requires a gradient, and matmul_fp8 is not differentiable (detach it, or "
+                                 "call under torch.no_grad())")
     if y is None and (dtype is None or dtype in (torch.float16, torch.bfloat16, torch.float32)):
         made = _tensors().matmul_fp8(_address("zpp_matmul_fp8"), a, a_scales, b, b_scales, bias,
                                      ZPP_BF16 if dtype is None else _dt(dtype))
@@ -1087,7 +1094,7 @@ def orthogonalize(x, steps=5, coefficients=NS_COEFFICIENTS, eps=1e-7, dtype=None
     fp32): X = x / max(|x|, eps), then steps of A = X X^T, X = a X + (b A + c A A) X, which brings every
     singular value near 1 (of the transpose where there are more rows than columns). coefficients:
     (a, b, c) for all steps, or a triple for each. Returns new matrices of `dtype`, fp16 or bf16 (default:
-    x's, bf16 for fp32), or fills `out` (which may be x)."""
+    x's, bf16 for fp32), or fills `out` (which may be x). An update's arithmetic, without a gradient to x."""
     torch = _torch()
     single = isinstance(x, torch.Tensor)
     xs = [x] if single else list(x)
