@@ -488,7 +488,8 @@ ZPP_API zpp_status zpp_matmul_fp8(const zpp_fp8_matrix* a, const zpp_fp8_matrix*
  * (for a matrix with more rows than columns the same of its transpose). Every value is held in two fp16
  * (the second one what the first lost), sums and the diagonals of A and B in fp32. After the usual five
  * steps 2e-6 (256 x 1024) to 1e-5 (4096 x 16384) of the result's norm is error, as with fp32 products.
- * Singular values have to stay below 8 through the steps and coefficients below 15 (the usual ones keep to 1.3). |x| beyond fp32's range (of its squares) gives NaN.
+ * Singular values have to stay below 8 through the steps and coefficients below 15 (the usual ones keep to 1.3). Elements
+ * whose squares leave fp32's range upwards (above 1.8e19) give NaN; small ones count whatever their squares are.
  */
 typedef struct zpp_newton_schulz {
   const double* coefficients; /* HOST [steps][3], finite */

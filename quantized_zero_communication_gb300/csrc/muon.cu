@@ -20,6 +20,11 @@ namespace zpp {
 
 constexpr int kMuonPer = kThreads * 8;    // elements of a CTA's round
 constexpr int kMuonPartials = 1024;       // of a matrix, at most
+// Squares of what is below 2^-63 leave fp32's range, and an eps may be as small as 2^-126: a second sum takes values times
+// 2^76, and counts where the first one is below 2^-60 (then none is above 2^-30, so the second one is finite; and
+// above that, what the first one lost is some 2^-150 a value).
+constexpr float kSmallScale = 75557863725914323419136.0f;  // 2^76
+constexpr float kSmallBelow = 1.0f / 1152921504606846976.0f;  // 2^-60
 
 struct MuonTable {
   int32_t count;
@@ -27,7 +32,7 @@ struct MuonTable {
   float mu, one_minus_mu, eps;
   int32_t x_kind;
   const float* factor;
-  float* partial;
+  double* partial;
   uint32_t* arrived;  // K14's count, zeroed by K13
   ChunkHints hints;
   int32_t first[kMuonMatrices + 1];  // CTAs of the matrices before this one
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) k_muon(const __grid_constant__ MuonT
   if constexpr (SCALE) {
     double total = 0.0;
     for (int i = t.first[m] + static_cast<int>(threadIdx.x); i < t.first[m + 1]; i += kThreads)
-      total += static_cast<double>(ld_after_f32(t.partial + i));
+      total += ld_after_f64(t.partial + i);
     total = cta_sum(total, part);
     const float norm = static_cast<float>(sqrt(total));
     // (a norm that is not a number passes through, and so does one that is infinite, as NaN)
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) k_muon(const __grid_constant__ MuonT
   }
   const bool x_vec = (reinterpret_cast<uintptr_t>(it.x) & 15) == 0;
   const bool m_vec = (reinterpret_cast<uintptr_t>(it.momentum) & 15) == 0;
-  float sum = 0.0f;
+  float sum = 0.0f, small = 0.0f;
 #pragma unroll 2
   for (int64_t i = begin + threadIdx.x * 8; i < end; i += kMuonPer) {
     float x[8], u[8];
@@ -150,7 +155,11 @@ __global__ void __launch_bounds__(kThreads) k_muon(const __grid_constant__ MuonT
     }
     if constexpr (!SCALE) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = __fmaf_rn(u[k], u[k], sum);
+      for (int k = 0; k < 8; ++k) {
+        const float up = __fmul_rn(u[k], kSmallScale);
+        sum = __fmaf_rn(u[k], u[k], sum);
+        small = __fmaf_rn(up, up, small);
+      }
     } else {
       uint32_t hi[4], lo[4];
 #pragma unroll
@@ -179,8 +188,9 @@ __global__ void __launch_bounds__(kThreads) k_muon(const __grid_constant__ MuonT
     }
   }
   if constexpr (!SCALE) {
-    const double all = cta_sum(static_cast<double>(sum), part);
-    if (threadIdx.x == 0) t.partial[blockIdx.x] = static_cast<float>(all);
+    constexpr double back = 1.0 / (static_cast<double>(kSmallScale) * static_cast<double>(kSmallScale));
+    const double all = cta_sum(sum < kSmallBelow ? static_cast<double>(small) * back : static_cast<double>(sum), part);
+    if (threadIdx.x == 0) t.partial[blockIdx.x] = all;
   }
 }
 
@@ -269,7 +279,7 @@ int64_t bytes_of(const Batch& b) {
   const Plan p = plan_of(b);
   if (p.join) n += p.parts * p.side * p.side * 4;
   if (p.runs) n += ns_run_floats(p.side) * 4;
-  return n + static_cast<int64_t>(b.order.size()) * kMuonPartials * 4;
+  return n + static_cast<int64_t>(b.order.size()) * kMuonPartials * 8;
 }
 constexpr int64_t kBatchElems = int64_t{1} << 28;  // more than this starts another batch
 
@@ -359,8 +369,8 @@ cudaError_t run_batch(const MuonMatrix* list, const Batch& b, const MuonArgs& a,
   t.eps = std::max(a.eps, std::numeric_limits<float>::min());
   t.x_kind = a.x_kind;
   t.factor = a.factor;
-  t.partial = reinterpret_cast<float*>(at);
-  at += static_cast<int64_t>(b.order.size()) * kMuonPartials * 4;
+  t.partial = reinterpret_cast<double*>(at);
+  at += static_cast<int64_t>(b.order.size()) * kMuonPartials * 8;
   float* parts = reinterpret_cast<float*>(at);  // of K14's split sums
   t.arrived = reinterpret_cast<uint32_t*>(workspace);
   t.first[0] = 0;

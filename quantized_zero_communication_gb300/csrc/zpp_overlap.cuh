@@ -57,6 +57,11 @@ __device__ __forceinline__ float ld_after_f32(const float* p) {
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p) : "memory");
   return r;
 }
+__device__ __forceinline__ double ld_after_f64(const double* p) {
+  double r;
+  asm volatile("ld.global.f64 %0, [%1];" : "=d"(r) : "l"(p) : "memory");
+  return r;
+}
 __device__ __forceinline__ uint16_t ld_after_u16(const uint16_t* p) {
   uint16_t r;
   asm volatile("ld.global.u16 %0, [%1];" : "=h"(r) : "l"(p) : "memory");
