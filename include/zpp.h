@@ -466,8 +466,10 @@ ZPP_API zpp_status zpp_quant_fp8(const void* x, zpp_dtype x_dt, int64_t x_stride
 /*
  * y = a b^T (+ bias): y[m][n] = sum_k a[m][k] b[n][k] (+ bias[n]) of the values that the codes stand
  * for. Sums are fp32: of the codes within a block of 128, then of the blocks times both scales, in
- * ascending order; y is rounded once. The product of two scales may be rounded to fp32 first. NaN codes
- * and non-finite scales give what such values give.
+ * ascending order; y is rounded once. Where there are few tiles of y the blocks are taken in up to 8
+ * parts, each in ascending order, and the parts added in theirs: as the sizes of the call say, so that
+ * the same call gives the same bits, and a row of a may get others beside another number of rows. The product
+ * of two scales may be rounded to fp32 first. NaN codes and non-finite scales give what such values give.
  *   a, b : HOST structs, read during the call; cols is the same in both. One may be the other
  *   bias : NULL or [b.rows] of y_dt
  *   y    : out, [a.rows][b.rows] of y_dt (any zpp_dtype), row m at y + m * y_stride elements,
