@@ -505,8 +505,21 @@ PyObject* matmul_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // The fp8 linear layer as an autograd function: see linear.py.
+// Raises binding.ZppError, as the other calls do (a backward pass runs outside Python: its exception travels as one).
 void demand(zpp_status st, const char* where) {
-  TORCH_CHECK(st == ZPP_OK, where, ": status ", static_cast<int>(st));
+  if (st == ZPP_OK) return;
+  const PyGILState_STATE gil = PyGILState_Ensure();
+  PyObject* binding = PyImport_ImportModule("quantized_zero_communication_gb300.binding");
+  PyObject* type = binding ? PyObject_GetAttrString(binding, "ZppError") : nullptr;
+  PyObject* error = type ? PyObject_CallFunction(type, "is", static_cast<int>(st), where) : nullptr;
+  if (error) PyErr_SetObject(type, error);
+  Py_XDECREF(error);
+  Py_XDECREF(type);
+  Py_XDECREF(binding);
+  python_error raised;
+  raised.persist();
+  PyGILState_Release(gil);
+  throw raised;
 }
 at::Tensor product(MatmulFp8 fn, const at::Tensor& a, const at::Tensor& a_scales, int64_t a_tile,
                    const at::Tensor& b, const at::Tensor& b_scales, int64_t b_tile, at::ScalarType type) {
