@@ -31,8 +31,9 @@ def linear_fp8(x, weight, quantized=None):
             raise ValueError(f"quantized: codes of {tuple(quantized[0].shape)} do not fit weight")
         if len(quantized) == 4 and tuple(quantized[2].shape) != tuple(weight.shape[::-1]):
             raise ValueError("quantized: quant_fp8(weight, 128, transposed=True)")
-        for name, codes, scales, tile in zip(("codes", "codes_t"), quantized[::2], quantized[1::2], (128, 128)):
-            _b._fp8(codes, scales, name, tile)
+        if weight.shape[0]:  # (the codes of a weight without rows have no columns in their transpose)
+            for name, codes, scales, tile in zip(("codes", "codes_t"), quantized[::2], quantized[1::2], (128, 128)):
+                _b._fp8(codes, scales, name, tile)
         quantized = tuple(quantized)
     _b._on_gpu(x, weight, *(quantized or ()))
     return _b._tensors().linear_fp8(_b._address("zpp_quant_fp8"), _b._address("zpp_matmul_fp8"), x, weight,
