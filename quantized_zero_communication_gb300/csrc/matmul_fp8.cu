@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
     tma_prefetch(&p_map);
     tma_prefetch(&q_map);
   }
+  __syncwarp();  // (what follows takes whole warps together)
   if (warp == kCopyWarp) {
     tmem_alloc<CTAS>(tmem_at, G::SLOT * G::SLOTS);
     tmem_alloc_done<CTAS>();
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1)
       }
     }
   }
+  __syncwarp();  // (as do the barrier and the release of tensor memory: the copies were one lane's)
   tc_fence_before();
   if constexpr (CTAS == 2) cluster_sync();
   else __syncthreads();

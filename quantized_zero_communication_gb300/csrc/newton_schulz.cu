@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
     mbar_init(drained, 1);
     mbar_init_fence();
   }
+  __syncwarp();  // (what follows takes whole warps together)
   if (warp == kCopyWarp) {
     tmem_alloc<CTAS>(tmem_at, TILE * kNsSlots);
     tmem_alloc_done<CTAS>();
@@ -775,6 +776,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) k_newton_schulz(const __gri
       }
     }
   }
+  __syncwarp();  // (as do the barrier and the release of tensor memory: the copies were one lane's)
   tc_fence_before();
   if constexpr (CTAS == 2) cluster_sync();
   else __syncthreads();
