@@ -469,7 +469,8 @@ ZPP_API zpp_status zpp_quant_fp8(const void* x, zpp_dtype x_dt, int64_t x_stride
  * ascending order; y is rounded once. Where there are few tiles of y the blocks are taken in up to 8
  * parts, each in ascending order, and the parts added in theirs: as the sizes of the call say, so that
  * the same call gives the same bits, and a row of a may get others beside another number of rows. The product
- * of two scales may be rounded to fp32 first. NaN codes and non-finite scales give what such values give.
+ * of two scales may be rounded to fp32 first, or that of a block's sum and one of them. NaN codes and non-finite
+ * scales give what such values give.
  *   a, b : HOST structs, read during the call; cols is the same in both. One may be the other
  *   bias : NULL or [b.rows] of y_dt
  *   y    : out, [a.rows][b.rows] of y_dt (any zpp_dtype), row m at y + m * y_stride elements,
